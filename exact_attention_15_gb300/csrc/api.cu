@@ -17,6 +17,7 @@
 
 #include "../../include/attn.h"
 #include "attn_common.cuh"
+#include "host.h"
 
 namespace attn {
 cudaError_t launch_attn_fwd(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -505,6 +506,15 @@ bool bwd_plan(int B, int H_q, int H_kv, int N_q, int N_k, int d, bool varlen, bo
 }  // namespace
 
 namespace attn {
+int host_setup(HostDevice* out) {
+  int st = current_device(&out->dev);
+  if (st != ATTN_OK) return st;
+  if ((st = device_setup(out->dev, &out->err)) != ATTN_OK) return st;
+  out->n_sm = sm_count(out->dev);
+  out->encode = g_encode;
+  out->wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+  return out->n_sm > 0 ? ATTN_OK : ATTN_ERR_CUDA;
+}
 int prof_begin(int kernel, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_prof_mu);
   if (!g_prof_on) return -1;
@@ -560,6 +570,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_NO_DEVICE: return "no usable CUDA device";
     case ATTN_ERR_UNSUPPORTED_DEVICE: return "device is not sm_103 (GB300 class)";
     case ATTN_ERR_SEQLENS: return "cu_seqlens is not 0, non-decreasing, ..., N_q";
+    case ATTN_ERR_PAGES: return "a page index or a cache length lies outside the paged cache";
     default: return "unknown status";
   }
 }
@@ -873,7 +884,7 @@ int attn_check(attn_stream_t stream) {
     const int zero = 0;
     if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return ATTN_ERR_CUDA;
-    return h == kErrSeqlens ? ATTN_ERR_SEQLENS : ATTN_ERR_TIMEOUT;
+    return h == kErrSeqlens ? ATTN_ERR_SEQLENS : h == kErrPages ? ATTN_ERR_PAGES : ATTN_ERR_TIMEOUT;
   }
   return ATTN_OK;
 }

@@ -31,8 +31,9 @@ constexpr float kTau = ATTN_TAU;
 #endif
 
 // Device error word values (the first failure is kept): a bounded wait ran
-// out; a packed-sequence offset array is not 0, non-decreasing, ..., T.
-enum DevErr : int { kErrNone = 0, kErrTimeout = 1, kErrSeqlens = 2 };
+// out; a packed-sequence offset array is not 0, non-decreasing, ..., T; a page
+// table or a cache length points outside the paged cache.
+enum DevErr : int { kErrNone = 0, kErrTimeout = 1, kErrSeqlens = 2, kErrPages = 3 };
 // Host-injected faults (attn_debug_inject); none of them can fault or hang the GPU.
 enum Fault : int { kFaultNone = 0, kFaultSkipDqRelease = 1 };
 
@@ -93,7 +94,8 @@ struct BwdParams {
 // returns a slot (or -1 when tracing is off); prof_end closes it.
 enum KernelId : int { kKFwd = 1, kKBwdPre = 2, kKBwdMain = 3, kKBwdPost = 4, kKExp2 = 5,
                       kKStall = 6, kKFwdPlan = 7, kKFwdPair = 8, kKBwdMain2 = 9,
-                      kKBwdPlan = 10 };
+                      kKBwdPlan = 10, kKPagedAppend = 11, kKPagedDecode = 12, kKPagedJoin = 13,
+                      kKPagedFwd = 14, kKPagedPlan = 15 };
 int prof_begin(int kernel, cudaStream_t stream);
 void prof_end(int slot, cudaStream_t stream);
 

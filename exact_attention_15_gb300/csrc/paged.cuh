@@ -1,0 +1,89 @@
+// What the kernels over a paged key-value cache share: the cache's description,
+// the sequences' lengths and the page look-up, all of them clamped so that no
+// access leaves the cache or the page table whatever the device arrays hold.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace attn {
+
+// Sequences, their lengths in the cache and their pages.
+struct PagedSeqs {
+  const int* cu_seqlens;  // new tokens: packed offsets [B + 1]; nullptr: one per sequence
+  const int* kv_lens;     // [B] keys of each sequence, its new tokens among them
+  const int* page_table;  // [B, max_pages], rows table_stride apart
+  int B, T;               // sequences; rows of q
+  int max_pages, num_pages;
+  long long table_stride;  // entries between rows of page_table
+  int page_shift;         // log2(page_size)
+  int* err;               // device error word
+};
+
+// Keys of sequence b, clamped into what its page table row can hold.
+__device__ __forceinline__ int kv_len(const PagedSeqs& s, int b) {
+  const long long most = static_cast<long long>(s.max_pages) << s.page_shift;
+  return static_cast<int>(min(static_cast<long long>(max(__ldg(s.kv_lens + b), 0)), most));
+}
+// Rows of q that belong to sequence b.
+__device__ __forceinline__ SeqSpan new_span(const PagedSeqs& s, int b) {
+  return s.cu_seqlens ? seq_span(s.cu_seqlens, b, s.T, 0) : SeqSpan{b, b < s.T ? 1 : 0};
+}
+// The page that holds place `i` of sequence b's page table row (i < max_pages).
+// An index outside the cache is recorded and page 0 taken for it.
+__device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int i) {
+  const int id = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + i);
+  if (static_cast<unsigned>(id) < static_cast<unsigned>(s.num_pages)) return id;
+  record_error(s.err, kErrPages);
+  return 0;
+}
+// Records lengths that the clamps above would change: thread `tid` of
+// `nthreads` checks its share. Rows of q behind the last sequence are allowed.
+__device__ __forceinline__ void check_paged_seqs(const PagedSeqs& s, int tid, int nthreads) {
+  const long long most = static_cast<long long>(s.max_pages) << s.page_shift;
+  for (int b = tid; b < s.B; b += nthreads) {
+    const int len = __ldg(s.kv_lens + b);
+    if (len < 0 || len > most) record_error(s.err, kErrPages);
+    if (s.cu_seqlens) {
+      const int a = __ldg(s.cu_seqlens + b), e = __ldg(s.cu_seqlens + b + 1);
+      if ((b == 0 && a != 0) || a > e || e > s.T) record_error(s.err, kErrSeqlens);
+    }
+  }
+}
+
+// ---- appending
+struct AppendParams {
+  PagedSeqs s;
+  const void* q; const void* k; const void* v;  // bf16, [T, heads, d], any token stride
+  void* q_out;
+  long long q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+  void* k_cache; void* v_cache;
+  long long k_page, v_page;  // elements between pages
+  const float* k_scale; const float* v_scale;  // e4m3: [H_kv] or nullptr
+  const double* inv_freq;    // [rotary_dim / 2] radians per position, or nullptr
+  int H_q, H_kv, d, rotary_dim, interleaved, e4m3;
+};
+cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
+
+// ---- streaming attention: few query rows per sequence
+constexpr int kStreamCtas = 304;  // CTAs the workspace holds partial results for
+constexpr int kStreamTile = 64;   // keys per tile
+
+struct StreamParams {
+  PagedSeqs s;
+  const void* q;  // bf16 [T, H_q, d]
+  void* o;        // bf16 [T, H_q, d]
+  float* lse;
+  long long lse_row, lse_head;  // elements between rows and between heads of lse
+  const float* k_scale; const float* v_scale;
+  int H_q, H_kv, group, causal;
+  float scale_log2;
+  long long* unit_start;  // workspace: [B + 1] first work unit of each sequence
+  float* part_ml;         // workspace: [2 kStreamCtas, 16, 2]
+  float* part_o;          // workspace: [2 kStreamCtas, 16, d]
+  int grid;
+  long long wait_limit;
+};
+cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
+                                int d, int rows, bool e4m3, cudaStream_t stream);
+
+}  // namespace attn

@@ -1,0 +1,223 @@
+// Host side of the paged key-value cache calls declared in include/attn.h:
+// argument checks, tensor maps over the cache, workspace plan and launches.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "host.h"
+#include "paged.cuh"
+
+using namespace attn;
+
+namespace {
+
+bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int check_cache(const attn_paged_cache* c) {
+  if (!c) return ATTN_ERR_NULL_PTR;
+  if (c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED_HEADDIM;
+  if (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3) return ATTN_ERR_BAD_SHAPE;
+  if (c->num_pages < 1 || c->H_kv < 1 || c->H_kv > 65535) return ATTN_ERR_BAD_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return ATTN_ERR_BAD_SHAPE;
+  if (!c->k || !c->v) return ATTN_ERR_NULL_PTR;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return ATTN_ERR_ALIGNMENT;
+  const long long page = static_cast<long long>(c->H_kv) * c->page_size * c->d;
+  const long long es = c->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  // tensor maps hold strides below 2^40 bytes
+  for (long long stride : {c->k_page_stride, c->v_page_stride}) {
+    if (stride < page || stride >= (1ll << 39)) return ATTN_ERR_BAD_SHAPE;
+    if ((stride * es) & 15) return ATTN_ERR_ALIGNMENT;
+  }
+  return ATTN_OK;
+}
+
+int check_seqs(const attn_paged_cache* c, int T, int B, int H_q, const int* seqlens,
+               const int* kv_lens, const int* page_table, int max_pages, long long table_stride) {
+  if (T < 0 || B < 0 || H_q < 0 || H_q > 65535 || max_pages < 0) return ATTN_ERR_BAD_SHAPE;
+  if (H_q % c->H_kv != 0) return ATTN_ERR_GQA_RATIO;
+  if (!seqlens && T != B) return ATTN_ERR_BAD_SHAPE;
+  if (T > 0 && B == 0) return ATTN_ERR_BAD_SHAPE;
+  if (max_pages > 0 && table_stride < max_pages) return ATTN_ERR_BAD_SHAPE;
+  if (static_cast<long long>(max_pages) * c->page_size > (1ll << 30)) return ATTN_ERR_BAD_SHAPE;
+  if (static_cast<long long>(T) * H_q > 0x7fffffffll) return ATTN_ERR_BAD_SHAPE;
+  if (T > 0 && (!kv_lens || (max_pages > 0 && !page_table))) return ATTN_ERR_NULL_PTR;
+  if (!aligned(seqlens, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4)) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
+PagedSeqs seqs_of(const attn_paged_cache* c, int T, int B, const int* seqlens, const int* kv_lens,
+                  const int* page_table, int max_pages, long long table_stride, int* err) {
+  PagedSeqs s;
+  s.cu_seqlens = seqlens;
+  s.kv_lens = kv_lens;
+  s.page_table = page_table;
+  s.B = B;
+  s.T = T;
+  s.max_pages = max_pages;
+  s.table_stride = table_stride;
+  s.num_pages = c->num_pages;
+  s.page_shift = 0;
+  while ((1 << s.page_shift) < c->page_size) ++s.page_shift;
+  s.err = err;
+  return s;
+}
+
+// 4-D map over the pages of k or v: boxes of `rows` rows of one head of one
+// page, at most 128 bytes of each, swizzled over the box's row width.
+int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cache* c, const void* base,
+                     long long page_stride, unsigned rows) {
+  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  const cuuint64_t es = e4m3 ? 1 : 2, d = static_cast<cuuint64_t>(c->d);
+  const cuuint64_t page = static_cast<cuuint64_t>(c->page_size);
+  cuuint64_t dims[4] = {d, page, static_cast<cuuint64_t>(c->H_kv), static_cast<cuuint64_t>(c->num_pages)};
+  cuuint64_t strides[3] = {d * es, d * es * page, static_cast<cuuint64_t>(page_stride) * es};
+  const unsigned width = static_cast<unsigned>(d * es < 128 ? d : 128 / es);
+  cuuint32_t box[4] = {width, rows, 1, 1};
+  cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = dev.encode(
+      m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+      const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      width * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Workspace: the first unit of each sequence, then the partial results.
+struct WorkPlan {
+  size_t ml_off, o_off, total;
+};
+WorkPlan work_plan(int B, int d) {
+  WorkPlan w;
+  w.ml_off = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
+  w.o_off = w.ml_off + align256(static_cast<size_t>(2 * kStreamCtas) * 16 * 2 * sizeof(float));
+  w.total = w.o_off + static_cast<size_t>(2 * kStreamCtas) * 16 * d * sizeof(float);
+  return w;
+}
+
+// Both attention calls, after the checks they share.
+int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* lse, int T, int B, int H_q,
+                    const int* seqlens, const int* kv_lens, const int* page_table, int max_pages,
+                    long long table_stride, int causal, float scale, void* workspace,
+                    size_t workspace_bytes, long long lse_row, long long lse_head, cudaStream_t cs) {
+  int st = check_cache(c);
+  if (st != ATTN_OK) return st;
+  if ((st = check_seqs(c, T, B, H_q, seqlens, kv_lens, page_table, max_pages, table_stride)) != ATTN_OK)
+    return st;
+  if (H_q < 1 || !std::isfinite(scale)) return ATTN_ERR_BAD_SHAPE;
+  if (T == 0) return ATTN_OK;
+  if (!q || !o || !lse) return ATTN_ERR_NULL_PTR;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return ATTN_ERR_ALIGNMENT;
+  const WorkPlan plan = work_plan(B, c->d);
+  if (!workspace || workspace_bytes < plan.total) return ATTN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
+  HostDevice dev;
+  if ((st = host_setup(&dev)) != ATTN_OK) return st;
+
+  const unsigned rows = c->page_size < kStreamTile ? c->page_size : kStreamTile;
+  CUtensorMap tk, tv;
+  if ((st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
+      (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
+    return st;
+  StreamParams p;
+  p.s = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.lse_row = lse_row;
+  p.lse_head = lse_head;
+  p.k_scale = c->type == ATTN_CACHE_E4M3 ? c->k_scale : nullptr;
+  p.v_scale = c->type == ATTN_CACHE_E4M3 ? c->v_scale : nullptr;
+  p.H_q = H_q;
+  p.H_kv = c->H_kv;
+  p.group = H_q / c->H_kv;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * kLog2e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.unit_start = reinterpret_cast<long long*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
+  p.grid = 2 * dev.n_sm < kStreamCtas ? 2 * dev.n_sm : kStreamCtas;
+  p.wait_limit = dev.wait_limit;
+  // 8 rows where a sequence's rows of one KV head fill no more
+  const int chunk = static_cast<long long>(T) * p.group <= 8ll * B ? 8 : 16;
+  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, cs) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* k, const void* v,
+                      void* q_out, long long q_stride, long long k_stride, long long v_stride,
+                      long long q_out_stride, int T, int B, int H_q, const int* seqlens,
+                      const int* kv_lens, const int* page_table, int max_pages,
+                      long long table_stride, const double* inv_freq, int rotary_dim,
+                      int interleaved, attn_stream_t stream) {
+  int st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  if ((st = check_seqs(cache, T, B, H_q, seqlens, kv_lens, page_table, max_pages, table_stride)) != ATTN_OK)
+    return st;
+  const int d = cache->d;
+  if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 16 != 0) return ATTN_ERR_BAD_SHAPE;
+  const long long kv_row = static_cast<long long>(cache->H_kv) * d, q_row = static_cast<long long>(H_q) * d;
+  if (k_stride < kv_row || v_stride < kv_row || (H_q > 0 && (q_stride < q_row || q_out_stride < q_row)))
+    return ATTN_ERR_BAD_SHAPE;
+  if (T == 0) return ATTN_OK;
+  if (!k || !v || (H_q > 0 && (!q || !q_out)) || (rotary_dim > 0 && !inv_freq)) return ATTN_ERR_NULL_PTR;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(inv_freq, 8) || ((k_stride | v_stride) & 7) || (H_q > 0 && ((q_stride | q_out_stride) & 7)))
+    return ATTN_ERR_ALIGNMENT;
+  HostDevice dev;
+  if ((st = host_setup(&dev)) != ATTN_OK) return st;
+  AppendParams p;
+  p.s = seqs_of(cache, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  p.q = q; p.k = k; p.v = v; p.q_out = q_out;
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.q_out_stride = q_out_stride;
+  p.k_cache = cache->k; p.v_cache = cache->v;
+  p.k_page = cache->k_page_stride; p.v_page = cache->v_page_stride;
+  p.e4m3 = cache->type == ATTN_CACHE_E4M3 ? 1 : 0;
+  p.k_scale = p.e4m3 ? cache->k_scale : nullptr;
+  p.v_scale = p.e4m3 ? cache->v_scale : nullptr;
+  p.inv_freq = inv_freq;
+  p.H_q = H_q; p.H_kv = cache->H_kv; p.d = d;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  return launch_paged_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                       : ATTN_ERR_CUDA;
+}
+
+size_t attn_paged_workspace_bytes(int T, int B, int H_q, int H_kv, int d) {
+  if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128))
+    return 0;
+  return work_plan(B, d).total;
+}
+
+int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
+                      const int* kv_lens, const int* page_table, int max_pages,
+                      long long table_stride, float scale, void* workspace, size_t workspace_bytes,
+                      attn_stream_t stream) {
+  return paged_attention(cache, q, o, lse, B, B, H_q, nullptr, kv_lens, page_table, max_pages,
+                         table_stride, 0, scale, workspace, workspace_bytes, H_q, 1,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float* lse, int T, int B,
+                   int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
+                   int max_pages, long long table_stride, int causal, float scale, void* workspace,
+                   size_t workspace_bytes, attn_stream_t stream) {
+  if (T > 0 && !seqlens) return ATTN_ERR_NULL_PTR;
+  return paged_attention(cache, q, o, lse, T, B, H_q, seqlens, kv_lens, page_table, max_pages,
+                         table_stride, causal, scale, workspace, workspace_bytes, 1, T,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

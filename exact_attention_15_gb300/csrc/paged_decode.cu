@@ -1,0 +1,671 @@
+// Attention of a few new query rows per sequence over a paged key-value cache:
+// one token per sequence (decoding), or chunks of a few tokens.
+//
+// Every key and value is read once and meets only the query rows of its KV
+// head, so the bytes bound the work. The query rows of a sequence that share a
+// KV head (tokens x heads of the group, row = token * group + head) are cut into
+// chunks of R = 8 or 16 rows; a work unit is one 64-key tile of one (sequence,
+// KV head, chunk). The units are numbered with the tile innermost and dealt out
+// evenly and in order, so every CTA streams the same number of tiles whatever
+// the sequences' lengths are. A CTA whose run ends inside an item leaves its
+// (m, l, O) in the workspace; paged_join_kernel merges the pieces of an item in
+// their order, so results do not depend on timing.
+//
+// Warp roles (160 threads): warps 0-3 each take 16 keys of a tile, S = Q K^T
+// and O += P V on mma.sync m16n8k16 with the online softmax in registers
+// (tcgen05 wants 128 rows; here there are 16 at most, and the tensor work is
+// small against the tile's bytes); warp 4 loads the tiles with TMA.
+#include <cuda_fp16.h>
+
+#include "paged.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kTile = kStreamTile;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * (kWarps + 1);
+
+template <int D, bool FP8>
+struct StreamCfg {
+  static constexpr int kEs = FP8 ? 1 : 2;
+  // a tile is kept as blocks of 64 rows x (at most) 128 bytes, swizzled
+  static constexpr int kRowBytes = D * kEs < 128 ? D * kEs : 128;
+  static constexpr int kBlocks = D * kEs / kRowBytes;
+  static constexpr int kBlockBytes = kTile * kRowBytes;
+  static constexpr int kTileBytes = kBlocks * kBlockBytes;  // K or V
+  static constexpr int kStages = kTileBytes == 16384 ? 3 : 6;
+  static constexpr int kMergeOff = kStages * 2 * kTileBytes;
+  static constexpr int kMergeBytes = 16384;
+  static constexpr int kMlOff = kMergeOff + kMergeBytes;
+  static constexpr int kBarOff = kMlOff + kWarps * 16 * 2 * 4;
+  static constexpr int kSmemBytes = kBarOff + 2 * kStages * 8;
+  // two CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
+  static_assert(2 * (kSmemBytes + 1024) <= 233472, "shared memory of two CTAs");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool FP16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (FP16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 bytes (low half of x) to two fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Work units of sequence b: key tiles x KV heads x chunks of R query rows.
+__device__ __forceinline__ long long units_of(const StreamParams& p, int b, int R) {
+  const int n = new_span(p.s, b).len;
+  const long long chunks = (static_cast<long long>(n) * p.group + R - 1) / R;
+  const long long tiles = (static_cast<long long>(kv_len(p.s, b)) + kTile - 1) / kTile;
+  return tiles * p.H_kv * chunks;
+}
+// CTAs that `total` units are dealt to (each of them has one unit at least).
+__device__ __forceinline__ int busy_ctas(long long total, int grid) {
+  return static_cast<int>(min(total, static_cast<long long>(grid)));
+}
+// First unit of CTA c of `grid` busy ones, and the CTA that holds unit u.
+__device__ __forceinline__ long long first_unit(long long total, int grid, int c) {
+  return total * c / grid;
+}
+__device__ __forceinline__ int owner_of(long long total, int grid, long long u) {
+  return static_cast<int>(((u + 1) * grid - 1) / total);
+}
+
+// The piece of an item that a CTA works on.
+struct Piece {
+  int b, h, rc;      // sequence, KV head, row chunk
+  int t0, t1;        // key tiles [t0, t1)
+  int tiles;         // of the whole item
+  int len, n, row0;  // keys; query rows of the sequence and the first of them
+};
+
+// Walks the units [u, end) of a CTA piece by piece.
+struct Walk {
+  long long u, end, base;  // next unit; first unit of sequence b
+  int b;
+};
+template <int R>
+__device__ __forceinline__ bool next_piece(const StreamParams& p, Walk& w, Piece& x) {
+  if (w.u >= w.end) return false;
+  for (;;) {
+    if (w.b >= p.s.B) return false;
+    const long long n = units_of(p, w.b, R);
+    if (w.u < w.base + n) break;
+    w.base += n;
+    ++w.b;
+  }
+  x.b = w.b;
+  x.len = kv_len(p.s, w.b);
+  const SeqSpan sp = new_span(p.s, w.b);
+  x.n = sp.len;
+  x.row0 = sp.start;
+  x.tiles = (x.len + kTile - 1) / kTile;
+  const int chunks = static_cast<int>((static_cast<long long>(x.n) * p.group + R - 1) / R);
+  const long long off = w.u - w.base;
+  const long long item = off / x.tiles;
+  x.t0 = static_cast<int>(off - item * x.tiles);
+  x.t1 = static_cast<int>(min(static_cast<long long>(x.tiles), x.t0 + (w.end - w.u)));
+  x.h = static_cast<int>(item / chunks);
+  x.rc = static_cast<int>(item - static_cast<long long>(x.h) * chunks);
+  w.u += x.t1 - x.t0;
+  return true;
+}
+
+template <int D, int R, bool FP8>
+__global__ void __launch_bounds__(kThreads, 2)
+paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const StreamParams p) {
+  using Cfg = StreamCfg<D, FP8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + Cfg::kMergeOff);
+  float* ml = reinterpret_cast<float*>(smem + Cfg::kMlOff);  // [warp][16][2]
+  const uint32_t full = smem_addr(smem + Cfg::kBarOff), empty = full + 8 * Cfg::kStages;
+  long long* pre = reinterpret_cast<long long*>(merge);  // [kThreads + 1], before the first merge
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long lim = p.wait_limit;
+
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kWarps);
+    }
+    fence_barrier_init();
+  }
+  // The units before each sequence: every thread sums a run of sequences, the
+  // sums are scanned, and the run that holds this CTA's first unit is walked.
+  const int run = (p.s.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.s.B, tid * run), b1 = min(p.s.B, b0 + run);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units_of(p, b, R);
+  pre[tid + 1] = mine;
+  if (tid == 0) pre[0] = 0;
+  if (blockIdx.x == 0) check_paged_seqs(p.s, tid, kThreads);
+  __syncthreads();
+  if (warp == 0) {
+    long long carry = 0;
+    for (int i = 0; i < kThreads; i += 32) {
+      long long x = pre[i + lane + 1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      pre[i + lane + 1] = x + carry;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  const long long total = pre[kThreads];
+  if (blockIdx.x == 0) {  // for the join
+    long long at = pre[tid];
+    for (int b = b0; b < b1; ++b) {
+      p.unit_start[b] = at;
+      at += units_of(p, b, R);
+    }
+    if (tid == 0) p.unit_start[p.s.B] = total;
+  }
+  const int grid = busy_ctas(total, gridDim.x), cta = blockIdx.x;
+  if (cta >= grid) return;
+  Walk w;
+  w.u = first_unit(total, grid, cta);
+  w.end = first_unit(total, grid, cta + 1);
+  {
+    int lo = 0, hi = kThreads;  // the last run that starts at or before the first unit
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= w.u) lo = mid; else hi = mid;
+    }
+    w.b = min(p.s.B, lo * run);
+    w.base = pre[lo];
+  }
+  __syncthreads();
+  const long long first = w.u;
+  Piece x;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ TMA producer
+    // Lane (page j of the tile, K or V, block) issues one box per tile.
+    const int box_shift = min(p.s.page_shift, 6);
+    const int n_box = kTile >> box_shift;  // pages (or the part of one) in a tile
+    constexpr int kPer = 2 * Cfg::kBlocks;
+    const int j = lane / kPer, which = (lane / Cfg::kBlocks) & 1, blk = lane % Cfg::kBlocks;
+    const int box_row = j << box_shift;
+    const bool has_box = j < n_box;
+    const uint32_t dst0 = smem_addr(smem) + which * Cfg::kTileBytes + blk * Cfg::kBlockBytes +
+                          box_row * Cfg::kRowBytes;
+    const CUtensorMap* map = which ? &tm_v : &tm_k;
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    bool ok = true;
+    while (ok && next_piece<R>(p, w, x)) {
+      auto page_at = [&](int t) {
+        const int key = t * kTile + box_row;
+        return has_box && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift) : 0;
+      };
+      int id = page_at(x.t0);
+      for (int t = x.t0; t < x.t1; ++t) {
+        const int key0 = t * kTile;
+        const int here = id;
+        if (t + 1 < x.t1) id = page_at(t + 1);
+        if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1, lim)) { ok = false; break; }
+        // boxes that hold a key; the rows of the others keep what they held
+        const int boxes = min(n_box, (x.len - key0 + (1 << box_shift) - 1) >> box_shift);
+        if (lane == 0)
+          mbar_arrive_expect_tx(full + 8 * stage, boxes * kPer * (Cfg::kRowBytes << box_shift));
+        __syncwarp();
+        if (j < boxes)
+          tma_load_4d(dst0 + stage * 2 * Cfg::kTileBytes, map, full + 8 * stage,
+                      blk * (Cfg::kRowBytes / Cfg::kEs),
+                      (key0 + box_row) & ((1 << p.s.page_shift) - 1), x.h, here);
+        if (++stage == Cfg::kStages) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int qd = lane & 3, r0 = lane >> 2;  // accumulator column pair, row
+  const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
+  // K: matrices (keys 0-7 | 8-15) x (two 16-byte chunks); V: the keys innermost
+  const int krow = warp * 16 + (mi >> 1) * 8 + mr, vrow = warp * 16 + (mi & 1) * 8 + mr;
+  // byte offset of this lane's row and first chunk; chunk c (even) lies at
+  // (offset + block) ^ (c << 4), since the swizzle is an XOR on those bits
+  auto row_off = [&](int row, int ch) {
+    const int sw = Cfg::kRowBytes == 128 ? row & 7 : (row >> 1) & 3;
+    return row * Cfg::kRowBytes + ((ch ^ sw) << 4);
+  };
+  const uint32_t koff = row_off(krow, mi & 1), voff = row_off(vrow, mi >> 1);
+  constexpr int kChunks = Cfg::kRowBytes / 16;  // 16-byte chunks of a block's row
+  auto chunk_at = [&](uint32_t base, int c) {
+    return (base + (c / kChunks) * Cfg::kBlockBytes) ^ ((c % kChunks) << 4);
+  };
+  constexpr int kHalves = R / 8;  // accumulator rows r0, and r0 + 8 with R = 16
+  bool ok = true;
+  while (next_piece<R>(p, w, x)) {
+    const int rows = min(R, x.n * p.group - x.rc * R);  // of this chunk
+    // Query rows r0 and r0 + 8 as A fragments. Over an e4m3 cache the products
+    // run in fp16, which holds every e4m3 value exactly; each row is brought to
+    // [1, 2) by a power of two first, so fp16's range does not matter and what
+    // it rounds is below 2^-25 of the row's largest value.
+    uint32_t qa[D / 16][4];
+    float c[2];  // exponent scale of the two rows
+    int last[2]; // keys that each row sees
+    const float k_scale = FP8 && p.k_scale ? __ldg(p.k_scale + x.h) : 1.0f;
+    const float v_scale = FP8 && p.v_scale ? __ldg(p.v_scale + x.h) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = p.scale_log2 * k_scale;
+      last[i] = 0;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) qa[kk][i] = qa[kk][i + 2] = 0u;
+      if (i >= kHalves) continue;
+      const int r = r0 + 8 * i;
+      if (r < rows) {
+        const int rr = x.rc * R + r;
+        const int tok = rr / p.group, head = rr - tok * p.group;
+        last[i] = p.causal ? min(x.len, x.len - x.n + tok + 1) : x.len;
+        const uint8_t* src = static_cast<const uint8_t*>(p.q) +
+            ((static_cast<size_t>(x.row0 + tok) * p.H_q + x.h * p.group + head) * D) * 2;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if constexpr (FP8) {  // the lane's four consecutive columns
+            const uint2 q4 = *reinterpret_cast<const uint2*>(src + kk * 32 + qd * 8);
+            qa[kk][i] = q4.x;
+            qa[kk][i + 2] = q4.y;
+          } else {
+            qa[kk][i] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4);
+            qa[kk][i + 2] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4 + 16);
+          }
+        }
+      }
+      if constexpr (FP8) {
+        float top = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int e = i; e < 4; e += 2)
+            top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(qa[kk][e])), fabsf(bf16hi_to_f32(qa[kk][e]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        ex = ex > 127 ? 0 : max(-126, min(126, ex));  // infinities stay infinities
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        c[i] *= __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int e = i; e < 4; e += 2)
+            qa[kk][e] = pack_f16x2(bf16lo_to_f32(qa[kk][e]) * down, bf16hi_to_f32(qa[kk][e]) * down);
+      }
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (int t = x.t0; t < x.t1; ++t) {
+      if (ok && !mbar_wait_warp(full + 8 * stage, phase, lim)) {
+        // the copies may still be on their way: one more bounded wait, then the
+        // rest of the work is walked without waiting so that every warp reaches
+        // the same barriers
+        if (lane == 0) record_error(p.s.err, kErrTimeout);
+        mbar_wait_warp(full + 8 * stage, phase, lim);
+        ok = false;
+      }
+      const int key0 = t * kTile + warp * 16;
+      if (key0 < x.len) {
+        const uint32_t tile = smem_addr(smem) + stage * 2 * Cfg::kTileBytes;
+        const uint32_t kb = tile + koff, vb = tile + Cfg::kTileBytes + voff;
+        float sc[2][4];  // S: keys 0-7 and 8-15 of this warp
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t f[4];
+            ldsm4(chunk_at(kb, 2 * cc), f);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              mma16816<true>(sc[0], qa[2 * cc + u], e4m3x2_to_f16x2(f[u]), e4m3x2_to_f16x2(f[u] >> 16));
+              mma16816<true>(sc[1], qa[2 * cc + u], e4m3x2_to_f16x2(f[2 + u]),
+                             e4m3x2_to_f16x2(f[2 + u] >> 16));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t f[4];
+            ldsm4(chunk_at(kb, 2 * kk), f);
+            mma16816<false>(sc[0], qa[kk], f[0], f[1]);
+            mma16816<false>(sc[1], qa[kk], f[2], f[3]);
+          }
+        }
+        // softmax step of rows r0 (e = 0, 1) and r0 + 8 (e = 2, 3)
+        float mx[2];
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+          mx[i] = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + n * 8 + 2 * qd + e;
+              float& v = sc[n][2 * i + e];
+              v = key < last[i] ? v * c[i] : -INFINITY;
+              mx[i] = fmaxf(mx[i], v);
+            }
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          mx[i] = fmaxf(mx[i], m[i]);
+        }
+        // the bias moves only when some row's maximum grew by more than 2^tau
+        bool moved = mx[0] - m[0] > kTau;
+        if (kHalves == 2) moved |= mx[kHalves - 1] - m[kHalves - 1] > kTau;
+        if (__any_sync(0xffffffffu, moved)) {
+          float f[2] = {1.0f, 1.0f};
+#pragma unroll
+          for (int i = 0; i < kHalves; ++i) {
+            f[i] = mx[i] > m[i] ? ex2_approx(m[i] - mx[i]) : 1.0f;
+            m[i] = fmaxf(m[i], mx[i]);
+            l[i] *= f[i];
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2 * kHalves; ++e) acc[j][e] *= f[e >> 1];
+        }
+        // P sums up in 32 bits before it is rounded to the product's 16-bit type
+        // (bf16 as in the prompt kernels, fp16 over an e4m3 cache)
+        uint32_t pa[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+          const float mb = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = ex2_approx(sc[n][2 * i] - mb), p1 = ex2_approx(sc[n][2 * i + 1] - mb);
+            l[i] += p0 + p1;
+            pa[2 * n + i] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+        }
+        // Rows of V past the sequence's end can hold anything (a page's unused
+        // rows, an earlier tile): they are replaced by zeros, since 0 x NaN is NaN.
+        uint32_t vm[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = key0 + n * 8 + 2 * qd;
+          vm[n] = (key < x.len ? 0x0000ffffu : 0u) | (key + 1 < x.len ? 0xffff0000u : 0u);
+        }
+        if constexpr (FP8) {
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t f[4];
+            ldsm4_t(chunk_at(vb, 2 * cc), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] &= vm[e & 1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // even and odd columns of chunk 2 cc + u
+              const int jb = 2 * (2 * cc + u);
+              mma16816<true>(acc[jb], pa, e4m3x2_to_f16x2(__byte_perm(f[2 * u], 0, 0x4420)),
+                             e4m3x2_to_f16x2(__byte_perm(f[2 * u + 1], 0, 0x4420)));
+              mma16816<true>(acc[jb + 1], pa, e4m3x2_to_f16x2(__byte_perm(f[2 * u], 0, 0x4431)),
+                             e4m3x2_to_f16x2(__byte_perm(f[2 * u + 1], 0, 0x4431)));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int jj = 0; jj < D / 16; ++jj) {
+            uint32_t f[4];
+            ldsm4_t(chunk_at(vb, 2 * jj), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] &= vm[e & 1];
+            mma16816<false>(acc[2 * jj], pa, f[0], f[1]);
+            mma16816<false>(acc[2 * jj + 1], pa, f[2], f[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      if (++stage == Cfg::kStages) { stage = 0; phase ^= 1; }
+    }
+
+    // ---- merge of the four warps' keys
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (qd == 0) {
+        ml[(warp * 16 + r0 + 8 * i) * 2] = m[i];
+        ml[(warp * 16 + r0 + 8 * i) * 2 + 1] = l[i];
+      }
+    }
+    named_bar_sync(1, 32 * kWarps);
+    const bool whole = x.t1 - x.t0 == x.tiles;
+    const int slot = 2 * cta + (w.u - (x.t1 - x.t0) == first ? 0 : 1);
+    // O passes through shared memory in runs of kCols columns, each 8-column
+    // group moved within its row so that the warps' stores spread over the banks
+    // (each thread's own row of the result: its statistics are read before the
+    // second barrier, after which the next piece may write its own)
+    constexpr int kCols = D * R * kWarps * 4 <= Cfg::kMergeBytes ? D : Cfg::kMergeBytes / (R * kWarps * 4);
+    constexpr int kPerRow = kCols / 8;  // threads per row of the result
+    static_assert(R * kPerRow <= 32 * kWarps, "one 8-column group per thread");
+    const int ro = tid / kPerRow, g8 = tid % kPerRow;
+    float top = -INFINITY, sum = 0.0f;
+    if (ro < rows) {
+#pragma unroll
+      for (int g = 0; g < kWarps; ++g) top = fmaxf(top, ml[(g * 16 + ro) * 2]);
+      const float mb = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int g = 0; g < kWarps; ++g)
+        sum += ml[(g * 16 + ro) * 2 + 1] * ex2_approx(ml[(g * 16 + ro) * 2] - mb);
+    }
+    float mine[kHalves];  // factor of this lane's accumulator rows
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i) {
+      float t = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < kWarps; ++g) t = fmaxf(t, ml[(g * 16 + r0 + 8 * i) * 2]);
+      mine[i] = ex2_approx(m[i] - (t == -INFINITY ? 0.0f : t));
+    }
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += kCols) {
+      if (c0 > 0) named_bar_sync(1, 32 * kWarps);
+#pragma unroll
+      for (int i = 0; i < kHalves; ++i) {
+        const int r = r0 + 8 * i;
+        const float f = mine[i];
+        float* dst = merge + (warp * R + r) * kCols;
+#pragma unroll
+        for (int j = c0 / 8; j < (c0 + kCols) / 8; ++j) {
+          // column of the lane's first value, and the step to its second
+          const int col = (FP8 ? (j >> 1) * 16 + 4 * qd + (j & 1) : j * 8 + 2 * qd) - c0;
+          const int sw = (r & 3) << 3;
+          if constexpr (FP8) {
+            dst[col ^ sw] = acc[j][2 * i] * f;
+            dst[(col + 2) ^ sw] = acc[j][2 * i + 1] * f;
+          } else {
+            *reinterpret_cast<float2*>(dst + (col ^ sw)) =
+                make_float2(acc[j][2 * i] * f, acc[j][2 * i + 1] * f);
+          }
+        }
+      }
+      named_bar_sync(1, 32 * kWarps);
+      if (ro < rows) {
+        const int r = ro;
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kWarps; ++g) {
+          const float* src = merge + (g * R + r) * kCols + ((g8 * 8) ^ ((r & 3) << 3));
+          const float4 a = *reinterpret_cast<const float4*>(src);
+          const float4 d4 = *reinterpret_cast<const float4*>(src + 4);
+          o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+          o[4] += d4.x; o[5] += d4.y; o[6] += d4.z; o[7] += d4.w;
+        }
+        const float f = whole ? (sum == 0.0f ? 0.0f : v_scale / sum) : v_scale;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f;
+        if (whole) {
+          const int rr = x.rc * R + r;
+          const int tok = rr / p.group, head = x.h * p.group + rr - tok * p.group;
+          const size_t row = static_cast<size_t>(x.row0 + tok);
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D + c0 +
+                                    g8 * 8) =
+              make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                         pack_bf16x2(o[6], o[7]));
+          if (c0 == 0 && g8 == 0)
+            p.lse[row * p.lse_row + head * p.lse_head] =
+                sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+        } else {
+          float* dst = p.part_o + (static_cast<size_t>(slot) * 16 + r) * D + c0 + g8 * 8;
+          *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          if (c0 == 0 && g8 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(top, sum);
+        }
+      }
+    }
+  }
+}
+
+// One CTA per query row and head: merges the pieces of its item, or writes the
+// empty result of a row whose sequence has no keys. Rows behind the last
+// sequence are left as they were.
+template <int D, int R>
+__global__ void __launch_bounds__(128)
+paged_join_kernel(const StreamParams p) {
+  __shared__ float sh_o[4][D];
+  __shared__ float sh_l[4];
+  const int head = blockIdx.x % p.H_q, t = blockIdx.x / p.H_q;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int b = t;
+  if (p.s.cu_seqlens) {
+    int lo = 0, hi = p.s.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
+    }
+    b = lo;
+  }
+  const SeqSpan sp = new_span(p.s, b);
+  if (t < sp.start || t >= sp.start + sp.len) return;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(t) * p.H_q + head) * D;
+  float* lse = p.lse + t * p.lse_row + head * p.lse_head;
+  const int tiles = (kv_len(p.s, b) + kTile - 1) / kTile;
+  if (tiles == 0) {
+    if (threadIdx.x < D / 8) reinterpret_cast<uint4*>(out)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) *lse = -INFINITY;
+    return;
+  }
+  const int h = head / p.group, rr = (t - sp.start) * p.group + head - h * p.group;
+  const int chunks = static_cast<int>((static_cast<long long>(sp.len) * p.group + R - 1) / R);
+  const int rc = rr / R, r = rr - rc * R;
+  const long long total = p.unit_start[p.s.B];
+  const long long u0 = p.unit_start[b] + (static_cast<long long>(h) * chunks + rc) * tiles;
+  const int grid = busy_ctas(total, p.grid);
+  const int c0 = owner_of(total, grid, u0), c1 = owner_of(total, grid, u0 + tiles - 1);
+  if (c0 == c1) return;  // written whole
+  const int s0 = 2 * c0 + (first_unit(total, grid, c0) == u0 ? 0 : 1);
+  const int pieces = c1 - c0 + 1;
+  auto at = [&](int i) { return static_cast<size_t>(i == 0 ? s0 : 2 * (c0 + i)) * 16 + r; };
+  float top = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.part_ml[at(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float mb = top == -INFINITY ? 0.0f : top;
+  constexpr int kV = D / 32;
+  float acc[kV], l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < pieces; i += 4) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(i) * 2);
+    const float f = ex2_approx(ml.x - mb);
+    l += ml.y * f;
+    const float* src = p.part_o + at(i) * D + lane * kV;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] += src[e] * f;
+  }
+#pragma unroll
+  for (int e = 0; e < kV; ++e) sh_o[warp][lane * kV + e] = acc[e];
+  if (lane == 0) sh_l[warp] = l;
+  __syncthreads();
+  const float sum = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (threadIdx.x < D / 2) {
+    const int e = 2 * threadIdx.x;
+    const float a = (sh_o[0][e] + sh_o[1][e]) + (sh_o[2][e] + sh_o[3][e]);
+    const float d = (sh_o[0][e + 1] + sh_o[1][e + 1]) + (sh_o[2][e + 1] + sh_o[3][e + 1]);
+    reinterpret_cast<uint32_t*>(out)[threadIdx.x] = pack_bf16x2(a * inv, d * inv);
+  }
+  if (threadIdx.x == 0) *lse = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+template <int D, int R, bool FP8>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
+                   cudaStream_t stream) {
+  constexpr int kSmem = StreamCfg<D, FP8>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(paged_stream_kernel<D, R, FP8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  int slot = prof_begin(kKPagedDecode, stream);
+  paged_stream_kernel<D, R, FP8><<<p.grid, kThreads, kSmem, stream>>>(tk, tv, p);
+  e = cudaGetLastError();
+  prof_end(slot, stream);
+  if (e != cudaSuccess) return e;
+  slot = prof_begin(kKPagedJoin, stream);
+  paged_join_kernel<D, R><<<static_cast<unsigned>(p.s.T) * p.H_q, 128, 0, stream>>>(p);
+  e = cudaGetLastError();
+  prof_end(slot, stream);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
+                                int d, int rows, bool e4m3, cudaStream_t stream) {
+  if (d == 128) {
+    if (rows == 8) return e4m3 ? launch<128, 8, true>(tk, tv, p, stream) : launch<128, 8, false>(tk, tv, p, stream);
+    return e4m3 ? launch<128, 16, true>(tk, tv, p, stream) : launch<128, 16, false>(tk, tv, p, stream);
+  }
+  if (rows == 8) return e4m3 ? launch<64, 8, true>(tk, tv, p, stream) : launch<64, 8, false>(tk, tv, p, stream);
+  return e4m3 ? launch<64, 16, true>(tk, tv, p, stream) : launch<64, 16, false>(tk, tv, p, stream);
+}
+
+}  // namespace attn

@@ -98,7 +98,8 @@ typedef enum {
   ATTN_ERR_TIMEOUT = 9,              /* a device-side bounded wait ran out */
   ATTN_ERR_NO_DEVICE = 10,           /* no usable CUDA device */
   ATTN_ERR_UNSUPPORTED_DEVICE = 11,  /* device is not sm_103 (GB300-class) */
-  ATTN_ERR_SEQLENS = 12              /* cu_seqlens is not 0, non-decreasing, ..., N_q */
+  ATTN_ERR_SEQLENS = 12,             /* cu_seqlens is not 0, non-decreasing, ..., N_q */
+  ATTN_ERR_PAGES = 13                /* a page index or cache length outside the paged cache */
 } attn_status;
 
 /*
@@ -245,11 +246,115 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
                      const int* seqlens, float scale, int deterministic, attn_stream_t stream);
 
 /*
+ * Paged key-value cache: keys and values of many sequences of changing lengths,
+ * kept between calls in pages of page_size tokens. attn_paged_append stores new
+ * tokens, attn_paged_decode answers one new token per sequence and attn_paged_fwd
+ * a chunk of new tokens per sequence.
+ *
+ * k and v are [num_pages, H_kv, page_size, d], pages k_page_stride and
+ * v_page_stride elements apart (at least H_kv * page_size * d, a multiple of 16
+ * bytes; so k and v may be the two halves of one [num_pages, 2, ...] tensor), in
+ * bf16 (ATTN_CACHE_BF16) or e4m3 (ATTN_CACHE_E4M3). An e4m3 value x of head h
+ * stands for x * k_scale[h] (v_scale[h]); the scales are device float arrays of
+ * H_kv entries, NULL for 1, and not read with bf16. d is 64 or 128; page_size is
+ * 16, 32, 64, 128 or 256; k and v are 16-byte aligned.
+ *
+ * Sequences are described by device arrays that the host does not read:
+ *   kv_lens     int32 [B]: keys of each sequence, its new tokens among them
+ *   page_table  int32 [B, max_pages], rows table_stride entries apart: token t
+ *               of sequence b lies in page page_table[b][t / page_size], row
+ *               t % page_size. Entries past a sequence's last page are not read.
+ *   seqlens     int32 [B + 1] packed offsets of the new tokens (0, non-decreasing,
+ *               at most T): sequence b owns rows seqlens[b] .. seqlens[b + 1] - 1
+ *               of q. Rows behind the last sequence are left as they were. NULL
+ *               (attn_paged_append): one token per sequence, T = B.
+ * New token i of the n of sequence b stands at position kv_lens[b] - n + i. A
+ * negative position is padding: nothing is appended for it and it sees no key.
+ * B * max_pages * page_size may be anything the arrays can hold, up to 2^30 tokens
+ * a sequence. The kernels clamp lengths into [0, max_pages * page_size] and take page 0
+ * for an index outside [0, num_pages) (an append there is skipped), so nothing
+ * outside the cache is read or written; either is recorded as ATTN_ERR_PAGES
+ * (attn_check), a bad seqlens array as ATTN_ERR_SEQLENS.
+ *
+ * Unused rows of a page may hold anything, infinities and NaN among it.
+ */
+#define ATTN_CACHE_BF16 0
+#define ATTN_CACHE_E4M3 1
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  long long k_page_stride, v_page_stride; /* elements */
+  int num_pages, page_size, H_kv, d;
+  int type;
+} attn_paged_cache;
+
+/*
+ * Appends T new tokens (k and v, bf16 [T, H_kv, d], tokens k_stride and v_stride
+ * elements apart) to the cache, with the rotary position embedding on the way:
+ * with rotary_dim > 0 the pairs of the first rotary_dim elements of every query
+ * and key head turn by the angle position * inv_freq[i] (device double array of
+ * rotary_dim / 2 entries, radians per position, e.g. base^(-2 i / rotary_dim)).
+ * Pair i is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved.
+ * The angles are exact to about 2^-24 turns at any position. Turned in 32 bits and
+ * rounded once. rotary_dim is a multiple of 16, at most d; 0 appends keys as
+ * they are.
+ * q (bf16 [T, H_q, d], tokens q_stride apart) is turned likewise into q_out (same
+ * shape, q_out_stride apart; q_out == q with the same stride turns in place).
+ * H_q = 0 leaves queries out (q and q_out may be NULL). For e4m3, k / k_scale[h]
+ * and v / v_scale[h] are rounded to nearest, values past +-448 to +-448.
+ * Strides are multiples of 8 elements, tensor pointers 16-byte aligned. The pages that
+ * a call writes must not be shared with another of its sequences. Rows of q_out
+ * at padding positions are left as they were.
+ */
+int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* k, const void* v,
+                      void* q_out, long long q_stride, long long k_stride, long long v_stride,
+                      long long q_out_stride, int T, int B, int H_q, const int* seqlens,
+                      const int* kv_lens, const int* page_table, int max_pages,
+                      long long table_stride, const double* inv_freq, int rotary_dim,
+                      int interleaved, attn_stream_t stream);
+
+/*
+ * Bytes of device workspace that attn_paged_decode (T = B) and attn_paged_fwd need
+ * for these sizes (0 on invalid sizes), whatever the sequences' lengths. It is caller-owned,
+ * 256-byte aligned, its contents do not matter between calls, and calls that may
+ * run at the same time need one each.
+ */
+size_t attn_paged_workspace_bytes(int T, int B, int H_q, int H_kv, int d);
+
+/*
+ * Attention of one query token per sequence over its kv_lens[b] cached keys:
+ * q and o bf16 [B, H_q, d], lse float [B, H_q]; grouped heads and the empty
+ * sequence (O = 0, LSE = -inf) as for attn_fwd. The cache is read once, split evenly
+ * over the GPU whatever the lengths, and the parts are joined in a fixed order: equal
+ * inputs give equal bits on the same device. Allocates nothing; can be captured.
+ */
+int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
+                      const int* kv_lens, const int* page_table, int max_pages,
+                      long long table_stride, float scale, void* workspace, size_t workspace_bytes,
+                      attn_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens per sequence (packed rows of q and o, bf16
+ * [T, H_q, d]; lse float [H_q, T]) over the cache, which already holds their keys
+ * and values: whole prompts, the next chunk of a prompt, or drafted tokens to
+ * verify. With causal, new token i of n sees key j when j <= kv_lens[b] - n + i;
+ * without, every key of its sequence. A row that sees no key gets O = 0 and LSE =
+ * -inf. Otherwise as attn_paged_decode.
+ */
+int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float* lse, int T, int B,
+                   int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
+                   int max_pages, long long table_stride, int causal, float scale, void* workspace,
+                   size_t workspace_bytes, attn_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns the first failure a kernel of this library
  * on the current device recorded since the last check (and clears the record):
  * ATTN_ERR_TIMEOUT for a timed-out wait, ATTN_ERR_SEQLENS for an inconsistent
- * packed-sequence offset array; ATTN_ERR_CUDA if the stream reports an error;
- * else ATTN_OK.
+ * packed-sequence offset array, ATTN_ERR_PAGES for a page index or a cache length
+ * outside the paged cache; ATTN_ERR_CUDA if the stream reports an error; else
+ * ATTN_OK.
  */
 int attn_check(attn_stream_t stream);
 
