@@ -86,4 +86,28 @@ struct StreamParams {
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
                                 int d, int rows, bool e4m3, cudaStream_t stream);
 
+// ---- tensor-core attention: many query rows per sequence
+constexpr int kFwdSms = 152;       // SMs that the workspace is planned for
+constexpr int kFwdMaxSplits = 32;  // pieces of a work tile's keys
+struct PagedFwdParams {
+  PagedSeqs s;
+  void* o;     // bf16 [T, H_q, d]
+  float* lse;  // [H_q, T]
+  int H_q, H_kv, group, causal;
+  int tok_tile;      // query tokens per 128-row tile: floor(128 / group)
+  int splits;        // pieces of a work tile's keys
+  int max_work;      // work items (tile, piece) that the host made room for
+  float scale_log2;
+  int* seq_order;    // workspace: sequences, longest first [B]
+  int* tile_start;   // workspace: first work tile of each of them [B + 1]
+  int* seq_tile;     // workspace: first work tile of each sequence in input order [B]
+  int* tile_ctr;     // workspace: claim counter
+  float* part_ml;    // workspace, splits > 1: [work item, 2, 128, 2]
+  float* part_o;     // workspace, splits > 1: [work item, 2, 128, d]
+  int grid;
+  long long wait_limit;
+};
+cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CUtensorMap& to, const PagedFwdParams& p, int d, cudaStream_t stream);
+
 }  // namespace attn

@@ -89,16 +89,151 @@ int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cac
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Workspace: the first unit of each sequence, then the partial results.
-struct WorkPlan {
+// 3-D map over q or o, [T, H_q, d] bf16: boxes of 64 columns, the heads of a group
+// and `tokens` tokens, 128-byte swizzle.
+int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int d, int H_q, int T,
+                    int group, int tokens) {
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {row, row * H_q};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
+  cuuint32_t step[3] = {1, 1, 1};
+  const CUresult r = dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                                box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Workspace of the streaming kernel: the first unit of each sequence, then the
+// partial results.
+struct StreamPlan {
   size_t ml_off, o_off, total;
 };
-WorkPlan work_plan(int B, int d) {
-  WorkPlan w;
+StreamPlan stream_plan(int B, int d) {
+  StreamPlan w;
   w.ml_off = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
   w.o_off = w.ml_off + align256(static_cast<size_t>(2 * kStreamCtas) * 16 * 2 * sizeof(float));
   w.total = w.o_off + static_cast<size_t>(2 * kStreamCtas) * 16 * d * sizeof(float);
   return w;
+}
+
+// Work tiles of the tensor-core kernel at most, and its workspace: order and
+// first tile of the sequences, the claim counter, and where the tiles are fewer
+// than the SMs the partial results of their pieces.
+struct FwdPlan {
+  int tok_tile;
+  long long tiles;
+  int most_splits;
+  size_t ml_off, o_off, total;
+};
+FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d) {
+  FwdPlan f;
+  f.tok_tile = kTileM / group;
+  const long long rows = 2ll * f.tok_tile;
+  // every sequence with new tokens has ceil(n / rows) blocks
+  f.tiles = (T + (rows - 1) * B) / rows;
+  if (f.tiles > T) f.tiles = T;
+  f.tiles *= H_kv;
+  f.most_splits = 1;
+  if (f.tiles > 0 && f.tiles < kFwdSms) {
+    const long long s = 2 * kFwdSms / f.tiles;
+    f.most_splits = static_cast<int>(s < kFwdMaxSplits ? s : kFwdMaxSplits);
+  }
+  const size_t slots = f.most_splits > 1 ? static_cast<size_t>(f.tiles) * f.most_splits * 2 * kTileM : 0;
+  f.ml_off = align256((3 * static_cast<size_t>(B) + 2) * sizeof(int));
+  f.o_off = f.ml_off + align256(slots * 2 * sizeof(float));
+  f.total = f.o_off + slots * d * sizeof(float);
+  return f;
+}
+
+// Chunks of 16 query rows at most go to the streaming kernel, which reads each key
+// once per 16 rows and deals the keys out evenly; more rows to the tensor-core
+// kernel, whose tiles hold 128. The host knows the mean of the sequences' rows.
+bool streams(int T, int B, int group, bool e4m3) {
+  return e4m3 || group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
+}
+
+size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d) {
+  const size_t stream = stream_plan(B, d).total;
+  if (streams(T, B, group, false)) return stream;
+  const size_t fwd = fwd_plan(T, B, group, H_kv, d).total;
+  return fwd > stream ? fwd : stream;
+}
+
+int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
+                  void* o, float* lse, int H_q, int causal, float scale, uint8_t* ws, long long lse_row,
+                  long long lse_head, cudaStream_t cs) {
+  const unsigned rows = c->page_size < kStreamTile ? c->page_size : kStreamTile;
+  CUtensorMap tk, tv;
+  int st;
+  if ((st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
+      (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
+    return st;
+  const StreamPlan plan = stream_plan(seqs.B, c->d);
+  StreamParams p;
+  p.s = seqs;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.lse_row = lse_row;
+  p.lse_head = lse_head;
+  p.k_scale = c->type == ATTN_CACHE_E4M3 ? c->k_scale : nullptr;
+  p.v_scale = c->type == ATTN_CACHE_E4M3 ? c->v_scale : nullptr;
+  p.H_q = H_q;
+  p.H_kv = c->H_kv;
+  p.group = H_q / c->H_kv;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * kLog2e;
+  p.unit_start = reinterpret_cast<long long*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
+  p.grid = 2 * dev.n_sm < kStreamCtas ? 2 * dev.n_sm : kStreamCtas;
+  p.wait_limit = dev.wait_limit;
+  // 8 rows where a sequence's rows of one KV head fill no more
+  const int chunk = static_cast<long long>(seqs.T) * p.group <= 8ll * seqs.B ? 8 : 16;
+  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, cs) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q, void* o,
+               float* lse, int H_q, int causal, float scale, uint8_t* ws, cudaStream_t cs) {
+  const int group = H_q / c->H_kv;
+  const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d);
+  const unsigned rows = c->page_size < kTileN ? c->page_size : kTileN;
+  CUtensorMap tq, tk, tv, to;
+  int st;
+  if ((st = encode_rows_map(dev, &tq, q, c->d, H_q, seqs.T, group, plan.tok_tile)) != ATTN_OK ||
+      (st = encode_rows_map(dev, &to, o, c->d, H_q, seqs.T, group, plan.tok_tile)) != ATTN_OK ||
+      (st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
+      (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
+    return st;
+  PagedFwdParams p;
+  p.s = seqs;
+  p.o = o;
+  p.lse = lse;
+  p.H_q = H_q;
+  p.H_kv = c->H_kv;
+  p.group = group;
+  p.causal = causal ? 1 : 0;
+  p.tok_tile = plan.tok_tile;
+  // pieces of at least four key tiles of the longest sequence that fits the table
+  const long long keys = static_cast<long long>(seqs.max_pages) * c->page_size;
+  const long long most = (keys + 4 * kTileN - 1) / (4 * kTileN);
+  p.splits = static_cast<int>(plan.most_splits < most ? plan.most_splits : most);
+  if (p.splits < 1) p.splits = 1;
+  if (plan.tiles * p.splits > 0x3fffffffll) return ATTN_ERR_BAD_SHAPE;
+  p.max_work = static_cast<int>(plan.tiles * p.splits);
+  p.scale_log2 = scale * kLog2e;
+  p.seq_order = reinterpret_cast<int*>(ws);
+  p.tile_start = p.seq_order + seqs.B;
+  p.seq_tile = p.tile_start + seqs.B + 1;
+  p.tile_ctr = p.seq_tile + seqs.B;
+  p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
+  p.grid = dev.n_sm < p.max_work ? dev.n_sm : p.max_work;
+  p.wait_limit = dev.wait_limit;
+  return launch_paged_fwd(tq, tk, tv, to, p, c->d, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Both attention calls, after the checks they share.
@@ -114,42 +249,16 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if (T == 0) return ATTN_OK;
   if (!q || !o || !lse) return ATTN_ERR_NULL_PTR;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return ATTN_ERR_ALIGNMENT;
-  const WorkPlan plan = work_plan(B, c->d);
-  if (!workspace || workspace_bytes < plan.total) return ATTN_ERR_WORKSPACE;
+  const int group = H_q / c->H_kv;
+  if (!workspace || workspace_bytes < workspace_bytes_of(T, B, group, c->H_kv, c->d)) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   HostDevice dev;
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
-
-  const unsigned rows = c->page_size < kStreamTile ? c->page_size : kStreamTile;
-  CUtensorMap tk, tv;
-  if ((st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
-      (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
-    return st;
-  StreamParams p;
-  p.s = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
-  p.q = q;
-  p.o = o;
-  p.lse = lse;
-  p.lse_row = lse_row;
-  p.lse_head = lse_head;
-  p.k_scale = c->type == ATTN_CACHE_E4M3 ? c->k_scale : nullptr;
-  p.v_scale = c->type == ATTN_CACHE_E4M3 ? c->v_scale : nullptr;
-  p.H_q = H_q;
-  p.H_kv = c->H_kv;
-  p.group = H_q / c->H_kv;
-  p.causal = causal ? 1 : 0;
-  p.scale_log2 = scale * kLog2e;
+  const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.unit_start = reinterpret_cast<long long*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
-  p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
-  p.grid = 2 * dev.n_sm < kStreamCtas ? 2 * dev.n_sm : kStreamCtas;
-  p.wait_limit = dev.wait_limit;
-  // 8 rows where a sequence's rows of one KV head fill no more
-  const int chunk = static_cast<long long>(T) * p.group <= 8ll * B ? 8 : 16;
-  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, cs) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_CUDA;
+  if (!seqlens || streams(T, B, group, c->type == ATTN_CACHE_E4M3))
+    return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, cs);
+  return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
 }
 
 }  // namespace
@@ -198,7 +307,7 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
 size_t attn_paged_workspace_bytes(int T, int B, int H_q, int H_kv, int d) {
   if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128))
     return 0;
-  return work_plan(B, d).total;
+  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d);
 }
 
 int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
