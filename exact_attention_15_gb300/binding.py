@@ -373,214 +373,14 @@ def backward(q, k, v, o, lse, dout, scale=None, causal=False, cu_seqlens=None,
 
 # ------------------------------------------------------------------ paged key-value cache
 
-CACHE_BF16 = 0
-CACHE_E4M3 = 1
+_PAGED = ("PagedCache", "paged_append", "paged_decode", "paged_forward", "paged_workspace_bytes")
 
 
-class _PagedCacheStruct(ctypes.Structure):
-    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("k_page_stride", _L),
-                ("v_page_stride", _L), ("num_pages", _I), ("page_size", _I), ("H_kv", _I), ("d", _I),
-                ("type", _I)]
-
-
-class PagedCache:
-    """The pages that hold the keys and values of many sequences.
-
-    k and v: [num_pages, H_kv, page_size, d], bf16 or float8_e4m3fn, on the GPU,
-    contiguous within a page (pages may be further apart, as in the halves of one
-    [num_pages, 2, ...] tensor). k_scale and v_scale (e4m3): fp32 [H_kv], the
-    factor a head's stored values stand for; None for 1. Keeps the tensors; their
-    contents may change between calls."""
-
-    def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
-        kinds = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
-        for name, t in (("k", k), ("v", v)):
-            if t.dim() != 4 or t.dtype not in kinds or not t.is_cuda:
-                raise ValueError(f"{name} must be a [num_pages, H_kv, page_size, d] bf16 or "
-                                 f"float8_e4m3fn CUDA tensor, got {t.dtype} {tuple(t.shape)}")
-        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
-            raise ValueError("k and v must agree in shape, dtype and device")
-        num_pages, H_kv, page_size, d = k.shape
-        for name, t in (("k", k), ("v", v)):
-            if num_pages > 0 and t[0].stride() != (page_size * d, d, 1):
-                raise ValueError(f"{name} must be contiguous within a page")
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None:
-                continue
-            if k.dtype == torch.bfloat16:
-                raise ValueError(f"{name}: a bf16 cache has no scales")
-            _check_tensor(name, t, (H_kv,), torch.float32, k.device)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.H_kv, self.page_size, self.d = num_pages, H_kv, page_size, d
-        self.device = k.device
-        page = H_kv * page_size * d
-        self._struct = _PagedCacheStruct(
-            k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-            k.stride(0) if num_pages > 1 else page, v.stride(0) if num_pages > 1 else page,
-            num_pages, page_size, H_kv, d, kinds[k.dtype])
-        self._ref = ctypes.addressof(self._struct)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _check_paged(cache, page_table, kv_lens, cu_seqlens, tokens):
-    """The arrays that describe the sequences; returns the number of sequences."""
-    import torch
-    dev, i32 = cache.device, torch.int32
-    if kv_lens.dtype != i32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous() or kv_lens.device != dev:
-        raise ValueError(f"kv_lens must be a contiguous 1-D int32 tensor on {dev}")
-    B = kv_lens.shape[0]
-    if (page_table.dtype != i32 or page_table.dim() != 2 or page_table.shape[0] != B
-            or page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError(f"page_table must be a [{B}, max_pages] int32 tensor with contiguous rows on {dev}")
-    if cu_seqlens is None:
-        if tokens != B:
-            raise ValueError(f"without cu_seqlens there is one token per sequence: {tokens} for {B}")
-    elif (cu_seqlens.dtype != i32 or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous()
-            or cu_seqlens.device != dev):
-        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor of {B + 1} entries on {dev}")
-    return B
-
-
-def _table_args(page_table):
-    """Pointer, columns and row stride (a single row, or none, may have any)."""
-    rows, cols = page_table.shape
-    return page_table.data_ptr(), cols, page_table.stride(0) if rows > 1 else cols
-
-
-def _check_tokens(name, t, heads, d, tokens, device):
-    import torch
-    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != device
-            or t.shape != (tokens if tokens is not None else t.shape[0], heads if heads is not None else t.shape[1], d)
-            or (t.numel() and ((t.shape[1] > 1 and t.stride(1) != d) or t.stride(2) != 1))):
-        raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, {d}] on {device} whose tokens are "
-                         f"contiguous, got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-
-
-def _token_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _on_device(device, call, *args):
-    """call(*args, stream) with torch's current stream of `device`, which the C
-    call takes as the current device."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        return call(*args, torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        return call(*args, torch.cuda.current_stream().cuda_stream)
-
-
-def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=None, interleaved=False,
-                 q_out=None):
-    """Appends new tokens to the cache, with the rotary position embedding.
-
-    k and v [T, H_kv, d] and q [T, H_q, d] (or None), bf16, tokens any distance
-    apart (views of one fused projection). kv_lens [B] counts each sequence's keys
-    with its new tokens; cu_seqlens [B + 1] packs them (None: one token each).
-    inv_freq: float64 [rotary_dim / 2] on the GPU, radians per position, or None to
-    append as is. Pairs are the halves of the first rotary_dim elements, or
-    neighbours with interleaved. Returns the turned q (written to q_out if given,
-    which may be q; q itself without inv_freq and q_out)."""
-    import torch
-    dev, d = cache.device, cache.d
-    _check_tokens("k", k, cache.H_kv, d, None, dev)
-    T = k.shape[0]
-    _check_tokens("v", v, cache.H_kv, d, T, dev)
-    B = _check_paged(cache, page_table, kv_lens, cu_seqlens, T)
-    rotary = 0
-    if inv_freq is not None:
-        if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
-                or inv_freq.device != dev):
-            raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {dev}")
-        rotary = 2 * inv_freq.shape[0]
-    heads = 0
-    result = q_out
-    if q is not None:
-        _check_tokens("q", q, None, d, T, dev)
-        if q_out is not None:
-            _check_tokens("q_out", q_out, q.shape[1], d, T, dev)
-        elif rotary:
-            result = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            result = q
-        # without a rotation there is nothing to write when q stays where it is
-        heads = 0 if result is q and not rotary else q.shape[1]
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _check(_on_device(dev, load().attn_paged_append, cache._ref, _ptr(q) if heads else None, k.data_ptr(),
-                      v.data_ptr(), _ptr(result) if heads else None, _token_stride(q) if heads else 0,
-                      _token_stride(k), _token_stride(v), _token_stride(result) if heads else 0, T, B,
-                      heads, _ptr(cu_seqlens), kv_lens.data_ptr(), *_table_args(page_table),
-                      _ptr(inv_freq), rotary, int(interleaved)),
-           "attn_paged_append")
-    return result
-
-
-def paged_workspace_bytes(tokens, sequences, H_q, H_kv, d) -> int:
-    return load().attn_paged_workspace_bytes(tokens, sequences, H_q, H_kv, d)
-
-
-def _paged_outputs(cache, q, B, lse_shape, out, lse, workspace):
-    import torch
-    dev = cache.device
-    T, H_q = q.shape[0], q.shape[1]
-    if H_q < 1 or H_q % cache.H_kv:
-        raise ValueError(f"q has {H_q} heads, not a multiple of the cache's {cache.H_kv}")
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _check_tensor("out", out, q.shape, torch.bfloat16, dev)
-    if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
-    else:
-        _check_tensor("lse", lse, lse_shape, torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(paged_workspace_bytes(T, B, H_q, cache.H_kv, cache.d), dtype=torch.uint8,
-                                device=dev)
-    elif not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    return out, lse, workspace
-
-
-def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, workspace=None):
-    """Attention of one new token per sequence over the cache: q [B, H_q, d] bf16.
-    Returns (o [B, H_q, d], lse [B, H_q]); a sequence without keys gives 0 and -inf.
-    The default scale is 1/sqrt(d). The workspace (paged_workspace_bytes) is
-    allocated with torch unless given."""
-    _check_tokens("q", q, None, cache.d, None, cache.device)
-    B = _check_paged(cache, page_table, kv_lens, None, q.shape[0])
-    o, lse, ws = _paged_outputs(cache, q, B, q.shape[:2], out, lse, workspace)
-    _check(_on_device(cache.device, load().attn_paged_decode, cache._ref, q.data_ptr(), o.data_ptr(),
-                      lse.data_ptr(), B, q.shape[1], kv_lens.data_ptr(), *_table_args(page_table),
-                      1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(),
-                      ws.numel() * ws.element_size()),
-           "attn_paged_decode")
-    return o, lse
-
-
-def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=True, out=None, lse=None,
-                  workspace=None):
-    """Attention of a chunk of new tokens per sequence over the cache, which holds
-    them already: q [T, H_q, d] bf16, packed by cu_seqlens. With causal, the last new
-    token sees all keys of its sequence and each one before sees one key less.
-    Returns (o [T, H_q, d], lse [H_q, T]); rows behind the last sequence are not
-    written."""
-    _check_tokens("q", q, None, cache.d, None, cache.device)
-    if cu_seqlens is None:
-        raise ValueError("cu_seqlens is required (paged_decode takes one token per sequence)")
-    T = q.shape[0]
-    B = _check_paged(cache, page_table, kv_lens, cu_seqlens, T)
-    o, lse, ws = _paged_outputs(cache, q, B, (q.shape[1], T), out, lse, workspace)
-    _check(_on_device(cache.device, load().attn_paged_fwd, cache._ref, q.data_ptr(), o.data_ptr(),
-                      lse.data_ptr(), T, B, q.shape[1], cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-                      *_table_args(page_table), int(causal),
-                      1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(),
-                      ws.numel() * ws.element_size()),
-           "attn_paged_fwd")
-    return o, lse
+def __getattr__(name):
+    """The paged cache's layer is a module of its own, which needs torch at import."""
+    if name in _PAGED:
+        from . import paged
+        for n in _PAGED:
+            globals()[n] = getattr(paged, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

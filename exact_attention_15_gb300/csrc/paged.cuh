@@ -3,6 +3,8 @@
 // access leaves the cache or the page table whatever the device arrays hold.
 #pragma once
 
+#include <atomic>
+
 #include "attn_common.cuh"
 
 namespace attn {
@@ -48,6 +50,36 @@ __device__ __forceinline__ void check_paged_seqs(const PagedSeqs& s, int tid, in
       if ((b == 0 && a != 0) || a > e || e > s.T) record_error(s.err, kErrSeqlens);
     }
   }
+}
+
+// Launches a kernel that calls grid_wait() in every thread before it touches
+// memory: its launch and set-up overlap the end of the grid before it. The
+// shared-memory size is set once per device.
+template <typename... Args>
+cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                           std::atomic<unsigned long long>& smem_set, const Args&... args) {
+  if (smem > 48 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(smem_set.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      smem_set.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ---- appending

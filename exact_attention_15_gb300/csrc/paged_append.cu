@@ -52,6 +52,8 @@ paged_append_kernel(const AppendParams p) {
   __shared__ float2 cs[64];
   const int t = blockIdx.x, tid = threadIdx.x;
   const PagedSeqs& s = p.s;
+  grid_wait();
+  grid_release();
   if (t == 0) check_paged_seqs(s, tid, kAppendThreads);
   int b = t;
   SeqSpan span{t, 1};
@@ -148,8 +150,8 @@ paged_append_kernel(const AppendParams p) {
 
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
   const int slot = prof_begin(kKPagedAppend, stream);
-  paged_append_kernel<<<p.s.T, kAppendThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e = launch_chained(paged_append_kernel, dim3(p.s.T), kAppendThreads, 0, stream, smem_set, p);
   prof_end(slot, stream);
   return e;
 }

@@ -158,6 +158,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
     fence_barrier_init();
   }
+  grid_wait();
+  grid_release();
   // The units before each sequence: every thread sums a run of sequences, the
   // sums are scanned, and the run that holds this CTA's first unit is walked.
   const int run = (p.s.B + kThreads - 1) / kThreads;
@@ -572,6 +574,8 @@ __global__ void __launch_bounds__(128)
 paged_join_kernel(const StreamParams p) {
   __shared__ float sh_o[4][D];
   __shared__ float sh_l[4];
+  grid_wait();
+  grid_release();
   const int head = blockIdx.x % p.H_q, t = blockIdx.x / p.H_q;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int b = t;
@@ -640,18 +644,15 @@ paged_join_kernel(const StreamParams p) {
 template <int D, int R, bool FP8>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
                    cudaStream_t stream) {
-  constexpr int kSmem = StreamCfg<D, FP8>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(paged_stream_kernel<D, R, FP8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> smem_set{0};
   int slot = prof_begin(kKPagedDecode, stream);
-  paged_stream_kernel<D, R, FP8><<<p.grid, kThreads, kSmem, stream>>>(tk, tv, p);
-  e = cudaGetLastError();
+  cudaError_t e = launch_chained(paged_stream_kernel<D, R, FP8>, dim3(p.grid), kThreads,
+                                 StreamCfg<D, FP8>::kSmemBytes, stream, smem_set, tk, tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  paged_join_kernel<D, R><<<static_cast<unsigned>(p.s.T) * p.H_q, 128, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_chained(paged_join_kernel<D, R>, dim3(static_cast<unsigned>(p.s.T) * p.H_q), 128, 0, stream,
+                     smem_set, p);
   prof_end(slot, stream);
   return e;
 }

@@ -168,6 +168,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const long long lim = p.wait_limit;
+  grid_wait();
+  grid_release();
 
   // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168.
   if (warp < 4) {
@@ -546,6 +548,8 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   int* ord = plan_smem + p.s.B;  // [B] when sorting
   __shared__ long long warp_sum[33];
   const int tid = threadIdx.x, B = p.s.B;
+  grid_wait();
+  grid_release();
   if (tid == 0) *p.tile_ctr = 0;
   check_paged_seqs(p.s, tid, blockDim.x);
   if (sort) {
@@ -606,6 +610,8 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
 template <int D>
 __global__ void __launch_bounds__(128)
 paged_fwd_join_kernel(const PagedFwdParams p) {
+  grid_wait();
+  grid_release();
   const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (at >= static_cast<long long>(p.s.T) * p.H_q || p.tile_start[p.s.B] == 0) return;
@@ -652,25 +658,23 @@ paged_fwd_join_kernel(const PagedFwdParams p) {
 template <int D>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& to, const PagedFwdParams& p, cudaStream_t stream) {
-  constexpr int kSmem = PagedFwdCfg<D>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(paged_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> smem_set{0};
   // sorting compares every pair of sequences and keeps them in shared memory
   const int sort = p.s.B <= 1024;
   int slot = prof_begin(kKPagedPlan, stream);
-  paged_plan_kernel<<<1, 1024, sort ? 2 * p.s.B * sizeof(int) : 0, stream>>>(p, sort);
-  e = cudaGetLastError();
+  cudaError_t e = launch_chained(paged_plan_kernel, dim3(1), 1024,
+                                 sort ? 2 * p.s.B * static_cast<int>(sizeof(int)) : 0, stream, smem_set, p, sort);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  paged_fwd_kernel<D><<<p.grid, 384, kSmem, stream>>>(tq, tk, tv, to, p);
-  e = cudaGetLastError();
+  e = launch_chained(paged_fwd_kernel<D>, dim3(p.grid), 384, PagedFwdCfg<D>::kSmemBytes, stream, smem_set, tq, tk,
+                     tv, to, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
   slot = prof_begin(kKPagedJoin, stream);
   const long long rows = static_cast<long long>(p.s.T) * p.H_q;
-  paged_fwd_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_chained(paged_fwd_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream,
+                     smem_set, p);
   prof_end(slot, stream);
   return e;
 }

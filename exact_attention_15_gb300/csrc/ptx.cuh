@@ -396,6 +396,14 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Programmatic dependent launch: waits until the grids before this one in the
+// stream are complete and their writes visible (at once where the launch was an
+// ordinary one); lets the grid after this one be launched.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- CTA pairs
 // (cluster of two CTAs working as one M = 256 unit through cta_group::2)
 __device__ __forceinline__ uint32_t cluster_ctarank() {

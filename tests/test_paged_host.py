@@ -7,7 +7,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from exact_attention_15_gb300 import binding, build  # noqa: E402
+from exact_attention_15_gb300 import binding, build, paged  # noqa: E402
 
 OK, NULL, ALIGN, HEADDIM, SHAPE, GQA, WORKSPACE = 0, 1, 2, 3, 4, 5, 7
 A = 0x10000  # a fake, aligned address: no call here may touch memory or a device
@@ -25,7 +25,7 @@ def _cache(**kw):
     page = a["H_kv"] * a["page_size"] * a["d"]
     a.setdefault("k_page_stride", page)
     a.setdefault("v_page_stride", page)
-    return binding._PagedCacheStruct(**a)
+    return paged._PagedCacheStruct(**a)
 
 
 def _call(lib, name, cache=None, **kw):
@@ -151,7 +151,7 @@ def test_binding_checks_sequences_and_tokens():
     _raises("kv_lens", binding.paged_decode, c, q, table, _t(6, dtype=i32)[::2])
     _raises("page_table", binding.paged_decode, c, q, table[:2], lens)
     _raises("page_table", binding.paged_decode, c, q, table.long(), lens)
-    _raises("page_table", binding.paged_decode, c, q, _t(5, 3, dtype=i32).t(), lens)
+    _raises("contiguous rows", binding.paged_decode, c, q, _t(5, 3, dtype=i32).t(), lens)
     _raises("one token per sequence", binding.paged_decode, c, _t(4, 4, 64), table, lens)
     _raises("q must be", binding.paged_decode, c, _t(3, 4, 128), table, lens)
     _raises("q must be", binding.paged_decode, c, q.float(), table, lens)
