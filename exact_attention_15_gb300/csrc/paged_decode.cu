@@ -79,6 +79,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// The transpose of an 8 x 8 block of 16-bit values held as accumulator columns.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // Work units of sequence b: key tiles x KV heads x chunks of R query rows.
 __device__ __forceinline__ long long units_of(const StreamParams& p, int b, int R) {
   const int n = new_span(p.s, b).len;
@@ -258,86 +265,97 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
 
   // -------------------------------------------------------------- consumers
-  const int qd = lane & 3, r0 = lane >> 2;  // accumulator column pair, row
+  // Both products keep the query rows in N = 8 columns: S^T = K Q^T (M = 16 keys)
+  // and O^T += V^T P^T (M = 16 columns of V), so 8 rows fill the instruction that
+  // 16 would need in M. Lane: accumulator rows ar and ar + 8 (keys, or columns
+  // of V), accumulator columns 2 qd and 2 qd + 1 (query rows).
+  const int qd = lane & 3, ar = lane >> 2;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
-  // K: matrices (keys 0-7 | 8-15) x (two 16-byte chunks); V: the keys innermost
-  const int krow = warp * 16 + (mi >> 1) * 8 + mr, vrow = warp * 16 + (mi & 1) * 8 + mr;
+  const int krow = warp * 16 + (mi & 1) * 8 + mr, vrow = warp * 16 + (mi >> 1) * 8 + mr;
   // byte offset of this lane's row and first chunk; chunk c (even) lies at
   // (offset + block) ^ (c << 4), since the swizzle is an XOR on those bits
   auto row_off = [&](int row, int ch) {
     const int sw = Cfg::kRowBytes == 128 ? row & 7 : (row >> 1) & 3;
     return row * Cfg::kRowBytes + ((ch ^ sw) << 4);
   };
-  const uint32_t koff = row_off(krow, mi & 1), voff = row_off(vrow, mi >> 1);
+  const uint32_t koff = row_off(krow, mi >> 1), voff = row_off(vrow, mi & 1);
   constexpr int kChunks = Cfg::kRowBytes / 16;  // 16-byte chunks of a block's row
   auto chunk_at = [&](uint32_t base, int c) {
     return (base + (c / kChunks) * Cfg::kBlockBytes) ^ ((c % kChunks) << 4);
   };
-  constexpr int kHalves = R / 8;  // accumulator rows r0, and r0 + 8 with R = 16
+  constexpr int NB = R / 8;  // blocks of 8 query rows
   bool ok = true;
   while (next_piece<R>(p, w, x)) {
     const int rows = min(R, x.n * p.group - x.rc * R);  // of this chunk
-    // Query rows r0 and r0 + 8 as A fragments. Over an e4m3 cache the products
+    // Query rows as B fragments: row nb * 8 + ar. Over an e4m3 cache the products
     // run in fp16, which holds every e4m3 value exactly; each row is brought to
     // [1, 2) by a power of two first, so fp16's range does not matter and what
     // it rounds is below 2^-25 of the row's largest value.
-    uint32_t qa[D / 16][4];
-    float c[2];  // exponent scale of the two rows
-    int last[2]; // keys that each row sees
+    uint32_t qb[NB][D / 16][2];
+    float c[NB][2];   // exponent scale of the lane's accumulator columns
+    int last[NB][2];  // keys that those rows see
     const float k_scale = FP8 && p.k_scale ? __ldg(p.k_scale + x.h) : 1.0f;
     const float v_scale = FP8 && p.v_scale ? __ldg(p.v_scale + x.h) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c[i] = p.scale_log2 * k_scale;
-      last[i] = 0;
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) qa[kk][i] = qa[kk][i + 2] = 0u;
-      if (i >= kHalves) continue;
-      const int r = r0 + 8 * i;
-      if (r < rows) {
-        const int rr = x.rc * R + r;
+      for (int kk = 0; kk < D / 16; ++kk) qb[nb][kk][0] = qb[nb][kk][1] = 0u;
+      if (nb * 8 + ar < rows) {
+        const int rr = x.rc * R + nb * 8 + ar;
         const int tok = rr / p.group, head = rr - tok * p.group;
-        last[i] = p.causal ? min(x.len, x.len - x.n + tok + 1) : x.len;
         const uint8_t* src = static_cast<const uint8_t*>(p.q) +
             ((static_cast<size_t>(x.row0 + tok) * p.H_q + x.h * p.group + head) * D) * 2;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if constexpr (FP8) {  // the lane's four consecutive columns
             const uint2 q4 = *reinterpret_cast<const uint2*>(src + kk * 32 + qd * 8);
-            qa[kk][i] = q4.x;
-            qa[kk][i + 2] = q4.y;
+            qb[nb][kk][0] = q4.x;
+            qb[nb][kk][1] = q4.y;
           } else {
-            qa[kk][i] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4);
-            qa[kk][i + 2] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4 + 16);
+            qb[nb][kk][0] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4);
+            qb[nb][kk][1] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + qd * 4 + 16);
           }
         }
       }
+      float up = 1.0f;  // the power of two that the row was divided by
       if constexpr (FP8) {
         float top = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-          for (int e = i; e < 4; e += 2)
-            top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(qa[kk][e])), fabsf(bf16hi_to_f32(qa[kk][e]))));
+          for (int e = 0; e < 2; ++e)
+            top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(qb[nb][kk][e])), fabsf(bf16hi_to_f32(qb[nb][kk][e]))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         ex = ex > 127 ? 0 : max(-126, min(126, ex));  // infinities stay infinities
         const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        c[i] *= __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-          for (int e = i; e < 4; e += 2)
-            qa[kk][e] = pack_f16x2(bf16lo_to_f32(qa[kk][e]) * down, bf16hi_to_f32(qa[kk][e]) * down);
+          for (int e = 0; e < 2; ++e)
+            qb[nb][kk][e] = pack_f16x2(bf16lo_to_f32(qb[nb][kk][e]) * down, bf16hi_to_f32(qb[nb][kk][e]) * down);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nb * 8 + 2 * qd + e, tok = (x.rc * R + r) / p.group;
+        c[nb][e] = p.scale_log2 * k_scale * __shfl_sync(0xffffffffu, up, (2 * qd + e) * 4);
+        last[nb][e] = r >= rows ? 0 : p.causal ? min(x.len, x.len - x.n + tok + 1) : x.len;
       }
     }
-    float acc[D / 8][4];
+    float acc[NB][D / 16][4];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nb][j][e] = 0.0f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) { m[nb][e] = -INFINITY; l[nb][e] = 0.0f; }
 
     for (int t = x.t0; t < x.t1; ++t) {
       if (ok && !mbar_wait_warp(full + 8 * stage, phase, lim)) {
@@ -352,11 +370,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       if (key0 < x.len) {
         const uint32_t tile = smem_addr(smem) + stage * 2 * Cfg::kTileBytes;
         const uint32_t kb = tile + koff, vb = tile + Cfg::kTileBytes + voff;
-        float sc[2][4];  // S: keys 0-7 and 8-15 of this warp
+        // S in two chains of half the columns each
+        float sc[NB][2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nb][h][e] = 0.0f;
         if constexpr (FP8) {
 #pragma unroll
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -364,9 +385,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ldsm4(chunk_at(kb, 2 * cc), f);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              mma16816<true>(sc[0], qa[2 * cc + u], e4m3x2_to_f16x2(f[u]), e4m3x2_to_f16x2(f[u] >> 16));
-              mma16816<true>(sc[1], qa[2 * cc + u], e4m3x2_to_f16x2(f[2 + u]),
-                             e4m3x2_to_f16x2(f[2 + u] >> 16));
+              const uint32_t a[4] = {e4m3x2_to_f16x2(f[2 * u]), e4m3x2_to_f16x2(f[2 * u + 1]),
+                                     e4m3x2_to_f16x2(f[2 * u] >> 16), e4m3x2_to_f16x2(f[2 * u + 1] >> 16)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<true>(sc[nb][u], a, qb[nb][2 * cc + u][0], qb[nb][2 * cc + u][1]);
             }
           }
         } else {
@@ -374,57 +397,58 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t f[4];
             ldsm4(chunk_at(kb, 2 * kk), f);
-            mma16816<false>(sc[0], qa[kk], f[0], f[1]);
-            mma16816<false>(sc[1], qa[kk], f[2], f[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<false>(sc[nb][kk & 1], f, qb[nb][kk][0], qb[nb][kk][1]);
           }
         }
-        // softmax step of rows r0 (e = 0, 1) and r0 + 8 (e = 2, 3)
-        float mx[2];
+        // scaled scores s[nb][e]: key ar + 8 (e >> 1), query row 2 qd + (e & 1)
+        float sv[NB][4];
+        bool grew = false;
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-          mx[i] = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + ar + 8 * (e >> 1);
+            const float v = (sc[nb][0][e] + sc[nb][1][e]) * c[nb][e & 1];
+            sv[nb][e] = key < last[nb][e & 1] ? v : -INFINITY;
+            grew |= sv[nb][e] - m[nb][e & 1] > kTau;
+          }
+        // The bias moves only when some score exceeds it by more than 2^tau;
+        // until then no maximum has to be taken at all.
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = key0 + n * 8 + 2 * qd + e;
-              float& v = sc[n][2 * i + e];
-              v = key < last[i] ? v * c[i] : -INFINITY;
-              mx[i] = fmaxf(mx[i], v);
+              float mx = fmaxf(fmaxf(sv[nb][e], sv[nb][e + 2]), m[nb][e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float f = mx > m[nb][e] ? ex2_approx(m[nb][e] - mx) : 1.0f;
+              m[nb][e] = mx;
+              l[nb][e] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                acc[nb][j][e] *= f;
+                acc[nb][j][e + 2] *= f;
+              }
             }
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-          mx[i] = fmaxf(mx[i], m[i]);
-        }
-        // the bias moves only when some row's maximum grew by more than 2^tau
-        bool moved = mx[0] - m[0] > kTau;
-        if (kHalves == 2) moved |= mx[kHalves - 1] - m[kHalves - 1] > kTau;
-        if (__any_sync(0xffffffffu, moved)) {
-          float f[2] = {1.0f, 1.0f};
-#pragma unroll
-          for (int i = 0; i < kHalves; ++i) {
-            f[i] = mx[i] > m[i] ? ex2_approx(m[i] - mx[i]) : 1.0f;
-            m[i] = fmaxf(m[i], mx[i]);
-            l[i] *= f[i];
-          }
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2 * kHalves; ++e) acc[j][e] *= f[e >> 1];
         }
         // P sums up in 32 bits before it is rounded to the product's 16-bit type
-        // (bf16 as in the prompt kernels, fp16 over an e4m3 cache)
-        uint32_t pa[4] = {0u, 0u, 0u, 0u};
+        // (bf16 as in the prompt kernels, fp16 over an e4m3 cache); its 8 x 8
+        // blocks are transposed into B fragments.
+        uint32_t pb[NB][2];
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-          const float mb = m[i] == -INFINITY ? 0.0f : m[i];
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = ex2_approx(sc[n][2 * i] - mb), p1 = ex2_approx(sc[n][2 * i + 1] - mb);
-            l[i] += p0 + p1;
-            pa[2 * n + i] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          for (int h = 0; h < 2; ++h) {
+            float pv[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              pv[e] = ex2_approx(sv[nb][2 * h + e] - (m[nb][e] == -INFINITY ? 0.0f : m[nb][e]));
+              l[nb][e] += pv[e];
+            }
+            pb[nb][h] = transpose8x8(FP8 ? pack_f16x2(pv[0], pv[1]) : pack_bf16x2(pv[0], pv[1]));
           }
-        }
         // Rows of V past the sequence's end can hold anything (a page's unused
         // rows, an earlier tile): they are replaced by zeros, since 0 x NaN is NaN.
         uint32_t vm[2];
@@ -439,14 +463,16 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             uint32_t f[4];
             ldsm4_t(chunk_at(vb, 2 * cc), f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] &= vm[e & 1];
+            for (int e = 0; e < 4; ++e) f[e] &= vm[e >> 1];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {  // even and odd columns of chunk 2 cc + u
-              const int jb = 2 * (2 * cc + u);
-              mma16816<true>(acc[jb], pa, e4m3x2_to_f16x2(__byte_perm(f[2 * u], 0, 0x4420)),
-                             e4m3x2_to_f16x2(__byte_perm(f[2 * u + 1], 0, 0x4420)));
-              mma16816<true>(acc[jb + 1], pa, e4m3x2_to_f16x2(__byte_perm(f[2 * u], 0, 0x4431)),
-                             e4m3x2_to_f16x2(__byte_perm(f[2 * u + 1], 0, 0x4431)));
+            for (int u = 0; u < 2; ++u) {  // rows ar and ar + 8: columns 2 ar and 2 ar + 1
+              const uint32_t a[4] = {e4m3x2_to_f16x2(__byte_perm(f[u], 0, 0x4420)),
+                                     e4m3x2_to_f16x2(__byte_perm(f[u], 0, 0x4431)),
+                                     e4m3x2_to_f16x2(__byte_perm(f[2 + u], 0, 0x4420)),
+                                     e4m3x2_to_f16x2(__byte_perm(f[2 + u], 0, 0x4431))};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<true>(acc[nb][2 * cc + u], a, pb[nb][0], pb[nb][1]);
             }
           }
         } else {
@@ -455,9 +481,9 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             uint32_t f[4];
             ldsm4_t(chunk_at(vb, 2 * jj), f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] &= vm[e & 1];
-            mma16816<false>(acc[2 * jj], pa, f[0], f[1]);
-            mma16816<false>(acc[2 * jj + 1], pa, f[2], f[3]);
+            for (int e = 0; e < 4; ++e) f[e] &= vm[e >> 1];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<false>(acc[nb][jj], f, pb[nb][0], pb[nb][1]);
           }
         }
       }
@@ -468,14 +494,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     // ---- merge of the four warps' keys
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (qd == 0) {
-        ml[(warp * 16 + r0 + 8 * i) * 2] = m[i];
-        ml[(warp * 16 + r0 + 8 * i) * 2 + 1] = l[i];
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
+        if (ar == 0)
+          *reinterpret_cast<float2*>(ml + (warp * 16 + nb * 8 + 2 * qd + e) * 2) = make_float2(m[nb][e], l[nb][e]);
       }
-    }
     named_bar_sync(1, 32 * kWarps);
     const bool whole = x.t1 - x.t0 == x.tiles;
     const int slot = 2 * cta + (w.u - (x.t1 - x.t0) == first ? 0 : 1);
@@ -496,36 +522,37 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       for (int g = 0; g < kWarps; ++g)
         sum += ml[(g * 16 + ro) * 2 + 1] * ex2_approx(ml[(g * 16 + ro) * 2] - mb);
     }
-    float mine[kHalves];  // factor of this lane's accumulator rows
+    float mine[NB][2];  // factors of this lane's accumulator columns
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      float t = -INFINITY;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int g = 0; g < kWarps; ++g) t = fmaxf(t, ml[(g * 16 + r0 + 8 * i) * 2]);
-      mine[i] = ex2_approx(m[i] - (t == -INFINITY ? 0.0f : t));
-    }
+      for (int e = 0; e < 2; ++e) {
+        float t = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kWarps; ++g) t = fmaxf(t, ml[(g * 16 + nb * 8 + 2 * qd + e) * 2]);
+        mine[nb][e] = ex2_approx(m[nb][e] - (t == -INFINITY ? 0.0f : t));
+      }
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += kCols) {
       if (c0 > 0) named_bar_sync(1, 32 * kWarps);
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i) {
-        const int r = r0 + 8 * i;
-        const float f = mine[i];
-        float* dst = merge + (warp * R + r) * kCols;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = c0 / 8; j < (c0 + kCols) / 8; ++j) {
-          // column of the lane's first value, and the step to its second
-          const int col = (FP8 ? (j >> 1) * 16 + 4 * qd + (j & 1) : j * 8 + 2 * qd) - c0;
-          const int sw = (r & 3) << 3;
-          if constexpr (FP8) {
-            dst[col ^ sw] = acc[j][2 * i] * f;
-            dst[(col + 2) ^ sw] = acc[j][2 * i + 1] * f;
-          } else {
-            *reinterpret_cast<float2*>(dst + (col ^ sw)) =
-                make_float2(acc[j][2 * i] * f, acc[j][2 * i + 1] * f);
+        for (int e = 0; e < 2; ++e) {
+          const float f = mine[nb][e];
+          float* dst = merge + (warp * R + nb * 8 + 2 * qd + e) * kCols;
+#pragma unroll
+          for (int j = c0 / 16; j < (c0 + kCols) / 16; ++j) {
+            const float a = acc[nb][j][e] * f, b = acc[nb][j][e + 2] * f;
+            const int col = j * 16 - c0;
+            if constexpr (FP8) {
+              *reinterpret_cast<float2*>(dst + ((col + 2 * ar) ^ (qd << 3))) = make_float2(a, b);
+            } else {
+              dst[(col + ar) ^ (qd << 3)] = a;
+              dst[(col + ar + 8) ^ (qd << 3)] = b;
+            }
           }
         }
-      }
       named_bar_sync(1, 32 * kWarps);
       if (ro < rows) {
         const int r = ro;
@@ -534,7 +561,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int e = 0; e < 8; ++e) o[e] = 0.0f;
 #pragma unroll
         for (int g = 0; g < kWarps; ++g) {
-          const float* src = merge + (g * R + r) * kCols + ((g8 * 8) ^ ((r & 3) << 3));
+          const float* src = merge + (g * R + r) * kCols + ((g8 * 8) ^ (((r >> 1) & 3) << 3));
           const float4 a = *reinterpret_cast<const float4*>(src);
           const float4 d4 = *reinterpret_cast<const float4*>(src + 4);
           o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
