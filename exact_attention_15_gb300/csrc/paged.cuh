@@ -109,7 +109,7 @@ struct StreamParams {
   const float* k_scale; const float* v_scale;
   int H_q, H_kv, group, causal;
   float scale_log2;
-  long long* unit_start;  // workspace: [B + 1] first work unit of each sequence
+  int4* heads;            // workspace: [kStreamCtas, 2] where the pieces of a split item begin
   float* part_ml;         // workspace: [2 kStreamCtas, 16, 2]
   float* part_o;          // workspace: [2 kStreamCtas, 16, d]
   int grid;

@@ -104,14 +104,14 @@ int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Workspace of the streaming kernel: the first unit of each sequence, then the
-// partial results.
+// Workspace of the streaming kernel: what each CTA says about the split item that
+// begins in it, then the partial results.
 struct StreamPlan {
   size_t ml_off, o_off, total;
 };
-StreamPlan stream_plan(int B, int d) {
+StreamPlan stream_plan(int d) {
   StreamPlan w;
-  w.ml_off = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
+  w.ml_off = align256(static_cast<size_t>(2 * kStreamCtas) * sizeof(int4));
   w.o_off = w.ml_off + align256(static_cast<size_t>(2 * kStreamCtas) * 16 * 2 * sizeof(float));
   w.total = w.o_off + static_cast<size_t>(2 * kStreamCtas) * 16 * d * sizeof(float);
   return w;
@@ -154,7 +154,7 @@ bool streams(int T, int B, int group, bool e4m3) {
 }
 
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d) {
-  const size_t stream = stream_plan(B, d).total;
+  const size_t stream = stream_plan(d).total;
   if (streams(T, B, group, false)) return stream;
   const size_t fwd = fwd_plan(T, B, group, H_kv, d).total;
   return fwd > stream ? fwd : stream;
@@ -169,7 +169,7 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   if ((st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
     return st;
-  const StreamPlan plan = stream_plan(seqs.B, c->d);
+  const StreamPlan plan = stream_plan(c->d);
   StreamParams p;
   p.s = seqs;
   p.q = q;
@@ -184,7 +184,7 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.group = H_q / c->H_kv;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * kLog2e;
-  p.unit_start = reinterpret_cast<long long*>(ws);
+  p.heads = reinterpret_cast<int4*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
   p.grid = 2 * dev.n_sm < kStreamCtas ? 2 * dev.n_sm : kStreamCtas;

@@ -145,6 +145,19 @@ __device__ __forceinline__ bool next_piece(const StreamParams& p, Walk& w, Piece
   return true;
 }
 
+// O = 0 and LSE = -inf for the query rows of a sequence without keys (one warp).
+template <int D>
+__device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows, int lane) {
+  uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
+                                      static_cast<size_t>(rows.start) * p.H_q * D);
+  const long long chunks = static_cast<long long>(rows.len) * p.H_q * (D / 8);
+  for (long long i = lane; i < chunks; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+  for (long long i = lane; i < static_cast<long long>(rows.len) * p.H_q; i += 32) {
+    const int r = static_cast<int>(i / p.H_q), head = static_cast<int>(i - static_cast<long long>(r) * p.H_q);
+    p.lse[(rows.start + r) * p.lse_row + head * p.lse_head] = -INFINITY;
+  }
+}
+
 template <int D, int R, bool FP8>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -154,7 +167,6 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   float* merge = reinterpret_cast<float*>(smem + Cfg::kMergeOff);
   float* ml = reinterpret_cast<float*>(smem + Cfg::kMlOff);  // [warp][16][2]
   const uint32_t full = smem_addr(smem + Cfg::kBarOff), empty = full + 8 * Cfg::kStages;
-  long long* pre = reinterpret_cast<long long*>(merge);  // [kThreads + 1], before the first merge
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long lim = p.wait_limit;
 
@@ -167,52 +179,37 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
   grid_wait();
   grid_release();
-  // The units before each sequence: every thread sums a run of sequences, the
-  // sums are scanned, and the run that holds this CTA's first unit is walked.
-  const int run = (p.s.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.s.B, tid * run), b1 = min(p.s.B, b0 + run);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(p, b, R);
-  pre[tid + 1] = mine;
-  if (tid == 0) pre[0] = 0;
-  if (blockIdx.x == 0) check_paged_seqs(p.s, tid, kThreads);
-  __syncthreads();
-  if (warp == 0) {
-    long long carry = 0;
-    for (int i = 0; i < kThreads; i += 32) {
-      long long x = pre[i + lane + 1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      pre[i + lane + 1] = x + carry;
-      carry += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();
-  const long long total = pre[kThreads];
-  if (blockIdx.x == 0) {  // for the join
-    long long at = pre[tid];
-    for (int b = b0; b < b1; ++b) {
-      p.unit_start[b] = at;
-      at += units_of(p, b, R);
-    }
-    if (tid == 0) p.unit_start[p.s.B] = total;
-  }
-  const int grid = busy_ctas(total, gridDim.x), cta = blockIdx.x;
-  if (cta >= grid) return;
-  Walk w;
-  w.u = first_unit(total, grid, cta);
-  w.end = first_unit(total, grid, cta + 1);
+  // The units before each sequence: every lane sums a run of sequences, the sums
+  // are scanned, and the run that holds this CTA's first unit is walked. Each
+  // warp does so for itself, so none waits for another.
+  const int cta = blockIdx.x;
+  const int run = (p.s.B + 31) >> 5;
+  long long before, total;
   {
-    int lo = 0, hi = kThreads;  // the last run that starts at or before the first unit
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= w.u) lo = mid; else hi = mid;
+    const int b1 = min(p.s.B, (lane + 1) * run);
+    long long mine = 0;
+#pragma unroll 4
+    for (int b = lane * run; b < b1; ++b) mine += units_of(p, b, R);
+    before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
     }
-    w.b = min(p.s.B, lo * run);
-    w.base = pre[lo];
+    total = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+  }
+  const int grid = busy_ctas(total, gridDim.x);
+  Walk w;
+  w.u = w.end = w.base = 0;
+  w.b = 0;
+  if (cta < grid) {
+    w.u = first_unit(total, grid, cta);
+    w.end = first_unit(total, grid, cta + 1);
+    // the last run that starts at or before the first unit (lane 0's does)
+    const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= w.u));
+    w.b = at * run;
+    w.base = __shfl_sync(0xffffffffu, before, at);
   }
   __syncthreads();
   const long long first = w.u;
@@ -261,6 +258,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
     }
     if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
+    // off the way of the loads: what no work unit covers
+    if (cta == 0) check_paged_seqs(p.s, lane, 32);
+    if (cta >= grid && lane == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
+    for (int b = cta; b < p.s.B; b += gridDim.x)
+      if (kv_len(p.s, b) == 0) write_empty<D>(p, new_span(p.s, b), lane);
     return;
   }
 
@@ -505,6 +507,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     named_bar_sync(1, 32 * kWarps);
     const bool whole = x.t1 - x.t0 == x.tiles;
     const int slot = 2 * cta + (w.u - (x.t1 - x.t0) == first ? 0 : 1);
+    if (w.u == w.end && tid == 0) {
+      // for the join: the item that begins in this CTA and ends in a later one
+      const bool head = x.t0 == 0 && !whole;
+      const int pieces = head ? owner_of(total, grid, w.u + (x.tiles - x.t1) - 1) - cta + 1 : 0;
+      p.heads[2 * cta] = make_int4(pieces, slot, x.row0, rows);
+      p.heads[2 * cta + 1] = make_int4(x.h, x.rc * R, 0, 0);
+    }
     // O passes through shared memory in runs of kCols columns, each 8-column
     // group moved within its row so that the warps' stores spread over the banks
     // (each thread's own row of the result: its statistics are read before the
@@ -593,79 +602,76 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
 }
 
-// One CTA per query row and head: merges the pieces of its item, or writes the
-// empty result of a row whose sequence has no keys. Rows behind the last
-// sequence are left as they were.
-template <int D, int R>
+// Merges the pieces of split items in their order. CTA (c, y) does every
+// kJoinRows-th query row of the item that begins in the streaming kernel's CTA c
+// and ends in a later one; there are fewer such items than CTAs. Each warp takes
+// every fourth piece with a running maximum, then the warps' sums are merged.
+constexpr int kJoinRows = 8;
+template <int D>
 __global__ void __launch_bounds__(128)
 paged_join_kernel(const StreamParams p) {
   __shared__ float sh_o[4][D];
-  __shared__ float sh_l[4];
+  __shared__ float2 sh_ml[4];
   grid_wait();
   grid_release();
-  const int head = blockIdx.x % p.H_q, t = blockIdx.x / p.H_q;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int b = t;
-  if (p.s.cu_seqlens) {
-    int lo = 0, hi = p.s.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
-    }
-    b = lo;
-  }
-  const SeqSpan sp = new_span(p.s, b);
-  if (t < sp.start || t >= sp.start + sp.len) return;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(t) * p.H_q + head) * D;
-  float* lse = p.lse + t * p.lse_row + head * p.lse_head;
-  const int tiles = (kv_len(p.s, b) + kTile - 1) / kTile;
-  if (tiles == 0) {
-    if (threadIdx.x < D / 8) reinterpret_cast<uint4*>(out)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) *lse = -INFINITY;
-    return;
-  }
-  const int h = head / p.group, rr = (t - sp.start) * p.group + head - h * p.group;
-  const int chunks = static_cast<int>((static_cast<long long>(sp.len) * p.group + R - 1) / R);
-  const int rc = rr / R, r = rr - rc * R;
-  const long long total = p.unit_start[p.s.B];
-  const long long u0 = p.unit_start[b] + (static_cast<long long>(h) * chunks + rc) * tiles;
-  const int grid = busy_ctas(total, p.grid);
-  const int c0 = owner_of(total, grid, u0), c1 = owner_of(total, grid, u0 + tiles - 1);
-  if (c0 == c1) return;  // written whole
-  const int s0 = 2 * c0 + (first_unit(total, grid, c0) == u0 ? 0 : 1);
-  const int pieces = c1 - c0 + 1;
-  auto at = [&](int i) { return static_cast<size_t>(i == 0 ? s0 : 2 * (c0 + i)) * 16 + r; };
-  float top = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.part_ml[at(i) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float mb = top == -INFINITY ? 0.0f : top;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 a = p.heads[2 * c], d = p.heads[2 * c + 1];
+  const int pieces = a.x, slot0 = a.y, row0 = a.z, rows = a.w;
+  if (pieces == 0) return;
   constexpr int kV = D / 32;
-  float acc[kV], l = 0.0f;
+  for (int r = blockIdx.y; r < rows; r += kJoinRows) {
+    float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
 #pragma unroll 4
-  for (int i = warp; i < pieces; i += 4) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(i) * 2);
-    const float f = ex2_approx(ml.x - mb);
-    l += ml.y * f;
-    const float* src = p.part_o + at(i) * D + lane * kV;
+    for (int i = warp; i < pieces; i += 4) {
+      const size_t at = static_cast<size_t>(i == 0 ? slot0 : 2 * (c + i)) * 16 + r;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+      float o[kV];
+      if constexpr (kV == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * 4);
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * 2);
+        o[0] = v.x; o[1] = v.y;
+      }
+      const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
+      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
+      m = top;
+      l = l * f + ml.y * g;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] += src[e] * f;
-  }
+      for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + o[e] * g;
+    }
 #pragma unroll
-  for (int e = 0; e < kV; ++e) sh_o[warp][lane * kV + e] = acc[e];
-  if (lane == 0) sh_l[warp] = l;
-  __syncthreads();
-  const float sum = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (threadIdx.x < D / 2) {
-    const int e = 2 * threadIdx.x;
-    const float a = (sh_o[0][e] + sh_o[1][e]) + (sh_o[2][e] + sh_o[3][e]);
-    const float d = (sh_o[0][e + 1] + sh_o[1][e + 1]) + (sh_o[2][e + 1] + sh_o[3][e + 1]);
-    reinterpret_cast<uint32_t*>(out)[threadIdx.x] = pack_bf16x2(a * inv, d * inv);
+    for (int e = 0; e < kV; ++e) sh_o[warp][lane * kV + e] = acc[e];
+    if (lane == 0) sh_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    float top = -INFINITY, sum = 0.0f, f[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) top = fmaxf(top, sh_ml[g].x);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f[g] = ex2_approx(sh_ml[g].x - (top == -INFINITY ? 0.0f : top));
+      sum += sh_ml[g].y * f[g];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = d.y + r, tok = rr / p.group, head = d.x * p.group + rr - tok * p.group;
+    const size_t row = static_cast<size_t>(row0) + tok;
+    if (threadIdx.x < D / 2) {
+      const int e = 2 * threadIdx.x;
+      float v[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        v[0] += sh_o[g][e] * f[g];
+        v[1] += sh_o[g][e + 1] * f[g];
+      }
+      reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D)[threadIdx.x] =
+          pack_bf16x2(v[0] * inv, v[1] * inv);
+    }
+    if (threadIdx.x == 0)
+      p.lse[row * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+    __syncthreads();
   }
-  if (threadIdx.x == 0) *lse = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
 template <int D, int R, bool FP8>
@@ -678,8 +684,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamPar
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained(paged_join_kernel<D, R>, dim3(static_cast<unsigned>(p.s.T) * p.H_q), 128, 0, stream,
-                     smem_set, p);
+  e = launch_chained(paged_join_kernel<D>, dim3(p.grid, kJoinRows), 128, 0, stream, smem_set, p);
   prof_end(slot, stream);
   return e;
 }
