@@ -401,6 +401,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int q0 = t.q0 + i * p.tok_tile;           // first token of this query tile
       const int see0 = t.len - t.n_new + q0;          // the last key that it sees (causal)
       const int tok = q0 + tok_r;
+      // keys that this row sees: one comparison per score covers both masks
+      const int see = p.causal ? min(t.len, see0 + tok_r + 1) : t.len;
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
         if (!mbar_wait(smem_addr(&bars->s_full[i]), sw & 1, lim)) { ok = false; break; }
@@ -419,10 +421,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool rescale_warp;
         float factor;
         const bool pos = c > 0.0f;
-        const float mb = pos ? softmax_row_max<true>(s, c, m_used, l, kv0, see0 + tok_r, t.len, need_mask,
-                                                     p.causal, rescale_warp, factor)
-                             : softmax_row_max<false>(s, c, m_used, l, kv0, see0 + tok_r, t.len, need_mask,
-                                                      p.causal, rescale_warp, factor);
+        const float mb = pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                     rescale_warp, factor)
+                             : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                      rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
         if (pos) softmax_row_exp<0, true, 0, 64>(s, c, mb, need_mask, pk, sum2);
         else softmax_row_exp<0, false, 0, 64>(s, c, mb, need_mask, pk, sum2);
@@ -484,43 +486,41 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // a row with a NaN score has l = NaN and keeps it
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
       const size_t row = static_cast<size_t>(t.row0) + tok;
-      // a tile that ends inside the sequence leaves through shared memory and TMA
-      // stores of whole rows; the last one row by row, since its box would reach
-      // into the next sequence
-      if (q0 + p.tok_tile <= t.n_new) {
-        uint32_t buf_off = Cfg::kEpiOff + i * Cfg::kBlockBytes;
-        asm volatile("" : "+r"(buf_off));  // computed here, not kept across the key loop
-        uint8_t* buf = smem + buf_off;
+      // O leaves through shared memory, 64 columns at a time: by one TMA store of
+      // whole rows where the tile ends inside the sequence, else (the store's box
+      // would reach into the next sequence) by 128-byte runs of the rows it has
+      const bool box = q0 + p.tok_tile <= t.n_new;
+      const int rows = min(p.tok_tile, t.n_new - q0) * p.group;
+      uint32_t buf_off = Cfg::kEpiOff + i * Cfg::kBlockBytes;
+      asm volatile("" : "+r"(buf_off));  // computed here, not kept across the key loop
+      uint8_t* buf = smem + buf_off;
 #pragma unroll
-        for (int hf = 0; hf < Cfg::kBlocks; ++hf) {
-          uint32_t w[32];
+      for (int hf = 0; hf < Cfg::kBlocks; ++hf) {
+        uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(ov[hf * 64 + 2 * e]) * inv_l,
-                               __uint_as_float(ov[hf * 64 + 2 * e + 1]) * inv_l);
-          if (r == 0) bulk_wait_group_read<0>();
-          named_bar_sync(2 + i, 128);
+        for (int e = 0; e < 32; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(ov[hf * 64 + 2 * e]) * inv_l,
+                             __uint_as_float(ov[hf * 64 + 2 * e + 1]) * inv_l);
+        if (r == 0) bulk_wait_group_read<0>();
+        named_bar_sync(2 + i, 128);
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(buf + sw128_offset(r, ch)) =
-                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-          fence_async_shared();
-          named_bar_sync(2 + i, 128);
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(buf + sw128_offset(r, ch)) =
+              make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        if (box) fence_async_shared();
+        named_bar_sync(2 + i, 128);
+        if (box) {
           if (r == 0) {
             tma_store_3d(&tm_o, smem_addr(buf), hf * 64, t.h * p.group, t.row0 + q0);
             bulk_commit_group();
           }
-        }
-      } else if (row_ok) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + hq) * D);
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(ov[8 * e + 2 * x]) * inv_l,
-                               __uint_as_float(ov[8 * e + 2 * x + 1]) * inv_l);
-          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          for (int x = r; x < rows * 8; x += 128) {
+            const int rr = x >> 3, tk = rr / p.group;
+            const size_t at = (static_cast<size_t>(t.row0 + q0 + tk) * p.H_q + t.h * p.group + rr - tk * p.group) * D;
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at + hf * 64 + (x & 7) * 8) =
+                *reinterpret_cast<const uint4*>(buf + sw128_offset(rr, x & 7));
+          }
         }
       }
       if (row_ok)
