@@ -119,23 +119,27 @@ cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, co
                                 int d, int rows, bool e4m3, cudaStream_t stream);
 
 // ---- tensor-core attention: many query rows per sequence
-constexpr int kFwdSms = 152;       // SMs that the workspace is planned for
-constexpr int kFwdMaxSplits = 32;  // pieces of a work tile's keys
+constexpr int kFwdSms = 152;               // CTAs that the workspace is planned for
+constexpr int kFwdListed = 4 * kFwdSms;    // work tiles that the planning kernel describes
+
 struct PagedFwdParams {
   PagedSeqs s;
   void* o;     // bf16 [T, H_q, d]
   float* lse;  // [H_q, T]
   int H_q, H_kv, group, causal;
   int tok_tile;      // query tokens per 128-row tile: floor(128 / group)
-  int splits;        // pieces of a work tile's keys
-  int max_work;      // work items (tile, piece) that the host made room for
+  int split;         // few work tiles: whole waves of them, the rest cut evenly
+  int max_work;      // work tiles that the host expects at most
   float scale_log2;
   int* seq_order;    // workspace: sequences, longest first [B]
   int* tile_start;   // workspace: first work tile of each of them [B + 1]
-  int* seq_tile;     // workspace: first work tile of each sequence in input order [B]
-  int* tile_ctr;     // workspace: claim counter
-  float* part_ml;    // workspace, splits > 1: [work item, 2, 128, 2]
-  float* part_o;     // workspace, splits > 1: [work item, 2, 128, d]
+  int* tile_ctr;     // workspace: claim counter (split == 0)
+  int4* tiles;       // workspace: the first kFwdListed work tiles, three words each
+  int4* shares;      // workspace, split: each CTA's share of the rest [grid]
+  int* rest_units;   // workspace, split: first unit of each work tile of the rest [grid + 1]
+  int2* rest_owners; // workspace, split: first and last CTA of each of them [grid]
+  float* part_ml;    // workspace, split: [2 grid, 2, 128, 2]
+  float* part_o;     // workspace, split: [2 grid, 2, 128, d]
   int grid;
   long long wait_limit;
 };

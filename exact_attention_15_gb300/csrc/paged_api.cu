@@ -118,13 +118,13 @@ StreamPlan stream_plan(int d) {
 }
 
 // Work tiles of the tensor-core kernel at most, and its workspace: order and
-// first tile of the sequences, the claim counter, and where the tiles are fewer
-// than the SMs the partial results of their pieces.
+// first tile of the sequences, the claim counter, and where there are few tiles for
+// each SM the shares of the rest and the partial results of its pieces.
 struct FwdPlan {
   int tok_tile;
   long long tiles;
-  int most_splits;
-  size_t ml_off, o_off, total;
+  bool split;
+  size_t tiles_off, ml_off, o_off, total;
 };
 FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d) {
   FwdPlan f;
@@ -134,13 +134,12 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d) {
   f.tiles = (T + (rows - 1) * B) / rows;
   if (f.tiles > T) f.tiles = T;
   f.tiles *= H_kv;
-  f.most_splits = 1;
-  if (f.tiles > 0 && f.tiles < kFwdSms) {
-    const long long s = 2 * kFwdSms / f.tiles;
-    f.most_splits = static_cast<int>(s < kFwdMaxSplits ? s : kFwdMaxSplits);
-  }
-  const size_t slots = f.most_splits > 1 ? static_cast<size_t>(f.tiles) * f.most_splits * 2 * kTileM : 0;
-  f.ml_off = align256((3 * static_cast<size_t>(B) + 2) * sizeof(int));
+  // From four waves on, claiming leaves an SM idle for less than the join costs.
+  f.split = f.tiles < kFwdListed;
+  const size_t slots = f.split ? static_cast<size_t>(2 * kFwdSms) * 2 * kTileM : 0;
+  // ints, then the listed tiles, the shares and the owners of the rest
+  f.tiles_off = align256((2 * static_cast<size_t>(B) + 2 + kFwdSms + 1) * sizeof(int));
+  f.ml_off = f.tiles_off + align256((3 * kFwdListed + kFwdSms) * sizeof(int4) + kFwdSms * sizeof(int2));
   f.o_off = f.ml_off + align256(slots * 2 * sizeof(float));
   f.total = f.o_off + slots * d * sizeof(float);
   return f;
@@ -217,21 +216,21 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = plan.tok_tile;
-  // pieces of at least four key tiles of the longest sequence that fits the table
-  const long long keys = static_cast<long long>(seqs.max_pages) * c->page_size;
-  const long long most = (keys + 4 * kTileN - 1) / (4 * kTileN);
-  p.splits = static_cast<int>(plan.most_splits < most ? plan.most_splits : most);
-  if (p.splits < 1) p.splits = 1;
-  if (plan.tiles * p.splits > 0x3fffffffll) return ATTN_ERR_BAD_SHAPE;
-  p.max_work = static_cast<int>(plan.tiles * p.splits);
+  if (plan.tiles > 0x3fffffffll) return ATTN_ERR_BAD_SHAPE;
+  p.split = plan.split ? 1 : 0;
+  p.max_work = static_cast<int>(plan.tiles);
   p.scale_log2 = scale * kLog2e;
   p.seq_order = reinterpret_cast<int*>(ws);
   p.tile_start = p.seq_order + seqs.B;
-  p.seq_tile = p.tile_start + seqs.B + 1;
-  p.tile_ctr = p.seq_tile + seqs.B;
+  p.tile_ctr = p.tile_start + seqs.B + 1;
+  p.rest_units = p.tile_ctr + 1;
+  p.tiles = reinterpret_cast<int4*>(ws + plan.tiles_off);
+  p.shares = p.tiles + 3 * kFwdListed;
+  p.rest_owners = reinterpret_cast<int2*>(p.shares + kFwdSms);
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
-  p.grid = dev.n_sm < p.max_work ? dev.n_sm : p.max_work;
+  const int sms = dev.n_sm < kFwdSms ? dev.n_sm : kFwdSms;
+  p.grid = plan.split ? sms : dev.n_sm < p.max_work ? dev.n_sm : p.max_work;
   p.wait_limit = dev.wait_limit;
   return launch_paged_fwd(tq, tk, tv, to, p, c->d, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -16,9 +16,11 @@
 // Rows of V past the sequence's end can hold anything, and 0 x NaN is NaN: the
 // MMA warp zeroes them in shared memory before the last P V product.
 //
-// With fewer work tiles than SMs the keys of a tile are cut into `splits` pieces
-// of equal length that different CTAs take; each leaves its (m, l, O) in the
-// workspace and paged_fwd_join_kernel merges them in order.
+// With many work tiles the CTAs claim them one by one. With few, what the last
+// wave leaves idle costs more: every CTA takes the same number of whole tiles, and
+// the rest (fewer tiles than CTAs) is cut by keys into one share per CTA, such that
+// all have the same work. A piece of a tile leaves its (m, l, O) in the workspace,
+// and paged_fwd_join_kernel merges the pieces in order.
 //
 // TMEM (512 columns): O_0 [0, d), O_1 [d, 2d), S_0/P_0 [2d, 2d + 128), S_1/P_1
 // [2d + 128, 2d + 256).
@@ -43,6 +45,7 @@ struct PagedFwdCfg {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
+static_assert(kFwdListed <= 1024, "one thread of the planning kernel per listed tile");
 struct __align__(16) PagedTile {
   int b, h;        // sequence (< 0 ends the list), KV head
   int row0;        // first packed row of the sequence
@@ -50,7 +53,7 @@ struct __align__(16) PagedTile {
   int n_new, len;  // tokens of the chunk, keys of the sequence
   int kt0;         // first key tile of this piece
   int n[2];        // key tiles that each query tile visits here
-  int item;        // work item, for the partial results
+  int slot;        // of the partial results, or -1: the piece is whole
   int pad[2];
 };
 
@@ -77,34 +80,37 @@ __device__ __forceinline__ int keys_seen(const PagedFwdParams& p, int q0, int n,
   if (q0 >= n) return 0;
   return p.causal ? max(0, len - n + min(q0 + p.tok_tile, n)) : len;
 }
-// The key tiles of piece `s` of a work tile: [first, first + count) of its `all`.
-__device__ __forceinline__ int piece_start(int all, int s, int splits) {
-  return static_cast<int>(static_cast<long long>(all) * s / splits);
-}
-
-// Work item w = (tile, piece); the tiles of a sequence run from its last block
-// of tokens (which sees most keys) to its first, the KV heads innermost.
-__device__ __forceinline__ void expand_item(const PagedFwdParams& p, int item, int b, int tile0,
-                                            PagedTile& t) {
-  const int tile = item / p.splits, piece = item - tile * p.splits;
+// Work tile `local` of sequence b: the tiles run from its last block of tokens
+// (which sees most keys) to its first, the KV heads innermost. All its keys.
+__device__ __forceinline__ void expand_tile(const PagedFwdParams& p, int local, int b, PagedTile& t) {
   const SeqSpan sp = new_span(p.s, b);
   t.b = b;
   t.row0 = sp.start;
   t.n_new = sp.len;
   t.len = kv_len(p.s, b);
-  const int local = tile - tile0;
   const int mi = local / p.H_kv;
   t.h = local - mi * p.H_kv;
   t.q0 = (m_blocks(p, sp.len) - 1 - mi) * 2 * p.tok_tile;
-  int n[2];
+  t.kt0 = 0;
   for (int i = 0; i < 2; ++i)
-    n[i] = (keys_seen(p, t.q0 + i * p.tok_tile, t.n_new, t.len) + kTileN - 1) / kTileN;
-  const int all = max(n[0], n[1]);
-  t.kt0 = piece_start(all, piece, p.splits);
-  const int end = piece_start(all, piece + 1, p.splits);
-  for (int i = 0; i < 2; ++i) t.n[i] = max(0, min(n[i], end) - t.kt0);
-  t.item = item;
+    t.n[i] = (keys_seen(p, t.q0 + i * p.tok_tile, t.n_new, t.len) + kTileN - 1) / kTileN;
+  t.slot = -1;
 }
+// The last of `count` entries of a non-decreasing array that is <= x (the first
+// one is). Entries without anything of their own share the next one's value and
+// are never found.
+__device__ __forceinline__ int find_last(const int* a, int count, int x) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+// Units of a work tile: its key tiles, and what beginning and ending it costs
+// (about two of them).
+constexpr int kItemCost = 2;
+__device__ __forceinline__ int tile_units(const PagedTile& t) { return max(t.n[0], t.n[1]) + kItemCost; }
 
 // The k-th work tile of this CTA, as the scheduler warp published it; false at
 // the end of the list, or when the wait ran out (`ok`).
@@ -328,58 +334,98 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (!ok && leader) record_error(p.s.err, kErrTimeout);
     } else if (warp == 2 && lane == 0) {
       // -------------------------------------------------------- scheduler
-      // The CTA starts with work item blockIdx.x and claims every further one
-      // from the counter that the planning kernel zeroed. Near the end of the
-      // list an item is claimed only once the producer has taken the one before,
-      // so no CTA holds items that an idle one could run.
-      const int total = p.tile_start[p.s.B] * p.splits;
-      constexpr int kNearRounds = 4;
-      int lo_item = 0, hi_item = -1, seq = 0, tile0 = 0;  // items of the last sequence found
-      int item = blockIdx.x;
-      for (int k = 0;; ++k) {
-        PagedTile t;
-        if (item < total) {
-          if (item < lo_item || item >= hi_item) {
-            const int tile = item / p.splits;
-            int lo = 0, hi = p.s.B;  // the last sequence whose first tile is <= tile
-            while (hi - lo > 1) {
-              const int mid = (lo + hi) >> 1;
-              if (p.tile_start[mid] <= tile) lo = mid; else hi = mid;
-            }
-            seq = p.seq_order[lo];
-            tile0 = p.tile_start[lo];
-            lo_item = tile0 * p.splits;
-            hi_item = p.tile_start[lo + 1] * p.splits;
-          }
-          expand_item(p, item, seq, tile0, t);
-        } else {
-          t = PagedTile{};
-          t.b = -1;
+      const int total = p.tile_start[p.s.B], grid = gridDim.x, cta = blockIdx.x;
+      int lo_tile = 0, hi_tile = -1, seq = 0;  // work tiles of the last sequence found
+      auto expand = [&](int tile, PagedTile& t) {
+        if (tile < kFwdListed) {
+          int4* w = reinterpret_cast<int4*>(&t);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) w[i] = p.tiles[3 * tile + i];
+          return;
         }
+        if (tile < lo_tile || tile >= hi_tile) {
+          const int v = find_last(p.tile_start, p.s.B, tile);
+          seq = p.seq_order[v];
+          lo_tile = p.tile_start[v];
+          hi_tile = p.tile_start[v + 1];
+        }
+        expand_tile(p, tile - lo_tile, seq, t);
+      };
+      int k = 0;
+      auto publish = [&](const PagedTile& t) {
         const int slot = k % kSlots;
         if (k >= kSlots &&
             !mbar_wait_sleep(smem_addr(&bars->sched_empty[slot]), ((k / kSlots) - 1) & 1, lim, 200)) {
           record_error(p.s.err, kErrTimeout);
-          break;
+          return false;
         }
         bars->sched_t[slot] = t;
         mbar_arrive(smem_addr(&bars->sched_full[slot]));
-        if (t.b < 0) break;
-        if (item + kNearRounds * static_cast<long long>(gridDim.x) >= total) {
-          bool taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) > k;
-          const long long t0 = clock64();
-          while (!taken && clock64() - t0 <= lim) {
-            __nanosleep(100);
-            taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) > k;
-          }
-          if (!taken) {  // the other roles' bounded waits end the CTA
-            record_error(p.s.err, kErrTimeout);
-            break;
-          }
+        ++k;
+        return true;
+      };
+      bool ok = true;
+      if (p.split) {
+        // whole waves, then this CTA's share of the rest
+        const int waves = total / grid;
+        for (int i = 0; ok && i < waves; ++i) {
+          PagedTile t;
+          expand(i * grid + cta, t);
+          ok = publish(t);
         }
-        const unsigned c = atomicAdd(reinterpret_cast<unsigned*>(p.tile_ctr), 1u);
-        item = c >= static_cast<unsigned>(total) ? total : static_cast<int>(min(
-                   static_cast<unsigned>(total), gridDim.x + c));
+        const int4 share = p.shares[cta];  // first unit, end, tile of the first unit
+        int u = share.x, x = share.z;
+        const int end = share.y;
+        while (ok && u < end) {
+          const int first = p.rest_units[x], next = p.rest_units[x + 1];
+          const int stop = min(end, next);
+          const int k0 = max(0, u - first - kItemCost), k1 = max(0, stop - first - kItemCost);
+          const bool empty = next - first == kItemCost;  // a tile that sees no key
+          if (k0 < k1 || (empty && u == first)) {
+            PagedTile t;
+            expand(waves * grid + x, t);
+            if (!empty && (k0 > 0 || stop < next)) {
+              t.slot = 2 * cta + (k0 == 0 ? 1 : 0);
+              t.kt0 = k0;
+              for (int i = 0; i < 2; ++i) t.n[i] = max(0, min(t.n[i], k1) - k0);
+            }
+            ok = publish(t);
+          }
+          u = stop;
+          ++x;
+        }
+      } else {
+        // The CTA starts with work tile blockIdx.x and claims every further one
+        // from the counter that the planning kernel zeroed. Near the end of the
+        // list a tile is claimed only once the producer has taken the one before,
+        // so no CTA holds tiles that an idle one could run.
+        constexpr int kNearRounds = 4;
+        int item = cta;
+        while (ok && item < total) {
+          PagedTile t;
+          expand(item, t);
+          if (!(ok = publish(t))) break;
+          if (item + kNearRounds * static_cast<long long>(grid) >= total) {
+            bool taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) >= k;
+            const long long t0 = clock64();
+            while (!taken && clock64() - t0 <= lim) {
+              __nanosleep(100);
+              taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) >= k;
+            }
+            if (!taken) {  // the other roles' bounded waits end the CTA
+              record_error(p.s.err, kErrTimeout);
+              ok = false;
+            }
+          }
+          const unsigned c = atomicAdd(reinterpret_cast<unsigned*>(p.tile_ctr), 1u);
+          item = c >= static_cast<unsigned>(total) ? total : static_cast<int>(min(
+                     static_cast<unsigned>(total), static_cast<unsigned>(grid) + c));
+        }
+      }
+      if (ok) {
+        PagedTile t = {};
+        t.b = -1;
+        publish(t);
       }
     }
     __syncwarp();
@@ -470,8 +516,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
         for (int e = 0; e < D; ++e) ov[e] = 0u;
       }
-      if (p.splits > 1) {
-        const size_t slot = (static_cast<size_t>(t.item) * 2 + i) * kTileM + r;
+      if (t.slot >= 0) {
+        const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM + r;
         if (row_ok) {
           *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m_used, l);
           if (my_n > 0) {
@@ -544,14 +590,39 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 __global__ void __launch_bounds__(1024)
 paged_plan_kernel(const PagedFwdParams p, int sort) {
   extern __shared__ int plan_smem[];
-  int* key = plan_smem;          // [B] when sorting
-  int* ord = plan_smem + p.s.B;  // [B] when sorting
+  // when sorting: keys, order [B], first tiles [B + 1]
+  int* key = plan_smem;
+  int* ord = plan_smem + p.s.B;
+  int* start = sort ? plan_smem + 2 * p.s.B : p.tile_start;
   __shared__ long long warp_sum[33];
-  const int tid = threadIdx.x, B = p.s.B;
+  __shared__ int unit[kFwdListed];
+  __shared__ int rest_units[kFwdSms + 1], rest_start[kFwdSms + 1];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, B = p.s.B;
   grid_wait();
   grid_release();
   if (tid == 0) *p.tile_ctr = 0;
   check_paged_seqs(p.s, tid, blockDim.x);
+  // the sum of x over the threads before this one, and over all
+  auto scan = [&](long long x, long long& all) {
+    long long in = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[w] = in;
+    __syncthreads();
+    long long sum = warp_sum[lane];
+    const long long own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    all = __shfl_sync(0xffffffffu, sum, 31);
+    return __shfl_sync(0xffffffffu, sum - own, w) + in - x;
+  };
   if (sort) {
     for (int b = tid; b < B; b += blockDim.x) key[b] = kv_len(p.s, b);
     __syncthreads();
@@ -568,91 +639,120 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   auto tiles_of = [&](int v) {
     return static_cast<long long>(m_blocks(p, new_span(p.s, sort ? ord[v] : v).len)) * p.H_kv;
   };
-  long long mine = 0;
+  long long mine = 0, all;
   for (int v = v0; v < v1; ++v) mine += tiles_of(v);
-  const int lane = tid & 31, w = tid >> 5;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[w] = incl;
-  __syncthreads();
-  if (w == 0) {
-    long long x = warp_sum[lane];
-    const long long own = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    warp_sum[lane] = x - own;
-    if (lane == 31) warp_sum[32] = x;
-  }
-  __syncthreads();
-  const bool fits = warp_sum[32] * p.splits <= p.max_work;
-  long long at = warp_sum[w] + incl - mine;
+  long long at = scan(mine, all);
+  const bool fits = all <= p.max_work;
+  const int total = fits ? static_cast<int>(all) : 0;
   for (int v = v0; v < v1; ++v) {
-    const int b = sort ? ord[v] : v;
-    p.seq_order[v] = b;
-    p.tile_start[v] = fits ? static_cast<int>(at) : 0;
-    p.seq_tile[b] = fits ? static_cast<int>(at) : 0;
+    const int first = fits ? static_cast<int>(at) : 0;
+    p.seq_order[v] = sort ? ord[v] : v;
+    p.tile_start[v] = first;
+    start[v] = first;
     at += tiles_of(v);
   }
   if (tid == 0) {
-    p.tile_start[B] = fits ? static_cast<int>(warp_sum[32]) : 0;
+    p.tile_start[B] = total;
     if (!fits) record_error(p.s.err, kErrSeqlens);
+  }
+  __syncthreads();
+  // the first tiles of the list, so that the CTAs need not look them up
+  if (tid < min(total, kFwdListed)) {
+    const int v = find_last(start, B, tid);
+    PagedTile t;
+    t.pad[0] = t.pad[1] = 0;
+    expand_tile(p, tid - start[v], sort ? ord[v] : v, t);
+    const int4* words = reinterpret_cast<const int4*>(&t);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p.tiles[3 * tid + i] = words[i];
+    unit[tid] = tile_units(t);
+  }
+  if (!p.split) return;
+  // Few work tiles: the units of every CTA's whole tiles, of each tile of the rest,
+  // and the shares of the rest that even the CTAs out.
+  __syncthreads();
+  const int grid = p.grid, waves = total / grid, rest = total - waves * grid;
+  long long rest_all, whole_all, share_all;
+  const long long first = scan(tid < rest ? unit[waves * grid + tid] : 0, rest_all);
+  if (tid <= rest) {
+    rest_units[tid] = static_cast<int>(tid < rest ? first : rest_all);
+    p.rest_units[tid] = rest_units[tid];
+  }
+  long long whole = 0;
+  if (tid < grid)
+    for (int i = 0; i < waves; ++i) whole += unit[i * grid + tid];
+  scan(whole, whole_all);
+  // Pieces of less than six units cost more than they spread: the last `wide` CTAs
+  // (whose whole tiles are the shortest) share the rest, each at least a tile's worth.
+  const long long wide = max(static_cast<long long>(rest), min(static_cast<long long>(grid), rest_all / 6));
+  const long long level = (whole_all + rest_all) / grid;
+  const long long share = tid >= grid || tid < grid - wide ? 0
+                          : waves == 0 || wide < grid      ? 1
+                                                           : max(0ll, level - whole);
+  const long long before = scan(share, share_all);
+  // (without room below the mean the last CTA takes the rest)
+  if (tid <= grid)
+    rest_start[tid] = tid == grid ? static_cast<int>(rest_all)
+                                  : share_all > 0 ? static_cast<int>(rest_all * before / share_all) : 0;
+  __syncthreads();
+  if (tid < grid) {
+    const int u = rest_start[tid], end = rest_start[tid + 1];
+    p.shares[tid] = make_int4(u, end, u < end ? find_last(rest_units, rest, u) : 0, 0);
+  }
+  if (tid < rest) {
+    const int begin = rest_units[tid] + kItemCost, end = rest_units[tid + 1];  // its key tiles' units
+    p.rest_owners[tid] = begin < end ? make_int2(find_last(rest_start, grid, begin), find_last(rest_start, grid, end - 1))
+                                     : make_int2(0, 0);
   }
 }
 
-// One warp per query row and head: merges the pieces of its work tile in order.
+// Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows
+// 8 y .. 8 y + 7 of tile x of the rest, one warp each.
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(256)
 paged_fwd_join_kernel(const PagedFwdParams p) {
   grid_wait();
   grid_release();
-  const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (at >= static_cast<long long>(p.s.T) * p.H_q || p.tile_start[p.s.B] == 0) return;
-  const int t = static_cast<int>(at / p.H_q), head = static_cast<int>(at - static_cast<long long>(t) * p.H_q);
-  int lo = 0, hi = p.s.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
+  const int total = p.tile_start[p.s.B], grid = p.grid, x = blockIdx.x;
+  const int2 own = p.rest_owners[x];  // the CTAs that hold its first and its last key tile
+  const int waves = total / grid, rest = total - waves * grid;
+  if (x >= rest || own.x == own.y) return;  // written whole
+  const int c0 = own.x, c1 = own.y;
+  PagedTile t;
+  {
+    int4* words = reinterpret_cast<int4*>(&t);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) words[i] = p.tiles[3 * (waves * grid + x) + i];
   }
-  const SeqSpan sp = new_span(p.s, lo);
-  if (t < sp.start || t >= sp.start + sp.len) return;
-  const int tok = t - sp.start, h = head / p.group;
-  const int mb = tok / (2 * p.tok_tile), in = tok - mb * 2 * p.tok_tile;
-  const int i = in >= p.tok_tile;
-  const int r = (in - i * p.tok_tile) * p.group + head - h * p.group;
-  const long long tile = p.seq_tile[lo] + static_cast<long long>(m_blocks(p, sp.len) - 1 - mb) * p.H_kv + h;
-  auto slot = [&](int s) { return ((tile * p.splits + s) * 2 + i) * kTileM + r; };
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[slot(s) * 2]);
-  const float mbias = top == -INFINITY ? 0.0f : top;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int i = row >> 7, r = row & 127;
+  const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
+  if (tok_r >= p.tok_tile || tok >= t.n_new) return;
   constexpr int kV = D / 32;
-  float acc[kV], l = 0.0f;
+  float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(s) * 2);
-    if (ml.y == 0.0f) continue;  // a piece without keys left no O
-    const float f = ex2_approx(ml.x - mbias);
-    l += ml.y * f;
-    const float* src = p.part_o + slot(s) * D + lane * kV;
+  for (int c = c0; c <= c1; ++c) {
+    const int4 share = p.shares[c];
+    if (share.x == share.y) continue;
+    const size_t at = (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+    if (ml.y == 0.0f) continue;  // a piece whose keys this row does not see leaves no O
+    const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
+    const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
+    m = top;
+    l = l * f + ml.y * g;
+    const float* src = p.part_o + at * D + lane * kV;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] += src[e] * f;
+    for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + src[e] * g;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                              (static_cast<size_t>(t) * p.H_q + head) * D + lane * kV);
+  const size_t to = static_cast<size_t>(t.row0) + tok;
+  const int head = t.h * p.group + r - tok_r * p.group;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
 #pragma unroll
   for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0)
-    p.lse[static_cast<size_t>(head) * p.s.T + t] = l == 0.0f ? -INFINITY : top * kLn2 + logf(l);
+  if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int D>
@@ -663,18 +763,16 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   const int sort = p.s.B <= 1024;
   int slot = prof_begin(kKPagedPlan, stream);
   cudaError_t e = launch_chained(paged_plan_kernel, dim3(1), 1024,
-                                 sort ? 2 * p.s.B * static_cast<int>(sizeof(int)) : 0, stream, smem_set, p, sort);
+                                 sort ? (3 * p.s.B + 1) * static_cast<int>(sizeof(int)) : 0, stream, smem_set, p, sort);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
   e = launch_chained(paged_fwd_kernel<D>, dim3(p.grid), 384, PagedFwdCfg<D>::kSmemBytes, stream, smem_set, tq, tk,
                      tv, to, p);
   prof_end(slot, stream);
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  const long long rows = static_cast<long long>(p.s.T) * p.H_q;
-  e = launch_chained(paged_fwd_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream,
-                     smem_set, p);
+  e = launch_chained(paged_fwd_join_kernel<D>, dim3(p.grid, 2 * kTileM / 8), 256, 0, stream, smem_set, p);
   prof_end(slot, stream);
   return e;
 }
