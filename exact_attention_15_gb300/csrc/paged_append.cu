@@ -15,8 +15,7 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -45,8 +44,46 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], flo
   *reinterpret_cast<uint2*>(p) = w;
 }
 
-// One CTA per token: the token's 64 angles at most are computed once for all
-// heads, then each thread turns or copies 16 elements of a head at a time.
+// 16 elements of a head: two runs of 8.
+struct Part {
+  uint4 a, b;
+};
+// Which 16 elements part i of a token is: the threads of a head take a pair of
+// 8-element runs half the rotated width apart (so that each holds whole pairs), or
+// 16 elements in a row.
+struct Place {
+  int kind;  // 0: q, 1: k, 2: v
+  int h, j;  // head, thread of the head
+  int e0, e1;
+  bool turn, split;
+};
+__device__ __forceinline__ Place place_of(const AppendParams& p, int i) {
+  Place x;
+  const int shift = p.d == 128 ? 3 : 2;  // log2(threads of a head)
+  const int head = i >> shift;
+  x.j = i & ((1 << shift) - 1);
+  x.kind = head < p.H_q ? 0 : head < p.H_q + p.H_kv ? 1 : 2;
+  x.h = x.kind == 0 ? head : x.kind == 1 ? head - p.H_q : head - p.H_q - p.H_kv;
+  x.turn = x.kind < 2 && 16 * x.j < p.rotary_dim;
+  x.split = x.turn && !p.interleaved;
+  x.e0 = x.split ? 8 * x.j : 16 * x.j;
+  x.e1 = x.split ? 8 * x.j + (p.rotary_dim >> 1) : 16 * x.j + 8;
+  return x;
+}
+__device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x, int t) {
+  const __nv_bfloat16* src =
+      x.kind == 0 ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride
+                  : x.kind == 1 ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride
+                                : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride;
+  src += x.h * p.d;
+  return Part{*reinterpret_cast<const uint4*>(src + x.e0), *reinterpret_cast<const uint4*>(src + x.e1)};
+}
+
+// One CTA per token. The first kAhead parts of every thread are loaded before the
+// token's sequence, position and page are looked up (three dependent loads) and
+// its angles computed, once for all heads; then they are turned and stored. What
+// bounds it is the bytes.
+constexpr int kAhead = 3;
 __global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(const AppendParams p) {
   __shared__ float2 cs[64];
@@ -54,6 +91,13 @@ paged_append_kernel(const AppendParams p) {
   const PagedSeqs& s = p.s;
   grid_wait();
   grid_release();
+  const int parts = (p.H_q + 2 * p.H_kv) * (p.d >> 4);
+  Part ahead[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = tid + k * kAppendThreads;
+    if (i < parts) ahead[k] = load_part(p, place_of(p, i), t);
+  }
   if (t == 0) check_paged_seqs(s, tid, kAppendThreads);
   int b = t;
   SeqSpan span{t, 1};
@@ -74,8 +118,7 @@ paged_append_kernel(const AppendParams p) {
   const bool page_ok = static_cast<unsigned>(page) < static_cast<unsigned>(s.num_pages);
   if (!page_ok && tid == 0) record_error(s.err, kErrPages);
   const int row = pos & ((1 << s.page_shift) - 1);
-  const int pairs = p.rotary_dim >> 1;
-  if (tid < pairs) {
+  if (tid < p.rotary_dim >> 1) {
     double turns = __ldg(p.inv_freq + tid) * 0.15915494309189533577;  // 1 / 2 pi
     turns -= floor(turns);
     const unsigned long long f = static_cast<unsigned long long>(turns * 18446744073709551616.0);
@@ -87,60 +130,49 @@ paged_append_kernel(const AppendParams p) {
     cs[tid] = make_float2(c, sn);
   }
   __syncthreads();
-  const int per_head = p.d >> 4;  // threads per head
-  const int heads = p.H_q + 2 * p.H_kv;
-  for (int i = tid; i < heads * per_head; i += kAppendThreads) {
-    const int head = i / per_head, j = i - head * per_head;
-    const bool is_q = head < p.H_q, is_v = head >= p.H_q + p.H_kv;
-    const int h = is_q ? head : is_v ? head - p.H_q - p.H_kv : head - p.H_q;
-    const __nv_bfloat16* src =
-        is_q ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + h * p.d
-             : is_v ? static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + h * p.d
-                    : static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + h * p.d;
-    // the thread's 16 elements: a pair of 8-element runs half the rotated width
-    // apart, or 16 in a row
-    const bool turn = !is_v && 16 * j < p.rotary_dim;
-    const bool split = turn && !p.interleaved;
-    const int e0 = split ? 8 * j : 16 * j, e1 = split ? 8 * j + pairs : 16 * j + 8;
+  for (int k = 0, i = tid; i < parts; ++k, i += kAppendThreads) {
+    const Place x = place_of(p, i);
+    const Part w = k == 0 ? ahead[0] : k == 1 ? ahead[1] : k == 2 ? ahead[2] : load_part(p, x, t);
     float x0[8], x1[8];
-    load8(src + e0, x0);
-    load8(src + e1, x1);
-    if (split) {
+    widen8(w.a, x0);
+    widen8(w.b, x1);
+    if (x.split) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 w = cs[8 * j + e];
+        const float2 r = cs[8 * x.j + e];
         const float a = x0[e], c = x1[e];
-        x0[e] = a * w.x - c * w.y;
-        x1[e] = a * w.y + c * w.x;
+        x0[e] = a * r.x - c * r.y;
+        x1[e] = a * r.y + c * r.x;
       }
-    } else if (turn) {
+    } else if (x.turn) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 w = cs[8 * j + e], u = cs[8 * j + 4 + e];
+        const float2 r = cs[8 * x.j + e], u = cs[8 * x.j + 4 + e];
         const float a = x0[2 * e], c = x0[2 * e + 1], a1 = x1[2 * e], c1 = x1[2 * e + 1];
-        x0[2 * e] = a * w.x - c * w.y;
-        x0[2 * e + 1] = a * w.y + c * w.x;
+        x0[2 * e] = a * r.x - c * r.y;
+        x0[2 * e + 1] = a * r.y + c * r.x;
         x1[2 * e] = a1 * u.x - c1 * u.y;
         x1[2 * e + 1] = a1 * u.y + c1 * u.x;
       }
     }
-    if (is_q) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + h * p.d;
-      store8(dst + e0, x0);
-      store8(dst + e1, x1);
+    if (x.kind == 0) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + x.h * p.d;
+      store8(dst + x.e0, x0);
+      store8(dst + x.e1, x1);
     } else if (page_ok) {
+      const bool is_v = x.kind == 2;
       const size_t at = static_cast<size_t>(page) * (is_v ? p.v_page : p.k_page) +
-                        ((static_cast<size_t>(h) << s.page_shift) + row) * p.d;
+                        ((static_cast<size_t>(x.h) << s.page_shift) + row) * p.d;
       if (p.e4m3) {
         const float* sc = is_v ? p.v_scale : p.k_scale;
-        const float scale = sc ? __ldg(sc + h) : 1.0f;
+        const float scale = sc ? __ldg(sc + x.h) : 1.0f;
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
-        store8_e4m3(dst + e0, x0, scale);
-        store8_e4m3(dst + e1, x1, scale);
+        store8_e4m3(dst + x.e0, x0, scale);
+        store8_e4m3(dst + x.e1, x1, scale);
       } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + at;
-        store8(dst + e0, x0);
-        store8(dst + e1, x1);
+        store8(dst + x.e0, x0);
+        store8(dst + x.e1, x1);
       }
     }
   }
