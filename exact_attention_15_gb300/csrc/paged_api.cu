@@ -249,7 +249,8 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if (!q || !o || !lse) return ATTN_ERR_NULL_PTR;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return ATTN_ERR_ALIGNMENT;
   const int group = H_q / c->H_kv;
-  if (!workspace || workspace_bytes < workspace_bytes_of(T, B, group, c->H_kv, c->d)) return ATTN_ERR_WORKSPACE;
+  const size_t need = seqlens ? workspace_bytes_of(T, B, group, c->H_kv, c->d) : stream_plan(c->d).total;
+  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   HostDevice dev;
   if ((st = host_setup(&dev)) != ATTN_OK) return st;

@@ -397,12 +397,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       if (key0 < x.len) {
         const uint32_t tile = smem_addr(smem) + stage * 2 * Cfg::kTileBytes;
         const uint32_t kb = tile + koff, vb = tile + Cfg::kTileBytes + voff;
-        // S in two chains of half the columns each
-        float sc[NB][2][4];
+        // S in two independent chains of products: half the columns each with 8
+        // rows, one per block with 16
+        constexpr int kChains = NB == 1 ? 2 : 1;
+        float sc[NB][kChains][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < kChains; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[nb][h][e] = 0.0f;
         if constexpr (FP8) {
@@ -416,7 +418,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                                      e4m3x2_to_f16x2(f[2 * u] >> 16), e4m3x2_to_f16x2(f[2 * u + 1] >> 16)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma16816<true>(sc[nb][u], a, qb[nb][2 * cc + u][0], qb[nb][2 * cc + u][1]);
+                mma16816<true>(sc[nb][u % kChains], a, qb[nb][2 * cc + u][0], qb[nb][2 * cc + u][1]);
             }
           }
         } else {
@@ -425,7 +427,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             uint32_t f[4];
             ldsm4(chunk_at(kb, 2 * kk), f);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<false>(sc[nb][kk & 1], f, qb[nb][kk][0], qb[nb][kk][1]);
+            for (int nb = 0; nb < NB; ++nb) mma16816<false>(sc[nb][kk % kChains], f, qb[nb][kk][0], qb[nb][kk][1]);
           }
         }
         // scaled scores s[nb][e]: key ar + 8 (e >> 1), query row 2 qd + (e & 1)
@@ -436,7 +438,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + ar + 8 * (e >> 1);
-            const float v = (sc[nb][0][e] + sc[nb][1][e]) * c[nb][e & 1];
+            const float v = (kChains == 2 ? sc[nb][0][e] + sc[nb][kChains - 1][e] : sc[nb][0][e]) * c[nb][e & 1];
             sv[nb][e] = key < last[nb][e & 1] ? v : -INFINITY;
             grew |= sv[nb][e] - m[nb][e & 1] > kTau;
           }
@@ -640,29 +642,31 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (!split_head && tid == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
 }
 
-// Merges the pieces of split items in their order. CTA (c, y) does every
-// kJoinRows-th query row of the item that begins in the streaming kernel's CTA c
-// and ends in a later one; there are fewer such items than CTAs. Each warp takes
-// every fourth piece with a running maximum, then the warps' sums are merged.
-constexpr int kJoinRows = 8;
-template <int D>
-__global__ void __launch_bounds__(128)
+// Merges the pieces of split items in their order. CTA (c, y) does kJoinRows query
+// rows of the item that begins in the streaming kernel's CTA c and ends in a later
+// one; there are fewer such items than CTAs. Four warps share a row, each takes
+// every fourth piece with a running maximum. Eight CTAs per item: with 16 rows one
+// CTA per row starts 1.5 us later, and with 8 rows half as many CTAs, of more
+// warps each, join the pieces of a long sequence 2 us later.
+template <int D, int kJoinRows>
+__global__ void __launch_bounds__(128 * kJoinRows)
 paged_join_kernel(const StreamParams p) {
-  __shared__ float sh_o[4][D];
-  __shared__ float2 sh_ml[4];
+  __shared__ float sh_o[kJoinRows][4][D];
+  __shared__ float2 sh_ml[kJoinRows][4];
   grid_wait();
   grid_release();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x, part = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int x = threadIdx.x & 127, at_row = threadIdx.x >> 7, r = blockIdx.y * kJoinRows + at_row;
   const int4 a = p.heads[2 * c], d = p.heads[2 * c + 1];
   const int pieces = a.x, slot0 = a.y, row0 = a.z, rows = a.w;
   if (pieces == 0) return;
   constexpr int kV = D / 32;
-  for (int r = blockIdx.y; r < rows; r += kJoinRows) {
-    float acc[kV], m = -INFINITY, l = 0.0f;
+  float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+  if (r < rows) {
 #pragma unroll 4
-    for (int i = warp; i < pieces; i += 4) {
+    for (int i = part; i < pieces; i += 4) {
       const size_t at = static_cast<size_t>(i == 0 ? slot0 : 2 * (c + i)) * 16 + r;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
       float o[kV];
@@ -680,35 +684,36 @@ paged_join_kernel(const StreamParams p) {
 #pragma unroll
       for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + o[e] * g;
     }
+  }
 #pragma unroll
-    for (int e = 0; e < kV; ++e) sh_o[warp][lane * kV + e] = acc[e];
-    if (lane == 0) sh_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f, f[4];
+  for (int e = 0; e < kV; ++e) sh_o[at_row][part][lane * kV + e] = acc[e];
+  if (lane == 0) sh_ml[at_row][part] = make_float2(m, l);
+  __syncthreads();
+  if (r >= rows || x > D / 2) return;
+  const float2* ml = sh_ml[at_row];
+  float top = -INFINITY, sum = 0.0f, f[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) top = fmaxf(top, sh_ml[g].x);
+  for (int g = 0; g < 4; ++g) top = fmaxf(top, ml[g].x);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    f[g] = ex2_approx(ml[g].x - (top == -INFINITY ? 0.0f : top));
+    sum += ml[g].y * f[g];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int rr = d.y + r, tok = rr / p.group, head = d.x * p.group + rr - tok * p.group;
+  const size_t row = static_cast<size_t>(row0) + tok;
+  if (x < D / 2) {
+    const int e = 2 * x;
+    float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      f[g] = ex2_approx(sh_ml[g].x - (top == -INFINITY ? 0.0f : top));
-      sum += sh_ml[g].y * f[g];
+      v[0] += sh_o[at_row][g][e] * f[g];
+      v[1] += sh_o[at_row][g][e + 1] * f[g];
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = d.y + r, tok = rr / p.group, head = d.x * p.group + rr - tok * p.group;
-    const size_t row = static_cast<size_t>(row0) + tok;
-    if (threadIdx.x < D / 2) {
-      const int e = 2 * threadIdx.x;
-      float v[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        v[0] += sh_o[g][e] * f[g];
-        v[1] += sh_o[g][e + 1] * f[g];
-      }
-      reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D)[threadIdx.x] =
-          pack_bf16x2(v[0] * inv, v[1] * inv);
-    }
-    if (threadIdx.x == 0)
-      p.lse[row * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
-    __syncthreads();
+    reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D)[x] =
+        pack_bf16x2(v[0] * inv, v[1] * inv);
+  } else {
+    p.lse[row * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
   }
 }
 
@@ -722,7 +727,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamPar
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained(paged_join_kernel<D>, dim3(p.grid, kJoinRows), 128, 0, stream, smem_set, p);
+  e = launch_chained(paged_join_kernel<D, R / 8>, dim3(p.grid, 8), 128 * (R / 8), 0, stream, smem_set, p);
   prof_end(slot, stream);
   return e;
 }

@@ -65,6 +65,8 @@ class PagedCache:
             k.stride(0) if num_pages > 1 else page, v.stride(0) if num_pages > 1 else page,
             num_pages, page_size, H_kv, d, _KINDS[k.dtype])
         self._ref = ctypes.addressof(self._struct)
+        # one token per sequence needs the same workspace whatever the batch
+        self._decode_bytes = load().attn_paged_workspace_bytes(1, 1, H_kv, H_kv, d)
 
 
 def _ptr(t):
@@ -196,9 +198,8 @@ def _outputs(cache, q, lse_shape, out, lse):
     return out, lse
 
 
-def _workspace(cache, lib, workspace, T, B, H_q):
+def _workspace(cache, workspace, size):
     if workspace is None:
-        size = lib.attn_paged_workspace_bytes(T, B, H_q, cache.H_kv, cache.d)
         return _empty(size, dtype=torch.uint8, device=cache.device), size
     if not workspace.is_contiguous() or workspace.device != cache.device:
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
@@ -214,7 +215,7 @@ def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, 
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, None, T)
     o, lse = _outputs(cache, q, (B, H_q), out, lse)
     lib = load()
-    ws, size = _workspace(cache, lib, workspace, B, B, H_q)
+    ws, size = _workspace(cache, workspace, cache._decode_bytes)
     status = _call(cache.device, lib.attn_paged_decode, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
                    B, H_q, kv_lens.data_ptr(), table, cols, stride,
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)
@@ -236,7 +237,7 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
     o, lse = _outputs(cache, q, (H_q, T), out, lse)
     lib = load()
-    ws, size = _workspace(cache, lib, workspace, T, B, H_q)
+    ws, size = _workspace(cache, workspace, lib.attn_paged_workspace_bytes(T, B, H_q, cache.H_kv, cache.d))
     status = _call(cache.device, lib.attn_paged_fwd, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T,
                    B, H_q, cu_seqlens.data_ptr(), kv_lens.data_ptr(), table, cols, stride, bool(causal),
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)
