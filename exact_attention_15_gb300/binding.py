@@ -44,7 +44,8 @@ _SIGS = {
                               ctypes.c_float, _I, _P]),
     "attn_paged_append": (_I, [_P, _P, _P, _P, _P, _L, _L, _L, _L, _I, _I, _I, _P, _P, _P, _I, _L, _P,
                                _I, _I, _P]),
-    "attn_paged_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "attn_paged_decode_workspace_bytes": (_Z, [_I]),
+    "attn_paged_fwd_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
     "attn_paged_decode": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _I, _L, _F, _P, _Z, _P]),
     "attn_paged_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _L, _I, _F, _P, _Z, _P]),
     "attn_check": (_I, [_P]),
@@ -65,7 +66,8 @@ KERNEL_NAMES = {1: "attn_fwd_kernel", 2: "attn_bwd_pre_kernel", 3: "attn_bwd_mai
                 4: "attn_bwd_post_kernel", 5: "exp2_probe_kernel", 6: "stall_probe_kernel",
                 7: "fwd_plan_kernel", 8: "attn_fwd_pair_kernel", 9: "attn_bwd_main_kernel_pass2",
                 10: "bwd_plan_kernel", 11: "paged_append_kernel", 12: "paged_stream_kernel",
-                13: "paged_join_kernel", 14: "paged_fwd_kernel", 15: "paged_plan_kernel"}
+                13: "paged_join_kernel", 14: "paged_fwd_kernel", 15: "paged_plan_kernel",
+                16: "queries_f16_kernel"}
 FAULT_NONE = 0
 FAULT_SKIP_DQ_RELEASE = 1
 BWD_ONE_CTA = 0

@@ -64,8 +64,8 @@ __device__ __forceinline__ float softmax_row_max(float (&s)[128], float c, float
 // p = 2^(x - mb) with x the scaled score, summed in fp32 before the bf16
 // rounding into two packed pair accumulators (sum2[i & 1] adds word i's pair).
 // The scale, bias and sum run on packed fp32 pairs, one instruction per key
-// pair.
-template <int EMU, bool POS_SCALE, int W0, int W1>
+// pair. F16 packs P as fp16 instead of bf16 (for fp16 operands).
+template <int EMU, bool POS_SCALE, int W0, int W1, bool F16 = false>
 __device__ __forceinline__ void softmax_row_exp(const float (&s)[128], float c, float mb,
                                                 bool need_mask, uint32_t (&pk)[64],
                                                 uint64_t (&sum2)[2]) {
@@ -84,7 +84,7 @@ __device__ __forceinline__ void softmax_row_exp(const float (&s)[128], float c, 
       p1 = ex2_approx(x1);
     }
     sum2[i & 1] = add_f32x2(sum2[i & 1], f32x2(p0, p1));
-    pk[i] = pack_bf16x2(p0, p1);
+    pk[i] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
   }
 }
 

@@ -82,6 +82,17 @@ cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, int 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A power of two that brings a row whose largest magnitude is `top` to [1, 2) when
+// it divides the row; its inverse is in `down`. fp16 then holds bf16 values exactly
+// but for what lies below 2^-25 of the largest, whatever their range was.
+// Infinities stay infinities.
+__device__ __forceinline__ float row_power(float top, float& down) {
+  int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  ex = ex > 127 ? 0 : max(-126, min(126, ex));
+  down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+}
+
 // ---- appending
 struct AppendParams {
   PagedSeqs s;
@@ -131,6 +142,8 @@ struct PagedFwdParams {
   int split;         // few work tiles: whole waves of them, the rest cut evenly
   int max_work;      // work tiles that the host expects at most
   float scale_log2;
+  const float* k_scale; const float* v_scale;  // e4m3: [H_kv] or nullptr
+  const float* q_up;  // e4m3, workspace: what each row of the fp16 queries was divided by [T, H_q]
   int* seq_order;    // workspace: sequences, longest first [B]
   int* tile_start;   // workspace: first work tile of each of them [B + 1]
   int* tile_ctr;     // workspace: claim counter (split == 0)
@@ -144,6 +157,11 @@ struct PagedFwdParams {
   long long wait_limit;
 };
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& to, const PagedFwdParams& p, int d, cudaStream_t stream);
+                             const CUtensorMap& to, const PagedFwdParams& p, int d, bool e4m3,
+                             cudaStream_t stream);
+// Queries as fp16 for products with an e4m3 cache: each row divided by a power of
+// two (kept in q_up) that brings its largest value to [1, 2).
+cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,
+                               cudaStream_t stream);
 
 }  // namespace attn

@@ -89,17 +89,17 @@ int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cac
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 3-D map over q or o, [T, H_q, d] bf16: boxes of 64 columns, the heads of a group
+// 3-D map over q or o, [T, H_q, d] bf16 (or fp16): boxes of 64 columns, the heads of a group
 // and `tokens` tokens, 128-byte swizzle.
 int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int d, int H_q, int T,
-                    int group, int tokens) {
+                    int group, int tokens, bool f16 = false) {
   const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(T)};
   cuuint64_t strides[2] = {row, row * H_q};
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
   cuuint32_t step[3] = {1, 1, 1};
-  const CUresult r = dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                                box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = dev.encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                                const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -124,9 +124,9 @@ struct FwdPlan {
   int tok_tile;
   long long tiles;
   bool split;
-  size_t tiles_off, ml_off, o_off, total;
+  size_t tiles_off, ml_off, o_off, q16_off, up_off, total;
 };
-FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d) {
+FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
   FwdPlan f;
   f.tok_tile = kTileM / group;
   const long long rows = 2ll * f.tok_tile;
@@ -141,22 +141,24 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d) {
   f.tiles_off = align256((2 * static_cast<size_t>(B) + 2 + kFwdSms + 1) * sizeof(int));
   f.ml_off = f.tiles_off + align256((3 * kFwdListed + kFwdSms) * sizeof(int4) + kFwdSms * sizeof(int2));
   f.o_off = f.ml_off + align256(slots * 2 * sizeof(float));
-  f.total = f.o_off + slots * d * sizeof(float);
+  // e4m3: the queries as fp16 and their rows' powers of two
+  const size_t rows_q = e4m3 ? static_cast<size_t>(T) * group * H_kv : 0;
+  f.q16_off = f.o_off + align256(slots * d * sizeof(float));
+  f.up_off = f.q16_off + align256(rows_q * d * 2);
+  f.total = f.up_off + rows_q * sizeof(float);
   return f;
 }
 
 // Chunks of 16 query rows at most go to the streaming kernel, which reads each key
 // once per 16 rows and deals the keys out evenly; more rows to the tensor-core
 // kernel, whose tiles hold 128. The host knows the mean of the sequences' rows.
-bool streams(int T, int B, int group, bool e4m3) {
-  return e4m3 || group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
+bool streams(int T, int B, int group) {
+  return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
 }
 
-size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d) {
-  const size_t stream = stream_plan(d).total;
-  if (streams(T, B, group, false)) return stream;
-  const size_t fwd = fwd_plan(T, B, group, H_kv, d).total;
-  return fwd > stream ? fwd : stream;
+size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
+  if (streams(T, B, group)) return stream_plan(d).total;
+  return fwd_plan(T, B, group, H_kv, d, e4m3).total;
 }
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
@@ -198,11 +200,13 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
 int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q, void* o,
                float* lse, int H_q, int causal, float scale, uint8_t* ws, cudaStream_t cs) {
   const int group = H_q / c->H_kv;
-  const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d);
+  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d, e4m3);
   const unsigned rows = c->page_size < kTileN ? c->page_size : kTileN;
   CUtensorMap tq, tk, tv, to;
   int st;
-  if ((st = encode_rows_map(dev, &tq, q, c->d, H_q, seqs.T, group, plan.tok_tile)) != ATTN_OK ||
+  const void* queries = e4m3 ? ws + plan.q16_off : q;
+  if ((st = encode_rows_map(dev, &tq, queries, c->d, H_q, seqs.T, group, plan.tok_tile, e4m3)) != ATTN_OK ||
       (st = encode_rows_map(dev, &to, o, c->d, H_q, seqs.T, group, plan.tok_tile)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
@@ -220,6 +224,9 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   p.split = plan.split ? 1 : 0;
   p.max_work = static_cast<int>(plan.tiles);
   p.scale_log2 = scale * kLog2e;
+  p.k_scale = e4m3 ? c->k_scale : nullptr;
+  p.v_scale = e4m3 ? c->v_scale : nullptr;
+  p.q_up = reinterpret_cast<const float*>(ws + plan.up_off);
   p.seq_order = reinterpret_cast<int*>(ws);
   p.tile_start = p.seq_order + seqs.B;
   p.tile_ctr = p.tile_start + seqs.B + 1;
@@ -232,7 +239,10 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   const int sms = dev.n_sm < kFwdSms ? dev.n_sm : kFwdSms;
   p.grid = plan.split ? sms : dev.n_sm < p.max_work ? dev.n_sm : p.max_work;
   p.wait_limit = dev.wait_limit;
-  return launch_paged_fwd(tq, tk, tv, to, p, c->d, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (e4m3 && launch_queries_f16(q, ws + plan.q16_off, reinterpret_cast<float*>(ws + plan.up_off),
+                                 static_cast<long long>(seqs.T) * H_q, c->d, cs) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return launch_paged_fwd(tq, tk, tv, to, p, c->d, e4m3, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Both attention calls, after the checks they share.
@@ -249,14 +259,14 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if (!q || !o || !lse) return ATTN_ERR_NULL_PTR;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return ATTN_ERR_ALIGNMENT;
   const int group = H_q / c->H_kv;
-  const size_t need = seqlens ? workspace_bytes_of(T, B, group, c->H_kv, c->d) : stream_plan(c->d).total;
+  const size_t need = seqlens ? workspace_bytes_of(T, B, group, c->H_kv, c->d, c->type == ATTN_CACHE_E4M3) : stream_plan(c->d).total;
   if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   HostDevice dev;
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
   const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (!seqlens || streams(T, B, group, c->type == ATTN_CACHE_E4M3))
+  if (!seqlens || streams(T, B, group))
     return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, cs);
   return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
 }
@@ -304,10 +314,13 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
                                                                                        : ATTN_ERR_CUDA;
 }
 
-size_t attn_paged_workspace_bytes(int T, int B, int H_q, int H_kv, int d) {
-  if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128))
+size_t attn_paged_decode_workspace_bytes(int d) { return d == 64 || d == 128 ? stream_plan(d).total : 0; }
+
+size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, int type) {
+  if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
+      (type != ATTN_CACHE_BF16 && type != ATTN_CACHE_E4M3))
     return 0;
-  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d);
+  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type == ATTN_CACHE_E4M3);
 }
 
 int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,

@@ -15,8 +15,6 @@
 // and O += P V on mma.sync m16n8k16 with the online softmax in registers
 // (tcgen05 wants 128 rows; here there are 16 at most, and the tensor work is
 // small against the tile's bytes); warp 4 loads the tiles with TMA.
-#include <cuda_fp16.h>
-
 #include "paged.cuh"
 
 namespace attn {
@@ -67,18 +65,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "{%0,%1,%2,%3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 bytes (low half of x) to two fp16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The transpose of an 8 x 8 block of 16-bit values held as accumulator columns.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -335,9 +321,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   while (have) {
     const int rows = min(R, x.n * p.group - x.rc * R);  // of this chunk
     // Over an e4m3 cache the products run in fp16, which holds every e4m3 value
-    // exactly; each query row is brought to [1, 2) by a power of two first, so
-    // fp16's range does not matter and what it rounds is below 2^-25 of the row's
-    // largest value.
+    // exactly; each query row is brought to [1, 2) by a power of two first.
     float c[NB][2];   // exponent scale of the lane's accumulator columns
     int last[NB][2];  // keys that those rows see
     const float k_scale = FP8 && p.k_scale ? __ldg(p.k_scale + x.h) : 1.0f;
@@ -354,10 +338,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             top = fmaxf(top, fmaxf(fabsf(bf16lo_to_f32(qb[nb][kk][e])), fabsf(bf16hi_to_f32(qb[nb][kk][e]))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        ex = ex > 127 ? 0 : max(-126, min(126, ex));  // infinities stay infinities
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        float down;
+        up = row_power(top, down);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll

@@ -16,6 +16,11 @@
 // Rows of V past the sequence's end can hold anything, and 0 x NaN is NaN: the
 // MMA warp zeroes them in shared memory before the last P V product.
 //
+// Over an e4m3 cache the products run in fp16, which holds every e4m3 value exactly
+// (the instructions take no operands of two types): the tiles land in a small ring
+// of their own, and warp 3 widens them into the K / V ring (and puts the zeros past
+// the end). The queries come as fp16 rows scaled by powers of two.
+//
 // With many work tiles the CTAs claim them one by one. With few, what the last
 // wave leaves idle costs more: every CTA takes the same number of whole tiles, and
 // the rest (fewer tiles than CTAs) is cut by keys into one share per CTA, such that
@@ -31,14 +36,19 @@ namespace attn {
 
 namespace {
 
-template <int D>
+template <int D, bool E4M3>
 struct PagedFwdCfg {
   static constexpr int kBlocks = D / 64;                // 64-column blocks of a tile
   static constexpr int kBlockBytes = kTileM * 64 * 2;   // 16 KB
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  // e4m3: tiles as they are in the cache, rows of D bytes swizzled over their width,
+  // take the place of a quarter of the K / V ring
+  static constexpr int kRawBytes = E4M3 ? kTileN * D : 0;
+  static constexpr int kRawStages = E4M3 ? 32768 / (kTileN * D) : 0;
+  static constexpr int kStages = (D == 128 ? 4 : 8) * (E4M3 ? 3 : 4) / 4;
   static constexpr int kKVOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
   static constexpr int kEpiOff = kBarOff + 1024;        // one staging block per warpgroup
   static constexpr int kSmemBytes = kEpiOff + 2 * kBlockBytes + 1024;
   static constexpr uint32_t kColS = 2 * D;
@@ -58,12 +68,13 @@ struct __align__(16) PagedTile {
 };
 
 constexpr int kSlots = 2;     // of the ring that hands out work tiles
-constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps
+constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (and the widening warp)
 
 struct PagedBars {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t kv_full[8], kv_empty[8];
+  uint64_t raw_full[4], raw_empty[4];  // e4m3
   uint64_t sched_full[kSlots], sched_empty[kSlots];
   int sched_taken;  // work tiles that the producer has taken so far
   PagedTile sched_t[kSlots];
@@ -133,12 +144,12 @@ __device__ __forceinline__ bool take_tile(PagedBars* bars, int k, PagedTile& t, 
   return t.b >= 0;
 }
 
-template <int D>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(384, 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                  const PagedFwdParams p) {
-  using Cfg = PagedFwdCfg<D>;
+  using Cfg = PagedFwdCfg<D, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -160,7 +171,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_addr(&bars->sched_full[i]), 1);
-      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders);
+      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders + E4M3);
+    }
+    for (int i = 0; i < Cfg::kRawStages; ++i) {
+      mbar_init(smem_addr(&bars->raw_full[i]), 1);
+      mbar_init(smem_addr(&bars->raw_empty[i]), 1);
     }
     bars->sched_taken = 0;
     fence_barrier_init();
@@ -185,9 +200,16 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // Lane (page j of a key tile, column block) issues one box per tile.
       const int box_shift = min(p.s.page_shift, 7);
       const int n_box = kTileN >> box_shift;
-      const int j_box = lane / Cfg::kBlocks, blk = lane % Cfg::kBlocks;
+      constexpr int kCols = E4M3 ? 1 : Cfg::kBlocks;  // boxes side by side in a row
+      constexpr int kRow = E4M3 ? D : 128;            // bytes of a box row
+      constexpr int kRing = E4M3 ? Cfg::kRawStages : Cfg::kStages;
+      constexpr int kStride = E4M3 ? Cfg::kRawBytes : Cfg::kTileBytes;
+      uint64_t* ring_full = E4M3 ? bars->raw_full : bars->kv_full;
+      uint64_t* ring_empty = E4M3 ? bars->raw_empty : bars->kv_empty;
+      const int j_box = lane / kCols, blk = lane % kCols;
       const int box_row = j_box << box_shift;
-      const uint32_t dst0 = smem_addr(smem + Cfg::kKVOff) + blk * Cfg::kBlockBytes + box_row * 128;
+      const uint32_t dst0 = smem_addr(smem + (E4M3 ? Cfg::kRawOff : Cfg::kKVOff)) + blk * Cfg::kBlockBytes +
+                            box_row * kRow;
       const int q_bytes = p.tok_tile * p.group * 128;  // one column block of a Q tile
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -231,16 +253,16 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const int boxes = min(n_box, (t.len - key0 + (1 << box_shift) - 1) >> box_shift);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++ld) {
-            const uint32_t stage = ld % Cfg::kStages, round = ld / Cfg::kStages;
-            if (!mbar_wait_warp(smem_addr(&bars->kv_empty[stage]), (round & 1) ^ 1, lim)) {
+            const uint32_t stage = ld % kRing, round = ld / kRing;
+            if (!mbar_wait_warp(smem_addr(&ring_empty[stage]), (round & 1) ^ 1, lim)) {
               ok = false;
               break;
             }
-            const uint32_t fbar = smem_addr(&bars->kv_full[stage]);
-            if (lane == 0) mbar_arrive_expect_tx(fbar, boxes * Cfg::kBlocks * (128 << box_shift));
+            const uint32_t fbar = smem_addr(&ring_full[stage]);
+            if (lane == 0) mbar_arrive_expect_tx(fbar, boxes * kCols * (kRow << box_shift));
             __syncwarp();
             if (j_box < boxes)
-              tma_load_4d(dst0 + stage * Cfg::kTileBytes, kv ? &tm_v : &tm_k, fbar, blk * 64,
+              tma_load_4d(dst0 + stage * kStride, kv ? &tm_v : &tm_k, fbar, blk * 64,
                           (key0 + box_row) & ((1 << p.s.page_shift) - 1), t.h, here);
           }
         }
@@ -249,8 +271,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const bool leader = elect_one_sync();
-      constexpr uint32_t kIdS = make_idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t kIdPV = make_idesc_bf16(128, D, 0, 1);
+      constexpr uint32_t kIdS = E4M3 ? make_idesc_f16(128, 128, 0, 0) : make_idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t kIdPV = E4M3 ? make_idesc_f16(128, D, 0, 1) : make_idesc_bf16(128, D, 0, 1);
       const uint32_t kv_base = smem_addr(smem + Cfg::kKVOff);
       const uint64_t q_desc = make_sdesc_sw128(smem_addr(smem), 16, 1024);  // K-major
       const uint64_t k_desc = make_sdesc_sw128(kv_base, 16, 1024);          // K-major
@@ -300,7 +322,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const bool next_k = j + 1 < n_kv;
           if (!(ok = wait_full(itv))) break;
           const int live = t.len - (t.kt0 + j) * kTileN;  // rows of V_j that are keys
-          if (live < kTileN) {
+          if (!E4M3 && live < kTileN) {
             const uint32_t vs = kv_base + stage_of(itv) * Cfg::kTileBytes;
             for (int x = lane; x < (kTileN - live) * 8 * Cfg::kBlocks; x += 32) {
               const int blk = x / ((kTileN - live) * 8), y = x - blk * (kTileN - live) * 8;
@@ -428,6 +450,59 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         publish(t);
       }
     }
+    if constexpr (E4M3) if (warp == 3) {
+      // -------------------------------------------------------- widening (e4m3)
+      // One row per lane, 16 values at a time; both rings are swizzled, so neither
+      // side's accesses meet in a bank.
+      const uint32_t raw0 = smem_addr(smem + Cfg::kRawOff), kv0 = smem_addr(smem + Cfg::kKVOff);
+      uint32_t ld = 0;
+      bool ok = true;
+      PagedTile t;
+      for (int k = 0; ok && take_tile(bars, k, t, lim, ok); ++k) {
+        const int n_kv = max(t.n[0], t.n[1]);
+        for (int it = 0; it < 2 * n_kv; ++it, ++ld) {
+          const uint32_t rs = ld % Cfg::kRawStages, rr = ld / Cfg::kRawStages;
+          const uint32_t ks = ld % Cfg::kStages, kr = ld / Cfg::kStages;
+          if (!mbar_wait_warp(smem_addr(&bars->raw_full[rs]), rr & 1, lim) ||
+              !mbar_wait_warp(smem_addr(&bars->kv_empty[ks]), (kr & 1) ^ 1, lim)) {
+            ok = false;
+            break;
+          }
+          // rows of V past the end become zeros
+          const int live = (it & 1) ? t.len - (t.kt0 + (it >> 1)) * kTileN : kTileN;
+          const uint32_t src = raw0 + rs * Cfg::kRawBytes, dst = kv0 + ks * Cfg::kTileBytes;
+#pragma unroll 1
+          for (int row = lane; row < kTileN; row += 32) {
+            const uint32_t from = src + row * D;
+            const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
+            const bool keep = row < live;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(from + ((c ^ sw) << 4)) : "memory");
+              const uint32_t to = dst + (c >> 2) * Cfg::kBlockBytes;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a = keep ? w[2 * h] : 0u, b = keep ? w[2 * h + 1] : 0u;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 to + sw128_offset(row, 2 * (c & 3) + h)),
+                             "r"(e4m3x2_to_f16x2(a)), "r"(e4m3x2_to_f16x2(a >> 16)), "r"(e4m3x2_to_f16x2(b)),
+                             "r"(e4m3x2_to_f16x2(b >> 16)) : "memory");
+              }
+            }
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&bars->kv_full[ks]));
+            mbar_arrive(smem_addr(&bars->raw_empty[rs]));
+          }
+        }
+      }
+      if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
+    }
     __syncwarp();
   } else {
     regs_inc<208>();
@@ -437,7 +512,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
     const uint32_t col_s = Cfg::kColS + i * 128, col_o = i * D;
     const int tok_r = r / p.group, head_r = r - tok_r * p.group;
-    const float c = p.scale_log2;
     int sw = 0, pvw = 0;  // s_full and pv_done waits so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -449,6 +523,12 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int tok = q0 + tok_r;
       // keys that this row sees: one comparison per score covers both masks
       const int see = p.causal ? min(t.len, see0 + tok_r + 1) : t.len;
+      float c = p.scale_log2;
+      if constexpr (E4M3) {
+        c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
+        if (tok_r < p.tok_tile && tok < t.n_new)
+          c *= p.q_up[(static_cast<size_t>(t.row0) + tok) * p.H_q + t.h * p.group + head_r];
+      }
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
         if (!mbar_wait(smem_addr(&bars->s_full[i]), sw & 1, lim)) { ok = false; break; }
@@ -472,8 +552,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                              : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
                                                       rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
-        if (pos) softmax_row_exp<0, true, 0, 64>(s, c, mb, need_mask, pk, sum2);
-        else softmax_row_exp<0, false, 0, 64>(s, c, mb, need_mask, pk, sum2);
+        if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb, need_mask, pk, sum2);
+        else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb, need_mask, pk, sum2);
         if (rescale_warp && j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
           // O is complete: the commit that signalled S_j came after PV_{j-1}
 #pragma unroll
@@ -516,6 +596,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
         for (int e = 0; e < D; ++e) ov[e] = 0u;
       }
+      const float v_scale = E4M3 && p.v_scale ? __ldg(p.v_scale + t.h) : 1.0f;
       if (t.slot >= 0) {
         const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM + r;
         if (row_ok) {
@@ -524,13 +605,17 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D);
 #pragma unroll
             for (int e = 0; e < D / 4; ++e)
-              dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              dst[e] = E4M3 ? make_uint4(__float_as_uint(__uint_as_float(ov[4 * e]) * v_scale),
+                                         __float_as_uint(__uint_as_float(ov[4 * e + 1]) * v_scale),
+                                         __float_as_uint(__uint_as_float(ov[4 * e + 2]) * v_scale),
+                                         __float_as_uint(__uint_as_float(ov[4 * e + 3]) * v_scale))
+                            : make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
           }
         }
         continue;
       }
       // a row with a NaN score has l = NaN and keeps it
-      const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv_l = l == 0.0f ? 0.0f : v_scale / l;
       const size_t row = static_cast<size_t>(t.row0) + tok;
       // O leaves through shared memory, 64 columns at a time: by one TMA store of
       // whole rows where the tile ends inside the sequence, else (the store's box
@@ -755,7 +840,29 @@ paged_fwd_join_kernel(const PagedFwdParams p) {
   if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
+// One warp per row of queries.
 template <int D>
+__global__ void __launch_bounds__(256)
+queries_f16_kernel(const uint2* q, uint2* q16, float* q_up, long long rows) {
+  grid_wait();
+  grid_release();
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const bool mine = lane < D / 4;
+  uint2 x = mine ? q[row * (D / 4) + lane] : make_uint2(0u, 0u);
+  const float v[4] = {bf16lo_to_f32(x.x), bf16hi_to_f32(x.x), bf16lo_to_f32(x.y), bf16hi_to_f32(x.y)};
+  float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float down;
+  const float up = row_power(top, down);
+  if (mine)
+    q16[row * (D / 4) + lane] = make_uint2(pack_f16x2(v[0] * down, v[1] * down), pack_f16x2(v[2] * down, v[3] * down));
+  if (lane == 0) q_up[row] = up;
+}
+
+template <int D, bool E4M3>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& to, const PagedFwdParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_set{0};
@@ -767,7 +874,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  e = launch_chained(paged_fwd_kernel<D>, dim3(p.grid), 384, PagedFwdCfg<D>::kSmemBytes, stream, smem_set, tq, tk,
+  e = launch_chained(paged_fwd_kernel<D, E4M3>, dim3(p.grid), 384, PagedFwdCfg<D, E4M3>::kSmemBytes, stream, smem_set, tq, tk,
                      tv, to, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
@@ -780,8 +887,23 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 }  // namespace
 
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& to, const PagedFwdParams& p, int d, cudaStream_t stream) {
-  return d == 128 ? launch<128>(tq, tk, tv, to, p, stream) : launch<64>(tq, tk, tv, to, p, stream);
+                             const CUtensorMap& to, const PagedFwdParams& p, int d, bool e4m3,
+                             cudaStream_t stream) {
+  if (e4m3) return d == 128 ? launch<128, true>(tq, tk, tv, to, p, stream) : launch<64, true>(tq, tk, tv, to, p, stream);
+  return d == 128 ? launch<128, false>(tq, tk, tv, to, p, stream) : launch<64, false>(tq, tk, tv, to, p, stream);
+}
+
+cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,
+                               cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const int slot = prof_begin(kKPagedQueries, stream);
+  const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
+  const uint2* from = static_cast<const uint2*>(q);
+  uint2* to = static_cast<uint2*>(q16);
+  const cudaError_t e = d == 128 ? launch_chained(queries_f16_kernel<128>, grid, 256, 0, stream, smem_set, from, to, q_up, rows)
+                                 : launch_chained(queries_f16_kernel<64>, grid, 256, 0, stream, smem_set, from, to, q_up, rows);
+  prof_end(slot, stream);
+  return e;
 }
 
 }  // namespace attn

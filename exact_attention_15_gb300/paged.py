@@ -59,14 +59,14 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.H_kv, self.page_size, self.d = num_pages, H_kv, page_size, d
         self.device = k.device
+        self._kind = _KINDS[k.dtype]
         page = H_kv * page_size * d
         self._struct = _PagedCacheStruct(
             k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
             k.stride(0) if num_pages > 1 else page, v.stride(0) if num_pages > 1 else page,
-            num_pages, page_size, H_kv, d, _KINDS[k.dtype])
+            num_pages, page_size, H_kv, d, self._kind)
         self._ref = ctypes.addressof(self._struct)
-        # one token per sequence needs the same workspace whatever the batch
-        self._decode_bytes = load().attn_paged_workspace_bytes(1, 1, H_kv, H_kv, d)
+        self._decode_bytes = load().attn_paged_decode_workspace_bytes(d)
 
 
 def _ptr(t):
@@ -177,8 +177,12 @@ def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=
     return q_out
 
 
-def paged_workspace_bytes(tokens, sequences, H_q, H_kv, d) -> int:
-    return load().attn_paged_workspace_bytes(tokens, sequences, H_q, H_kv, d)
+def paged_workspace_bytes(cache, H_q, tokens=None, sequences=None) -> int:
+    """Bytes of workspace of paged_forward for that many packed tokens and sequences,
+    or of paged_decode without them."""
+    if tokens is None:
+        return cache._decode_bytes
+    return load().attn_paged_fwd_workspace_bytes(tokens, sequences, H_q, cache.H_kv, cache.d, cache._kind)
 
 
 def _outputs(cache, q, lse_shape, out, lse):
@@ -237,7 +241,7 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
     o, lse = _outputs(cache, q, (H_q, T), out, lse)
     lib = load()
-    ws, size = _workspace(cache, workspace, lib.attn_paged_workspace_bytes(T, B, H_q, cache.H_kv, cache.d))
+    ws, size = _workspace(cache, workspace, lib.attn_paged_fwd_workspace_bytes(T, B, H_q, cache.H_kv, cache.d, cache._kind))
     status = _call(cache.device, lib.attn_paged_fwd, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T,
                    B, H_q, cu_seqlens.data_ptr(), kv_lens.data_ptr(), table, cols, stride, bool(causal),
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)

@@ -316,12 +316,15 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
                       int interleaved, attn_stream_t stream);
 
 /*
- * Bytes of device workspace that attn_paged_decode (T = B) and attn_paged_fwd need
- * for these sizes (0 on invalid sizes), whatever the sequences' lengths. It is caller-owned,
- * 256-byte aligned, its contents do not matter between calls, and calls that may
- * run at the same time need one each.
+ * Bytes of device workspace that attn_paged_decode and attn_paged_fwd need, whatever
+ * the sequences' lengths (0 on invalid sizes; T, B, H_q, H_kv, d and type as in the
+ * call). The workspace is caller-owned, 256-byte aligned, its contents do not matter
+ * between calls, and calls that may run at the same time need one each. A decoding
+ * call needs about 5 MB; a chunk call at most 41 MB for the parts of divided tiles,
+ * and over an e4m3 cache 2 d + 4 bytes per query row and head besides.
  */
-size_t attn_paged_workspace_bytes(int T, int B, int H_q, int H_kv, int d);
+size_t attn_paged_decode_workspace_bytes(int d);
+size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, int type);
 
 /*
  * Attention of one query token per sequence over its kv_lens[b] cached keys:

@@ -96,7 +96,7 @@ def test_decode_layouts_streams_and_given_buffers():
     wide[:, :c.width] = c.table
     out = torch.empty_like(q)
     lse = torch.empty(3, 6, device="cuda")
-    ws = torch.full((binding.paged_workspace_bytes(3, 3, 6, 2, 64),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((binding.paged_workspace_bytes(c.handle(), 6),), 255, dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
@@ -114,6 +114,18 @@ def test_decode_large_query_values_over_e4m3():
         scale = 1.0 / math.sqrt(128) / factor
         o, lse = binding.paged_decode(c.handle(), q, c.table, c.kv_lens, scale=scale)
         assert_attention(o, lse, *_decode_want(c, q, scale), what=factor)
+
+
+def test_chunk_large_query_values_over_e4m3():
+    """The same in the tensor-core kernel's fp16 queries, and given buffers."""
+    c = Cache([300, 200], 2, 128, 16, "e4m3")
+    new, h = [150, 200], c.handle()
+    ws = torch.full((binding.paged_workspace_bytes(h, 8, 350, 2),), 255, dtype=torch.uint8, device="cuda")
+    for factor in (2.0 ** 40, 2.0 ** -60):
+        q = (_q(350, 8, 128).float() * factor).to(torch.bfloat16)
+        scale = 1.0 / math.sqrt(128) / factor
+        o, lse = binding.paged_forward(h, q, c.table, c.kv_lens, _offsets(new), scale=scale, workspace=ws)
+        assert_attention(o, lse, *_chunk_want(c, q, new, scale, True), what=factor)
 
 
 def test_decode_spread_scores():

@@ -101,7 +101,8 @@ def test_attention_refusals(lib, name):
     for arg in ("q", "o", "lse"):
         assert _call(lib, name, **{arg: None}) == NULL
         assert _call(lib, name, **{arg: A + 8}) == ALIGN
-    need = lib.attn_paged_workspace_bytes(3, 3, 4, 2, 64)
+    need = (lib.attn_paged_decode_workspace_bytes(64) if name == "decode" else
+            lib.attn_paged_fwd_workspace_bytes(3, 3, 4, 2, 64, 0))
     assert need > 0
     assert _call(lib, name, size=need - 1) == WORKSPACE
     assert _call(lib, name, ws=None) == WORKSPACE
@@ -115,11 +116,14 @@ def test_fwd_needs_offsets(lib):
 
 
 def test_workspace_bytes(lib):
-    f = lib.attn_paged_workspace_bytes
-    assert f(1, 1, 1, 1, 128) > 0 and f(0, 0, 1, 1, 64) > 0
-    for bad in ((-1, 1, 1, 1, 64), (1, -1, 1, 1, 64), (1, 1, 0, 1, 64), (1, 1, 3, 2, 64), (1, 1, 1, 0, 64),
-                (1, 1, 1, 1, 96), (1, 1, 1 << 20, 1, 64)):
+    f = lib.attn_paged_fwd_workspace_bytes
+    assert f(1, 1, 1, 1, 128, 0) > 0 and f(0, 0, 1, 1, 64, 1) > 0
+    # fp16 queries for an e4m3 cache, where the call has many rows per sequence
+    assert f(4096, 1, 8, 2, 128, 1) >= f(4096, 1, 8, 2, 128, 0) + 4096 * 8 * (2 * 128 + 4)
+    for bad in ((-1, 1, 1, 1, 64, 0), (1, -1, 1, 1, 64, 0), (1, 1, 0, 1, 64, 0), (1, 1, 3, 2, 64, 0),
+                (1, 1, 1, 0, 64, 0), (1, 1, 1, 1, 96, 0), (1, 1, 1 << 20, 1, 64, 0), (1, 1, 1, 1, 64, 2)):
         assert f(*bad) == 0
+    assert lib.attn_paged_decode_workspace_bytes(64) > 0 and lib.attn_paged_decode_workspace_bytes(96) == 0
 
 
 def _t(*shape, dtype=torch.bfloat16):
