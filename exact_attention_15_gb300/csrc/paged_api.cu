@@ -202,7 +202,8 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   const int group = H_q / c->H_kv;
   const bool e4m3 = c->type == ATTN_CACHE_E4M3;
   const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d, e4m3);
-  const unsigned rows = c->page_size < kTileN ? c->page_size : kTileN;
+  const int box = e4m3 ? kTileN / 2 : kTileN;  // rows that land together
+  const unsigned rows = c->page_size < box ? c->page_size : box;
   CUtensorMap tq, tk, tv, to;
   int st;
   const void* queries = e4m3 ? ws + plan.q16_off : q;

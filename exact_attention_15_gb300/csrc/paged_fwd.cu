@@ -17,9 +17,13 @@
 // MMA warp zeroes them in shared memory before the last P V product.
 //
 // Over an e4m3 cache the products run in fp16, which holds every e4m3 value exactly
-// (the instructions take no operands of two types): the tiles land in a small ring
-// of their own, and warp 3 widens them into the K / V ring (and puts the zeros past
-// the end). The queries come as fp16 rows scaled by powers of two.
+// (the instructions take no operands of two types): half tiles of 64 keys land in a
+// small ring of their own, and warps 2 and 3 widen one half each of every tile into
+// the K / V ring (and put the zeros past the end); lane 0 of warp 2 looks for work
+// between the tiles. The queries come as fp16 rows scaled by powers of two. One
+// widening warp, which loads, converts and stores 16 values at a time, took 1181 us
+// for the next 1024 tokens of two prompts of 25,000 (32 heads on 8, d 128); with a
+// row's loads ahead of its conversions 773; two warps 661 (bf16: 506).
 //
 // With many work tiles the CTAs claim them one by one. With few, what the last
 // wave leaves idle costs more: every CTA takes the same number of whole tiles, and
@@ -41,14 +45,15 @@ struct PagedFwdCfg {
   static constexpr int kBlocks = D / 64;                // 64-column blocks of a tile
   static constexpr int kBlockBytes = kTileM * 64 * 2;   // 16 KB
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
-  // e4m3: tiles as they are in the cache, rows of D bytes swizzled over their width,
-  // take the place of a quarter of the K / V ring
-  static constexpr int kRawBytes = E4M3 ? kTileN * D : 0;
-  static constexpr int kRawStages = E4M3 ? 32768 / (kTileN * D) : 0;
+  // e4m3: half tiles as they are in the cache, rows of D bytes swizzled over their
+  // width, take the place of a quarter of the K / V ring
+  static constexpr int kHalf = kTileN / 2;
+  static constexpr int kRawBytes = kHalf * D;
+  static constexpr int kRawStages = E4M3 ? 32768 / kRawBytes : 1;
   static constexpr int kStages = (D == 128 ? 4 : 8) * (E4M3 ? 3 : 4) / 4;
   static constexpr int kKVOff = 2 * kTileBytes;
   static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
+  static constexpr int kBarOff = kRawOff + (E4M3 ? kRawStages * kRawBytes : 0);
   static constexpr int kEpiOff = kBarOff + 1024;        // one staging block per warpgroup
   static constexpr int kSmemBytes = kEpiOff + 2 * kBlockBytes + 1024;
   static constexpr uint32_t kColS = 2 * D;
@@ -68,13 +73,13 @@ struct __align__(16) PagedTile {
 };
 
 constexpr int kSlots = 2;     // of the ring that hands out work tiles
-constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (and the widening warp)
+constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (e4m3: and two that widen)
 
 struct PagedBars {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t raw_full[4], raw_empty[4];  // e4m3
+  uint64_t raw_full[8], raw_empty[8];  // e4m3
   uint64_t sched_full[kSlots], sched_empty[kSlots];
   int sched_taken;  // work tiles that the producer has taken so far
   PagedTile sched_t[kSlots];
@@ -144,6 +149,100 @@ __device__ __forceinline__ bool take_tile(PagedBars* bars, int k, PagedTile& t, 
   return t.b >= 0;
 }
 
+// Publishes work tile k in the ring once every reader has taken tile k - kSlots.
+__device__ __forceinline__ bool publish_tile(PagedBars* bars, int k, const PagedTile& t,
+                                             const PagedFwdParams& p) {
+  const int slot = k % kSlots;
+  if (k >= kSlots &&
+      !mbar_wait_sleep(smem_addr(&bars->sched_empty[slot]), ((k / kSlots) - 1) & 1, p.wait_limit, 200)) {
+    record_error(p.s.err, kErrTimeout);
+    return false;
+  }
+  bars->sched_t[slot] = t;
+  mbar_arrive(smem_addr(&bars->sched_full[slot]));
+  return true;
+}
+
+// The work tiles of a CTA, one after the other (one thread). Split: whole waves, then
+// the CTA's share of the rest. Else the CTA starts with work tile blockIdx.x and claims
+// every further one from the counter that the planning kernel zeroed.
+struct TileSource {
+  const PagedFwdParams& p;
+  int total, grid, cta;
+  int lo_tile = 0, hi_tile = -1, seq = 0;  // work tiles of the last sequence looked up
+  int item = -1;                           // the last tile (claimed), or wave (split)
+  int u = 0, end = 0, x = -1;              // split: units left of the share, and their tile
+
+  __device__ explicit TileSource(const PagedFwdParams& params) : p(params) {
+    total = p.tile_start[p.s.B];
+    grid = gridDim.x;
+    cta = blockIdx.x;
+  }
+  __device__ void expand(int tile, PagedTile& t) {
+    if (tile < kFwdListed) {
+      int4* w = reinterpret_cast<int4*>(&t);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) w[i] = p.tiles[3 * tile + i];
+      return;
+    }
+    if (tile < lo_tile || tile >= hi_tile) {
+      const int v = find_last(p.tile_start, p.s.B, tile);
+      seq = p.seq_order[v];
+      lo_tile = p.tile_start[v];
+      hi_tile = p.tile_start[v + 1];
+    }
+    expand_tile(p, tile - lo_tile, seq, t);
+  }
+  __device__ bool near_end() const {
+    constexpr int kNearRounds = 4;
+    return !p.split && item + kNearRounds * static_cast<long long>(grid) >= total;
+  }
+  // t.b < 0 behind the last one
+  __device__ void next(PagedTile& t) {
+    if (!p.split) {
+      if (item < 0) {
+        item = cta;
+      } else {
+        const unsigned c = atomicAdd(reinterpret_cast<unsigned*>(p.tile_ctr), 1u);
+        item = c >= static_cast<unsigned>(total)
+                   ? total
+                   : static_cast<int>(min(static_cast<unsigned>(total), static_cast<unsigned>(grid) + c));
+      }
+      if (item < total) expand(item, t); else t.b = -1;
+      return;
+    }
+    const int waves = total / grid;
+    if (item + 1 < waves) {
+      ++item;
+      expand(item * grid + cta, t);
+      return;
+    }
+    if (x < 0) {
+      const int4 share = p.shares[cta];  // first unit, end, tile of the first unit
+      u = share.x;
+      end = share.y;
+      x = share.z;
+    }
+    while (u < end) {
+      const int first = p.rest_units[x], after = p.rest_units[x + 1], stop = min(end, after);
+      const int k0 = max(0, u - first - kItemCost), k1 = max(0, stop - first - kItemCost);
+      const bool empty = after - first == kItemCost;  // a tile that sees no key
+      const bool mine = k0 < k1 || (empty && u == first), part = !empty && (k0 > 0 || stop < after);
+      u = stop;
+      ++x;
+      if (!mine) continue;
+      expand(waves * grid + x - 1, t);
+      if (part) {
+        t.slot = 2 * cta + (k0 == 0 ? 1 : 0);
+        t.kt0 = k0;
+        for (int i = 0; i < 2; ++i) t.n[i] = max(0, min(t.n[i], k1) - k0);
+      }
+      return;
+    }
+    t.b = -1;
+  }
+};
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(384, 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -166,14 +265,14 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mbar_init(smem_addr(&bars->pv_done[i]), 1);
     }
     for (int i = 0; i < Cfg::kStages; ++i) {
-      mbar_init(smem_addr(&bars->kv_full[i]), 1);
+      mbar_init(smem_addr(&bars->kv_full[i]), 1 + E4M3);  // the copies, or two warps
       mbar_init(smem_addr(&bars->kv_empty[i]), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_addr(&bars->sched_full[i]), 1);
-      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders + E4M3);
+      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders + 2 * E4M3);
     }
-    for (int i = 0; i < Cfg::kRawStages; ++i) {
+    for (int i = 0; E4M3 && i < Cfg::kRawStages; ++i) {
       mbar_init(smem_addr(&bars->raw_full[i]), 1);
       mbar_init(smem_addr(&bars->raw_empty[i]), 1);
     }
@@ -198,25 +297,20 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       // Lane (page j of a key tile, column block) issues one box per tile.
-      const int box_shift = min(p.s.page_shift, 7);
+      const int box_shift = min(p.s.page_shift, E4M3 ? 6 : 7);
       const int n_box = kTileN >> box_shift;
       constexpr int kCols = E4M3 ? 1 : Cfg::kBlocks;  // boxes side by side in a row
-      constexpr int kRow = E4M3 ? D : 128;            // bytes of a box row
-      constexpr int kRing = E4M3 ? Cfg::kRawStages : Cfg::kStages;
-      constexpr int kStride = E4M3 ? Cfg::kRawBytes : Cfg::kTileBytes;
-      uint64_t* ring_full = E4M3 ? bars->raw_full : bars->kv_full;
-      uint64_t* ring_empty = E4M3 ? bars->raw_empty : bars->kv_empty;
       const int j_box = lane / kCols, blk = lane % kCols;
       const int box_row = j_box << box_shift;
-      const uint32_t dst0 = smem_addr(smem + (E4M3 ? Cfg::kRawOff : Cfg::kKVOff)) + blk * Cfg::kBlockBytes +
-                            box_row * kRow;
+      const uint32_t dst0 = smem_addr(smem + Cfg::kKVOff) + blk * Cfg::kBlockBytes + box_row * 128;
+      const uint32_t raw0 = smem_addr(smem + Cfg::kRawOff) + (box_row & (Cfg::kHalf - 1)) * D;
       const int q_bytes = p.tok_tile * p.group * 128;  // one column block of a Q tile
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      uint32_t ld = 0;  // K/V tiles loaded so far
+      uint32_t ld = 0;  // K/V tiles (e4m3: half tiles) loaded so far
       int qk = 0;       // work tiles whose Q was loaded
       bool ok = true;
       PagedTile t;
@@ -252,18 +346,33 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           // boxes that hold a key; the rows of the others keep what they held
           const int boxes = min(n_box, (t.len - key0 + (1 << box_shift) - 1) >> box_shift);
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++ld) {
-            const uint32_t stage = ld % kRing, round = ld / kRing;
-            if (!mbar_wait_warp(smem_addr(&ring_empty[stage]), (round & 1) ^ 1, lim)) {
-              ok = false;
-              break;
+          for (int kv = 0; kv < 2; ++kv) {
+            const CUtensorMap* map = kv ? &tm_v : &tm_k;
+            const int in_page = (key0 + box_row) & ((1 << p.s.page_shift) - 1);
+            if constexpr (E4M3) {
+              const int per = n_box >> 1;  // boxes of a half
+#pragma unroll
+              for (int half = 0; half < 2; ++half, ++ld) {
+                const uint32_t stage = ld % Cfg::kRawStages, round = ld / Cfg::kRawStages;
+                if (!mbar_wait_warp(smem_addr(&bars->raw_empty[stage]), (round & 1) ^ 1, lim)) { ok = false; break; }
+                const uint32_t fbar = smem_addr(&bars->raw_full[stage]);
+                if (lane == 0)
+                  mbar_arrive_expect_tx(fbar, max(0, min(per, boxes - half * per)) * (D << box_shift));
+                __syncwarp();
+                if (j_box < boxes && j_box >= half * per && j_box < (half + 1) * per)
+                  tma_load_4d(raw0 + stage * Cfg::kRawBytes, map, fbar, 0, in_page, t.h, here);
+              }
+              if (!ok) break;
+            } else {
+              const uint32_t stage = ld % Cfg::kStages, round = ld / Cfg::kStages;
+              if (!mbar_wait_warp(smem_addr(&bars->kv_empty[stage]), (round & 1) ^ 1, lim)) { ok = false; break; }
+              const uint32_t fbar = smem_addr(&bars->kv_full[stage]);
+              if (lane == 0) mbar_arrive_expect_tx(fbar, boxes * Cfg::kBlocks * (128 << box_shift));
+              __syncwarp();
+              if (j_box < boxes)
+                tma_load_4d(dst0 + stage * Cfg::kTileBytes, map, fbar, blk * 64, in_page, t.h, here);
+              ++ld;
             }
-            const uint32_t fbar = smem_addr(&ring_full[stage]);
-            if (lane == 0) mbar_arrive_expect_tx(fbar, boxes * kCols * (kRow << box_shift));
-            __syncwarp();
-            if (j_box < boxes)
-              tma_load_4d(dst0 + stage * kStride, kv ? &tm_v : &tm_k, fbar, blk * 64,
-                          (key0 + box_row) & ((1 << p.s.page_shift) - 1), t.h, here);
           }
         }
       }
@@ -354,114 +463,55 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ld += 2 * n_kv;
       }
       if (!ok && leader) record_error(p.s.err, kErrTimeout);
-    } else if (warp == 2 && lane == 0) {
+    } else if (!E4M3 && warp == 2 && lane == 0) {
       // -------------------------------------------------------- scheduler
-      const int total = p.tile_start[p.s.B], grid = gridDim.x, cta = blockIdx.x;
-      int lo_tile = 0, hi_tile = -1, seq = 0;  // work tiles of the last sequence found
-      auto expand = [&](int tile, PagedTile& t) {
-        if (tile < kFwdListed) {
-          int4* w = reinterpret_cast<int4*>(&t);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) w[i] = p.tiles[3 * tile + i];
-          return;
-        }
-        if (tile < lo_tile || tile >= hi_tile) {
-          const int v = find_last(p.tile_start, p.s.B, tile);
-          seq = p.seq_order[v];
-          lo_tile = p.tile_start[v];
-          hi_tile = p.tile_start[v + 1];
-        }
-        expand_tile(p, tile - lo_tile, seq, t);
-      };
-      int k = 0;
-      auto publish = [&](const PagedTile& t) {
-        const int slot = k % kSlots;
-        if (k >= kSlots &&
-            !mbar_wait_sleep(smem_addr(&bars->sched_empty[slot]), ((k / kSlots) - 1) & 1, lim, 200)) {
-          record_error(p.s.err, kErrTimeout);
-          return false;
-        }
-        bars->sched_t[slot] = t;
-        mbar_arrive(smem_addr(&bars->sched_full[slot]));
-        ++k;
-        return true;
-      };
-      bool ok = true;
-      if (p.split) {
-        // whole waves, then this CTA's share of the rest
-        const int waves = total / grid;
-        for (int i = 0; ok && i < waves; ++i) {
-          PagedTile t;
-          expand(i * grid + cta, t);
-          ok = publish(t);
-        }
-        const int4 share = p.shares[cta];  // first unit, end, tile of the first unit
-        int u = share.x, x = share.z;
-        const int end = share.y;
-        while (ok && u < end) {
-          const int first = p.rest_units[x], next = p.rest_units[x + 1];
-          const int stop = min(end, next);
-          const int k0 = max(0, u - first - kItemCost), k1 = max(0, stop - first - kItemCost);
-          const bool empty = next - first == kItemCost;  // a tile that sees no key
-          if (k0 < k1 || (empty && u == first)) {
-            PagedTile t;
-            expand(waves * grid + x, t);
-            if (!empty && (k0 > 0 || stop < next)) {
-              t.slot = 2 * cta + (k0 == 0 ? 1 : 0);
-              t.kt0 = k0;
-              for (int i = 0; i < 2; ++i) t.n[i] = max(0, min(t.n[i], k1) - k0);
-            }
-            ok = publish(t);
+      // Near the end of a claimed list a tile is claimed only once the producer has
+      // taken the one before, so no CTA holds tiles that an idle one could run.
+      TileSource source(p);
+      for (int k = 0;; ++k) {
+        PagedTile t;
+        source.next(t);
+        if (!publish_tile(bars, k, t, p)) break;
+        if (t.b < 0) break;
+        if (source.near_end()) {
+          bool taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) > k;
+          const long long t0 = clock64();
+          while (!taken && clock64() - t0 <= lim) {
+            __nanosleep(100);
+            taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) > k;
           }
-          u = stop;
-          ++x;
-        }
-      } else {
-        // The CTA starts with work tile blockIdx.x and claims every further one
-        // from the counter that the planning kernel zeroed. Near the end of the
-        // list a tile is claimed only once the producer has taken the one before,
-        // so no CTA holds tiles that an idle one could run.
-        constexpr int kNearRounds = 4;
-        int item = cta;
-        while (ok && item < total) {
-          PagedTile t;
-          expand(item, t);
-          if (!(ok = publish(t))) break;
-          if (item + kNearRounds * static_cast<long long>(grid) >= total) {
-            bool taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) >= k;
-            const long long t0 = clock64();
-            while (!taken && clock64() - t0 <= lim) {
-              __nanosleep(100);
-              taken = *reinterpret_cast<volatile int*>(&bars->sched_taken) >= k;
-            }
-            if (!taken) {  // the other roles' bounded waits end the CTA
-              record_error(p.s.err, kErrTimeout);
-              ok = false;
-            }
+          if (!taken) {  // the other roles' bounded waits end the CTA
+            record_error(p.s.err, kErrTimeout);
+            break;
           }
-          const unsigned c = atomicAdd(reinterpret_cast<unsigned*>(p.tile_ctr), 1u);
-          item = c >= static_cast<unsigned>(total) ? total : static_cast<int>(min(
-                     static_cast<unsigned>(total), static_cast<unsigned>(grid) + c));
         }
       }
-      if (ok) {
-        PagedTile t = {};
-        t.b = -1;
-        publish(t);
-      }
-    }
-    if constexpr (E4M3) if (warp == 3) {
+    } else if (E4M3 && warp >= 2) {
       // -------------------------------------------------------- widening (e4m3)
-      // One row per lane, 16 values at a time; both rings are swizzled, so neither
-      // side's accesses meet in a bank.
+      // Warp 2 the first, warp 3 the second half of every tile, a row per lane; both
+      // rings are swizzled, so neither side's accesses meet in a bank. Lane 0 of
+      // warp 2 publishes the next work tile when it takes one.
+      const int half = warp - 2;
       const uint32_t raw0 = smem_addr(smem + Cfg::kRawOff), kv0 = smem_addr(smem + Cfg::kKVOff);
-      uint32_t ld = 0;
+      uint32_t ld = 0;  // tiles widened so far
       bool ok = true;
+      TileSource source(p);
       PagedTile t;
+      if (half == 0 && lane == 0) {
+        source.next(t);
+        publish_tile(bars, 0, t, p);
+      }
+      __syncwarp();
       for (int k = 0; ok && take_tile(bars, k, t, lim, ok); ++k) {
+        if (half == 0 && lane == 0) {
+          PagedTile next;
+          source.next(next);
+          publish_tile(bars, k + 1, next, p);
+        }
+        __syncwarp();
         const int n_kv = max(t.n[0], t.n[1]);
         for (int it = 0; it < 2 * n_kv; ++it, ++ld) {
-          const uint32_t rs = ld % Cfg::kRawStages, rr = ld / Cfg::kRawStages;
+          const uint32_t rs = (2 * ld + half) % Cfg::kRawStages, rr = (2 * ld + half) / Cfg::kRawStages;
           const uint32_t ks = ld % Cfg::kStages, kr = ld / Cfg::kStages;
           if (!mbar_wait_warp(smem_addr(&bars->raw_full[rs]), rr & 1, lim) ||
               !mbar_wait_warp(smem_addr(&bars->kv_empty[ks]), (kr & 1) ^ 1, lim)) {
@@ -472,24 +522,28 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const int live = (it & 1) ? t.len - (t.kt0 + (it >> 1)) * kTileN : kTileN;
           const uint32_t src = raw0 + rs * Cfg::kRawBytes, dst = kv0 + ks * Cfg::kTileBytes;
 #pragma unroll 1
-          for (int row = lane; row < kTileN; row += 32) {
-            const uint32_t from = src + row * D;
+          for (int in = lane; in < Cfg::kHalf; in += 32) {
+            const int row = half * Cfg::kHalf + in;
+            const uint32_t from = src + in * D;
             const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
             const bool keep = row < live;
+            // all loads of the row first: one latency for them
+            uint32_t w[D / 16][4];
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                           : "r"(from + ((c ^ sw) << 4)));
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(from + ((c ^ sw) << 4)) : "memory");
               const uint32_t to = dst + (c >> 2) * Cfg::kBlockBytes;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t a = keep ? w[2 * h] : 0u, b = keep ? w[2 * h + 1] : 0u;
+                const uint32_t a = keep ? w[c][2 * h] : 0u, b = keep ? w[c][2 * h + 1] : 0u;
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                                  to + sw128_offset(row, 2 * (c & 3) + h)),
                              "r"(e4m3x2_to_f16x2(a)), "r"(e4m3x2_to_f16x2(a >> 16)), "r"(e4m3x2_to_f16x2(b)),
-                             "r"(e4m3x2_to_f16x2(b >> 16)) : "memory");
+                             "r"(e4m3x2_to_f16x2(b >> 16)));
               }
             }
           }
