@@ -647,24 +647,42 @@ paged_join_kernel(const StreamParams p) {
 #pragma unroll
   for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
   if (r < rows) {
-#pragma unroll 4
-    for (int i = part; i < pieces; i += 4) {
-      const size_t at = static_cast<size_t>(i == 0 ? slot0 : 2 * (c + i)) * 16 + r;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      float o[kV];
-      if constexpr (kV == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * 4);
-        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * 2);
-        o[0] = v.x; o[1] = v.y;
-      }
-      const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
-      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
-      m = top;
-      l = l * f + ml.y * g;
+    // four pieces at a time, all their loads before the first is used (a place
+    // behind the last piece loads the last again, with no weight)
+    const auto* ml_at = reinterpret_cast<const float2*>(p.part_ml) + r;
+    const float* o_at = p.part_o + static_cast<size_t>(r) * D + lane * kV;
+    for (int i0 = part; i0 < pieces; i0 += 16) {
+      float2 ml[4];
+      float o[4][kV];
 #pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + o[e] * g;
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + 4 * k, pieces - 1);
+        const int slot = i == 0 ? slot0 : 2 * (c + i);
+        ml[k] = ml_at[slot * 16];
+        const float* src = o_at + static_cast<size_t>(slot) * 16 * D;
+        if constexpr (kV == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          o[k][0] = v.x; o[k][1] = v.y; o[k][2] = v.z; o[k][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          o[k][0] = v.x; o[k][1] = v.y;
+        }
+      }
+      const float before = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, ml[k].x);
+      const float bias = m == -INFINITY ? 0.0f : m, f = ex2_approx(before - bias);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] *= f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool live = i0 + 4 * k < pieces;
+        const float g = ex2_approx(ml[k].x - bias);
+        l += live ? ml[k].y * g : 0.0f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] += live ? o[k][e] * g : 0.0f;
+      }
     }
   }
 #pragma unroll
