@@ -344,7 +344,11 @@ int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, flo
  * and values: whole prompts, the next chunk of a prompt, or drafted tokens to
  * verify. With causal, new token i of n sees key j when j <= kv_lens[b] - n + i;
  * without, every key of its sequence. A row that sees no key gets O = 0 and LSE =
- * -inf. Otherwise as attn_paged_decode.
+ * -inf. As with attn_fwd, a NaN or infinity among the values of a chunk's own tokens
+ * can reach rows of the chunk for which the causal mask hides it. Chunks of at most 16
+ * query rows per sequence and KV head (T * H_q / H_kv against 16 * B) run on the
+ * streaming kernel of attn_paged_decode, larger ones on the tensor cores; either way
+ * equal inputs give equal bits. Otherwise as attn_paged_decode.
  */
 int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float* lse, int T, int B,
                    int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
