@@ -20,8 +20,11 @@ CACHE_E4M3 = 1
 _KINDS = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
-_bf16, _i32 = torch.bfloat16, torch.int32
-_empty = torch.empty
+_bf16, _f64, _i32 = torch.bfloat16, torch.float64, torch.int32
+_empty, _empty_like = torch.empty, torch.empty_like
+_current_device = torch.cuda.current_device
+# torch's current stream of a device as a pointer: a Stream object costs the host 3 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _PagedCacheStruct(ctypes.Structure):
@@ -59,6 +62,7 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.H_kv, self.page_size, self.d = num_pages, H_kv, page_size, d
         self.device = k.device
+        self._index = k.get_device()
         self._kind = _KINDS[k.dtype]
         page = H_kv * page_size * d
         self._struct = _PagedCacheStruct(
@@ -66,7 +70,8 @@ class PagedCache:
             k.stride(0) if num_pages > 1 else page, v.stride(0) if num_pages > 1 else page,
             num_pages, page_size, H_kv, d, self._kind)
         self._ref = ctypes.addressof(self._struct)
-        self._decode_bytes = load().attn_paged_decode_workspace_bytes(d)
+        self._lib = load()
+        self._decode_bytes = self._lib.attn_paged_decode_workspace_bytes(d)
 
 
 def _ptr(t):
@@ -76,13 +81,13 @@ def _ptr(t):
 def _check_seqs(cache, page_table, kv_lens, cu_seqlens, tokens):
     """Checks the arrays that describe the sequences. Returns their number and the
     page table's pointer, columns and row stride (one row may have any)."""
-    dev = cache.device
-    if (kv_lens.dtype != _i32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous()
-            or kv_lens.device != dev):
-        raise ValueError(f"kv_lens must be a contiguous 1-D int32 tensor on {dev}")
+    index = cache._index
+    if (kv_lens.dtype is not _i32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous()
+            or kv_lens.get_device() != index):
+        raise ValueError(f"kv_lens must be a contiguous 1-D int32 tensor on {cache.device}")
     B = kv_lens.numel()
-    if page_table.dtype != _i32 or page_table.dim() != 2 or page_table.device != dev:
-        raise ValueError(f"page_table must be a [{B}, max_pages] int32 tensor on {dev}")
+    if page_table.dtype is not _i32 or page_table.dim() != 2 or page_table.get_device() != index:
+        raise ValueError(f"page_table must be a [{B}, max_pages] int32 tensor on {cache.device}")
     rows, cols = page_table.shape
     stride = cols
     if rows != B:
@@ -94,17 +99,17 @@ def _check_seqs(cache, page_table, kv_lens, cu_seqlens, tokens):
     if cu_seqlens is None:
         if tokens != B:
             raise ValueError(f"without cu_seqlens there is one token per sequence: {tokens} for {B}")
-    elif (cu_seqlens.dtype != _i32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() != B + 1
-          or not cu_seqlens.is_contiguous() or cu_seqlens.device != dev):
-        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor of {B + 1} entries on {dev}")
+    elif (cu_seqlens.dtype is not _i32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() != B + 1
+          or not cu_seqlens.is_contiguous() or cu_seqlens.get_device() != index):
+        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor of {B + 1} entries on {cache.device}")
     return B, page_table.data_ptr(), cols, stride
 
 
 def _tokens(name, t, cache):
     """Checks [tokens, heads, d] whose tokens are contiguous but may lie apart.
     Returns tokens, heads and the elements between tokens."""
-    d = cache.d
-    if t.dim() == 3 and t.dtype == _bf16 and t.device == cache.device:
+    if t.dtype is _bf16 and t.get_device() == cache._index and t.dim() == 3:
+        d = cache.d
         T, H, width = t.shape
         if width == d:
             if t.is_contiguous():
@@ -112,18 +117,17 @@ def _tokens(name, t, cache):
             a, b, c = t.stride()
             if c == 1 and (H <= 1 or b == d):
                 return T, H, a if T > 1 else H * d
-    raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, {d}] on {cache.device} whose tokens are "
+    raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, {cache.d}] on {cache.device} whose tokens are "
                      f"contiguous, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _call(device, fn, *args):
-    """fn(*args, stream) with torch's current stream of `device`, which the C call
-    takes as the current device."""
-    index = device.index
-    if torch.cuda.current_device() == index:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(device):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+def _call(index, fn, *args):
+    """fn(*args, stream) with torch's current stream of device `index`, which the C
+    call takes as the current device."""
+    if _current_device() == index:
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
 
 
 def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=None, interleaved=False,
@@ -146,8 +150,8 @@ def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
     rotary, freq = 0, None
     if inv_freq is not None:
-        if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
-                or inv_freq.device != cache.device):
+        if (inv_freq.dtype is not _f64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
+                or inv_freq.get_device() != cache._index):
             raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {cache.device}")
         rotary, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
     H_q = qs = os = 0
@@ -169,8 +173,8 @@ def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=
             q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    status = _call(cache.device, load().attn_paged_append, cache._ref, q_ptr, k.data_ptr(), v.data_ptr(),
-                   out_ptr, qs, ks, vs, os, T, B, H_q, _ptr(cu_seqlens), kv_lens.data_ptr(), table, cols,
+    status = _call(cache._index, cache._lib.attn_paged_append, cache._ref, q_ptr, k.data_ptr(), v.data_ptr(),
+                   out_ptr, qs, ks, vs, os, T, B, H_q, None if cu_seqlens is None else cu_seqlens.data_ptr(), kv_lens.data_ptr(), table, cols,
                    stride, freq, rotary, bool(interleaved))
     if status:
         _check(status, "attn_paged_append")
@@ -192,7 +196,7 @@ def _outputs(cache, q, lse_shape, out, lse):
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q)
     else:
         _check_tensor("out", out, q.shape, _bf16, cache.device)
     if lse is None:
@@ -218,9 +222,9 @@ def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, 
     T, H_q, _ = _tokens("q", q, cache)
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, None, T)
     o, lse = _outputs(cache, q, (B, H_q), out, lse)
-    lib = load()
+    lib = cache._lib
     ws, size = _workspace(cache, workspace, cache._decode_bytes)
-    status = _call(cache.device, lib.attn_paged_decode, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
+    status = _call(cache._index, lib.attn_paged_decode, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
                    B, H_q, kv_lens.data_ptr(), table, cols, stride,
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)
     if status:
@@ -240,9 +244,9 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
         raise ValueError("cu_seqlens is required (paged_decode takes one token per sequence)")
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
     o, lse = _outputs(cache, q, (H_q, T), out, lse)
-    lib = load()
+    lib = cache._lib
     ws, size = _workspace(cache, workspace, lib.attn_paged_fwd_workspace_bytes(T, B, H_q, cache.H_kv, cache.d, cache._kind))
-    status = _call(cache.device, lib.attn_paged_fwd, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T,
+    status = _call(cache._index, lib.attn_paged_fwd, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T,
                    B, H_q, cu_seqlens.data_ptr(), kv_lens.data_ptr(), table, cols, stride, bool(causal),
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)
     if status:

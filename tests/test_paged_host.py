@@ -132,7 +132,8 @@ def _t(*shape, dtype=torch.bfloat16):
 
 class _HostCache:
     """Stands in for a PagedCache so that the other arguments' checks run here."""
-    device, d, H_kv, page_size, num_pages, _decode_bytes = torch.device("cpu"), 64, 2, 16, 4, 256
+    device, d, H_kv, page_size, num_pages = torch.device("cpu"), 64, 2, 16, 4
+    _index, _decode_bytes, _lib = -1, 256, None  # (host tensors report the index -1)
 
 
 def _raises(match, fn, *a, **kw):
