@@ -539,25 +539,32 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int kPerRow = kCols / 8;  // threads per row of the result
     static_assert(R * kPerRow <= 32 * kWarps, "one 8-column group per thread");
     const int ro = tid / kPerRow, g8 = tid % kPerRow;
-    float top = -INFINITY, sum = 0.0f;
-    if (ro < rows) {
+    // Lane r works out row r: its maximum and sum over the warps, and the factor of
+    // this warp's part. The lanes that need a row's values take them from there.
+    float row_top = -INFINITY, row_sum = 0.0f, row_mine;
+    {
+      const int r = lane & (R - 1);
+      float2 w[kWarps];
 #pragma unroll
-      for (int g = 0; g < kWarps; ++g) top = fmaxf(top, ml[(g * 16 + ro) * 2]);
-      const float mb = top == -INFINITY ? 0.0f : top;
+      for (int g = 0; g < kWarps; ++g) {
+        w[g] = *reinterpret_cast<const float2*>(ml + (g * 16 + r) * 2);
+        row_top = fmaxf(row_top, w[g].x);
+      }
+      const float mb = row_top == -INFINITY ? 0.0f : row_top;
 #pragma unroll
-      for (int g = 0; g < kWarps; ++g)
-        sum += ml[(g * 16 + ro) * 2 + 1] * ex2_approx(ml[(g * 16 + ro) * 2] - mb);
+      for (int g = 0; g < kWarps; ++g) {
+        w[g].x = ex2_approx(w[g].x - mb);
+        row_sum += w[g].y * w[g].x;
+      }
+      row_mine = warp < 2 ? (warp == 0 ? w[0].x : w[1].x) : (warp == 2 ? w[2].x : w[3].x);
     }
+    const float top = __shfl_sync(0xffffffffu, row_top, ro & (R - 1));
+    const float sum = __shfl_sync(0xffffffffu, row_sum, ro & (R - 1));
     float mine[NB][2];  // factors of this lane's accumulator columns
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float t = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kWarps; ++g) t = fmaxf(t, ml[(g * 16 + nb * 8 + 2 * qd + e) * 2]);
-        mine[nb][e] = ex2_approx(m[nb][e] - (t == -INFINITY ? 0.0f : t));
-      }
+      for (int e = 0; e < 2; ++e) mine[nb][e] = __shfl_sync(0xffffffffu, row_mine, nb * 8 + 2 * qd + e);
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += kCols) {
       if (c0 > 0) named_bar_sync(1, 32 * kWarps);
