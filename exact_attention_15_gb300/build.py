@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,9 +22,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libattn_gb300.so")
+CALLS_LIB = os.path.join(LIBDIR, "_paged_call.so")
 
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_fwd_pair.cu", "attn_bwd.cu", "attn_bwd_pair.cu",
            "noalloc.cu", "paged_api.cu", "paged_append.cu", "paged_decode.cu", "paged_fwd.cu"]
+CALLS = "paged_call.c"  # a CPython module: the paged cache's torch calls
 HEADERS = ["ptx.cuh", "attn_common.cuh", "fwd_softmax.cuh", "host.h", "paged.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -38,7 +41,7 @@ def _nvcc():
 
 
 def _newest_dep_mtime():
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [CALLS]]
     paths.append(os.path.join(ROOT, "include", "attn.h"))
     return max(os.path.getmtime(p) for p in paths if os.path.exists(p))
 
@@ -52,17 +55,31 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
+def _compile_calls():
+    """gcc for the CPython module (it includes no torch or CUDA header)."""
+    tmp = CALLS_LIB + ".tmp"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, CALLS), "-o", tmp, "-lm"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for {CALLS}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_LIB)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compiles and links the library if any source is newer than it. Returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_dep_mtime():
+    if (not force and os.path.exists(LIB) and os.path.exists(CALLS_LIB)
+            and os.path.getmtime(LIB) >= _newest_dep_mtime()):
         return LIB
     extra = list(extra_flags)
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         results = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+    calls.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

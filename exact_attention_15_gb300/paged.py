@@ -3,17 +3,22 @@
 Checks of arguments, allocation of the outputs and of the workspace, and the
 C calls on torch's current stream; the computation runs in the library's CUDA
 kernels. One call costs the host several microseconds, as much as the GPU needs
-for a small one, so the checks are plain attribute comparisons.
+for a small one: ``csrc/paged_call.c`` makes the common calls (no given outputs,
+the cache on the current device), and what it does not take goes through the
+checks here.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
+import os
 
 import torch
 
-from .binding import _check, _check_tensor, load
+from .binding import _check, _check_tensor, library_path, load
 
 CACHE_BF16 = 0
 CACHE_E4M3 = 1
@@ -25,6 +30,28 @@ _empty, _empty_like = torch.empty, torch.empty_like
 _current_device = torch.cuda.current_device
 # torch's current stream of a device as a pointer: a Stream object costs the host 3 us
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_calls = None
+
+
+def _load_calls():
+    """The compiled calls, bound to the library and torch (once). Raises if they
+    have not been built."""
+    global _calls
+    if _calls is None:
+        path = os.path.join(os.path.dirname(library_path()), "_paged_call.so")
+        if not os.path.exists(path):
+            raise ImportError(f"not built: {path} is missing (run `python -c 'import __graft_entry__ as g; g.build()'`)")
+        spec = importlib.util.spec_from_file_location(
+            "_paged_call", path, loader=importlib.machinery.ExtensionFileLoader("_paged_call", path))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        lib = load()
+        module.setup(*(ctypes.cast(getattr(lib, name), _P).value for name in (
+            "attn_paged_append", "attn_paged_decode", "attn_paged_fwd", "attn_paged_fwd_workspace_bytes")), torch)
+        _calls = module
+    return _calls
 
 
 class _PagedCacheStruct(ctypes.Structure):
@@ -71,6 +98,7 @@ class PagedCache:
             num_pages, page_size, H_kv, d, self._kind)
         self._ref = ctypes.addressof(self._struct)
         self._lib = load()
+        self._calls = _load_calls()
         self._decode_bytes = self._lib.attn_paged_decode_workspace_bytes(d)
 
 
@@ -141,6 +169,12 @@ def paged_append(cache, q, k, v, page_table, kv_lens, cu_seqlens=None, inv_freq=
     append as is. Pairs are the halves of the first rotary_dim elements, or
     neighbours with interleaved. Returns the turned q (written to q_out if given,
     which may be q; q itself without inv_freq and q_out)."""
+    r = cache._calls.append(cache._ref, cache._index, q, k, v, page_table, kv_lens, cu_seqlens, inv_freq,
+                            interleaved, q_out)
+    if r is not NotImplemented:
+        if type(r) is int:
+            _check(r, "attn_paged_append")
+        return r
     T, heads, ks = _tokens("k", k, cache)
     if heads != cache.H_kv:
         raise ValueError(f"k must be [tokens, {cache.H_kv} heads, d], got {heads} heads")
@@ -219,6 +253,13 @@ def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, 
     Returns (o [B, H_q, d], lse [B, H_q]); a sequence without keys gives 0 and -inf.
     The default scale is 1/sqrt(d). The workspace (paged_workspace_bytes) is
     allocated with torch unless given."""
+    if out is None and lse is None and workspace is None:
+        r = cache._calls.decode(cache._ref, cache._index, cache.device, cache._decode_bytes, q, page_table, kv_lens,
+                                scale)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r, "attn_paged_decode")
+            return r
     T, H_q, _ = _tokens("q", q, cache)
     B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, None, T)
     o, lse = _outputs(cache, q, (B, H_q), out, lse)
@@ -239,6 +280,13 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
     token sees all keys of its sequence and each one before sees one key less.
     Returns (o [T, H_q, d], lse [H_q, T]); rows behind the last sequence are not
     written."""
+    if out is None and lse is None and workspace is None:
+        r = cache._calls.forward(cache._ref, cache._index, cache.device, q, page_table, kv_lens, cu_seqlens, scale,
+                                 causal)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r, "attn_paged_fwd")
+            return r
     T, H_q, _ = _tokens("q", q, cache)
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required (paged_decode takes one token per sequence)")

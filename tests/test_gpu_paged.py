@@ -2,6 +2,7 @@
 one-token attention and chunk attention, against definitions in 64 bits, and a
 run of all of them as a serving loop makes it."""
 
+import ctypes
 import math
 
 import pytest
@@ -436,3 +437,48 @@ def test_serving_loop(kind):
         graph.replay()
         check(*outs)
         advance(i)
+
+
+def test_compiled_calls_and_python_checks_agree():
+    """The calls that allocate their outputs are checked and made in C, those with
+    given outputs in Python: the same bits, the same refusals."""
+    c = Cache([40, 30], 2, 64, 16)
+    h, q, cu = c.handle(), _q(2, 4, 64), _offsets([1, 1])
+    for call in (lambda **kw: binding.paged_decode(h, q, c.table, c.kv_lens, **kw),
+                 lambda **kw: binding.paged_forward(h, q, c.table, c.kv_lens, cu, **kw)):
+        a = call()
+        b = call(out=torch.empty_like(q), lse=torch.empty_like(a[1]))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    k, freq = _q(2, 2, 64), torch.ones(32, dtype=torch.float64, device="cuda")
+    bad = [
+        lambda: binding.paged_decode(h, q.float(), c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, q.cpu(), c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, _q(3, 4, 64), c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, _q(2, 3, 64), c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, _q(2, 4, 128), c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, _q(2, 8, 64)[:, :4], c.table, c.kv_lens),
+        lambda: binding.paged_decode(h, q, c.table.long(), c.kv_lens),
+        lambda: binding.paged_decode(h, q, c.table[:1], c.kv_lens),
+        lambda: binding.paged_decode(h, q, c.table, c.kv_lens.cpu()),
+        lambda: binding.paged_forward(h, q, c.table, c.kv_lens, cu[:2]),
+        lambda: binding.paged_forward(h, q, c.table, c.kv_lens, None),
+        lambda: binding.paged_append(h, q, _q(2, 1, 64), k, c.table, c.kv_lens),
+        lambda: binding.paged_append(h, q, k, _q(3, 2, 64), c.table, c.kv_lens),
+        lambda: binding.paged_append(h, _q(1, 4, 64), k, k, c.table, c.kv_lens),
+        lambda: binding.paged_append(h, q, k, k, c.table, c.kv_lens, inv_freq=freq.float()),
+        lambda: binding.paged_append(h, q, k, k, c.table, c.kv_lens, q_out=_q(2, 2, 64)),
+        lambda: binding.paged_append(h, None, k, k, c.table, c.kv_lens, q_out=q),
+        lambda: binding.PagedCache(c.k, c.v, k_scale=torch.ones(2, device="cuda")),
+        lambda: binding.PagedCache(c.k.transpose(1, 2), c.v.transpose(1, 2)),
+        lambda: binding.PagedCache(c.k, c.v[:1]),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: binding.paged_append(h, q, k, k, c.table, c.kv_lens, inv_freq=freq[:4]),  # 8 elements
+              lambda: binding.paged_decode(h, q, c.table, c.kv_lens, scale=float("nan"))):
+        with pytest.raises(binding.AttnError) as e:
+            f()
+        assert e.value.status == 4
+    with pytest.raises(ctypes.ArgumentError):
+        binding.paged_decode(h, q, c.table, c.kv_lens, scale="1")

@@ -134,6 +134,7 @@ class _HostCache:
     """Stands in for a PagedCache so that the other arguments' checks run here."""
     device, d, H_kv, page_size, num_pages = torch.device("cpu"), 64, 2, 16, 4
     _index, _decode_bytes, _lib = -1, 256, None  # (host tensors report the index -1)
+    _ref, _calls = 0, None  # set in the test below
 
 
 def _raises(match, fn, *a, **kw):
@@ -148,8 +149,12 @@ def test_cache_rejects_host_tensors_and_wrong_types():
     _raises("bf16 or", binding.PagedCache, f, f)
 
 
-def test_binding_checks_sequences_and_tokens():
+def test_binding_checks_sequences_and_tokens(lib):
+    """Through both the compiled calls (which refuse to take any of these) and the
+    checks behind them."""
     c, i32 = _HostCache(), torch.int32
+    struct = _cache()
+    c._ref, c._calls = ctypes.addressof(struct), paged._load_calls()
     q, k = _t(3, 4, 64), _t(3, 2, 64)
     lens, table, cu = _t(3, dtype=i32), _t(3, 5, dtype=i32), _t(4, dtype=i32)
     _raises("kv_lens", binding.paged_decode, c, q, table, lens.long())
