@@ -82,7 +82,11 @@ __device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x,
 // One CTA per token. The first kAhead parts of every thread are loaded before the
 // token's sequence, position and page are looked up (three dependent loads) and
 // its angles computed, once for all heads; then they are turned and stored. What
-// bounds it is the bytes.
+// bounds it is the bytes: 36,696 tokens of 16 ragged prompts (32 query and 8 KV heads
+// of 128, 902 MB) take 145 us, 6.2 TB/s, 91% of a plain copy's rate. Measured
+// beside it: without the loads ahead 155 us, with a read of the angles from shared
+// memory for every part 158, with a warp or 64 threads per token 158 or more, with
+// registers held down for more CTAs 156 or more.
 constexpr int kAhead = 3;
 __global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(const AppendParams p) {
@@ -127,9 +131,20 @@ paged_append_kernel(const AppendParams p) {
     const float half = static_cast<float>(static_cast<int>(whole >> 32)) * (1.0f / 2147483648.0f);
     float sn, c;
     sincospif(half, &sn, &c);
-    cs[tid] = make_float2(c, sn);
+    cs[(tid & 7) * (p.rotary_dim >> 4) + (tid >> 3)] = make_float2(c, sn);
   }
   __syncthreads();
+  // A thread has the same place in every head, so its eight angles stay with it
+  // (pair 8 j + e lies at e times the threads + j: neighbours read neighbours).
+  float2 turn[8];
+  {
+    const Place x = place_of(p, tid);
+    const int j = 16 * x.j < p.rotary_dim ? x.j : 0;
+    if (p.rotary_dim > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) turn[e] = cs[e * (p.rotary_dim >> 4) + j];
+    }
+  }
   for (int k = 0, i = tid; i < parts; ++k, i += kAppendThreads) {
     const Place x = place_of(p, i);
     const Part w = k == 0 ? ahead[0] : k == 1 ? ahead[1] : k == 2 ? ahead[2] : load_part(p, x, t);
@@ -139,7 +154,7 @@ paged_append_kernel(const AppendParams p) {
     if (x.split) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 r = cs[8 * x.j + e];
+        const float2 r = turn[e];
         const float a = x0[e], c = x1[e];
         x0[e] = a * r.x - c * r.y;
         x1[e] = a * r.y + c * r.x;
@@ -147,7 +162,7 @@ paged_append_kernel(const AppendParams p) {
     } else if (x.turn) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 r = cs[8 * x.j + e], u = cs[8 * x.j + 4 + e];
+        const float2 r = turn[e], u = turn[4 + e];
         const float a = x0[2 * e], c = x0[2 * e + 1], a1 = x1[2 * e], c1 = x1[2 * e + 1];
         x0[2 * e] = a * r.x - c * r.y;
         x0[2 * e + 1] = a * r.y + c * r.x;
