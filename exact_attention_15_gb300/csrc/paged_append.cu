@@ -83,7 +83,7 @@ __device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x,
 // token's sequence, position and page are looked up (three dependent loads) and
 // its angles computed, once for all heads; then they are turned and stored. What
 // bounds it is the bytes: 36,696 tokens of 16 ragged prompts (32 query and 8 KV heads
-// of 128, 902 MB) take 145 us, 6.2 TB/s, 91% of a plain copy's rate. Measured
+// of 128, 902 MB) take 137 to 145 us, 6.2 to 6.6 TB/s, 91 to 97% of a plain copy's rate. Measured
 // beside it: without the loads ahead 155 us, with a read of the angles from shared
 // memory for every part 158, with a warp or 64 threads per token 158 or more, with
 // registers held down for more CTAs 156 or more.
