@@ -4,6 +4,7 @@ run of all of them as a serving loop makes it."""
 
 import ctypes
 import math
+import random
 
 import pytest
 
@@ -174,6 +175,85 @@ def _chunk_want(c, q, new, scale, causal):
         o.append(r[0]), a.append(r[1]), lse.append(r[2])
         t0 += n
     return torch.cat(o), torch.cat(a), torch.cat(lse, 1)
+
+
+def _many(B, H_q, H_kv, d, page, new_lo, new_hi, ctx_hi, seed):
+    """A larger ragged batch: new tokens, lengths and the rest of a CHUNK case."""
+    r = random.Random(seed)
+    new = [r.randint(new_lo, new_hi) for _ in range(B)]
+    return new, [n + r.randint(0, ctx_hi) for n in new], H_q, H_kv, d, page
+
+
+# the tensor-core kernel's ways of dealing out work: claimed tiles beyond the listed
+# ones; whole waves and a rest that is cut; more sequences than are sorted
+MANY = [
+    _many(24, 16, 16, 64, 16, 257, 300, 200, 1),
+    _many(10, 16, 16, 64, 32, 200, 256, 900, 2),
+    _many(21, 32, 16, 64, 64, 65, 128, 40, 3),
+    _many(1100, 4, 1, 64, 16, 0, 12, 30, 4),
+    _many(1, 4, 4, 128, 64, 700, 700, 9000, 5),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_chunk_of_many(case, kind):
+    new, lens, H_q, H_kv, d, page = MANY[case]
+    c = Cache(lens, H_kv, d, page, kind, seed=case)
+    q = _q(sum(new), H_q, d)
+    o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new))
+    assert_attention(o, lse, *_chunk_want(c, q, new, 1.0 / math.sqrt(d), True))
+    again = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new))
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """Two streams, each with its own decoding and chunk calls over one cache: the
+    same bits as one after the other (workspaces are the calls' own)."""
+    c = Cache([5000, 300, 2000], 4, 128, 64)
+    h, new = c.handle(), [40, 300, 129]
+    qs = [(_q(3, 16, 128, seed=i), _q(sum(new), 16, 128, seed=10 + i)) for i in range(2)]
+    cu = _offsets(new)
+
+    def calls(q1, qn):
+        return [*binding.paged_decode(h, q1, c.table, c.kv_lens), *binding.paged_forward(h, qn, c.table, c.kv_lens, cu)]
+
+    want = [calls(*q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(calls(*qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_pages_behind_2_to_the_31_elements(kind):
+    """Pages whose offsets need more than 32 bits, read and written."""
+    H_kv, page, d = 8, 256, 128
+    pages = (1 << 31) // (H_kv * page * d) + 40
+    dtype = torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16
+    k, v = (torch.empty(pages, H_kv, page, d, dtype=dtype, device="cuda") for _ in range(2))
+    ids = [pages - 1, pages - 7, pages - 3]
+    table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([600], dtype=torch.int32, device="cuda")
+    h, cu = binding.PagedCache(k, v), _offsets([600])
+    new_k, new_v, q = _q(600, H_kv, d, 2), _q(600, H_kv, d, 3), _q(600, 16, d)
+    binding.paged_append(h, None, new_k, new_v, table, lens, cu_seqlens=cu)
+    stored = [torch.cat([t[i].transpose(0, 1) for i in ids])[:600].double() for t in (k, v)]
+    if kind == "bf16":
+        assert torch.equal(stored[0], new_k.double()) and torch.equal(stored[1], new_v.double())
+    last = torch.arange(1, 601, device="cuda")
+    o, lse = binding.paged_forward(h, q, table, lens, cu)
+    assert_attention(o, lse, *attention(q, *stored, 1.0 / math.sqrt(d), last))
+    o, lse = binding.paged_decode(h, q[599:], table, lens)
+    want = attention(q[599:], *stored, 1.0 / math.sqrt(d), last[599:])
+    assert_attention(o, lse, want[0], want[1], want[2].t())
 
 
 def _offsets(new):
