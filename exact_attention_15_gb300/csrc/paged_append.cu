@@ -33,15 +33,29 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// The scale divides (not its rounded inverse), so the stored value is the
-// nearest to x / scale.
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
-  uint2 w;
-  w.x = pack_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
-        pack_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16;
-  w.y = pack_e4m3x2(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale)) |
-        pack_e4m3x2(__fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale)) << 16;
-  *reinterpret_cast<uint2*>(p) = w;
+// x / s, rounded to nearest, from the rounded inverse of s: the product's residual
+// corrects it (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). For infinities and NaN the residual is NaN, and the
+// product stands. The inverse alone would now and then land on the other side of a
+// rounding border of e4m3; a division per value cost a sixth of the kernel's time
+// over an e4m3 cache.
+__device__ __forceinline__ float quotient(float x, float s, float inverse) {
+  const float q = x * inverse, r = __fmaf_rn(-q, s, x);
+  return r == r ? __fmaf_rn(r, inverse, q) : q;
+}
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale, float inverse) {
+  float y[8];
+  // (an inverse outside the normal numbers cannot be corrected)
+  const float size = fabsf(scale);
+  if (size > 1e-30f && size < 1e30f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], scale, inverse);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_e4m3x2(y[0], y[1]) | pack_e4m3x2(y[2], y[3]) << 16,
+                                            pack_e4m3x2(y[4], y[5]) | pack_e4m3x2(y[6], y[7]) << 16);
 }
 
 // 16 elements of a head: two runs of 8.
@@ -87,53 +101,65 @@ __device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x,
 // beside it: without the loads ahead 155 us, with a read of the angles from shared
 // memory for every part 158, with a warp or 64 threads per token 158 or more, with
 // registers held down for more CTAs 156 or more.
+//
+// W threads work on a token (a multiple of a head's 8 or 4, so that each keeps its
+// place in every head), kAppendThreads / W tokens in a CTA: with few heads a CTA per
+// token would leave most threads idle.
 constexpr int kAhead = 3;
+template <int W>
 __global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(const AppendParams p) {
-  __shared__ float2 cs[64];
-  const int t = blockIdx.x, tid = threadIdx.x;
+  __shared__ float2 shared_cs[kAppendThreads / W][64];
+  const int t = blockIdx.x * (kAppendThreads / W) + threadIdx.x / W, tid = threadIdx.x % W;
+  float2* cs = shared_cs[threadIdx.x / W];
   const PagedSeqs& s = p.s;
   grid_wait();
   grid_release();
   const int parts = (p.H_q + 2 * p.H_kv) * (p.d >> 4);
+  bool live = t < s.T;
   Part ahead[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    const int i = tid + k * kAppendThreads;
-    if (i < parts) ahead[k] = load_part(p, place_of(p, i), t);
+    const int i = tid + k * W;
+    if (live && i < parts) ahead[k] = load_part(p, place_of(p, i), t);
   }
-  if (t == 0) check_paged_seqs(s, tid, kAppendThreads);
-  int b = t;
-  SeqSpan span{t, 1};
-  if (s.cu_seqlens) {
-    // the last sequence that starts at or before row t
-    int lo = 0, hi = s.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
+  if (blockIdx.x == 0) check_paged_seqs(s, threadIdx.x, kAppendThreads);
+  int b = t, pos = 0, page = 0;
+  if (live) {
+    SeqSpan span{t, 1};
+    if (s.cu_seqlens) {
+      // the last sequence that starts at or before row t
+      int lo = 0, hi = s.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
+      }
+      b = lo;
+      span = seq_span(s.cu_seqlens, b, s.T, 0);
+      live = t >= span.start && t < span.start + span.len;  // else behind the last sequence
     }
-    b = lo;
-    span = seq_span(s.cu_seqlens, b, s.T, 0);
-    if (t < span.start || t >= span.start + span.len) return;  // behind the last sequence
+    pos = kv_len(s, b) - span.len + (t - span.start);
+    live = live && pos >= 0;  // else padding: the sequence is shorter than its rows
   }
-  const int pos = kv_len(s, b) - span.len + (t - span.start);
-  if (pos < 0) return;  // padding: the sequence is shorter than its rows
-  const int page = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + (pos >> s.page_shift));
+  if (live) {
+    page = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + (pos >> s.page_shift));
+    for (int i = tid; i < p.rotary_dim >> 1; i += W) {
+      double turns = __ldg(p.inv_freq + i) * 0.15915494309189533577;  // 1 / 2 pi
+      turns -= floor(turns);
+      const unsigned long long f = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+      const long long whole = static_cast<long long>(f * static_cast<unsigned long long>(pos));
+      // half turns in [-1, 1)
+      const float half = static_cast<float>(static_cast<int>(whole >> 32)) * (1.0f / 2147483648.0f);
+      float sn, c;
+      sincospif(half, &sn, &c);
+      cs[(i & 7) * (p.rotary_dim >> 4) + (i >> 3)] = make_float2(c, sn);
+    }
+  }
+  if (W <= 32) __syncwarp(); else __syncthreads();
+  if (!live) return;
   const bool page_ok = static_cast<unsigned>(page) < static_cast<unsigned>(s.num_pages);
   if (!page_ok && tid == 0) record_error(s.err, kErrPages);
   const int row = pos & ((1 << s.page_shift) - 1);
-  if (tid < p.rotary_dim >> 1) {
-    double turns = __ldg(p.inv_freq + tid) * 0.15915494309189533577;  // 1 / 2 pi
-    turns -= floor(turns);
-    const unsigned long long f = static_cast<unsigned long long>(turns * 18446744073709551616.0);
-    const long long whole = static_cast<long long>(f * static_cast<unsigned long long>(pos));
-    // half turns in [-1, 1)
-    const float half = static_cast<float>(static_cast<int>(whole >> 32)) * (1.0f / 2147483648.0f);
-    float sn, c;
-    sincospif(half, &sn, &c);
-    cs[(tid & 7) * (p.rotary_dim >> 4) + (tid >> 3)] = make_float2(c, sn);
-  }
-  __syncthreads();
   // A thread has the same place in every head, so its eight angles stay with it
   // (pair 8 j + e lies at e times the threads + j: neighbours read neighbours).
   float2 turn[8];
@@ -145,7 +171,7 @@ paged_append_kernel(const AppendParams p) {
       for (int e = 0; e < 8; ++e) turn[e] = cs[e * (p.rotary_dim >> 4) + j];
     }
   }
-  for (int k = 0, i = tid; i < parts; ++k, i += kAppendThreads) {
+  for (int k = 0, i = tid; i < parts; ++k, i += W) {
     const Place x = place_of(p, i);
     const Part w = k == 0 ? ahead[0] : k == 1 ? ahead[1] : k == 2 ? ahead[2] : load_part(p, x, t);
     float x0[8], x1[8];
@@ -180,10 +206,10 @@ paged_append_kernel(const AppendParams p) {
                         ((static_cast<size_t>(x.h) << s.page_shift) + row) * p.d;
       if (p.e4m3) {
         const float* sc = is_v ? p.v_scale : p.k_scale;
-        const float scale = sc ? __ldg(sc + x.h) : 1.0f;
+        const float scale = sc ? __ldg(sc + x.h) : 1.0f, inverse = __frcp_rn(scale);
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
-        store8_e4m3(dst + x.e0, x0, scale);
-        store8_e4m3(dst + x.e1, x1, scale);
+        store8_e4m3(dst + x.e0, x0, scale, inverse);
+        store8_e4m3(dst + x.e1, x1, scale, inverse);
       } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + at;
         store8(dst + x.e0, x0);
@@ -193,12 +219,29 @@ paged_append_kernel(const AppendParams p) {
   }
 }
 
+template <int W>
+cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  constexpr int kTokens = kAppendThreads / W;
+  return launch_chained(paged_append_kernel<W>, dim3((p.s.T + kTokens - 1) / kTokens), kAppendThreads, 0, stream,
+                        smem_set, p);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
   const int slot = prof_begin(kKPagedAppend, stream);
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = launch_chained(paged_append_kernel, dim3(p.s.T), kAppendThreads, 0, stream, smem_set, p);
+  const int parts = (p.H_q + 2 * p.H_kv) * (p.d >> 4);
+  // About four parts a thread (14,000 tokens of 28 heads of 64: 47 us with a CTA per
+  // token, 28.9 with two parts a thread, 26.9 with four; 17,000 of 6 heads: 46, 12.3,
+  // 11.8); few tokens take all the threads they can get.
+  const int want = (parts + 3) / 4;
+  const cudaError_t e = p.s.T < 304   ? launch<128>(p, stream)
+                        : want <= 8  ? launch<8>(p, stream)
+                        : want <= 16 ? launch<16>(p, stream)
+                        : want <= 32 ? launch<32>(p, stream)
+                        : want <= 64 ? launch<64>(p, stream)
+                                     : launch<128>(p, stream);
   prof_end(slot, stream);
   return e;
 }

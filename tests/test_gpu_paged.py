@@ -562,3 +562,27 @@ def test_compiled_calls_and_python_checks_agree():
         assert e.value.status == 4
     with pytest.raises(ctypes.ArgumentError):
         binding.paged_decode(h, q, c.table, c.kv_lens, scale="1")
+
+
+def test_append_divides_by_the_scale_exactly():
+    """e4m3 values are those of the 32-bit quotient, rounded to nearest: on scales of
+    many mantissas, on quotients at and next to the borders between two of e4m3's
+    values, and with scales outside the normal range of a rounded inverse."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    H_kv, d, n = 8, 64, 512
+    c = Cache([n], H_kv, d, 64, "e4m3")
+    grid = torch.arange(0, 127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()  # 0 .. 448
+    border = (grid[1:] + grid[:-1]) / 2
+    for mantissa in ([1.0] * H_kv, None, [1e-38, 3e-39, 2e38, 1e-31, 1e31, 1.5, 1.9999999, 1.0000001]):
+        if mantissa is None:
+            c.k_scale.copy_(torch.rand(H_kv, generator=g, device="cuda") + 1e-3)
+        else:
+            c.k_scale.copy_(torch.tensor(mantissa))
+        c.v_scale.copy_(c.k_scale)
+        pick = torch.randint(0, border.numel(), (n, H_kv, d), generator=g, device="cuda")
+        x = (border[pick] * c.k_scale[:, None]).to(torch.bfloat16)
+        x = torch.where(torch.rand(n, H_kv, d, generator=g, device="cuda") < 0.5, x, -x)
+        binding.paged_append(c.handle(), None, x, x, c.table, c.kv_lens, cu_seqlens=_offsets([n]))
+        want = (x.float() / c.k_scale[:, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+        assert torch.equal(as_int(c.get(c.k, 0, 0, n)) & 0x7f, as_int(want) & 0x7f)
+        assert torch.equal(c.get(c.v, 0, 0, n).float(), want.float())
