@@ -152,13 +152,24 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
 // Chunks of 16 query rows at most go to the streaming kernel, which reads each key
 // once per 16 rows and deals the keys out evenly; more rows to the tensor-core
 // kernel, whose tiles hold 128. The host knows the mean of the sequences' rows.
-bool streams(int T, int B, int group) {
+bool few_rows(int T, int B, int group) {
   return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
+}
+// So does little work, by its units (tiles of 64 keys of 16 rows, at most ten for
+// each CTA) and what the page table can hold: 20 new tokens of one prompt, 32 heads
+// on 8 (48 units), take 8.8 us there and 21.4 with the planning kernel and its tiles,
+// 256 (2080 units) 23.8 and 31.5, 512 (8256) 47.3 and 33.6.
+bool little_work(int T, int B, int group, int H_kv, long long keys) {
+  const long long chunks = (static_cast<long long>(T) * group + 15) / 16 + B;
+  const long long tiles = (keys + kStreamTile - 1) / kStreamTile;
+  return chunks * H_kv * tiles <= 10 * kStreamCtas;
 }
 
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
-  if (streams(T, B, group)) return stream_plan(d).total;
-  return fwd_plan(T, B, group, H_kv, d, e4m3).total;
+  const size_t stream = stream_plan(d).total;
+  if (few_rows(T, B, group)) return stream;
+  const size_t fwd = fwd_plan(T, B, group, H_kv, d, e4m3).total;
+  return fwd > stream ? fwd : stream;
 }
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
@@ -267,7 +278,8 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
   const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (!seqlens || streams(T, B, group))
+  if (!seqlens || few_rows(T, B, group) ||
+      little_work(T, B, group, c->H_kv, static_cast<long long>(max_pages) * c->page_size))
     return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, cs);
   return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
 }

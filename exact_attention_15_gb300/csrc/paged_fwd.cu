@@ -846,7 +846,8 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
 }
 
 // Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows
-// 8 y .. 8 y + 7 of tile x of the rest, one warp each.
+// 16 y .. 16 y + 15 of tile x of the rest, two for each warp.
+constexpr int kJoinRows = 16;
 template <int D>
 __global__ void __launch_bounds__(256)
 paged_fwd_join_kernel(const PagedFwdParams p) {
@@ -863,35 +864,37 @@ paged_fwd_join_kernel(const PagedFwdParams p) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) words[i] = p.tiles[3 * (waves * grid + x) + i];
   }
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int i = row >> 7, r = row & 127;
-  const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
-  if (tok_r >= p.tok_tile || tok >= t.n_new) return;
+  const int lane = threadIdx.x & 31;
   constexpr int kV = D / 32;
-  float acc[kV], m = -INFINITY, l = 0.0f;
+  for (int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5); row < (blockIdx.y + 1) * kJoinRows; row += 8) {
+    const int i = row >> 7, r = row & 127;
+    const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
+    if (tok_r >= p.tok_tile || tok >= t.n_new) continue;
+    float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-  for (int c = c0; c <= c1; ++c) {
-    const int4 share = p.shares[c];
-    if (share.x == share.y) continue;
-    const size_t at = (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-    if (ml.y == 0.0f) continue;  // a piece whose keys this row does not see leaves no O
-    const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
-    const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
-    m = top;
-    l = l * f + ml.y * g;
-    const float* src = p.part_o + at * D + lane * kV;
+    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+    for (int c = c0; c <= c1; ++c) {
+      const int4 share = p.shares[c];
+      if (share.x == share.y) continue;
+      const size_t at = (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+      if (ml.y == 0.0f) continue;  // a piece whose keys this row does not see leaves no O
+      const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
+      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
+      m = top;
+      l = l * f + ml.y * g;
+      const float* src = p.part_o + at * D + lane * kV;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + src[e] * g;
+      for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + src[e] * g;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const size_t to = static_cast<size_t>(t.row0) + tok;
+    const int head = t.h * p.group + r - tok_r * p.group;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
+#pragma unroll
+    for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t to = static_cast<size_t>(t.row0) + tok;
-  const int head = t.h * p.group + r - tok_r * p.group;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
-#pragma unroll
-  for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // One warp per row of queries.
@@ -933,7 +936,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained(paged_fwd_join_kernel<D>, dim3(p.grid, 2 * kTileM / 8), 256, 0, stream, smem_set, p);
+  e = launch_chained(paged_fwd_join_kernel<D>, dim3(p.grid, 2 * kTileM / kJoinRows), 256, 0, stream, smem_set, p);
   prof_end(slot, stream);
   return e;
 }
