@@ -14,7 +14,8 @@
 // Warp roles (160 threads): warps 0-3 each take 16 keys of a tile, S = Q K^T
 // and O += P V on mma.sync m16n8k16 with the online softmax in registers
 // (tcgen05 wants 128 rows; here there are 16 at most, and the tensor work is
-// small against the tile's bytes); warp 4 loads the tiles with TMA.
+// small against the tile's bytes); warp 4 walks the work, hands its pieces to the
+// others through a ring and loads the tiles with TMA.
 #include "paged.cuh"
 
 namespace attn {
@@ -24,6 +25,7 @@ namespace {
 constexpr int kTile = kStreamTile;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRing = 4;  // pieces that the loading warp can be ahead
 
 template <int D, bool FP8>
 struct StreamCfg {
@@ -37,8 +39,9 @@ struct StreamCfg {
   static constexpr int kMergeOff = kStages * 2 * kTileBytes;
   static constexpr int kMergeBytes = 16384;
   static constexpr int kMlOff = kMergeOff + kMergeBytes;
-  static constexpr int kBarOff = kMlOff + kWarps * 16 * 2 * 4;
-  static constexpr int kSmemBytes = kBarOff + 2 * kStages * 8;
+  static constexpr int kRingOff = kMlOff + kWarps * 16 * 2 * 4;
+  static constexpr int kBarOff = kRingOff + kRing * 48;
+  static constexpr int kSmemBytes = kBarOff + (2 * kStages + 2 * kRing + 1) * 8;
   // two CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
   static_assert(2 * (kSmemBytes + 1024) <= 233472, "shared memory of two CTAs");
 };
@@ -99,12 +102,15 @@ __device__ __forceinline__ int owner_of(long long total, int grid, long long u) 
 }
 
 // The piece of an item that a CTA works on.
-struct Piece {
-  int b, h, rc;      // sequence, KV head, row chunk
+struct __align__(16) Piece {
+  int b, h, rc;      // sequence (< 0: no piece more), KV head, row chunk
   int t0, t1;        // key tiles [t0, t1)
   int tiles;         // of the whole item
   int len, n, row0;  // keys; query rows of the sequence and the first of them
+  int slot;          // of the partial results, or -1: the piece is a whole item
+  int pad[2];
 };
+static_assert(sizeof(Piece) == 48, "a place of the ring");
 
 // Walks the units [u, end) of a CTA piece by piece.
 struct Walk {
@@ -167,7 +173,10 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   extern __shared__ __align__(1024) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + Cfg::kMergeOff);
   float* ml = reinterpret_cast<float*>(smem + Cfg::kMlOff);  // [warp][16][2]
+  Piece* ring = reinterpret_cast<Piece*>(smem + Cfg::kRingOff);
   const uint32_t full = smem_addr(smem + Cfg::kBarOff), empty = full + 8 * Cfg::kStages;
+  const uint32_t given = empty + 8 * Cfg::kStages, taken = given + 8 * kRing;  // of the ring
+  const uint32_t merge_free = taken + 8 * kRing;  // the merge buffer has been read
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long lim = p.wait_limit;
 
@@ -176,49 +185,52 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, kWarps);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(given + 8 * i, 1);
+      mbar_init(taken + 8 * i, kWarps);
+    }
+    mbar_init(merge_free, kWarps);
     fence_barrier_init();
   }
+  const int cta = blockIdx.x;
+  __syncthreads();
   grid_wait();
   grid_release();
-  // The units before each sequence: every lane sums a run of sequences, the sums
-  // are scanned, and the run that holds this CTA's first unit is walked. Each
-  // warp does so for itself, so none waits for another.
-  const int cta = blockIdx.x;
-  const int run = (p.s.B + 31) >> 5;
-  long long before, total;
-  {
-    const int b1 = min(p.s.B, (lane + 1) * run);
-    long long mine = 0;
-#pragma unroll 4
-    for (int b = lane * run; b < b1; ++b) mine += units_of(p, b, R);
-    before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-    }
-    total = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
-  }
-  const int grid = busy_ctas(total, gridDim.x);
-  Walk w;
-  w.u = w.end = w.base = 0;
-  w.b = 0;
-  if (cta < grid) {
-    w.u = first_unit(total, grid, cta);
-    w.end = first_unit(total, grid, cta + 1);
-    // the last run that starts at or before the first unit (lane 0's does)
-    const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= w.u));
-    w.b = at * run;
-    w.base = __shfl_sync(0xffffffffu, before, at);
-  }
-  __syncthreads();
-  Piece x;
   int stage = 0;
   uint32_t phase = 0;
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ TMA producer
+    // The units before each sequence: every lane sums a run of sequences, the sums
+    // are scanned, and the run that holds this CTA's first unit is walked.
+    const int run = (p.s.B + 31) >> 5;
+    long long before, total;
+    {
+      const int b1 = min(p.s.B, (lane + 1) * run);
+      long long mine = 0;
+#pragma unroll 4
+      for (int b = lane * run; b < b1; ++b) mine += units_of(p, b, R);
+      before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      total = __shfl_sync(0xffffffffu, before, 31);
+      before -= mine;
+    }
+    const int grid = busy_ctas(total, gridDim.x);
+    Walk w;
+    w.u = w.end = w.base = 0;
+    w.b = 0;
+    if (cta < grid) {
+      w.u = first_unit(total, grid, cta);
+      w.end = first_unit(total, grid, cta + 1);
+      // the last run that starts at or before the first unit (lane 0's does)
+      const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= w.u));
+      w.b = at * run;
+      w.base = __shfl_sync(0xffffffffu, before, at);
+    }
     // Lane (page j of the tile, K or V, block) issues one box per tile.
     const int box_shift = min(p.s.page_shift, 6);
     const int n_box = kTile >> box_shift;  // pages (or the part of one) in a tile
@@ -233,8 +245,34 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    bool ok = true;
-    while (ok && next_piece<R>(p, w, x)) {
+    bool ok = true, split_head = false;
+    Piece x;
+    // Gives piece number k to the other warps.
+    auto give = [&](int k) {
+      const int at = k % kRing;
+      if (k >= kRing && !mbar_wait_warp(taken + 8 * at, ((k / kRing) - 1) & 1, lim)) return false;
+      if (lane == 0) {
+        ring[at] = x;
+        mbar_arrive(given + 8 * at);
+      }
+      __syncwarp();
+      return true;
+    };
+    int nth = 0;
+    for (; ok && next_piece<R>(p, w, x); ++nth) {
+      // a CTA's first and last piece can be parts of an item
+      const bool whole = x.t1 - x.t0 == x.tiles;
+      x.slot = whole ? -1 : 2 * cta + (nth == 0 ? 0 : 1);
+      if (!(ok = give(nth))) break;
+      if (x.t0 == 0 && !whole) {
+        // for the join: the item begins in this CTA and ends in a later one
+        split_head = true;
+        if (lane == 0) {
+          const int end = owner_of(total, grid, w.u + (x.tiles - x.t1) - 1);
+          p.heads[2 * cta] = make_int4(end - cta + 1, x.slot, x.row0, min(R, x.n * p.group - x.rc * R));
+          p.heads[2 * cta + 1] = make_int4(x.h, x.rc * R, 0, 0);
+        }
+      }
       auto page_at = [&](int t) {
         const int key = t * kTile + box_row;
         return has_box && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift) : 0;
@@ -257,8 +295,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (++stage == Cfg::kStages) { stage = 0; phase ^= 1; }
       }
     }
+    if (ok) {
+      x.b = -1;
+      ok = give(nth);
+    }
     if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
     // off the way of the loads: what no work unit covers
+    if (!split_head && lane == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
     if (cta == 0) check_paged_seqs(p.s, lane, 32);
     for (int b = cta; b < p.s.B; b += gridDim.x)
       if (kv_len(p.s, b) == 0) write_empty<D>(p, new_span(p.s, b), lane);
@@ -286,9 +329,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   };
   constexpr int NB = R / 8;  // blocks of 8 query rows
   // Query rows as B fragments: row nb * 8 + ar. The next piece's rows are loaded
-  // before the merge of the last one, which hides their latency (after it with 16
-  // rows of 128 columns, where the registers do not hold both).
-  constexpr bool kEarlyQ = R * D <= 1024;
+  // before the merge of the last one, which hides their latency.
   uint32_t qb[NB][D / 16][2];
   auto load_q = [&](const Piece& x) {
     const int rows = min(R, x.n * p.group - x.rc * R);
@@ -314,9 +355,26 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
     }
   };
-  bool ok = true, split_head = false;
-  int nth = 0;  // pieces done
-  bool have = next_piece<R>(p, w, x);
+  bool ok = true;
+  Piece x;
+  int nth = 0;  // pieces taken
+  auto take = [&]() {  // the next piece, in every lane
+    const int at = nth % kRing;
+    if (!mbar_wait_warp(given + 8 * at, (nth / kRing) & 1, lim)) {
+      if (lane == 0) record_error(p.s.err, kErrTimeout);
+      return false;
+    }
+    const int4* src = reinterpret_cast<const int4*>(&ring[at]);
+    int4* dst = reinterpret_cast<int4*>(&x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) dst[i] = src[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(taken + 8 * at);
+    ++nth;
+    return x.b >= 0;
+  };
+  uint32_t merges = 0;  // uses of the merge buffer
+  bool have = take();
   if (have) load_q(x);
   while (have) {
     const int rows = min(R, x.n * p.group - x.rc * R);  // of this chunk
@@ -505,78 +563,45 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     // ---- merge of the four warps' keys
     const Piece y = x;
-    const long long done = w.u;  // the unit after this piece
-    if constexpr (kEarlyQ) {
-      have = next_piece<R>(p, w, x);
-      if (have) load_q(x);
-    }
+    have = take();
+    if (have) load_q(x);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
-        if (ar == 0)
-          *reinterpret_cast<float2*>(ml + (warp * 16 + nb * 8 + 2 * qd + e) * 2) = make_float2(m[nb][e], l[nb][e]);
-      }
-    named_bar_sync(1, 32 * kWarps);
-    const bool whole = y.t1 - y.t0 == y.tiles;
-    const int slot = 2 * cta + (nth++ == 0 ? 0 : 1);  // a CTA's first and last piece can be parts
-    if (y.t0 == 0 && !whole) {
-      // for the join: the item begins in this CTA and ends in a later one
-      split_head = true;
-      if (tid == 0) {
-        const int end = owner_of(total, grid, done + (y.tiles - y.t1) - 1);
-        p.heads[2 * cta] = make_int4(end - cta + 1, slot, y.row0, rows);
-        p.heads[2 * cta + 1] = make_int4(y.h, y.rc * R, 0, 0);
-      }
-    }
+    const bool whole = y.slot < 0;
     // O passes through shared memory in runs of kCols columns, each 8-column
-    // group moved within its row so that the warps' stores spread over the banks
-    // (each thread's own row of the result: its statistics are read before the
-    // second barrier, after which the next piece may write its own)
+    // group moved within its row so that the warps' stores spread over the banks.
+    // The warps leave their sums as they are; who adds them up knows the factors.
     constexpr int kCols = D * R * kWarps * 4 <= Cfg::kMergeBytes ? D : Cfg::kMergeBytes / (R * kWarps * 4);
     constexpr int kPerRow = kCols / 8;  // threads per row of the result
     static_assert(R * kPerRow <= 32 * kWarps, "one 8-column group per thread");
-    const int ro = tid / kPerRow, g8 = tid % kPerRow;
-    // Lane r works out row r: its maximum and sum over the warps, and the factor of
-    // this warp's part. The lanes that need a row's values take them from there.
-    float row_top = -INFINITY, row_sum = 0.0f, row_mine;
-    {
-      const int r = lane & (R - 1);
-      float2 w[kWarps];
-#pragma unroll
-      for (int g = 0; g < kWarps; ++g) {
-        w[g] = *reinterpret_cast<const float2*>(ml + (g * 16 + r) * 2);
-        row_top = fmaxf(row_top, w[g].x);
-      }
-      const float mb = row_top == -INFINITY ? 0.0f : row_top;
-#pragma unroll
-      for (int g = 0; g < kWarps; ++g) {
-        w[g].x = ex2_approx(w[g].x - mb);
-        row_sum += w[g].y * w[g].x;
-      }
-      row_mine = warp < 2 ? (warp == 0 ? w[0].x : w[1].x) : (warp == 2 ? w[2].x : w[3].x);
-    }
-    const float top = __shfl_sync(0xffffffffu, row_top, ro & (R - 1));
-    const float sum = __shfl_sync(0xffffffffu, row_sum, ro & (R - 1));
-    float mine[NB][2];  // factors of this lane's accumulator columns
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) mine[nb][e] = __shfl_sync(0xffffffffu, row_mine, nb * 8 + 2 * qd + e);
+    const int r = tid / kPerRow, g8 = tid % kPerRow;
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += kCols) {
-      if (c0 > 0) named_bar_sync(1, 32 * kWarps);
+      // the buffer's last readers are done
+      if (merges > 0 && ok && !mbar_wait_warp(merge_free, (merges - 1) & 1, lim)) {
+        if (lane == 0) record_error(p.s.err, kErrTimeout);
+        ok = false;
+      }
+      ++merges;
+      if (c0 == 0 && ar == 0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(ml + (warp * 16 + nb * 8 + 2 * qd + e) * 2) = make_float2(m[nb][e], l[nb][e]);
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = mine[nb][e];
           float* dst = merge + (warp * R + nb * 8 + 2 * qd + e) * kCols;
 #pragma unroll
           for (int j = c0 / 16; j < (c0 + kCols) / 16; ++j) {
-            const float a = acc[nb][j][e] * f, b = acc[nb][j][e + 2] * f;
+            const float a = acc[nb][j][e], b = acc[nb][j][e + 2];
             const int col = j * 16 - c0;
             if constexpr (FP8) {
               *reinterpret_cast<float2*>(dst + ((col + 2 * ar) ^ (qd << 3))) = make_float2(a, b);
@@ -587,8 +612,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           }
         }
       named_bar_sync(1, 32 * kWarps);
-      if (ro < rows) {
-        const int r = ro;
+      if (r < rows) {
+        float2 w[kWarps];
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kWarps; ++g) {
+          w[g] = *reinterpret_cast<const float2*>(ml + (g * 16 + r) * 2);
+          top = fmaxf(top, w[g].x);
+        }
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.0f;
@@ -597,8 +628,10 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           const float* src = merge + (g * R + r) * kCols + ((g8 * 8) ^ (((r >> 1) & 3) << 3));
           const float4 a = *reinterpret_cast<const float4*>(src);
           const float4 d4 = *reinterpret_cast<const float4*>(src + 4);
-          o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
-          o[4] += d4.x; o[5] += d4.y; o[6] += d4.z; o[7] += d4.w;
+          const float f = ex2_approx(w[g].x - (top == -INFINITY ? 0.0f : top));
+          sum += w[g].y * f;
+          o[0] += a.x * f; o[1] += a.y * f; o[2] += a.z * f; o[3] += a.w * f;
+          o[4] += d4.x * f; o[5] += d4.y * f; o[6] += d4.z * f; o[7] += d4.w * f;
         }
         const float f = whole ? (sum == 0.0f ? 0.0f : v_scale / sum) : v_scale;
 #pragma unroll
@@ -615,20 +648,17 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             p.lse[row * p.lse_row + head * p.lse_head] =
                 sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
         } else {
-          float* dst = p.part_o + (static_cast<size_t>(slot) * 16 + r) * D + c0 + g8 * 8;
+          float* dst = p.part_o + (static_cast<size_t>(y.slot) * 16 + r) * D + c0 + g8 * 8;
           *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
           if (c0 == 0 && g8 == 0)
-            *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(top, sum);
+            *reinterpret_cast<float2*>(p.part_ml + (y.slot * 16 + r) * 2) = make_float2(top, sum);
         }
       }
-    }
-    if constexpr (!kEarlyQ) {
-      have = next_piece<R>(p, w, x);
-      if (have) load_q(x);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merge_free);
     }
   }
-  if (!split_head && tid == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
 }
 
 // Merges the pieces of split items in their order. CTA (c, y) does kJoinRows query
