@@ -108,7 +108,7 @@ struct AppendParams {
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
 
 // ---- streaming attention: few query rows per sequence
-constexpr int kStreamCtas = 304;  // CTAs the workspace holds partial results for
+constexpr int kStreamCtas = 456;  // CTAs the workspace holds partial results for
 constexpr int kStreamTile = 64;   // keys per tile
 
 struct StreamParams {
@@ -123,11 +123,11 @@ struct StreamParams {
   int4* heads;            // workspace: [kStreamCtas, 2] where the pieces of a split item begin
   float* part_ml;         // workspace: [2 kStreamCtas, 16, 2]
   float* part_o;          // workspace: [2 kStreamCtas, 16, d]
-  int grid;
+  int grid;  // set by the launch
   long long wait_limit;
 };
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
-                                int d, int rows, bool e4m3, cudaStream_t stream);
+                                int d, int rows, bool e4m3, int n_sm, cudaStream_t stream);
 
 // ---- tensor-core attention: many query rows per sequence
 constexpr int kFwdSms = 152;               // CTAs that the workspace is planned for

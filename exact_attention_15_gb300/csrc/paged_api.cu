@@ -155,14 +155,14 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
 bool few_rows(int T, int B, int group) {
   return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
 }
-// So does little work, by its units (tiles of 64 keys of 16 rows, at most ten for
-// each CTA) and what the page table can hold: 20 new tokens of one prompt, 32 heads
+// So does little work, by its units (tiles of 64 keys of 16 rows, at most 20 for
+// each SM) and what the page table can hold: 20 new tokens of one prompt, 32 heads
 // on 8 (48 units), take 8.8 us there and 21.4 with the planning kernel and its tiles,
 // 256 (2080 units) 23.8 and 31.5, 512 (8256) 47.3 and 33.6.
 bool little_work(int T, int B, int group, int H_kv, long long keys) {
   const long long chunks = (static_cast<long long>(T) * group + 15) / 16 + B;
   const long long tiles = (keys + kStreamTile - 1) / kStreamTile;
-  return chunks * H_kv * tiles <= 10 * kStreamCtas;
+  return chunks * H_kv * tiles <= 3040;
 }
 
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
@@ -199,11 +199,10 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.heads = reinterpret_cast<int4*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
-  p.grid = 2 * dev.n_sm < kStreamCtas ? 2 * dev.n_sm : kStreamCtas;
   p.wait_limit = dev.wait_limit;
   // 8 rows where a sequence's rows of one KV head fill no more
   const int chunk = static_cast<long long>(seqs.T) * p.group <= 8ll * seqs.B ? 8 : 16;
-  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, cs) == cudaSuccess
+  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, dev.n_sm, cs) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }

@@ -27,23 +27,25 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRing = 4;  // pieces that the loading warp can be ahead
 
-template <int D, bool FP8>
+template <int D, int R, bool FP8>
 struct StreamCfg {
   static constexpr int kEs = FP8 ? 1 : 2;
+  // CTAs on an SM: three where the registers and shorter tiles allow it
+  static constexpr int kCtas = R == 8 && D * kEs <= 128 ? 3 : 2;
   // a tile is kept as blocks of 64 rows x (at most) 128 bytes, swizzled
   static constexpr int kRowBytes = D * kEs < 128 ? D * kEs : 128;
   static constexpr int kBlocks = D * kEs / kRowBytes;
   static constexpr int kBlockBytes = kTile * kRowBytes;
   static constexpr int kTileBytes = kBlocks * kBlockBytes;  // K or V
-  static constexpr int kStages = kTileBytes == 16384 ? 3 : 6;
+  static constexpr int kStages = kCtas == 3 ? 49152 / (2 * kTileBytes) : kTileBytes == 16384 ? 3 : 6;
   static constexpr int kMergeOff = kStages * 2 * kTileBytes;
   static constexpr int kMergeBytes = 16384;
   static constexpr int kMlOff = kMergeOff + kMergeBytes;
   static constexpr int kRingOff = kMlOff + kWarps * 16 * 2 * 4;
   static constexpr int kBarOff = kRingOff + kRing * 48;
   static constexpr int kSmemBytes = kBarOff + (2 * kStages + 2 * kRing + 1) * 8;
-  // two CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
-  static_assert(2 * (kSmemBytes + 1024) <= 233472, "shared memory of two CTAs");
+  // the CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
+  static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -166,10 +168,10 @@ __device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows,
 }
 
 template <int D, int R, bool FP8>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, StreamCfg<D, R, FP8>::kCtas)
 paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const StreamParams p) {
-  using Cfg = StreamCfg<D, FP8>;
+  using Cfg = StreamCfg<D, R, FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + Cfg::kMergeOff);
   float* ml = reinterpret_cast<float*>(smem + Cfg::kMlOff);  // [warp][16][2]
@@ -755,12 +757,14 @@ paged_join_kernel(const StreamParams p) {
 }
 
 template <int D, int R, bool FP8>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p, int n_sm,
                    cudaStream_t stream) {
+  using Cfg = StreamCfg<D, R, FP8>;
+  p.grid = min(Cfg::kCtas * n_sm, kStreamCtas);
   static std::atomic<unsigned long long> smem_set{0};
   int slot = prof_begin(kKPagedDecode, stream);
   cudaError_t e = launch_chained(paged_stream_kernel<D, R, FP8>, dim3(p.grid), kThreads,
-                                 StreamCfg<D, FP8>::kSmemBytes, stream, smem_set, tk, tv, p);
+                                 Cfg::kSmemBytes, stream, smem_set, tk, tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
@@ -772,13 +776,13 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const StreamPar
 }  // namespace
 
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
-                                int d, int rows, bool e4m3, cudaStream_t stream) {
+                                int d, int rows, bool e4m3, int n_sm, cudaStream_t stream) {
   if (d == 128) {
-    if (rows == 8) return e4m3 ? launch<128, 8, true>(tk, tv, p, stream) : launch<128, 8, false>(tk, tv, p, stream);
-    return e4m3 ? launch<128, 16, true>(tk, tv, p, stream) : launch<128, 16, false>(tk, tv, p, stream);
+    if (rows == 8) return e4m3 ? launch<128, 8, true>(tk, tv, p, n_sm, stream) : launch<128, 8, false>(tk, tv, p, n_sm, stream);
+    return e4m3 ? launch<128, 16, true>(tk, tv, p, n_sm, stream) : launch<128, 16, false>(tk, tv, p, n_sm, stream);
   }
-  if (rows == 8) return e4m3 ? launch<64, 8, true>(tk, tv, p, stream) : launch<64, 8, false>(tk, tv, p, stream);
-  return e4m3 ? launch<64, 16, true>(tk, tv, p, stream) : launch<64, 16, false>(tk, tv, p, stream);
+  if (rows == 8) return e4m3 ? launch<64, 8, true>(tk, tv, p, n_sm, stream) : launch<64, 8, false>(tk, tv, p, n_sm, stream);
+  return e4m3 ? launch<64, 16, true>(tk, tv, p, n_sm, stream) : launch<64, 16, false>(tk, tv, p, n_sm, stream);
 }
 
 }  // namespace attn
