@@ -55,18 +55,18 @@ __device__ __forceinline__ void check_paged_seqs(const PagedSeqs& s, int tid, in
 // Launches a kernel that calls grid_wait() in every thread before it touches
 // memory: its launch and set-up overlap the end of the grid before it. The
 // shared-memory size is set once per device.
-template <typename... Args>
-cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                           std::atomic<unsigned long long>& smem_set, const Args&... args) {
+template <auto Kernel, typename... Args>
+cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
   if (smem > 48 * 1024) {
+    static std::atomic<unsigned long long> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
-    if (!(smem_set.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
-      smem_set.fetch_or(bit, std::memory_order_relaxed);
+      ready.fetch_or(bit, std::memory_order_relaxed);
     }
   }
   cudaLaunchAttribute attr;
@@ -79,7 +79,7 @@ cudaError_t launch_chained(void (*kernel)(Args...), dim3 grid, int threads, int 
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, Kernel, args...);
 }
 
 // A power of two that brings a row whose largest magnitude is `top` to [1, 2) when

@@ -221,10 +221,8 @@ paged_append_kernel(const AppendParams p) {
 
 template <int W>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
   constexpr int kTokens = kAppendThreads / W;
-  return launch_chained(paged_append_kernel<W>, dim3((p.s.T + kTokens - 1) / kTokens), kAppendThreads, 0, stream,
-                        smem_set, p);
+  return launch_chained<paged_append_kernel<W>>(dim3((p.s.T + kTokens - 1) / kTokens), kAppendThreads, 0, stream, p);
 }
 
 }  // namespace

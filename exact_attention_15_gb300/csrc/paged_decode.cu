@@ -197,7 +197,6 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const int cta = blockIdx.x;
   __syncthreads();
   grid_wait();
-  grid_release();
   int stage = 0;
   uint32_t phase = 0;
 
@@ -663,97 +662,110 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
 }
 
-// Merges the pieces of split items in their order. CTA (c, y) does kJoinRows query
-// rows of the item that begins in the streaming kernel's CTA c and ends in a later
-// one; there are fewer such items than CTAs. Four warps share a row, each takes
-// every fourth piece with a running maximum. Eight CTAs per item: with 16 rows one
-// CTA per row starts 1.5 us later, and with 8 rows half as many CTAs, of more
-// warps each, join the pieces of a long sequence 2 us later.
-template <int D, int kJoinRows>
-__global__ void __launch_bounds__(128 * kJoinRows)
-paged_join_kernel(const StreamParams p) {
-  __shared__ float sh_o[kJoinRows][4][D];
-  __shared__ float2 sh_ml[kJoinRows][4];
-  grid_wait();
-  grid_release();
-  const int c = blockIdx.x, part = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int x = threadIdx.x & 127, at_row = threadIdx.x >> 7, r = blockIdx.y * kJoinRows + at_row;
-  const int4 a = p.heads[2 * c], d = p.heads[2 * c + 1];
-  const int pieces = a.x, slot0 = a.y, row0 = a.z, rows = a.w;
-  if (pieces == 0) return;
+// Sums pieces part, part + step, ... of an item's row r: maximum, sum and the lane's
+// D / 32 columns of O. Four pieces at a time, all their loads before the first is
+// used (a place behind the last piece loads the last again, with no weight).
+template <int D>
+__device__ __forceinline__ void sum_pieces(const StreamParams& p, int c, int pieces, int slot0, int r, int part,
+                                           int step, int lane, float& m, float& l, float (&acc)[D / 32]) {
   constexpr int kV = D / 32;
-  float acc[kV], m = -INFINITY, l = 0.0f;
+  const auto* ml_at = reinterpret_cast<const float2*>(p.part_ml) + r;
+  const float* o_at = p.part_o + static_cast<size_t>(r) * D + lane * kV;
+  m = -INFINITY;
+  l = 0.0f;
 #pragma unroll
   for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+  for (int i0 = part; i0 < pieces; i0 += 4 * step) {
+    float2 ml[4];
+    float o[4][kV];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = min(i0 + step * k, pieces - 1);
+      const int slot = i == 0 ? slot0 : 2 * (c + i);
+      ml[k] = ml_at[slot * 16];
+      const float* src = o_at + static_cast<size_t>(slot) * 16 * D;
+      if constexpr (kV == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[k][0] = v.x; o[k][1] = v.y; o[k][2] = v.z; o[k][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[k][0] = v.x; o[k][1] = v.y;
+      }
+    }
+    const float before = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = fmaxf(m, ml[k].x);
+    const float bias = m == -INFINITY ? 0.0f : m, f = ex2_approx(before - bias);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool live = i0 + step * k < pieces;
+      const float g = ex2_approx(ml[k].x - bias);
+      l += live ? ml[k].y * g : 0.0f;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] += live ? o[k][e] * g : 0.0f;
+    }
+  }
+}
+
+// Merges the pieces of split items in their order. CTA (c, y) does some query rows of
+// the item that begins in the streaming kernel's CTA c and ends in a later one; there
+// are fewer such items than CTAs. kShare warps share a row: four where there are fewer
+// items than SMs and so many pieces of each (with one, the pieces of a long sequence
+// are joined 3 us later), one else, which takes fewer CTAs (32 ragged sequences of 16
+// heads of 64: 30.6 us with four, 29.2 with one).
+//
+// Neither this kernel nor the streaming one lets the next grid launch early: the
+// next streaming kernel's CTAs would find some SMs still full, and two of three would
+// run there to the end (37 us for the same sequences).
+template <int D, int kRows, int kShare>
+__global__ void __launch_bounds__(32 * kRows * kShare)
+paged_join_kernel(const StreamParams p) {
+  __shared__ float sh_o[kShare > 1 ? kRows : 1][kShare][D];
+  __shared__ float2 sh_ml[kShare > 1 ? kRows : 1][kShare];
+  grid_wait();
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, part = warp % kShare, lane = threadIdx.x & 31;
+  const int at_row = warp / kShare, r = blockIdx.y * kRows + at_row;
+  const int4 a = p.heads[2 * c], d = p.heads[2 * c + 1];
+  const int pieces = a.x, rows = a.w;
+  if (pieces == 0) return;
+  constexpr int kV = D / 32;
+  float acc[kV], m, l;
   if (r < rows) {
-    // four pieces at a time, all their loads before the first is used (a place
-    // behind the last piece loads the last again, with no weight)
-    const auto* ml_at = reinterpret_cast<const float2*>(p.part_ml) + r;
-    const float* o_at = p.part_o + static_cast<size_t>(r) * D + lane * kV;
-    for (int i0 = part; i0 < pieces; i0 += 16) {
-      float2 ml[4];
-      float o[4][kV];
+    sum_pieces<D>(p, c, pieces, a.y, r, part, kShare, lane, m, l, acc);
+    if constexpr (kShare > 1) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = min(i0 + 4 * k, pieces - 1);
-        const int slot = i == 0 ? slot0 : 2 * (c + i);
-        ml[k] = ml_at[slot * 16];
-        const float* src = o_at + static_cast<size_t>(slot) * 16 * D;
-        if constexpr (kV == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          o[k][0] = v.x; o[k][1] = v.y; o[k][2] = v.z; o[k][3] = v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          o[k][0] = v.x; o[k][1] = v.y;
-        }
-      }
-      const float before = m;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m = fmaxf(m, ml[k].x);
-      const float bias = m == -INFINITY ? 0.0f : m, f = ex2_approx(before - bias);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] *= f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool live = i0 + 4 * k < pieces;
-        const float g = ex2_approx(ml[k].x - bias);
-        l += live ? ml[k].y * g : 0.0f;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] += live ? o[k][e] * g : 0.0f;
-      }
+      for (int e = 0; e < kV; ++e) sh_o[at_row][part][lane * kV + e] = acc[e];
+      if (lane == 0) sh_ml[at_row][part] = make_float2(m, l);
     }
   }
+  if constexpr (kShare > 1) __syncthreads();
+  if (r >= rows || part > 0) return;
+  if constexpr (kShare > 1) {
+    float top = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < kV; ++e) sh_o[at_row][part][lane * kV + e] = acc[e];
-  if (lane == 0) sh_ml[at_row][part] = make_float2(m, l);
-  __syncthreads();
-  if (r >= rows || x > D / 2) return;
-  const float2* ml = sh_ml[at_row];
-  float top = -INFINITY, sum = 0.0f, f[4];
+    for (int g = 0; g < kShare; ++g) top = fmaxf(top, sh_ml[at_row][g].x);
+    l = 0.0f;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) top = fmaxf(top, ml[g].x);
+    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    f[g] = ex2_approx(ml[g].x - (top == -INFINITY ? 0.0f : top));
-    sum += ml[g].y * f[g];
+    for (int g = 0; g < kShare; ++g) {
+      const float f = ex2_approx(sh_ml[at_row][g].x - (top == -INFINITY ? 0.0f : top));
+      l += sh_ml[at_row][g].y * f;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] += sh_o[at_row][g][lane * kV + e] * f;
+    }
+    m = top;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int rr = d.y + r, tok = rr / p.group, head = d.x * p.group + rr - tok * p.group;
-  const size_t row = static_cast<size_t>(row0) + tok;
-  if (x < D / 2) {
-    const int e = 2 * x;
-    float v[2] = {0.0f, 0.0f};
+  const size_t row = static_cast<size_t>(a.z) + tok;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D + lane * kV);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      v[0] += sh_o[at_row][g][e] * f[g];
-      v[1] += sh_o[at_row][g][e + 1] * f[g];
-    }
-    reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row * p.H_q + head) * D)[x] =
-        pack_bf16x2(v[0] * inv, v[1] * inv);
-  } else {
-    p.lse[row * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
-  }
+  for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) p.lse[row * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int D, int R, bool FP8>
@@ -761,14 +773,17 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p,
                    cudaStream_t stream) {
   using Cfg = StreamCfg<D, R, FP8>;
   p.grid = min(Cfg::kCtas * n_sm, kStreamCtas);
-  static std::atomic<unsigned long long> smem_set{0};
   int slot = prof_begin(kKPagedDecode, stream);
-  cudaError_t e = launch_chained(paged_stream_kernel<D, R, FP8>, dim3(p.grid), kThreads,
-                                 Cfg::kSmemBytes, stream, smem_set, tk, tv, p);
+  cudaError_t e = launch_chained<paged_stream_kernel<D, R, FP8>>(dim3(p.grid), kThreads,
+                                 Cfg::kSmemBytes, stream, tk, tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained(paged_join_kernel<D, R / 8>, dim3(p.grid, 8), 128 * (R / 8), 0, stream, smem_set, p);
+  if (static_cast<long long>(p.s.B) * p.H_kv < n_sm)
+    e = launch_chained<paged_join_kernel<D, R / 8, 4>>(dim3(p.grid, 8), 128 * (R / 8), 0, stream, p);
+  else
+    
+    e = launch_chained<paged_join_kernel<D, 4, 1>>(dim3(p.grid, R / 4), 128, 0, stream, p);
   prof_end(slot, stream);
   return e;
 }

@@ -289,7 +289,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = bars->tmem_base;
   const long long lim = p.wait_limit;
   grid_wait();
-  grid_release();
 
   // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168.
   if (warp < 4) {
@@ -852,7 +851,6 @@ template <int D>
 __global__ void __launch_bounds__(256)
 paged_fwd_join_kernel(const PagedFwdParams p) {
   grid_wait();
-  grid_release();
   const int total = p.tile_start[p.s.B], grid = p.grid, x = blockIdx.x;
   const int2 own = p.rest_owners[x];  // the CTAs that hold its first and its last key tile
   const int waves = total / grid, rest = total - waves * grid;
@@ -922,21 +920,20 @@ queries_f16_kernel(const uint2* q, uint2* q16, float* q_up, long long rows) {
 template <int D, bool E4M3>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& to, const PagedFwdParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
   // sorting compares every pair of sequences and keeps them in shared memory
   const int sort = p.s.B <= 1024;
   int slot = prof_begin(kKPagedPlan, stream);
-  cudaError_t e = launch_chained(paged_plan_kernel, dim3(1), 1024,
-                                 sort ? (3 * p.s.B + 1) * static_cast<int>(sizeof(int)) : 0, stream, smem_set, p, sort);
+  cudaError_t e = launch_chained<paged_plan_kernel>(dim3(1), 1024,
+                                 sort ? (3 * p.s.B + 1) * static_cast<int>(sizeof(int)) : 0, stream, p, sort);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  e = launch_chained(paged_fwd_kernel<D, E4M3>, dim3(p.grid), 384, PagedFwdCfg<D, E4M3>::kSmemBytes, stream, smem_set, tq, tk,
+  e = launch_chained<paged_fwd_kernel<D, E4M3>>(dim3(p.grid), 384, PagedFwdCfg<D, E4M3>::kSmemBytes, stream, tq, tk,
                      tv, to, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained(paged_fwd_join_kernel<D>, dim3(p.grid, 2 * kTileM / kJoinRows), 256, 0, stream, smem_set, p);
+  e = launch_chained<paged_fwd_join_kernel<D>>(dim3(p.grid, 2 * kTileM / kJoinRows), 256, 0, stream, p);
   prof_end(slot, stream);
   return e;
 }
@@ -952,13 +949,12 @@ cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const
 
 cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,
                                cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
   const int slot = prof_begin(kKPagedQueries, stream);
   const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
   const uint2* from = static_cast<const uint2*>(q);
   uint2* to = static_cast<uint2*>(q16);
-  const cudaError_t e = d == 128 ? launch_chained(queries_f16_kernel<128>, grid, 256, 0, stream, smem_set, from, to, q_up, rows)
-                                 : launch_chained(queries_f16_kernel<64>, grid, 256, 0, stream, smem_set, from, to, q_up, rows);
+  const cudaError_t e = d == 128 ? launch_chained<queries_f16_kernel<128>>(grid, 256, 0, stream, from, to, q_up, rows)
+                                 : launch_chained<queries_f16_kernel<64>>(grid, 256, 0, stream, from, to, q_up, rows);
   prof_end(slot, stream);
   return e;
 }
