@@ -60,7 +60,6 @@ struct PagedFwdCfg {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-static_assert(kFwdListed <= 1024, "one thread of the planning kernel per listed tile");
 struct __align__(16) PagedTile {
   int b, h;        // sequence (< 0 ends the list), KV head
   int row0;        // first packed row of the sequence
@@ -96,17 +95,18 @@ __device__ __forceinline__ int keys_seen(const PagedFwdParams& p, int q0, int n,
   if (q0 >= n) return 0;
   return p.causal ? max(0, len - n + min(q0 + p.tok_tile, n)) : len;
 }
-// Work tile `local` of sequence b: the tiles run from its last block of tokens
-// (which sees most keys) to its first, the KV heads innermost. All its keys.
-__device__ __forceinline__ void expand_tile(const PagedFwdParams& p, int local, int b, PagedTile& t) {
-  const SeqSpan sp = new_span(p.s, b);
+// Work tile `local` of sequence b (rows row0 .. row0 + n of q, len keys): the tiles
+// run from its last block of tokens (which sees most keys) to its first, the KV heads
+// innermost. All its keys.
+__device__ __forceinline__ void expand_tile(const PagedFwdParams& p, int local, int b, int row0, int n, int len,
+                                            PagedTile& t) {
   t.b = b;
-  t.row0 = sp.start;
-  t.n_new = sp.len;
-  t.len = kv_len(p.s, b);
+  t.row0 = row0;
+  t.n_new = n;
+  t.len = len;
   const int mi = local / p.H_kv;
   t.h = local - mi * p.H_kv;
-  t.q0 = (m_blocks(p, sp.len) - 1 - mi) * 2 * p.tok_tile;
+  t.q0 = (m_blocks(p, n) - 1 - mi) * 2 * p.tok_tile;
   t.kt0 = 0;
   for (int i = 0; i < 2; ++i)
     t.n[i] = (keys_seen(p, t.q0 + i * p.tok_tile, t.n_new, t.len) + kTileN - 1) / kTileN;
@@ -191,7 +191,8 @@ struct TileSource {
       lo_tile = p.tile_start[v];
       hi_tile = p.tile_start[v + 1];
     }
-    expand_tile(p, tile - lo_tile, seq, t);
+    const SeqSpan sp = new_span(p.s, seq);
+    expand_tile(p, tile - lo_tile, seq, sp.start, sp.len, kv_len(p.s, seq), t);
   }
   __device__ bool near_end() const {
     constexpr int kNearRounds = 4;
@@ -725,21 +726,27 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // Orders the sequences by their keys, longest first (ties in input order), and
 // numbers their work tiles; zeroes the claim counter. One CTA. Offsets that make
 // more work items than the host made room for (they overlap) leave no work.
-__global__ void __launch_bounds__(1024)
+constexpr int kPlanThreads = 640;
+static_assert(kFwdListed <= kPlanThreads && kPlanThreads <= 1024, "one thread per listed tile");
+__global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const PagedFwdParams p, int sort) {
   extern __shared__ int plan_smem[];
-  // when sorting: keys, order [B], first tiles [B + 1]
+  // when sorting: keys, first rows, rows and order of the sequences [B] and the first
+  // tiles [B]; otherwise they are looked up where they are needed
   int* key = plan_smem;
-  int* ord = plan_smem + p.s.B;
-  int* start = sort ? plan_smem + 2 * p.s.B : p.tile_start;
+  int* row0 = key + p.s.B;
+  int* rows = row0 + p.s.B;
+  int* ord = rows + p.s.B;
+  int* start = sort ? ord + p.s.B : p.tile_start;
   __shared__ long long warp_sum[33];
   __shared__ int unit[kFwdListed];
   __shared__ int rest_units[kFwdSms + 1], rest_start[kFwdSms + 1];
+  __shared__ int longest;  // CTA's units when the rest's tiles stay whole
+  if (threadIdx.x == 0) longest = 0;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, B = p.s.B;
   grid_wait();
   grid_release();
   if (tid == 0) *p.tile_ctr = 0;
-  check_paged_seqs(p.s, tid, blockDim.x);
   // the sum of x over the threads before this one, and over all
   auto scan = [&](long long x, long long& all) {
     long long in = x;
@@ -751,7 +758,7 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
     __syncthreads();
     if (lane == 31) warp_sum[w] = in;
     __syncthreads();
-    long long sum = warp_sum[lane];
+    long long sum = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
     const long long own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -762,7 +769,12 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
     return __shfl_sync(0xffffffffu, sum - own, w) + in - x;
   };
   if (sort) {
-    for (int b = tid; b < B; b += blockDim.x) key[b] = kv_len(p.s, b);
+    for (int b = tid; b < B; b += blockDim.x) {
+      key[b] = kv_len(p.s, b);
+      const SeqSpan sp = new_span(p.s, b);
+      row0[b] = sp.start;
+      rows[b] = sp.len;
+    }
     __syncthreads();
     for (int b = tid; b < B; b += blockDim.x) {
       const int mine = key[b];
@@ -775,7 +787,7 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   const int run = (B + blockDim.x - 1) / blockDim.x;
   const int v0 = min(B, tid * run), v1 = min(B, v0 + run);
   auto tiles_of = [&](int v) {
-    return static_cast<long long>(m_blocks(p, new_span(p.s, sort ? ord[v] : v).len)) * p.H_kv;
+    return static_cast<long long>(m_blocks(p, sort ? rows[ord[v]] : new_span(p.s, v).len)) * p.H_kv;
   };
   long long mine = 0, all;
   for (int v = v0; v < v1; ++v) mine += tiles_of(v);
@@ -799,12 +811,19 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
     const int v = find_last(start, B, tid);
     PagedTile t;
     t.pad[0] = t.pad[1] = 0;
-    expand_tile(p, tid - start[v], sort ? ord[v] : v, t);
+    if (sort) {
+      const int b = ord[v];
+      expand_tile(p, tid - start[v], b, row0[b], rows[b], key[b], t);
+    } else {
+      const SeqSpan sp = new_span(p.s, v);
+      expand_tile(p, tid - start[v], v, sp.start, sp.len, kv_len(p.s, v), t);
+    }
     const int4* words = reinterpret_cast<const int4*>(&t);
 #pragma unroll
     for (int i = 0; i < 3; ++i) p.tiles[3 * tid + i] = words[i];
     unit[tid] = tile_units(t);
   }
+  check_paged_seqs(p.s, tid, blockDim.x);
   if (!p.split) return;
   // Few work tiles: the units of every CTA's whole tiles, of each tile of the rest,
   // and the shares of the rest that even the CTAs out.
@@ -820,18 +839,27 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   if (tid < grid)
     for (int i = 0; i < waves; ++i) whole += unit[i * grid + tid];
   scan(whole, whole_all);
-  // Pieces of less than six units cost more than they spread: the last `wide` CTAs
-  // (whose whole tiles are the shortest) share the rest, each at least a tile's worth.
+  // Kept whole, tile x of the rest goes to CTA grid - rest + x (the last ones' whole
+  // tiles are the shortest).
+  const int spare = grid - rest;
+  if (tid >= spare && tid < grid) atomicMax(&longest, static_cast<int>(whole) + unit[waves * grid + tid - spare]);
+  // Cut, pieces of less than six units cost more than they spread: the last `wide`
+  // CTAs share the rest, each at least a tile's worth.
   const long long wide = max(static_cast<long long>(rest), min(static_cast<long long>(grid), rest_all / 6));
   const long long level = (whole_all + rest_all) / grid;
   const long long share = tid >= grid || tid < grid - wide ? 0
                           : waves == 0 || wide < grid      ? 1
                                                            : max(0ll, level - whole);
   const long long before = scan(share, share_all);
+  // Leaving and joining the pieces takes as long as about eight units: below that the
+  // tiles stay whole.
+  const long long even = waves == 0 ? (wide > 0 ? rest_all / wide : 0) : level;
+  const bool cut = longest > even + 8;
   // (without room below the mean the last CTA takes the rest)
   if (tid <= grid)
     rest_start[tid] = tid == grid ? static_cast<int>(rest_all)
-                                  : share_all > 0 ? static_cast<int>(rest_all * before / share_all) : 0;
+                      : !cut      ? rest_units[max(0, tid - spare)]
+                      : share_all > 0 ? static_cast<int>(rest_all * before / share_all) : 0;
   __syncthreads();
   if (tid < grid) {
     const int u = rest_start[tid], end = rest_start[tid + 1];
@@ -923,8 +951,8 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   // sorting compares every pair of sequences and keeps them in shared memory
   const int sort = p.s.B <= 1024;
   int slot = prof_begin(kKPagedPlan, stream);
-  cudaError_t e = launch_chained<paged_plan_kernel>(dim3(1), 1024,
-                                 sort ? (3 * p.s.B + 1) * static_cast<int>(sizeof(int)) : 0, stream, p, sort);
+  cudaError_t e = launch_chained<paged_plan_kernel>(dim3(1), kPlanThreads,
+                                 sort ? 5 * p.s.B * static_cast<int>(sizeof(int)) : 0, stream, p, sort);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
