@@ -155,14 +155,14 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
 bool few_rows(int T, int B, int group) {
   return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
 }
-// So does little work, by its units (tiles of 64 keys of 16 rows, at most 20 for
-// each SM) and what the page table can hold: 20 new tokens of one prompt, 32 heads
-// on 8 (48 units), take 8.8 us there and 21.4 with the planning kernel and its tiles,
-// 256 (2080 units) 23.8 and 31.5, 512 (8256) 47.3 and 33.6.
+// So does little work, by its units (tiles of 64 keys of 16 rows) and what the page
+// table can hold: 20 new tokens of one prompt, 32 heads on 8 (48 units), take 7.5 us
+// there and 17.2 with the planning kernel and its tiles, 128 (528 units) 13.2 and
+// 16.2, 256 (2080) 20.6 and 17.5.
 bool little_work(int T, int B, int group, int H_kv, long long keys) {
   const long long chunks = (static_cast<long long>(T) * group + 15) / 16 + B;
   const long long tiles = (keys + kStreamTile - 1) / kStreamTile;
-  return chunks * H_kv * tiles <= 3040;
+  return chunks * H_kv * tiles <= 2000;
 }
 
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {

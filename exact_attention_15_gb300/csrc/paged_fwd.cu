@@ -899,19 +899,41 @@ paged_fwd_join_kernel(const PagedFwdParams p) {
     float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-      const int4 share = p.shares[c];
-      if (share.x == share.y) continue;
-      const size_t at = (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      if (ml.y == 0.0f) continue;  // a piece whose keys this row does not see leaves no O
-      const float top = fmaxf(m, ml.x), bias = top == -INFINITY ? 0.0f : top;
-      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
-      m = top;
-      l = l * f + ml.y * g;
-      const float* src = p.part_o + at * D + lane * kV;
+    for (int base = c0; base <= c1; base += 32) {
+      // lane k: maximum, sum and weight of piece base + k (a share can be empty, and a
+      // piece whose keys this row does not see left no O)
+      const int c = base + lane;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (c <= c1) {
+        const int4 share = p.shares[c];
+        if (share.x != share.y)
+          ml = *reinterpret_cast<const float2*>(
+              p.part_ml + ((static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * 2);
+      }
+      float top = fmaxf(m, ml.x);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] = acc[e] * f + src[e] * g;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float bias = top == -INFINITY ? 0.0f : top;
+      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
+      const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
+      float sum = ml.y * g;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = l * f + sum;
+      m = top;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] *= f;
+      const int count = min(32, c1 - base + 1);
+#pragma unroll 4
+      for (int k = 0; k < count; ++k) {
+        const float w = __shfl_sync(0xffffffffu, g, k);
+        if (!(live >> k & 1)) continue;
+        const int ck = base + k;
+        const float* src = p.part_o +
+            ((static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * D + lane * kV;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] += src[e] * w;
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const size_t to = static_cast<size_t>(t.row0) + tok;
