@@ -54,9 +54,9 @@ __device__ __forceinline__ void check_paged_seqs(const PagedSeqs& s, int tid, in
 
 // Launches a kernel that calls grid_wait() in every thread before it touches
 // memory: its launch and set-up overlap the end of the grid before it. The
-// shared-memory size is set once per device.
+// shared-memory size is set once per device. Clusters of `cluster` CTAs.
 template <auto Kernel, typename... Args>
-cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_clusters(int cluster, dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
   if (smem > 48 * 1024) {
     static std::atomic<unsigned long long> ready{0};
     int dev = 0;
@@ -69,17 +69,24 @@ cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream
       ready.fetch_or(bit, std::memory_order_relaxed);
     }
   }
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, Kernel, args...);
+}
+template <auto Kernel, typename... Args>
+cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+  return launch_clusters<Kernel>(1, grid, threads, smem, stream, args...);
 }
 
 // A power of two that brings a row whose largest magnitude is `top` to [1, 2) when
@@ -123,7 +130,7 @@ struct StreamParams {
   int4* heads;            // workspace: [kStreamCtas, 2] where the pieces of a split item begin
   float* part_ml;         // workspace: [2 kStreamCtas, 16, 2]
   float* part_o;          // workspace: [2 kStreamCtas, 16, d]
-  int grid;  // set by the launch
+  int grid, cluster_shift;  // set by the launch
   long long wait_limit;
 };
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,

@@ -11,6 +11,11 @@
 // (m, l, O) in the workspace; paged_join_kernel merges the pieces of an item in
 // their order, so results do not depend on timing.
 //
+// Of one token per sequence and short contexts, dealing out and the second kernel
+// would be most of the time: a cluster of 1 to 8 CTAs takes an item whole, each an
+// even run of its tiles, and its CTAs join their pieces through each other's shared
+// memory (one sequence of 777 keys, 32 heads on 8: 7.3 -> 5.6 us; 16 of 256: 9.0 -> 6.1).
+//
 // Warp roles (160 threads): warps 0-3 each take 16 keys of a tile, S = Q K^T
 // and O += P V on mma.sync m16n8k16 with the online softmax in registers
 // (tcgen05 wants 128 rows; here there are 16 at most, and the tensor work is
@@ -43,7 +48,8 @@ struct StreamCfg {
   static constexpr int kMlOff = kMergeOff + kMergeBytes;
   static constexpr int kRingOff = kMlOff + kWarps * 16 * 2 * 4;
   static constexpr int kBarOff = kRingOff + kRing * 48;
-  static constexpr int kSmemBytes = kBarOff + (2 * kStages + 2 * kRing + 1) * 8;
+  static constexpr int kPieceOff = kBarOff + (2 * kStages + 2 * kRing + 1) * 8;  // clusters: [16][2]
+  static constexpr int kSmemBytes = kPieceOff + 16 * 2 * 4;
   // the CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
   static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory of an SM");
 };
@@ -154,6 +160,28 @@ __device__ __forceinline__ bool next_piece(const StreamParams& p, Walk& w, Piece
   return false;
 }
 
+// Clusters of 2^cluster_shift CTAs for an item each: this CTA's piece (one token per
+// sequence). Returns whether a CTA of the cluster has the whole item.
+constexpr int kMaxCluster = 8;
+__device__ __forceinline__ int cluster_tile(const StreamParams& p, int tiles, int rank) {
+  return (tiles * rank) >> p.cluster_shift;  // (2^25 tiles at most)
+}
+template <int R>
+__device__ __forceinline__ bool cluster_piece(const StreamParams& p, Piece& x) {
+  const int item = blockIdx.x >> p.cluster_shift, rank = blockIdx.x - (item << p.cluster_shift);
+  const int chunks = (p.group + R - 1) / R, row = item / chunks;
+  x.rc = item - row * chunks;
+  x.b = row / p.H_kv;
+  x.h = row - x.b * p.H_kv;
+  x.len = kv_len(p.s, x.b);
+  x.n = 1;
+  x.row0 = x.b;
+  x.tiles = (x.len + kTile - 1) / kTile;
+  x.t0 = cluster_tile(p, x.tiles, rank);
+  x.t1 = cluster_tile(p, x.tiles, rank + 1);
+  return x.tiles == 1 || (p.cluster_shift == 0 && x.tiles > 0);
+}
+
 // O = 0 and LSE = -inf for the query rows of a sequence without keys (one warp).
 template <int D>
 __device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows, int lane) {
@@ -167,7 +195,9 @@ __device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows,
   }
 }
 
-template <int D, int R, bool FP8>
+// CLUSTER: the CTAs of a cluster share one item, of one token, and join their pieces
+// through each other's shared memory.
+template <int D, int R, bool FP8, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, StreamCfg<D, R, FP8>::kCtas)
 paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const StreamParams p) {
@@ -194,6 +224,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     mbar_init(merge_free, kWarps);
     fence_barrier_init();
   }
+  float* piece_o = reinterpret_cast<float*>(smem);  // clusters: [R][D], once the tiles are read
+  float* piece_ml = reinterpret_cast<float*>(smem + Cfg::kPieceOff);
   const int cta = blockIdx.x;
   __syncthreads();
   grid_wait();
@@ -204,9 +236,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // ------------------------------------------------------------ TMA producer
     // The units before each sequence: every lane sums a run of sequences, the sums
     // are scanned, and the run that holds this CTA's first unit is walked.
-    const int run = (p.s.B + 31) >> 5;
-    long long before, total;
-    {
+    long long total = 0;
+    int grid = 0;
+    Walk w;
+    if constexpr (!CLUSTER) {
+      const int run = (p.s.B + 31) >> 5;
+      long long before;
       const int b1 = min(p.s.B, (lane + 1) * run);
       long long mine = 0;
 #pragma unroll 4
@@ -219,18 +254,17 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       total = __shfl_sync(0xffffffffu, before, 31);
       before -= mine;
-    }
-    const int grid = busy_ctas(total, gridDim.x);
-    Walk w;
-    w.u = w.end = w.base = 0;
-    w.b = 0;
-    if (cta < grid) {
-      w.u = first_unit(total, grid, cta);
-      w.end = first_unit(total, grid, cta + 1);
-      // the last run that starts at or before the first unit (lane 0's does)
-      const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= w.u));
-      w.b = at * run;
-      w.base = __shfl_sync(0xffffffffu, before, at);
+      grid = busy_ctas(total, gridDim.x);
+      w.u = w.end = w.base = 0;
+      w.b = 0;
+      if (cta < grid) {
+        w.u = first_unit(total, grid, cta);
+        w.end = first_unit(total, grid, cta + 1);
+        // the last run that starts at or before the first unit (lane 0's does)
+        const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= w.u));
+        w.b = at * run;
+        w.base = __shfl_sync(0xffffffffu, before, at);
+      }
     }
     // Lane (page j of the tile, K or V, block) issues one box per tile.
     const int box_shift = min(p.s.page_shift, 6);
@@ -260,12 +294,18 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       return true;
     };
     int nth = 0;
-    for (; ok && next_piece<R>(p, w, x); ++nth) {
+    auto next = [&]() {
+      if constexpr (!CLUSTER) return next_piece<R>(p, w, x);
+      if (nth > 0) return false;
+      cluster_piece<R>(p, x);
+      return x.t0 < x.t1;
+    };
+    for (; ok && next(); ++nth) {
       // a CTA's first and last piece can be parts of an item
       const bool whole = x.t1 - x.t0 == x.tiles;
       x.slot = whole ? -1 : 2 * cta + (nth == 0 ? 0 : 1);
       if (!(ok = give(nth))) break;
-      if (x.t0 == 0 && !whole) {
+      if (!CLUSTER && x.t0 == 0 && !whole) {
         // for the join: the item begins in this CTA and ends in a later one
         split_head = true;
         if (lane == 0) {
@@ -302,10 +342,17 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
     if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
     // off the way of the loads: what no work unit covers
-    if (!split_head && lane == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
+    if (!CLUSTER && !split_head && lane == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
     if (cta == 0) check_paged_seqs(p.s, lane, 32);
-    for (int b = cta; b < p.s.B; b += gridDim.x)
+    for (int b = cta; !CLUSTER && b < p.s.B; b += gridDim.x)
       if (kv_len(p.s, b) == 0) write_empty<D>(p, new_span(p.s, b), lane);
+    if constexpr (CLUSTER) {
+      __syncwarp();
+      if (!cluster_piece<R>(p, x)) {
+        cluster_sync_all();
+        cluster_sync_all();
+      }
+    }
     return;
   }
 
@@ -649,16 +696,68 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             p.lse[row * p.lse_row + head * p.lse_head] =
                 sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
         } else {
-          float* dst = p.part_o + (static_cast<size_t>(y.slot) * 16 + r) * D + c0 + g8 * 8;
+          float* dst = (CLUSTER ? piece_o + r * D : p.part_o + (static_cast<size_t>(y.slot) * 16 + r) * D) + c0 + g8 * 8;
           *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
           if (c0 == 0 && g8 == 0)
-            *reinterpret_cast<float2*>(p.part_ml + (y.slot * 16 + r) * 2) = make_float2(top, sum);
+            *reinterpret_cast<float2*>(CLUSTER ? piece_ml + r * 2 : p.part_ml + (y.slot * 16 + r) * 2) =
+                make_float2(top, sum);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(merge_free);
     }
+  }
+  if constexpr (CLUSTER) {
+    // ---- join: row r of the item in CTA r mod the cluster's size, a warp each
+    __syncwarp();
+    if (cluster_piece<R>(p, x)) return;
+    cluster_sync_all();
+    const int cluster = 1 << p.cluster_shift;
+    const int rows = min(R, p.group - x.rc * R);
+    for (int r = (cta & (cluster - 1)) + cluster * warp; r < rows; r += cluster * kWarps) {
+      constexpr int kV = D / 32;
+      float2 w[kMaxCluster];
+      float o[kMaxCluster][kV];
+#pragma unroll
+      for (int g = 0; g < kMaxCluster; ++g) {
+        // (a CTA without a tile left nothing)
+        const bool live = g < cluster && cluster_tile(p, x.tiles, g) < cluster_tile(p, x.tiles, g + 1);
+        w[g] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) o[g][e] = 0.0f;
+        if (live) {
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(w[g].x), "=f"(w[g].y)
+                       : "r"(cluster_map(smem_addr(piece_ml + r * 2), g)) : "memory");
+#pragma unroll
+          for (int e = 0; e < kV; e += 2)
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(o[g][e]), "=f"(o[g][e + 1])
+                         : "r"(cluster_map(smem_addr(piece_o + r * D + lane * kV + e), g)) : "memory");
+        }
+      }
+      float top = -INFINITY, sum = 0.0f, acc[kV];
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kMaxCluster; ++g) top = fmaxf(top, w[g].x);
+#pragma unroll
+      for (int g = 0; g < kMaxCluster; ++g) {
+        const float f = ex2_approx(w[g].x - (top == -INFINITY ? 0.0f : top));
+        sum += w[g].y * f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] += o[g][e] * f;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int head = x.h * p.group + x.rc * R + r;
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
+                                                  (static_cast<size_t>(x.row0) * p.H_q + head) * D + lane * kV);
+#pragma unroll
+      for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (lane == 0)
+        p.lse[x.row0 * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while another one reads its pieces
   }
 }
 
@@ -768,21 +867,48 @@ paged_join_kernel(const StreamParams p) {
   if (lane == 0) p.lse[row * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
+// CTAs of a cluster for each of `items` of `tiles` key tiles at most, 0 where the units
+// are dealt out instead. More CTAs shorten an item's run of tiles but join longer and
+// share the SMs: a cluster of c is worth more CTAs from 1, 3 or 6 tiles for each of c
+// on, where that makes one, two or three CTAs on an SM. The clusters all run at
+// once (with 304 CTAs in places for 304, clusters of 8 do not fit: 38 sequences of 100
+// keys, one head: 11.7 us, dealt out 6.9; with 264 5.3). Above 8 tiles for each CTA, dealing
+// out evens ragged lengths better than it costs (20 sequences of 1 to 4096 keys, 32
+// heads on 4, 16 tiles each: 13.4 us, dealt out 11.4).
+int cluster_of(long long items, long long tiles, int grid, int n_sm) {
+  int c = 1;
+  while (2 * c <= kMaxCluster && 8 * items * 2 * c <= 7ll * grid) {
+    const long long per_sm = (items * 2 * c + n_sm - 1) / n_sm;
+    if (tiles <= c * per_sm * (per_sm + 1) / 2) break;
+    c *= 2;
+  }
+  return 8 * items * c <= 7ll * grid && tiles <= 8 * c ? c : 0;
+}
+
 template <int D, int R, bool FP8>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p, int n_sm,
                    cudaStream_t stream) {
   using Cfg = StreamCfg<D, R, FP8>;
   p.grid = min(Cfg::kCtas * n_sm, kStreamCtas);
   int slot = prof_begin(kKPagedDecode, stream);
-  cudaError_t e = launch_chained<paged_stream_kernel<D, R, FP8>>(dim3(p.grid), kThreads,
-                                 Cfg::kSmemBytes, stream, tk, tv, p);
+  cudaError_t e;
+  const long long items = static_cast<long long>(p.s.B) * p.H_kv * ((p.group + R - 1) / R);
+  const long long tiles = ((static_cast<long long>(p.s.max_pages) << p.s.page_shift) + kTile - 1) / kTile;
+  const int cluster = p.s.cu_seqlens ? 0 : cluster_of(items, tiles, p.grid, n_sm);
+  if (cluster > 0) {
+    for (p.cluster_shift = 0; 1 << p.cluster_shift < cluster;) ++p.cluster_shift;
+    e = launch_clusters<paged_stream_kernel<D, R, FP8, true>>(
+        cluster, dim3(static_cast<unsigned>(items * cluster)), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
+    prof_end(slot, stream);
+    return e;
+  }
+  e = launch_chained<paged_stream_kernel<D, R, FP8, false>>(dim3(p.grid), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
   if (static_cast<long long>(p.s.B) * p.H_kv < n_sm)
     e = launch_chained<paged_join_kernel<D, R / 8, 4>>(dim3(p.grid, 8), 128 * (R / 8), 0, stream, p);
   else
-    
     e = launch_chained<paged_join_kernel<D, 4, 1>>(dim3(p.grid, R / 4), 128, 0, stream, p);
   prof_end(slot, stream);
   return e;

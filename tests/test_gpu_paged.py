@@ -67,6 +67,61 @@ def test_decode(case, kind):
         assert_attention(o, lse, *_decode_want(c, q, scale), what=scale)
 
 
+SHORT = [
+    # lens, H_q, H_kv, d, page
+    ([777], 32, 8, 128, 16),
+    ([0, 1, 64, 65, 127, 129, 2048, 500], 4, 1, 128, 64),
+    ([512, 0, 511, 63, 64, 65, 1, 300], 32, 8, 128, 16),
+    ([1, 40, 0, 128, 129, 500, 512, 448] * 2, 16, 8, 128, 32),
+    ([512, 1, 2, 64, 65, 300, 0, 449] * 4, 8, 8, 64, 16),
+    ([1000, 200, 0, 64], 40, 1, 64, 256),  # three chunks of 16 query rows
+    ([4096], 16, 2, 128, 128),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", range(len(SHORT)))
+def test_decode_of_short_and_of_wide_tables(case, kind):
+    """A table that holds little sends a call to clusters that share a (sequence, KV
+    head) each; the same sequences in a wide table are dealt out to all CTAs."""
+    lens, H_q, H_kv, d, page = SHORT[case]
+    c = Cache(lens, H_kv, d, page, kind, seed=case)
+    wide = torch.full((len(lens), 100000 // page), -7, dtype=torch.int32, device="cuda")
+    wide[:, :c.width] = c.table
+    h, q = c.handle(), _q(len(lens), H_q, d)
+    want = _decode_want(c, q, 1.0 / math.sqrt(d))
+    for table in (c.table, wide):
+        o, lse = binding.paged_decode(h, q, table, c.kv_lens)
+        assert_attention(o, lse, *want, what=tuple(table.shape))
+        again = binding.paged_decode(h, q, table, c.kv_lens)
+        assert torch.equal(as_int(o), as_int(again[0])) and torch.equal(lse, again[1])
+
+
+def test_short_decode_captured():
+    """A captured short call replays with other lengths, none of them among these, and
+    with an infinite score, which the sequence's own output alone shows."""
+    c = Cache([600, 17, 0, 450], 2, 128, 32, width=20)
+    h, q = c.handle(), _q(4, 8, 128)
+    graph = torch.cuda.CUDAGraph()
+    binding.paged_decode(h, q, c.table, c.kv_lens)
+    with torch.cuda.graph(graph):
+        o, lse = binding.paged_decode(h, q, c.table, c.kv_lens)
+    for lens in ([600, 17, 0, 450], [1, 0, 0, 449], [64, 16, 0, 65], [0, 0, 0, 0]):
+        c.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        cut = Cache.__new__(Cache)
+        cut.lens = lens
+        cut.keys = [x[:n] for x, n in zip(c.keys, lens)]
+        cut.values = [x[:n] for x, n in zip(c.values, lens)]
+        assert_attention(o, lse, *_decode_want(cut, q, 1.0 / math.sqrt(128)), what=lens)
+    c.kv_lens.copy_(torch.tensor([600, 17, 0, 450], dtype=torch.int32))
+    c.put(c.k, 0, 599, torch.full((1, 2, 128), math.inf, dtype=torch.bfloat16, device="cuda"))
+    graph.replay()
+    assert not bool(torch.isfinite(lse[0]).any())
+    want = _decode_want(c, q, 1.0 / math.sqrt(128))
+    assert_attention(o[1:], lse[1:], *(x[1:] for x in want))
+
+
 def test_decode_is_bit_exact_and_captured():
     """Two calls give the same bits; a captured call replays with new contents,
     lengths and pages, in its own outputs and workspace."""
