@@ -872,11 +872,14 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   }
 }
 
-// Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows
-// 16 y .. 16 y + 15 of tile x of the rest, two for each warp.
-constexpr int kJoinRows = 16;
+// Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows 8 y ..
+// 8 y + 7 of tile x of the rest, one for each warp. Latency is what it costs: with
+// two rows to a warp, one piece after the other, 3 sequences of 198 new tokens behind
+// 15000 keys (5 heads on 1, d 64) took 43 us in all, with four pieces' loads side by
+// side 33, with one row to a warp 31.
+constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kJoinRows)
 paged_fwd_join_kernel(const PagedFwdParams p) {
   grid_wait();
   const int total = p.tile_start[p.s.B], grid = p.grid, x = blockIdx.x;
@@ -892,57 +895,66 @@ paged_fwd_join_kernel(const PagedFwdParams p) {
   }
   const int lane = threadIdx.x & 31;
   constexpr int kV = D / 32;
-  for (int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5); row < (blockIdx.y + 1) * kJoinRows; row += 8) {
-    const int i = row >> 7, r = row & 127;
-    const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
-    if (tok_r >= p.tok_tile || tok >= t.n_new) continue;
-    float acc[kV], m = -INFINITY, l = 0.0f;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int i = row >> 7, r = row & 127;
+  const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
+  if (tok_r >= p.tok_tile || tok >= t.n_new) return;
+  float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-    for (int base = c0; base <= c1; base += 32) {
-      // lane k: maximum, sum and weight of piece base + k (a share can be empty, and a
-      // piece whose keys this row does not see left no O)
-      const int c = base + lane;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (c <= c1) {
-        const int4 share = p.shares[c];
-        if (share.x != share.y)
-          ml = *reinterpret_cast<const float2*>(
-              p.part_ml + ((static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * 2);
-      }
-      float top = fmaxf(m, ml.x);
+  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
+  for (int base = c0; base <= c1; base += 32) {
+    // lane k: maximum, sum and weight of piece base + k (a share can be empty, and a
+    // piece whose keys this row does not see left no O)
+    const int c = base + lane;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (c <= c1) {
+      const int4 share = p.shares[c];
+      const float2 left = *reinterpret_cast<const float2*>(
+          p.part_ml + ((static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * 2);
+      if (share.x != share.y) ml = left;
+    }
+    float top = fmaxf(m, ml.x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float bias = top == -INFINITY ? 0.0f : top;
-      const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
-      const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
-      float sum = ml.y * g;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float bias = top == -INFINITY ? 0.0f : top;
+    const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
+    const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
+    float sum = ml.y * g;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l = l * f + sum;
-      m = top;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * f + sum;
+    m = top;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] *= f;
-      const int count = min(32, c1 - base + 1);
-#pragma unroll 4
-      for (int k = 0; k < count; ++k) {
-        const float w = __shfl_sync(0xffffffffu, g, k);
-        if (!(live >> k & 1)) continue;
-        const int ck = base + k;
+    for (int e = 0; e < kV; ++e) acc[e] *= f;
+    const int count = min(32, c1 - base + 1);
+    constexpr int kAtOnce = 4;
+    for (int k0 = 0; k0 < count; k0 += kAtOnce) {
+      float o[kAtOnce][kV];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int ck = base + k0 + k;
+        const bool use = k0 + k < count && (live >> (k0 + k) & 1);
         const float* src = p.part_o +
             ((static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * D + lane * kV;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] += src[e] * w;
+        for (int e = 0; e < kV; ++e) o[k][e] = use ? src[e] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float w = __shfl_sync(0xffffffffu, g, (k0 + k) & 31);
+        const bool use = k0 + k < count && (live >> (k0 + k) & 1);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] += use ? o[k][e] * w : 0.0f;
       }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const size_t to = static_cast<size_t>(t.row0) + tok;
-    const int head = t.h * p.group + r - tok_r * p.group;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
-#pragma unroll
-    for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t to = static_cast<size_t>(t.row0) + tok;
+  const int head = t.h * p.group + r - tok_r * p.group;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
+#pragma unroll
+  for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // One warp per row of queries.
@@ -983,7 +995,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained<paged_fwd_join_kernel<D>>(dim3(p.grid, 2 * kTileM / kJoinRows), 256, 0, stream, p);
+  e = launch_chained<paged_fwd_join_kernel<D>>(dim3(min(p.grid, p.max_work), 2 * kTileM / kJoinRows), 32 * kJoinRows, 0, stream, p);
   prof_end(slot, stream);
   return e;
 }
