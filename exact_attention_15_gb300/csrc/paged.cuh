@@ -144,7 +144,7 @@ struct PagedFwdParams {
   PagedSeqs s;
   void* o;     // bf16 [T, H_q, d]
   float* lse;  // [H_q, T]
-  int H_q, H_kv, group, causal;
+  int H_q, H_kv, group, d, causal;
   int tok_tile;      // query tokens per 128-row tile: floor(128 / group)
   int split;         // few work tiles: whole waves of them, the rest cut evenly
   int max_work;      // work tiles that the host expects at most
@@ -155,6 +155,7 @@ struct PagedFwdParams {
   int* tile_start;   // workspace: first work tile of each of them [B + 1]
   int* tile_ctr;     // workspace: claim counter (split == 0)
   int4* tiles;       // workspace: the first kFwdListed work tiles, three words each
+  int4* rest_tiles;  // workspace, split: the work tiles of the rest [grid], three words each
   int4* shares;      // workspace, split: each CTA's share of the rest [grid]
   int* rest_units;   // workspace, split: first unit of each work tile of the rest [grid + 1]
   int2* rest_owners; // workspace, split: first and last CTA of each of them [grid]

@@ -137,9 +137,9 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
   // From four waves on, claiming leaves an SM idle for less than the join costs.
   f.split = f.tiles < kFwdListed;
   const size_t slots = f.split ? static_cast<size_t>(2 * kFwdSms) * 2 * kTileM : 0;
-  // ints, then the listed tiles, the shares and the owners of the rest
+  // ints, then the listed and the rest's tiles, the shares and the owners of the rest
   f.tiles_off = align256((2 * static_cast<size_t>(B) + 2 + kFwdSms + 1) * sizeof(int));
-  f.ml_off = f.tiles_off + align256((3 * kFwdListed + kFwdSms) * sizeof(int4) + kFwdSms * sizeof(int2));
+  f.ml_off = f.tiles_off + align256((3 * (kFwdListed + kFwdSms) + kFwdSms) * sizeof(int4) + kFwdSms * sizeof(int2));
   f.o_off = f.ml_off + align256(slots * 2 * sizeof(float));
   // e4m3: the queries as fp16 and their rows' powers of two
   const size_t rows_q = e4m3 ? static_cast<size_t>(T) * group * H_kv : 0;
@@ -229,6 +229,7 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   p.H_q = H_q;
   p.H_kv = c->H_kv;
   p.group = group;
+  p.d = c->d;
   p.causal = causal ? 1 : 0;
   p.tok_tile = plan.tok_tile;
   if (plan.tiles > 0x3fffffffll) return ATTN_ERR_BAD_SHAPE;
@@ -243,7 +244,8 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   p.tile_ctr = p.tile_start + seqs.B + 1;
   p.rest_units = p.tile_ctr + 1;
   p.tiles = reinterpret_cast<int4*>(ws + plan.tiles_off);
-  p.shares = p.tiles + 3 * kFwdListed;
+  p.rest_tiles = p.tiles + 3 * kFwdListed;
+  p.shares = p.rest_tiles + 3 * kFwdSms;
   p.rest_owners = reinterpret_cast<int2*>(p.shares + kFwdSms);
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);

@@ -651,19 +651,38 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int e = 0; e < D; ++e) ov[e] = 0u;
       }
       const float v_scale = E4M3 && p.v_scale ? __ldg(p.v_scale + t.h) : 1.0f;
+      uint32_t buf_off = Cfg::kEpiOff + i * Cfg::kBlockBytes;
+      asm volatile("" : "+r"(buf_off));  // computed here, not kept across the key loop
+      uint8_t* buf = smem + buf_off;
+      const int rows = min(p.tok_tile, t.n_new - q0) * p.group;
       if (t.slot >= 0) {
-        const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM + r;
-        if (row_ok) {
-          *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m_used, l);
-          if (my_n > 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D);
+        // A piece: maxima, sums and O as they are. O passes through the warp's part of the
+        // staging block, 32 columns at a time, so that the stores are whole lines: row
+        // by row from the registers they cost 10 us more where every SM has a piece.
+        const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM;
+        if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used, l);
+        if (my_n > 0) {
+          if (r == 0) bulk_wait_group_read<0>();
+          named_bar_sync(2 + i, 128);
+          const int row0 = r & ~31;
 #pragma unroll
-            for (int e = 0; e < D / 4; ++e)
-              dst[e] = E4M3 ? make_uint4(__float_as_uint(__uint_as_float(ov[4 * e]) * v_scale),
-                                         __float_as_uint(__uint_as_float(ov[4 * e + 1]) * v_scale),
-                                         __float_as_uint(__uint_as_float(ov[4 * e + 2]) * v_scale),
-                                         __float_as_uint(__uint_as_float(ov[4 * e + 3]) * v_scale))
-                            : make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          for (int c0 = 0; c0 < D; c0 += 32) {
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              float f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(ov[c0 + 4 * ch + e]) * v_scale;
+              *reinterpret_cast<float4*>(buf + sw128_offset(r, ch)) = make_float4(f[0], f[1], f[2], f[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = lane; x < 256; x += 32) {
+              const int rr = row0 + (x >> 3);
+              if (rr < rows)
+                *reinterpret_cast<float4*>(p.part_o + (slot + rr) * D + c0 + (x & 7) * 4) =
+                    *reinterpret_cast<const float4*>(buf + sw128_offset(rr, x & 7));
+            }
+            __syncwarp();
           }
         }
         continue;
@@ -675,10 +694,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // whole rows where the tile ends inside the sequence, else (the store's box
       // would reach into the next sequence) by 128-byte runs of the rows it has
       const bool box = q0 + p.tok_tile <= t.n_new;
-      const int rows = min(p.tok_tile, t.n_new - q0) * p.group;
-      uint32_t buf_off = Cfg::kEpiOff + i * Cfg::kBlockBytes;
-      asm volatile("" : "+r"(buf_off));  // computed here, not kept across the key loop
-      uint8_t* buf = smem + buf_off;
 #pragma unroll
       for (int hf = 0; hf < Cfg::kBlocks; ++hf) {
         uint32_t w[32];
@@ -819,8 +834,12 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
       expand_tile(p, tid - start[v], v, sp.start, sp.len, kv_len(p.s, v), t);
     }
     const int4* words = reinterpret_cast<const int4*>(&t);
+    const int first_rest = p.split ? total / p.grid * p.grid : total;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) p.tiles[3 * tid + i] = words[i];
+    for (int i = 0; i < 3; ++i) {
+      p.tiles[3 * tid + i] = words[i];
+      if (tid >= first_rest) p.rest_tiles[3 * (tid - first_rest) + i] = words[i];
+    }
     unit[tid] = tile_units(t);
   }
   check_paged_seqs(p.s, tid, blockDim.x);
@@ -851,10 +870,12 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
                           : waves == 0 || wide < grid      ? 1
                                                            : max(0ll, level - whole);
   const long long before = scan(share, share_all);
-  // Leaving and joining the pieces takes as long as about eight units: below that the
-  // tiles stay whole.
+  // Leaving and joining the pieces takes as long as about three units, and one more for
+  // every 16 tiles of the rest (d 128; 32 for 64): below that the tiles stay whole. 1000
+  // new tokens of one prompt, 32 heads on 8, 128 tiles: whole 26.7 us, cut 35.0; 1500 of 8
+  // heads of 64, 48 tiles: 27.4 and 23.5.
   const long long even = waves == 0 ? (wide > 0 ? rest_all / wide : 0) : level;
-  const bool cut = longest > even + 8;
+  const bool cut = longest > even + 3 + (rest * p.d >> 11);
   // (without room below the mean the last CTA takes the rest)
   if (tid <= grid)
     rest_start[tid] = tid == grid ? static_cast<int>(rest_all)
@@ -865,96 +886,108 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
     const int u = rest_start[tid], end = rest_start[tid + 1];
     p.shares[tid] = make_int4(u, end, u < end ? find_last(rest_units, rest, u) : 0, 0);
   }
-  if (tid < rest) {
-    const int begin = rest_units[tid] + kItemCost, end = rest_units[tid + 1];  // its key tiles' units
+  if (tid < grid) {
+    const int begin = tid < rest ? rest_units[tid] + kItemCost : 0;  // its key tiles' units
+    const int end = tid < rest ? rest_units[tid + 1] : 0;
     p.rest_owners[tid] = begin < end ? make_int2(find_last(rest_start, grid, begin), find_last(rest_start, grid, end - 1))
                                      : make_int2(0, 0);
   }
 }
 
-// Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows 8 y ..
-// 8 y + 7 of tile x of the rest, one for each warp. Latency is what it costs: with
-// two rows to a warp, one piece after the other, 3 sequences of 198 new tokens behind
-// 15000 keys (5 heads on 1, d 64) took 43 us in all, with four pieces' loads side by
-// side 33, with one row to a warp 31.
-constexpr int kJoinRows = 8;
+// Merges the pieces of the rest's split work tiles in order. CTA (x, y): rows 16 y ..
+// 16 y + 15 of tile x of the rest, two at once for each warp. Latency is what it costs,
+// so all loads of four pieces are on their way together: of 3 sequences of 198 new tokens behind
+// 15000 keys (5 heads on 1, d 64), a call takes 31 us, with one load after the other 43.
+// Four rows at once leave one CTA on an SM (two prompts of 512 behind 4000 to 8000 keys,
+// 32 heads on 8: 96 us; two rows 84, one row 86).
+constexpr int kJoinRows = 16;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinRows)
+__global__ void __launch_bounds__(256)
 paged_fwd_join_kernel(const PagedFwdParams p) {
   grid_wait();
-  const int total = p.tile_start[p.s.B], grid = p.grid, x = blockIdx.x;
-  const int2 own = p.rest_owners[x];  // the CTAs that hold its first and its last key tile
-  const int waves = total / grid, rest = total - waves * grid;
-  if (x >= rest || own.x == own.y) return;  // written whole
-  const int c0 = own.x, c1 = own.y;
+  const int2 own = p.rest_owners[blockIdx.x];  // the CTAs that hold its first and its last key tile
   PagedTile t;
   {
     int4* words = reinterpret_cast<int4*>(&t);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) words[i] = p.tiles[3 * (waves * grid + x) + i];
+    for (int i = 0; i < 3; ++i) words[i] = p.rest_tiles[3 * blockIdx.x + i];
   }
+  if (own.x == own.y) return;  // written whole, or no tile
+  const int c0 = own.x, c1 = own.y;
   const int lane = threadIdx.x & 31;
-  constexpr int kV = D / 32;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  const int i = row >> 7, r = row & 127;
-  const int tok_r = r / p.group, tok = t.q0 + i * p.tok_tile + tok_r;
-  if (tok_r >= p.tok_tile || tok >= t.n_new) return;
-  float acc[kV], m = -INFINITY, l = 0.0f;
+  constexpr int kV = D / 32, kRows = kJoinRows / 8, kAtOnce = 4;
+  const int row0 = blockIdx.y * kJoinRows + (threadIdx.x >> 5) * kRows;
+  const int i = row0 >> 7, r0 = row0 & 127;
+  // rows of this query tile
+  const int rows = max(0, min(p.tok_tile, t.n_new - t.q0 - i * p.tok_tile)) * p.group;
+  if (r0 >= rows) return;
+  auto slot_row = [&](int c, int n) {
+    return (static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + min(r0 + n, rows - 1);
+  };
+  float acc[kRows][kV], m[kRows], l[kRows];
 #pragma unroll
-  for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-  for (int base = c0; base <= c1; base += 32) {
-    // lane k: maximum, sum and weight of piece base + k (a share can be empty, and a
-    // piece whose keys this row does not see left no O)
-    const int c = base + lane;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (c <= c1) {
+  for (int n = 0; n < kRows; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[n][e] = 0.0f;
+  }
+  // Four pieces at a time, all loads before the first is used (the last piece again
+  // behind it, with no weight). A share can be empty, and a piece whose keys a row does
+  // not see left no O.
+  for (int base = c0; base <= c1; base += kAtOnce) {
+    float o[kAtOnce][kRows][kV];
+    float2 ml[kAtOnce][kRows];
+    bool some[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = min(base + k, c1);
       const int4 share = p.shares[c];
-      const float2 left = *reinterpret_cast<const float2*>(
-          p.part_ml + ((static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * 2);
-      if (share.x != share.y) ml = left;
-    }
-    float top = fmaxf(m, ml.x);
+      some[k] = base + k <= c1 && share.x != share.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float bias = top == -INFINITY ? 0.0f : top;
-    const float f = ex2_approx(m - bias), g = ex2_approx(ml.x - bias);
-    const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
-    float sum = ml.y * g;
+      for (int n = 0; n < kRows; ++n) {
+        const size_t at = slot_row(c, n);
+        ml[k][n] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+        const float* src = p.part_o + at * D + lane * kV;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * f + sum;
-    m = top;
-#pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] *= f;
-    const int count = min(32, c1 - base + 1);
-    constexpr int kAtOnce = 4;
-    for (int k0 = 0; k0 < count; k0 += kAtOnce) {
-      float o[kAtOnce][kV];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int ck = base + k0 + k;
-        const bool use = k0 + k < count && (live >> (k0 + k) & 1);
-        const float* src = p.part_o +
-            ((static_cast<size_t>(2 * ck + (ck == c0 ? 1 : 0)) * 2 + i) * kTileM + r) * D + lane * kV;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) o[k][e] = use ? src[e] : 0.0f;
+        for (int e = 0; e < kV; ++e) o[k][n][e] = src[e];
       }
+    }
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      float top = m[n];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (some[k]) top = fmaxf(top, ml[k][n].x);
+      const float bias = top == -INFINITY ? 0.0f : top, f = ex2_approx(m[n] - bias);
+      m[n] = top;
+      l[n] *= f;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[n][e] *= f;
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const float w = __shfl_sync(0xffffffffu, g, (k0 + k) & 31);
-        const bool use = k0 + k < count && (live >> (k0 + k) & 1);
+        if (!some[k] || ml[k][n].y == 0.0f) continue;
+        const float g = ex2_approx(ml[k][n].x - bias);
+        l[n] += ml[k][n].y * g;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] += use ? o[k][e] * w : 0.0f;
+        for (int e = 0; e < kV; ++e) acc[n][e] += o[k][n][e] * g;
       }
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t to = static_cast<size_t>(t.row0) + tok;
-  const int head = t.h * p.group + r - tok_r * p.group;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
 #pragma unroll
-  for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) p.lse[static_cast<size_t>(head) * p.s.T + to] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+  for (int n = 0; n < kRows; ++n) {
+    const int r = r0 + n;
+    if (r >= rows) break;
+    const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+    const int tok_r = r / p.group;
+    const size_t to = static_cast<size_t>(t.row0) + t.q0 + i * p.tok_tile + tok_r;
+    const int head = t.h * p.group + r - tok_r * p.group;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (to * p.H_q + head) * D + lane * kV);
+#pragma unroll
+    for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[n][2 * e] * inv, acc[n][2 * e + 1] * inv);
+    if (lane == 0)
+      p.lse[static_cast<size_t>(head) * p.s.T + to] = l[n] == 0.0f ? -INFINITY : m[n] * kLn2 + logf(l[n]);
+  }
 }
 
 // One warp per row of queries.
@@ -995,7 +1028,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
-  e = launch_chained<paged_fwd_join_kernel<D>>(dim3(min(p.grid, p.max_work), 2 * kTileM / kJoinRows), 32 * kJoinRows, 0, stream, p);
+  e = launch_chained<paged_fwd_join_kernel<D>>(dim3(min(p.grid, p.max_work), 2 * kTileM / kJoinRows), 256, 0, stream, p);
   prof_end(slot, stream);
   return e;
 }
