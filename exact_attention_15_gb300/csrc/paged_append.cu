@@ -93,18 +93,18 @@ __device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x,
   return Part{*reinterpret_cast<const uint4*>(src + x.e0), *reinterpret_cast<const uint4*>(src + x.e1)};
 }
 
-// One CTA per token. The first kAhead parts of every thread are loaded before the
+// W threads per token. The first kAhead parts of every thread are loaded before the
 // token's sequence, position and page are looked up (three dependent loads) and
 // its angles computed, once for all heads; then they are turned and stored. What
 // bounds it is the bytes: 36,696 tokens of 16 ragged prompts (32 query and 8 KV heads
-// of 128, 902 MB) take 137 to 145 us, 6.2 to 6.6 TB/s, 91 to 97% of a plain copy's rate. Measured
+// of 128, 902 MB) take 135 to 145 us, 6.2 to 6.7 TB/s, 91 to 98% of a plain copy's rate. Measured
 // beside it: without the loads ahead 155 us, with a read of the angles from shared
 // memory for every part 158, with a warp or 64 threads per token 158 or more, with
 // registers held down for more CTAs 156 or more.
 //
-// W threads work on a token (a multiple of a head's 8 or 4, so that each keeps its
-// place in every head), kAppendThreads / W tokens in a CTA: with few heads a CTA per
-// token would leave most threads idle.
+// W is a multiple of a head's 8 or 4 threads, so that each keeps its place in every
+// head; a CTA takes kAppendThreads / W tokens: with few heads a CTA per token would
+// leave most threads idle.
 constexpr int kAhead = 3;
 template <int W>
 __global__ void __launch_bounds__(kAppendThreads)

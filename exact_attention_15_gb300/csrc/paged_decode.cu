@@ -86,9 +86,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // Beginning and ending an item (its queries' latency, the merge of the warps)
 // costs a CTA about as much as two tiles of it: it counts as units of its own, so
 // that runs of short items are not dealt out as if they were free. Measured on
-// 128 ragged e4m3 sequences of 64 to 4096 keys, 4 KV heads: 57.1 us with 0 units,
-// 50.8 with 1, 49.9 with 2, 49.4 with 3; on 32 ragged ones with 16 heads of 64: 37.6,
-// 31.4, 31.1, 31.1.
+// 128 ragged e4m3 sequences of 64 to 4096 keys, 4 KV heads: 48.3 us with 0 units,
+// 46.7 with 1, 2 or 3; on 32 ragged ones with 16 heads of 64: 29.5, 28.7, 29.0, 29.1.
 constexpr int kItemCost = 2;
 // Work units of sequence b: (key tiles + kItemCost) x KV heads x chunks of R rows.
 __device__ __forceinline__ long long units_of(const StreamParams& p, int b, int R) {

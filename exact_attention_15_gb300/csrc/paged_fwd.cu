@@ -657,8 +657,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int rows = min(p.tok_tile, t.n_new - q0) * p.group;
       if (t.slot >= 0) {
         // A piece: maxima, sums and O as they are. O passes through the warp's part of the
-        // staging block, 32 columns at a time, so that the stores are whole lines: row
-        // by row from the registers they cost 10 us more where every SM has a piece.
+        // staging block, 32 columns at a time, so that the stores are whole lines: straight
+        // from the registers, 16 bytes of a row each, two prompts of 512 behind 4000 to 8000
+        // keys (32 heads on 8) took 91 us for 87.
         const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM;
         if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used, l);
         if (my_n > 0) {

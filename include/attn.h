@@ -320,7 +320,7 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
  * the sequences' lengths (0 on invalid sizes; T, B, H_q, H_kv, d and type as in the
  * call). The workspace is caller-owned, 256-byte aligned, its contents do not matter
  * between calls, and calls that may run at the same time need one each. A decoding
- * call needs about 5 MB; a chunk call at most 41 MB for the parts of divided tiles,
+ * call needs 8 MB at most; a chunk call at most 41 MB for the parts of divided tiles,
  * and over an e4m3 cache 2 d + 4 bytes per query row and head besides.
  */
 size_t attn_paged_decode_workspace_bytes(int d);
@@ -330,8 +330,9 @@ size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, in
  * Attention of one query token per sequence over its kv_lens[b] cached keys:
  * q and o bf16 [B, H_q, d], lse float [B, H_q]; grouped heads and the empty
  * sequence (O = 0, LSE = -inf) as for attn_fwd. The cache is read once, split evenly
- * over the GPU whatever the lengths, and the parts are joined in a fixed order: equal
- * inputs give equal bits on the same device. Allocates nothing; can be captured.
+ * over the GPU whatever the lengths (behind a short page table, over clusters of CTAs for
+ * each sequence and KV head), and the parts are joined in a fixed order: equal inputs
+ * and sizes give equal bits on the same device. Allocates nothing; can be captured.
  */
 int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
                       const int* kv_lens, const int* page_table, int max_pages,
@@ -346,9 +347,9 @@ int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, flo
  * without, every key of its sequence. A row that sees no key gets O = 0 and LSE =
  * -inf. As with attn_fwd, a NaN or infinity among the values of a chunk's own tokens
  * can reach rows of the chunk for which the causal mask hides it. Chunks of at most 16
- * query rows per sequence and KV head (T * H_q / H_kv against 16 * B) run on the
- * streaming kernel of attn_paged_decode, larger ones on the tensor cores; either way
- * equal inputs give equal bits. Otherwise as attn_paged_decode.
+ * query rows per sequence and KV head (T * H_q / H_kv against 16 * B), and calls of
+ * little work, run on the streaming kernel of attn_paged_decode, larger ones on the
+ * tensor cores; either way equal inputs and sizes give equal bits. Otherwise as attn_paged_decode.
  */
 int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float* lse, int T, int B,
                    int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
