@@ -100,6 +100,11 @@ __device__ __forceinline__ float row_power(float top, float& down) {
   return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 }
 
+// Over an e4m3 cache P goes into its product as fp16, at 2^kLift times its value (which
+// the sums share): at most 2^15, and what lies above 2^-21 of a row's largest keeps its
+// 11 bits.
+constexpr float kLift = kTau < 15.0f ? 15.0f - kTau : 0.0f;
+
 // ---- appending
 struct AppendParams {
   PagedSeqs s;

@@ -420,6 +420,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     ++nth;
     return x.b >= 0;
   };
+  constexpr float lift = FP8 ? kLift : 0.0f;
   uint32_t merges = 0;  // uses of the merge buffer
   bool have = take();
   if (have) load_q(x);
@@ -560,7 +561,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             float pv[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              pv[e] = ex2_approx(sv[nb][2 * h + e] - (m[nb][e] == -INFINITY ? 0.0f : m[nb][e]));
+              pv[e] = ex2_approx(sv[nb][2 * h + e] - (m[nb][e] == -INFINITY ? 0.0f : m[nb][e] - lift));
               l[nb][e] += pv[e];
             }
             pb[nb][h] = transpose8x8(FP8 ? pack_f16x2(pv[0], pv[1]) : pack_bf16x2(pv[0], pv[1]));
@@ -639,7 +640,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float2*>(ml + (warp * 16 + nb * 8 + 2 * qd + e) * 2) = make_float2(m[nb][e], l[nb][e]);
+            *reinterpret_cast<float2*>(ml + (warp * 16 + nb * 8 + 2 * qd + e) * 2) = make_float2(m[nb][e] - lift, l[nb][e]);
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)

@@ -567,6 +567,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t col_s = Cfg::kColS + i * 128, col_o = i * D;
     const int tok_r = r / p.group, head_r = r - tok_r * p.group;
     int sw = 0, pvw = 0;  // s_full and pv_done waits so far
+    constexpr float lift = E4M3 ? kLift : 0.0f;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       PagedTile t;
@@ -606,8 +607,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                              : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
                                                       rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
-        if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb, need_mask, pk, sum2);
-        else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb, need_mask, pk, sum2);
+        if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
+        else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
         if (rescale_warp && j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
           // O is complete: the commit that signalled S_j came after PV_{j-1}
 #pragma unroll
@@ -661,7 +662,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // from the registers, 16 bytes of a row each, two prompts of 512 behind 4000 to 8000
         // keys (32 heads on 8) took 91 us for 87.
         const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM;
-        if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used, l);
+        if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used - lift, l);
         if (my_n > 0) {
           if (r == 0) bulk_wait_group_read<0>();
           named_bar_sync(2 + i, 128);
@@ -725,7 +726,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
       if (row_ok)
-        p.lse[static_cast<size_t>(hq) * p.s.T + row] = l == 0.0f ? -INFINITY : m_used * kLn2 + logf(l);
+        p.lse[static_cast<size_t>(hq) * p.s.T + row] = l == 0.0f ? -INFINITY : (m_used - lift) * kLn2 + logf(l);
     }
     // the O stores have read the staging buffer before the CTA's shared memory goes
     if (r == 0) bulk_wait_group<0>();

@@ -185,6 +185,32 @@ def test_chunk_large_query_values_over_e4m3():
         assert_attention(o, lse, *_chunk_want(c, q, new, scale, True), what=factor)
 
 
+@pytest.mark.parametrize("n", [1, 130])
+def test_small_weights_over_e4m3(n):
+    """A key with weight 1 and no value next to 199 with weights of 2^-19: they keep the
+    accuracy of larger ones (as fp16 numbers of their own they would have 5 bits)."""
+    c = Cache([200], 1, 128, 16, "e4m3")
+    c.k_scale.fill_(0.25)
+    c.v_scale.fill_(0.5)
+    k = torch.zeros(200, 1, 128, device="cuda")
+    k[0, 0, 0] = 4.0
+    v = torch.randint(1, 8, (200, 1, 128), device="cuda").float()
+    v[0] = 0.0
+    for cache, x in ((c.k, k), (c.v, v)):
+        c.put(cache, 0, 0, x.to(torch.float8_e4m3fn))
+    c.keys, c.values = [k.double() * 0.25], [v.double() * 0.5]
+    q = torch.zeros(n, 2, 128, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 19.0
+    scale = math.log(2.0)
+    if n == 1:
+        o, lse = binding.paged_decode(c.handle(), q, c.table, c.kv_lens, scale=scale)
+        want = _decode_want(c, q, scale)
+    else:
+        o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets([n]), scale=scale, causal=False)
+        want = _chunk_want(c, q, [n], scale, False)
+    assert_attention(o, lse, *want)
+
+
 def test_decode_spread_scores():
     """Scores with a wide spread: the running maximum moves many times."""
     c = Cache([2000], 1, 64, 16)
