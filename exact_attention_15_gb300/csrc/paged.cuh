@@ -122,6 +122,10 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
 // ---- streaming attention: few query rows per sequence
 constexpr int kStreamCtas = 456;  // CTAs the workspace holds partial results for
 constexpr int kStreamTile = 64;   // keys per tile
+constexpr int kStreamCluster = 8;  // CTAs of a cluster at most
+// CTAs on an SM: three where the registers (8 query rows) and shorter tiles (rows of
+// `row_bytes` of K or V) allow it.
+constexpr int stream_ctas(int rows, int row_bytes) { return rows == 8 && row_bytes <= 128 ? 3 : 2; }
 
 struct StreamParams {
   PagedSeqs s;
@@ -135,6 +139,8 @@ struct StreamParams {
   int4* heads;            // workspace: [kStreamCtas, 2] where the pieces of a split item begin
   float* part_ml;         // workspace: [2 kStreamCtas, 16, 2]
   float* part_o;          // workspace: [2 kStreamCtas, 16, d]
+  int cluster;        // CTAs of a cluster, 0: the units are dealt out
+  long long items;    // clusters
   int grid, cluster_shift;  // set by the launch
   long long wait_limit;
 };

@@ -156,13 +156,51 @@ bool few_rows(int T, int B, int group) {
   return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
 }
 // So does little work, by its units (tiles of 64 keys of 16 rows) and what the page
-// table can hold: 20 new tokens of one prompt, 32 heads on 8 (48 units), take 7.5 us
-// there and 17.2 with the planning kernel and its tiles, 128 (528 units) 13.2 and
-// 16.2, 256 (2080) 20.6 and 17.5.
+// table can hold: 100 new tokens of each of 2 prompts behind 1000, 8 heads on 2 (1872
+// units), take 16.3 us there and 30 with the planning kernel and its tiles, 256 of one prompt, 32
+// heads on 8 (2080), 20.6 and 17.
 bool little_work(int T, int B, int group, int H_kv, long long keys) {
   const long long chunks = (static_cast<long long>(T) * group + 15) / 16 + B;
   const long long tiles = (keys + kStreamTile - 1) / kStreamTile;
   return chunks * H_kv * tiles <= 2000;
+}
+
+// How the streaming kernel runs a call: chunks of 8 query rows where a sequence's rows of
+// one KV head fill no more, else 16; `items` clusters of `cluster` CTAs, one for each
+// (sequence, KV head, chunk), or 0 where the units are dealt out instead.
+//
+// More CTAs of a cluster shorten an item's run of tiles but join longer and share the
+// SMs: a cluster of c is worth twice the CTAs from 1, 3 or 6 tiles for each of c on, where
+// that makes one, two or three CTAs on an SM. Clusters all run at once (with 304 CTAs in places
+// for 304, clusters of 8 do not fit: 38 sequences of 100 keys, one head: 11.7 us, dealt out 6.9;
+// with 264 5.3). Above 8 tiles for each CTA, dealing out evens ragged lengths better
+// than it costs (20 sequences of 1 to 4096 keys, 32 heads on 4, 16 tiles each: 13.4 us,
+// dealt out 11.4). Single CTAs may take two turns of 4 tiles (64 sequences of 256 keys, 32 heads on
+// 8: 16.4 us, dealt out 18.1; of 1024 in 4 turns 31.9 and 29.4). Where the tensor-core kernel
+// is the other choice, twice that (4 chunks of 64 behind 200 keys: 16.7 us, there 21.5).
+struct StreamShape {
+  int rows, cluster;
+  long long items;
+};
+StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, bool packed, int max_pages,
+                         bool or_tensor_cores, int n_sm) {
+  StreamShape s;
+  s.rows = static_cast<long long>(T) * group <= 8ll * B ? 8 : 16;
+  // no sequence has more than rows - 1 rows too few for its last chunk
+  const long long chunks = packed ? (static_cast<long long>(T) * group + (s.rows - 1ll) * B) / s.rows
+                                  : static_cast<long long>(B) * ((group + s.rows - 1) / s.rows);
+  s.items = chunks * c->H_kv;
+  const long long tiles = (static_cast<long long>(max_pages) * c->page_size + kStreamTile - 1) / kStreamTile;
+  const long long grid = static_cast<long long>(stream_ctas(s.rows, c->d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2))) * n_sm;
+  s.cluster = 1;
+  while (2 * s.cluster <= kStreamCluster && 8 * s.items * 2 * s.cluster <= 7 * grid) {
+    const long long per_sm = (s.items * 2 * s.cluster + n_sm - 1) / n_sm;
+    if (tiles <= s.cluster * per_sm * (per_sm + 1) / 2) break;
+    s.cluster *= 2;
+  }
+  const long long turns = s.cluster > 1 ? 1 : (s.items + grid - 1) / grid, more = or_tensor_cores ? 2 : 1;
+  if (turns > 1 + more || turns * tiles > 8 * more * s.cluster) s.cluster = 0;
+  return s;
 }
 
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
@@ -174,7 +212,7 @@ size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
                   void* o, float* lse, int H_q, int causal, float scale, uint8_t* ws, long long lse_row,
-                  long long lse_head, cudaStream_t cs) {
+                  long long lse_head, const StreamShape& shape, cudaStream_t cs) {
   const unsigned rows = c->page_size < kStreamTile ? c->page_size : kStreamTile;
   CUtensorMap tk, tv;
   int st;
@@ -200,9 +238,9 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
   p.wait_limit = dev.wait_limit;
-  // 8 rows where a sequence's rows of one KV head fill no more
-  const int chunk = static_cast<long long>(seqs.T) * p.group <= 8ll * seqs.B ? 8 : 16;
-  return launch_paged_stream(tk, tv, p, c->d, chunk, c->type == ATTN_CACHE_E4M3, dev.n_sm, cs) == cudaSuccess
+  p.cluster = shape.cluster;
+  p.items = shape.items;
+  return launch_paged_stream(tk, tv, p, c->d, shape.rows, c->type == ATTN_CACHE_E4M3, dev.n_sm, cs) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }
@@ -279,9 +317,11 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
   const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (!seqlens || few_rows(T, B, group) ||
+  const bool few = !seqlens || few_rows(T, B, group);
+  const StreamShape shape = stream_shape(c, T, B, group, seqlens != nullptr, max_pages, !few, dev.n_sm);
+  if (few || shape.cluster > 0 ||
       little_work(T, B, group, c->H_kv, static_cast<long long>(max_pages) * c->page_size))
-    return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, cs);
+    return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, shape, cs);
   return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
 }
 

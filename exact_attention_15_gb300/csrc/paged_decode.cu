@@ -11,10 +11,10 @@
 // (m, l, O) in the workspace; paged_join_kernel merges the pieces of an item in
 // their order, so results do not depend on timing.
 //
-// Of one token per sequence and short contexts, dealing out and the second kernel
-// would be most of the time: a cluster of 1 to 8 CTAs takes an item whole, each an
-// even run of its tiles, and its CTAs join their pieces through each other's shared
-// memory (one sequence of 777 keys, 32 heads on 8: 7.3 -> 5.6 us; 16 of 256: 9.0 -> 6.1).
+// Of short contexts, dealing out and the second kernel would be most of the time: a
+// cluster of 1 to 8 CTAs takes an item whole, each an even run of its tiles, and its CTAs
+// join their pieces through each other's shared memory (one sequence of 777 keys, 32
+// heads on 8: 7.3 -> 5.6 us; 16 of 256: 9.0 -> 6.1; 64 new tokens: 8.5 -> 4.9).
 //
 // Warp roles (160 threads): warps 0-3 each take 16 keys of a tile, S = Q K^T
 // and O += P V on mma.sync m16n8k16 with the online softmax in registers
@@ -35,8 +35,7 @@ constexpr int kRing = 4;  // pieces that the loading warp can be ahead
 template <int D, int R, bool FP8>
 struct StreamCfg {
   static constexpr int kEs = FP8 ? 1 : 2;
-  // CTAs on an SM: three where the registers and shorter tiles allow it
-  static constexpr int kCtas = R == 8 && D * kEs <= 128 ? 3 : 2;
+  static constexpr int kCtas = stream_ctas(R, D * kEs);
   // a tile is kept as blocks of 64 rows x (at most) 128 bytes, swizzled
   static constexpr int kRowBytes = D * kEs < 128 ? D * kEs : 128;
   static constexpr int kBlocks = D * kEs / kRowBytes;
@@ -159,26 +158,59 @@ __device__ __forceinline__ bool next_piece(const StreamParams& p, Walk& w, Piece
   return false;
 }
 
-// Clusters of 2^cluster_shift CTAs for an item each: this CTA's piece (one token per
-// sequence). Returns whether a CTA of the cluster has the whole item.
-constexpr int kMaxCluster = 8;
+// Clusters of 2^cluster_shift CTAs for an item each: this CTA's piece (one warp, the
+// same in every lane). There can be more clusters than items (b < 0).
+constexpr int kMaxCluster = kStreamCluster;
 __device__ __forceinline__ int cluster_tile(const StreamParams& p, int tiles, int rank) {
   return (tiles * rank) >> p.cluster_shift;  // (2^25 tiles at most)
 }
+// A CTA of the cluster has the whole item.
+__device__ __forceinline__ bool cluster_whole(const StreamParams& p, int tiles) {
+  return tiles == 1 || (p.cluster_shift == 0 && tiles > 0);
+}
 template <int R>
-__device__ __forceinline__ bool cluster_piece(const StreamParams& p, Piece& x) {
+__device__ __forceinline__ void cluster_piece(const StreamParams& p, int lane, Piece& x) {
   const int item = blockIdx.x >> p.cluster_shift, rank = blockIdx.x - (item << p.cluster_shift);
-  const int chunks = (p.group + R - 1) / R, row = item / chunks;
-  x.rc = item - row * chunks;
-  x.b = row / p.H_kv;
-  x.h = row - x.b * p.H_kv;
+  const int row = item / p.H_kv;  // chunk of query rows, counted over the sequences
+  x.h = item - row * p.H_kv;
+  x.t0 = x.t1 = x.tiles = x.len = x.n = 0;
+  if (!p.s.cu_seqlens) {
+    const int chunks = (p.group + R - 1) / R;
+    x.b = row / chunks;
+    x.rc = row - x.b * chunks;
+  } else {
+    auto chunks_of = [&](int b) {
+      return (static_cast<long long>(new_span(p.s, b).len) * p.group + R - 1) / R;
+    };
+    // every lane sums a run of sequences, and the run that holds the chunk is walked
+    const int run = (p.s.B + 31) >> 5, b1 = min(p.s.B, (lane + 1) * run);
+    long long mine = 0;
+    for (int b = lane * run; b < b1; ++b) mine += chunks_of(b);
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    x.b = -1;
+    if (row >= __shfl_sync(0xffffffffu, before, 31)) return;
+    before -= mine;
+    const int at = 31 - __clz(__ballot_sync(0xffffffffu, before <= row));
+    x.b = at * run;
+    long long base = __shfl_sync(0xffffffffu, before, at);
+    for (long long n = chunks_of(x.b); row >= base + n; n = chunks_of(x.b)) {
+      base += n;
+      ++x.b;
+    }
+    x.rc = static_cast<int>(row - base);
+  }
   x.len = kv_len(p.s, x.b);
-  x.n = 1;
-  x.row0 = x.b;
+  const SeqSpan sp = new_span(p.s, x.b);
+  x.n = sp.len;
+  x.row0 = sp.start;
   x.tiles = (x.len + kTile - 1) / kTile;
   x.t0 = cluster_tile(p, x.tiles, rank);
   x.t1 = cluster_tile(p, x.tiles, rank + 1);
-  return x.tiles == 1 || (p.cluster_shift == 0 && x.tiles > 0);
 }
 
 // O = 0 and LSE = -inf for the query rows of a sequence without keys (one warp).
@@ -194,8 +226,8 @@ __device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows,
   }
 }
 
-// CLUSTER: the CTAs of a cluster share one item, of one token, and join their pieces
-// through each other's shared memory.
+// CLUSTER: the CTAs of a cluster share one item and join their pieces through each
+// other's shared memory.
 template <int D, int R, bool FP8, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, StreamCfg<D, R, FP8>::kCtas)
 paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -295,9 +327,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int nth = 0;
     auto next = [&]() {
       if constexpr (!CLUSTER) return next_piece<R>(p, w, x);
-      if (nth > 0) return false;
-      cluster_piece<R>(p, x);
-      return x.t0 < x.t1;
+      if (nth == 0) cluster_piece<R>(p, lane, x);
+      return nth == 0;
     };
     for (; ok && next(); ++nth) {
       // a CTA's first and last piece can be parts of an item
@@ -335,7 +366,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (++stage == Cfg::kStages) { stage = 0; phase ^= 1; }
       }
     }
-    if (ok) {
+    if (!CLUSTER && ok) {
       x.b = -1;
       ok = give(nth);
     }
@@ -347,7 +378,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       if (kv_len(p.s, b) == 0) write_empty<D>(p, new_span(p.s, b), lane);
     if constexpr (CLUSTER) {
       __syncwarp();
-      if (!cluster_piece<R>(p, x)) {
+      if (x.b >= 0 && !cluster_whole(p, x.tiles)) {
         cluster_sync_all();
         cluster_sync_all();
       }
@@ -404,6 +435,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   };
   bool ok = true;
   Piece x;
+  x.b = -2;     // not known
   int nth = 0;  // pieces taken
   auto take = [&]() {  // the next piece, in every lane
     const int at = nth % kRing;
@@ -423,6 +455,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   constexpr float lift = FP8 ? kLift : 0.0f;
   uint32_t merges = 0;  // uses of the merge buffer
   bool have = take();
+  if (CLUSTER) have = have && x.t0 < x.t1;
   if (have) load_q(x);
   while (have) {
     const int rows = min(R, x.n * p.group - x.rc * R);  // of this chunk
@@ -611,7 +644,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     // ---- merge of the four warps' keys
     const Piece y = x;
-    have = take();
+    have = !CLUSTER && take();
     if (have) load_q(x);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -711,10 +744,10 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if constexpr (CLUSTER) {
     // ---- join: row r of the item in CTA r mod the cluster's size, a warp each
     __syncwarp();
-    if (cluster_piece<R>(p, x)) return;
+    if (x.b == -1 || (x.b >= 0 && cluster_whole(p, x.tiles))) return;
     cluster_sync_all();
     const int cluster = 1 << p.cluster_shift;
-    const int rows = min(R, p.group - x.rc * R);
+    const int rows = x.b < 0 ? 0 : min(R, x.n * p.group - x.rc * R);
     for (int r = (cta & (cluster - 1)) + cluster * warp; r < rows; r += cluster * kWarps) {
       constexpr int kV = D / 32;
       float2 w[kMaxCluster];
@@ -748,13 +781,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int e = 0; e < kV; ++e) acc[e] += o[g][e] * f;
       }
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int head = x.h * p.group + x.rc * R + r;
+      const int rr = x.rc * R + r, tok = rr / p.group, head = x.h * p.group + rr - tok * p.group;
+      const size_t row = static_cast<size_t>(x.row0) + tok;
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                                  (static_cast<size_t>(x.row0) * p.H_q + head) * D + lane * kV);
+                                                  (row * p.H_q + head) * D + lane * kV);
 #pragma unroll
       for (int e = 0; e < kV / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
       if (lane == 0)
-        p.lse[x.row0 * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+        p.lse[row * p.lse_row + head * p.lse_head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
     }
     __syncwarp();
     cluster_sync_all();  // no CTA leaves while another one reads its pieces
@@ -867,24 +901,6 @@ paged_join_kernel(const StreamParams p) {
   if (lane == 0) p.lse[row * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-// CTAs of a cluster for each of `items` of `tiles` key tiles at most, 0 where the units
-// are dealt out instead. More CTAs shorten an item's run of tiles but join longer and
-// share the SMs: a cluster of c is worth more CTAs from 1, 3 or 6 tiles for each of c
-// on, where that makes one, two or three CTAs on an SM. The clusters all run at
-// once (with 304 CTAs in places for 304, clusters of 8 do not fit: 38 sequences of 100
-// keys, one head: 11.7 us, dealt out 6.9; with 264 5.3). Above 8 tiles for each CTA, dealing
-// out evens ragged lengths better than it costs (20 sequences of 1 to 4096 keys, 32
-// heads on 4, 16 tiles each: 13.4 us, dealt out 11.4).
-int cluster_of(long long items, long long tiles, int grid, int n_sm) {
-  int c = 1;
-  while (2 * c <= kMaxCluster && 8 * items * 2 * c <= 7ll * grid) {
-    const long long per_sm = (items * 2 * c + n_sm - 1) / n_sm;
-    if (tiles <= c * per_sm * (per_sm + 1) / 2) break;
-    c *= 2;
-  }
-  return 8 * items * c <= 7ll * grid && tiles <= 8 * c ? c : 0;
-}
-
 template <int D, int R, bool FP8>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p, int n_sm,
                    cudaStream_t stream) {
@@ -892,13 +908,10 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p,
   p.grid = min(Cfg::kCtas * n_sm, kStreamCtas);
   int slot = prof_begin(kKPagedDecode, stream);
   cudaError_t e;
-  const long long items = static_cast<long long>(p.s.B) * p.H_kv * ((p.group + R - 1) / R);
-  const long long tiles = ((static_cast<long long>(p.s.max_pages) << p.s.page_shift) + kTile - 1) / kTile;
-  const int cluster = p.s.cu_seqlens ? 0 : cluster_of(items, tiles, p.grid, n_sm);
-  if (cluster > 0) {
-    for (p.cluster_shift = 0; 1 << p.cluster_shift < cluster;) ++p.cluster_shift;
+  if (p.cluster > 0) {
+    for (p.cluster_shift = 0; 1 << p.cluster_shift < p.cluster;) ++p.cluster_shift;
     e = launch_clusters<paged_stream_kernel<D, R, FP8, true>>(
-        cluster, dim3(static_cast<unsigned>(items * cluster)), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
+        p.cluster, dim3(static_cast<unsigned>(p.items * p.cluster)), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
     prof_end(slot, stream);
     return e;
   }

@@ -349,7 +349,8 @@ int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, flo
  * can reach rows of the chunk for which the causal mask hides it. Chunks of at most 16
  * query rows per sequence and KV head (T * H_q / H_kv against 16 * B), and calls of
  * little work, run on the streaming kernel of attn_paged_decode, larger ones on the
- * tensor cores; either way equal inputs and sizes give equal bits. Otherwise as attn_paged_decode.
+ * tensor cores (sizes, max_pages among them, decide); either way equal inputs and sizes give
+ * equal bits. Otherwise as attn_paged_decode.
  */
 int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float* lse, int T, int B,
                    int H_q, const int* seqlens, const int* kv_lens, const int* page_table,

@@ -31,6 +31,16 @@ def _q(n, H_q, d, seed=1):
     return torch.randn(n, H_q, d, generator=g, device="cuda").to(torch.bfloat16)
 
 
+def _table(c, wide):
+    """The page table, or a wide one with the same pages: where a table holds little, a
+    call of little work runs on clusters of the streaming kernel whatever its rows."""
+    if not wide:
+        return c.table
+    table = torch.full((len(c.lens), 100000 // c.page), -7, dtype=torch.int32, device="cuda")
+    table[:, :c.width] = c.table
+    return table
+
+
 def _decode_want(c, q, scale):
     parts = [attention(q[b:b + 1], c.keys[b], c.values[b], scale, torch.tensor([n], device="cuda"))
              for b, n in enumerate(c.lens)]
@@ -86,11 +96,9 @@ def test_decode_of_short_and_of_wide_tables(case, kind):
     head) each; the same sequences in a wide table are dealt out to all CTAs."""
     lens, H_q, H_kv, d, page = SHORT[case]
     c = Cache(lens, H_kv, d, page, kind, seed=case)
-    wide = torch.full((len(lens), 100000 // page), -7, dtype=torch.int32, device="cuda")
-    wide[:, :c.width] = c.table
     h, q = c.handle(), _q(len(lens), H_q, d)
     want = _decode_want(c, q, 1.0 / math.sqrt(d))
-    for table in (c.table, wide):
+    for table in (c.table, _table(c, True)):
         o, lse = binding.paged_decode(h, q, table, c.kv_lens)
         assert_attention(o, lse, *want, what=tuple(table.shape))
         again = binding.paged_decode(h, q, table, c.kv_lens)
@@ -173,7 +181,8 @@ def test_decode_large_query_values_over_e4m3():
         assert_attention(o, lse, *_decode_want(c, q, scale), what=factor)
 
 
-def test_chunk_large_query_values_over_e4m3():
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk_large_query_values_over_e4m3(wide):
     """The same in the tensor-core kernel's fp16 queries, and given buffers."""
     c = Cache([300, 200], 2, 128, 16, "e4m3")
     new, h = [150, 200], c.handle()
@@ -181,12 +190,13 @@ def test_chunk_large_query_values_over_e4m3():
     for factor in (2.0 ** 40, 2.0 ** -60):
         q = (_q(350, 8, 128).float() * factor).to(torch.bfloat16)
         scale = 1.0 / math.sqrt(128) / factor
-        o, lse = binding.paged_forward(h, q, c.table, c.kv_lens, _offsets(new), scale=scale, workspace=ws)
+        o, lse = binding.paged_forward(h, q, _table(c, wide), c.kv_lens, _offsets(new), scale=scale, workspace=ws)
         assert_attention(o, lse, *_chunk_want(c, q, new, scale, True), what=factor)
 
 
 @pytest.mark.parametrize("n", [1, 130])
-def test_small_weights_over_e4m3(n):
+@pytest.mark.parametrize("wide", [False, True])
+def test_small_weights_over_e4m3(wide, n):
     """A key with weight 1 and no value next to 199 with weights of 2^-19: they keep the
     accuracy of larger ones (as fp16 numbers of their own they would have 5 bits)."""
     c = Cache([200], 1, 128, 16, "e4m3")
@@ -203,10 +213,10 @@ def test_small_weights_over_e4m3(n):
     q[:, :, 0] = 19.0
     scale = math.log(2.0)
     if n == 1:
-        o, lse = binding.paged_decode(c.handle(), q, c.table, c.kv_lens, scale=scale)
+        o, lse = binding.paged_decode(c.handle(), q, _table(c, wide), c.kv_lens, scale=scale)
         want = _decode_want(c, q, scale)
     else:
-        o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets([n]), scale=scale, causal=False)
+        o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets([n]), scale=scale, causal=False)
         want = _chunk_want(c, q, [n], scale, False)
     assert_attention(o, lse, *want)
 
@@ -278,13 +288,15 @@ MANY = [
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("case", range(len(MANY)))
-def test_chunk_of_many(case, kind):
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk_of_many(wide, case, kind):
     new, lens, H_q, H_kv, d, page = MANY[case]
     c = Cache(lens, H_kv, d, page, kind, seed=case)
     q = _q(sum(new), H_q, d)
-    o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new))
+    table = _table(c, wide)
+    o, lse = binding.paged_forward(c.handle(), q, table, c.kv_lens, _offsets(new))
     assert_attention(o, lse, *_chunk_want(c, q, new, 1.0 / math.sqrt(d), True))
-    again = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new))
+    again = binding.paged_forward(c.handle(), q, table, c.kv_lens, _offsets(new))
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
@@ -292,7 +304,7 @@ def test_calls_on_two_streams_at_once():
     """Two streams, each with its own decoding and chunk calls over one cache: the
     same bits as one after the other (workspaces are the calls' own)."""
     c = Cache([5000, 300, 2000], 4, 128, 64)
-    h, new = c.handle(), [40, 300, 129]
+    h, new = c.handle(), [40, 300, 129]  # (on the tensor cores)
     qs = [(_q(3, 16, 128, seed=i), _q(sum(new), 16, 128, seed=10 + i)) for i in range(2)]
     cu = _offsets(new)
 
@@ -344,37 +356,41 @@ def _offsets(new):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("case", range(len(CHUNK)))
-def test_chunk(case, kind, causal):
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk(wide, case, kind, causal):
     new, lens, H_q, H_kv, d, page = CHUNK[case]
     c = Cache(lens, H_kv, d, page, kind, seed=case)
     q = _q(sum(new), H_q, d)
     for scale in (1.0 / math.sqrt(d), -0.05):
-        o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new), scale=scale, causal=causal)
+        o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new), scale=scale,
+                                       causal=causal)
         assert_attention(o, lse, *_chunk_want(c, q, new, scale, causal), what=scale)
 
 
 @pytest.mark.parametrize("n", [3, 200])
-def test_chunk_leaves_rows_behind_the_last_sequence(n):
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk_leaves_rows_behind_the_last_sequence(wide, n):
     new = [n, 2 * n]
     c = Cache([n, 500], 2, 128, 16)
     T = 3 * n + 50
     q = _q(T, 8, 128)
     out = torch.full_like(q, 7.0)
     lse = torch.full((8, T), 3.0, device="cuda")
-    binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new), out=out, lse=lse)
+    binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new), out=out, lse=lse)
     assert bool((out[3 * n:] == 7.0).all()) and bool((lse[:, 3 * n:] == 3.0).all())
     assert_attention(out[:3 * n], lse[:, :3 * n], *_chunk_want(c, q, new, 1.0 / math.sqrt(128), True))
 
 
 @pytest.mark.parametrize("n", [2, 300])
-def test_chunk_captured(n):
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk_captured(wide, n):
     """A captured call replays over other lengths in the same buffers."""
     c = Cache([1000, 400], 2, 64, 16, width=70)
-    h, q, cu = c.handle(), _q(2 * n, 4, 64), _offsets([n, n])
-    binding.paged_forward(h, q, c.table, c.kv_lens, cu)
+    h, q, cu, table = c.handle(), _q(2 * n, 4, 64), _offsets([n, n]), _table(c, wide)
+    binding.paged_forward(h, q, table, c.kv_lens, cu)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        o, lse = binding.paged_forward(h, q, c.table, c.kv_lens, cu)
+        o, lse = binding.paged_forward(h, q, table, c.kv_lens, cu)
     c.lens = [999, 302]
     c.kv_lens.copy_(torch.tensor(c.lens, dtype=torch.int32))
     c.keys = [x[:m] for x, m in zip(c.keys, c.lens)]
@@ -385,13 +401,14 @@ def test_chunk_captured(n):
         assert_attention(o, lse, *_chunk_want(c, q, new, 1.0 / 8.0, True))
 
 
-def test_chunk_agrees_with_the_packed_forward():
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunk_agrees_with_the_packed_forward(wide):
     """A fresh prompt through the cache gives what attn_fwd gives on its rows: both
     within bf16's rounding of P and of O of the same value."""
     new = [300, 129, 64]
     c = Cache(new, 2, 128, 16)
     q = _q(sum(new), 8, 128)
-    o, lse = binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets(new))
+    o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new))
     k, v = (torch.cat([x.to(torch.bfloat16) for x in y]) for y in (c.keys, c.values))
     o2, lse2 = binding.forward(q, k, v, causal=True, cu_seqlens=_offsets(new))
     _, size, _ = _chunk_want(c, q, new, 1.0 / math.sqrt(128), True)
