@@ -46,6 +46,7 @@ _SIGS = {
                                _I, _I, _P]),
     "attn_paged_decode_workspace_bytes": (_Z, [_I]),
     "attn_paged_fwd_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "attn_paged_call_workspace_bytes": (_Z, [_P, _I, _I, _I, _I, _I]),
     "attn_paged_decode": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _I, _L, _F, _P, _Z, _P]),
     "attn_paged_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _L, _I, _F, _P, _Z, _P]),
     "attn_check": (_I, [_P]),

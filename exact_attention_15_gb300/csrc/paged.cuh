@@ -148,7 +148,7 @@ cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, co
                                 int d, int rows, bool e4m3, int n_sm, cudaStream_t stream);
 
 // ---- tensor-core attention: many query rows per sequence
-constexpr int kFwdSms = 152;               // CTAs that the workspace is planned for
+constexpr int kFwdSms = 152;               // SMs that calls and workspaces are planned for
 constexpr int kFwdListed = 4 * kFwdSms;    // work tiles that the planning kernel describes
 
 struct PagedFwdParams {

@@ -182,8 +182,9 @@ struct StreamShape {
   int rows, cluster;
   long long items;
 };
-StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, bool packed, int max_pages,
-                         bool or_tensor_cores, int n_sm) {
+StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, bool packed, int max_pages) {
+  constexpr int n_sm = kFwdSms;
+  const bool or_tensor_cores = packed && !few_rows(T, B, group);
   StreamShape s;
   s.rows = static_cast<long long>(T) * group <= 8ll * B ? 8 : 16;
   // no sequence has more than rows - 1 rows too few for its last chunk
@@ -203,11 +204,16 @@ StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, boo
   return s;
 }
 
+// Workspace of a call whatever its page table, and of one call.
 size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
   const size_t stream = stream_plan(d).total;
   if (few_rows(T, B, group)) return stream;
   const size_t fwd = fwd_plan(T, B, group, H_kv, d, e4m3).total;
   return fwd > stream ? fwd : stream;
+}
+size_t workspace_of_call(const attn_paged_cache* c, int T, int B, int group, bool packed, const StreamShape& shape) {
+  if (shape.cluster > 0) return 0;
+  return packed ? workspace_bytes_of(T, B, group, c->H_kv, c->d, c->type == ATTN_CACHE_E4M3) : stream_plan(c->d).total;
 }
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
@@ -310,16 +316,15 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if (!q || !o || !lse) return ATTN_ERR_NULL_PTR;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return ATTN_ERR_ALIGNMENT;
   const int group = H_q / c->H_kv;
-  const size_t need = seqlens ? workspace_bytes_of(T, B, group, c->H_kv, c->d, c->type == ATTN_CACHE_E4M3) : stream_plan(c->d).total;
-  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  const StreamShape shape = stream_shape(c, T, B, group, seqlens != nullptr, max_pages);
+  const size_t need = workspace_of_call(c, T, B, group, seqlens != nullptr, shape);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   HostDevice dev;
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
   const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const bool few = !seqlens || few_rows(T, B, group);
-  const StreamShape shape = stream_shape(c, T, B, group, seqlens != nullptr, max_pages, !few, dev.n_sm);
-  if (few || shape.cluster > 0 ||
+  if (!seqlens || few_rows(T, B, group) || shape.cluster > 0 ||
       little_work(T, B, group, c->H_kv, static_cast<long long>(max_pages) * c->page_size))
     return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, shape, cs);
   return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
@@ -375,6 +380,14 @@ size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, in
       (type != ATTN_CACHE_BF16 && type != ATTN_CACHE_E4M3))
     return 0;
   return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type == ATTN_CACHE_E4M3);
+}
+
+size_t attn_paged_call_workspace_bytes(const attn_paged_cache* cache, int T, int B, int H_q, int packed, int max_pages) {
+  if (check_cache(cache) != ATTN_OK || T < 1 || B < 1 || H_q < 1 || H_q > 65535 || H_q % cache->H_kv != 0 ||
+      max_pages < 0 || (!packed && T != B))
+    return 0;
+  const int group = H_q / cache->H_kv;
+  return workspace_of_call(cache, T, B, group, packed != 0, stream_shape(cache, T, B, group, packed != 0, max_pages));
 }
 
 int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,

@@ -49,7 +49,7 @@ def _load_calls():
         spec.loader.exec_module(module)
         lib = load()
         module.setup(*(ctypes.cast(getattr(lib, name), _P).value for name in (
-            "attn_paged_append", "attn_paged_decode", "attn_paged_fwd", "attn_paged_fwd_workspace_bytes")), torch)
+            "attn_paged_append", "attn_paged_decode", "attn_paged_fwd", "attn_paged_call_workspace_bytes")), torch)
         _calls = module
     return _calls
 
@@ -254,8 +254,7 @@ def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, 
     The default scale is 1/sqrt(d). The workspace (paged_workspace_bytes) is
     allocated with torch unless given."""
     if out is None and lse is None and workspace is None:
-        r = cache._calls.decode(cache._ref, cache._index, cache.device, cache._decode_bytes, q, page_table, kv_lens,
-                                scale)
+        r = cache._calls.decode(cache._ref, cache._index, cache.device, q, page_table, kv_lens, scale)
         if r is not NotImplemented:
             if type(r) is int:
                 _check(r, "attn_paged_decode")

@@ -322,9 +322,14 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
  * between calls, and calls that may run at the same time need one each. A decoding
  * call needs 8 MB at most; a chunk call at most 41 MB for the parts of divided tiles,
  * and over an e4m3 cache 2 d + 4 bytes per query row and head besides.
+ * attn_paged_call_workspace_bytes is what one call needs with that page table width: 0
+ * for short work, whose workspace may be NULL, else the same (packed: a chunk call, with
+ * seqlens; without T == B).
  */
 size_t attn_paged_decode_workspace_bytes(int d);
 size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, int type);
+size_t attn_paged_call_workspace_bytes(const attn_paged_cache* cache, int T, int B, int H_q, int packed,
+                                       int max_pages);
 
 /*
  * Attention of one query token per sequence over its kv_lens[b] cached keys:

@@ -104,8 +104,12 @@ def test_attention_refusals(lib, name):
     need = (lib.attn_paged_decode_workspace_bytes(64) if name == "decode" else
             lib.attn_paged_fwd_workspace_bytes(3, 3, 4, 2, 64, 0))
     assert need > 0
-    assert _call(lib, name, size=need - 1) == WORKSPACE
-    assert _call(lib, name, ws=None) == WORKSPACE
+    c, wide = _cache(), dict(max_pages=10000, stride=10000)
+    of_call = lambda pages: lib.attn_paged_call_workspace_bytes(ctypes.addressof(c), 3, 3, 4, name == "fwd", pages)  # noqa: E731
+    assert of_call(10000) == need and of_call(5) == 0
+    assert _call(lib, name, size=need - 1, **wide) == WORKSPACE
+    assert _call(lib, name, ws=None, **wide) == WORKSPACE
+    assert _call(lib, name, ws=A + 128, **wide) == ALIGN
     assert _call(lib, name, ws=A + 128) == ALIGN
 
 
@@ -123,6 +127,10 @@ def test_workspace_bytes(lib):
     for bad in ((-1, 1, 1, 1, 64, 0), (1, -1, 1, 1, 64, 0), (1, 1, 0, 1, 64, 0), (1, 1, 3, 2, 64, 0),
                 (1, 1, 1, 0, 64, 0), (1, 1, 1, 1, 96, 0), (1, 1, 1 << 20, 1, 64, 0), (1, 1, 1, 1, 64, 2)):
         assert f(*bad) == 0
+    c, of_call = _cache(), lib.attn_paged_call_workspace_bytes
+    for bad in ((0, 0, 4, 0, 5), (3, 3, 0, 0, 5), (3, 3, 5, 0, 5), (3, 3, 4, 0, -1), (3, 2, 4, 0, 10000)):
+        assert of_call(ctypes.addressof(c), *bad) == 0
+    assert of_call(None, 3, 3, 4, 0, 10000) == 0
     assert lib.attn_paged_decode_workspace_bytes(64) > 0 and lib.attn_paged_decode_workspace_bytes(96) == 0
 
 
