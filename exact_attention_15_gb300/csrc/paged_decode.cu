@@ -370,7 +370,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       x.b = -1;
       ok = give(nth);
     }
-    if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
+    if (!ok) {
+      if (lane == 0) record_error(p.s.err, kErrTimeout);
+      // no copy may still be on its way when the CTA's shared memory goes
+      for (int s = 0; s < Cfg::kStages; ++s) mbar_wait_warp(full + 8 * s, s < stage ? phase : phase ^ 1, lim);
+    }
     // off the way of the loads: what no work unit covers
     if (!CLUSTER && !split_head && lane == 0) p.heads[2 * cta] = make_int4(0, 0, 0, 0);
     if (cta == 0) check_paged_seqs(p.s, lane, 32);

@@ -80,6 +80,7 @@ struct PagedBars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t raw_full[8], raw_empty[8];  // e4m3
   uint64_t sched_full[kSlots], sched_empty[kSlots];
+  uint64_t drained;  // after a failure: the products in flight
   int sched_taken;  // work tiles that the producer has taken so far
   PagedTile sched_t[kSlots];
   uint32_t tmem_base;
@@ -277,6 +278,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mbar_init(smem_addr(&bars->raw_full[i]), 1);
       mbar_init(smem_addr(&bars->raw_empty[i]), 1);
     }
+    mbar_init(smem_addr(&bars->drained), 1);
     bars->sched_taken = 0;
     fence_barrier_init();
   }
@@ -376,7 +378,15 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-      if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
+      if (!ok) {
+        if (lane == 0) record_error(p.s.err, kErrTimeout);
+        // no copy may still be on its way when the CTA's shared memory goes
+        constexpr uint32_t kRing = E4M3 ? Cfg::kRawStages : Cfg::kStages;
+        uint64_t* landed = E4M3 ? bars->raw_full : bars->kv_full;
+        for (uint32_t n = ld > kRing ? ld - kRing : 0; n < ld; ++n)
+          mbar_wait_warp(smem_addr(&landed[n % kRing]), (n / kRing) & 1, lim);
+        if (qk > 0) mbar_wait_warp(smem_addr(&bars->q_full), (qk - 1) & 1, lim);
+      }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const bool leader = elect_one_sync();
@@ -462,7 +472,12 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         ld += 2 * n_kv;
       }
-      if (!ok && leader) record_error(p.s.err, kErrTimeout);
+      if (!ok) {
+        if (leader) record_error(p.s.err, kErrTimeout);
+        // nor may a product be when its memory goes
+        mma_commit_by(leader, smem_addr(&bars->drained));
+        mbar_wait_warp(smem_addr(&bars->drained), 0, lim);
+      }
     } else if (!E4M3 && warp == 2 && lane == 0) {
       // -------------------------------------------------------- scheduler
       // Near the end of a claimed list a tile is claimed only once the producer has
