@@ -780,21 +780,21 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   grid_release();
   if (tid == 0) *p.tile_ctr = 0;
   // the sum of x over the threads before this one, and over all
-  auto scan = [&](long long x, long long& all) {
-    long long in = x;
+  auto scan = [&](auto x, auto& all) {
+    auto in = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, in, o);
+      const auto y = __shfl_up_sync(0xffffffffu, in, o);
       if (lane >= o) in += y;
     }
     __syncthreads();
     if (lane == 31) warp_sum[w] = in;
     __syncthreads();
-    long long sum = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
-    const long long own = sum;
+    auto sum = static_cast<decltype(x)>(lane < kPlanThreads / 32 ? warp_sum[lane] : 0);
+    const auto own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      const auto y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
     all = __shfl_sync(0xffffffffu, sum, 31);
@@ -865,49 +865,59 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   // and the shares of the rest that even the CTAs out.
   __syncthreads();
   const int grid = p.grid, waves = total / grid, rest = total - waves * grid;
-  long long rest_all, whole_all, share_all;
-  const long long first = scan(tid < rest ? unit[waves * grid + tid] : 0, rest_all);
+  int rest_all;  // (less than 152 tiles of 2^23 units)
+  const int first = scan(tid < rest ? unit[waves * grid + tid] : 0, rest_all);
   if (tid <= rest) {
-    rest_units[tid] = static_cast<int>(tid < rest ? first : rest_all);
+    rest_units[tid] = tid < rest ? first : rest_all;
     p.rest_units[tid] = rest_units[tid];
   }
-  long long whole = 0;
-  if (tid < grid)
-    for (int i = 0; i < waves; ++i) whole += unit[i * grid + tid];
-  scan(whole, whole_all);
+  long long whole = 0, whole_all = 0, share_all;
+  if (waves > 0) {
+    if (tid < grid)
+      for (int i = 0; i < waves; ++i) whole += unit[i * grid + tid];
+    scan(whole, whole_all);
+  }
   // Kept whole, tile x of the rest goes to CTA grid - rest + x (the last ones' whole
   // tiles are the shortest).
   const int spare = grid - rest;
   if (tid >= spare && tid < grid) atomicMax(&longest, static_cast<int>(whole) + unit[waves * grid + tid - spare]);
   // Cut, pieces of less than six units cost more than they spread: the last `wide`
   // CTAs share the rest, each at least a tile's worth.
-  const long long wide = max(static_cast<long long>(rest), min(static_cast<long long>(grid), rest_all / 6));
-  const long long level = (whole_all + rest_all) / grid;
-  const long long share = tid >= grid || tid < grid - wide ? 0
-                          : waves == 0 || wide < grid      ? 1
-                                                           : max(0ll, level - whole);
-  const long long before = scan(share, share_all);
+  const int wide = max(rest, min(grid, rest_all / 6));
+  const long long level = waves > 0 ? (whole_all + rest_all) / grid : 0;
   // Leaving and joining the pieces takes as long as about three units, and one more for
   // every 16 tiles of the rest (d 128; 32 for 64): below that the tiles stay whole. 1000
   // new tokens of one prompt, 32 heads on 8, 128 tiles: whole 26.7 us, cut 35.0; 1500 of 8
   // heads of 64, 48 tiles: 27.4 and 23.5.
-  const long long even = waves == 0 ? (wide > 0 ? rest_all / wide : 0) : level;
-  const bool cut = longest > even + 3 + (rest * p.d >> 11);
+  const long long even = waves > 0 ? level : wide > 0 ? rest_all / wide : 0;
+  __syncthreads();
+  if (longest <= even + 3 + (rest * p.d >> 11)) {
+    if (tid < grid) {
+      const int x = tid - spare;
+      p.shares[tid] = x >= 0 ? make_int4(rest_units[x], rest_units[x + 1], x, 0) : make_int4(0, 0, 0, 0);
+      p.rest_owners[tid] = make_int2(0, 0);
+    }
+    return;
+  }
+  const long long share = tid >= grid || tid < grid - wide ? 0
+                          : waves == 0 || wide < grid      ? 1
+                                                           : max(0ll, level - whole);
+  const long long before = scan(share, share_all);
   // (without room below the mean the last CTA takes the rest)
   if (tid <= grid)
-    rest_start[tid] = tid == grid ? static_cast<int>(rest_all)
-                      : !cut      ? rest_units[max(0, tid - spare)]
-                      : share_all > 0 ? static_cast<int>(rest_all * before / share_all) : 0;
+    rest_start[tid] = tid == grid ? rest_all : share_all > 0 ? static_cast<int>(rest_all * before / share_all) : 0;
   __syncthreads();
-  if (tid < grid) {
-    const int u = rest_start[tid], end = rest_start[tid + 1];
-    p.shares[tid] = make_int4(u, end, u < end ? find_last(rest_units, rest, u) : 0, 0);
-  }
-  if (tid < grid) {
-    const int begin = tid < rest ? rest_units[tid] + kItemCost : 0;  // its key tiles' units
-    const int end = tid < rest ? rest_units[tid + 1] : 0;
-    p.rest_owners[tid] = begin < end ? make_int2(find_last(rest_start, grid, begin), find_last(rest_start, grid, end - 1))
-                                     : make_int2(0, 0);
+  // three searches, by different threads
+  const int part = tid / kFwdSms, c = tid - part * kFwdSms;
+  if (c >= grid) return;
+  if (part == 0) {
+    const int u = rest_start[c], end = rest_start[c + 1];
+    p.shares[c] = make_int4(u, end, u < end ? find_last(rest_units, rest, u) : 0, 0);
+  } else if (part < 3) {
+    // the CTAs that hold the first and the last unit of tile c's keys
+    const int begin = c < rest ? rest_units[c] + kItemCost : 0, end = c < rest ? rest_units[c + 1] : 0;
+    reinterpret_cast<int*>(p.rest_owners)[2 * c + part - 1] =
+        begin < end ? find_last(rest_start, grid, part == 1 ? begin : end - 1) : 0;
   }
 }
 
