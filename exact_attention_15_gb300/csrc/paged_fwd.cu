@@ -779,6 +779,7 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   grid_wait();
   grid_release();
   if (tid == 0) *p.tile_ctr = 0;
+  check_paged_seqs(p.s, tid, blockDim.x);  // (its loads are those that follow)
   // the sum of x over the threads before this one, and over all
   auto scan = [&](auto x, auto& all) {
     auto in = x;
@@ -859,7 +860,6 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
     }
     unit[tid] = tile_units(t);
   }
-  check_paged_seqs(p.s, tid, blockDim.x);
   if (!p.split) return;
   // Few work tiles: the units of every CTA's whole tiles, of each tile of the rest,
   // and the shares of the rest that even the CTAs out.
