@@ -155,14 +155,16 @@ FwdPlan fwd_plan(int T, int B, int group, int H_kv, int d, bool e4m3) {
 bool few_rows(int T, int B, int group) {
   return group > kTileM || static_cast<long long>(T) * group <= 16ll * B;
 }
-// So does little work, by its units (tiles of 64 keys of 16 rows) and what the page
-// table can hold: 100 new tokens of each of 2 prompts behind 1000, 8 heads on 2 (1872
-// units), take 16.3 us there and 30 with the planning kernel and its tiles, 256 of one prompt, 32
-// heads on 8 (2080), 20.6 and 17.
-bool little_work(int T, int B, int group, int H_kv, long long keys) {
-  const long long chunks = (static_cast<long long>(T) * group + 15) / 16 + B;
-  const long long tiles = (keys + kStreamTile - 1) / kStreamTile;
-  return chunks * H_kv * tiles <= 2000;
+// So does little work, by its items (16 rows of a KV head) and what the page table can
+// hold: tiles of 64 keys, by their bytes, and about ten more for each item. 20 new tokens
+// of each of 2 prompts behind 2500 keys, 32 heads on 8 (4800 units), take 19.4 us there and 26.0
+// with the planning kernel and its tiles, 20 of one behind 9000 (7200) 27.4 and 30.3, 64 behind
+// 4000 (10,000) 31.9 and 28.0; 350 of a prompt over an e4m3 cache (9200) 27.7 and 20.1.
+bool little_work(const attn_paged_cache* c, int T, int B, int group, int max_pages) {
+  const long long items = ((static_cast<long long>(T) * group + 15) / 16 + B) * c->H_kv;
+  const long long keys = static_cast<long long>(max_pages) * c->page_size;
+  const long long bytes = keys * c->d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2);
+  return items * (bytes / (kStreamTile * 256) + 10) <= 8000;
 }
 
 // How the streaming kernel runs a call: chunks of 8 query rows where a sequence's rows of
@@ -325,7 +327,7 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (!seqlens || few_rows(T, B, group) || shape.cluster > 0 ||
-      little_work(T, B, group, c->H_kv, static_cast<long long>(max_pages) * c->page_size))
+      little_work(c, T, B, group, max_pages))
     return launch_stream(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, lse_row, lse_head, shape, cs);
   return launch_fwd(dev, c, seqs, q, o, lse, H_q, causal, scale, ws, cs);
 }

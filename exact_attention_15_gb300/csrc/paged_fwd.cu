@@ -674,8 +674,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (t.slot >= 0) {
         // A piece: maxima, sums and O as they are. O passes through the warp's part of the
         // staging block, 32 columns at a time, so that the stores are whole lines: straight
-        // from the registers, 16 bytes of a row each, two prompts of 512 behind 4000 to 8000
-        // keys (32 heads on 8) took 91 us for 87.
+        // from the registers, 16 bytes of a row each, they cost 4 us more where 128 tiles are
+        // cut (d 128).
         const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM;
         if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used - lift, l);
         if (my_n > 0) {
@@ -887,8 +887,8 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
   const long long level = waves > 0 ? (whole_all + rest_all) / grid : 0;
   // Leaving and joining the pieces takes as long as about three units, and one more for
   // every 16 tiles of the rest (d 128; 32 for 64): below that the tiles stay whole. 1000
-  // new tokens of one prompt, 32 heads on 8, 128 tiles: whole 26.7 us, cut 35.0; 1500 of 8
-  // heads of 64, 48 tiles: 27.4 and 23.5.
+  // new tokens of one prompt, 32 heads on 8, 128 tiles: whole 24.9 us, cut 34.4; 1500 of 8
+  // heads of 64, 48 tiles: 25.6 and 23.0.
   const long long even = waves > 0 ? level : wide > 0 ? rest_all / wide : 0;
   __syncthreads();
   if (longest <= even + 3 + (rest * p.d >> 11)) {
@@ -925,8 +925,8 @@ paged_plan_kernel(const PagedFwdParams p, int sort) {
 // 16 y + 15 of tile x of the rest, two at once for each warp. Latency is what it costs,
 // so all loads of four pieces are on their way together: of 3 sequences of 198 new tokens behind
 // 15000 keys (5 heads on 1, d 64), a call takes 31 us, with one load after the other 43.
-// Four rows at once leave one CTA on an SM (two prompts of 512 behind 4000 to 8000 keys,
-// 32 heads on 8: 96 us; two rows 84, one row 86).
+// Where 128 tiles are cut (d 128), one row at a time costs 2 us more, and four, which
+// leave one CTA on an SM, 12.
 constexpr int kJoinRows = 16;
 template <int D>
 __global__ void __launch_bounds__(256)
