@@ -31,12 +31,13 @@ def _q(n, H_q, d, seed=1):
     return torch.randn(n, H_q, d, generator=g, device="cuda").to(torch.bfloat16)
 
 
-def _table(c, wide):
-    """The page table, or a wide one with the same pages: where a table holds little, a
-    call of little work runs on clusters of the streaming kernel whatever its rows."""
-    if not wide:
+def _table(c, tokens):
+    """The page table, or one that could hold that many tokens a sequence: what a table
+    can hold decides which kernel a call of little work runs on (clusters, dealt-out
+    units, the tensor cores)."""
+    if not tokens:
         return c.table
-    table = torch.full((len(c.lens), 100000 // c.page), -7, dtype=torch.int32, device="cuda")
+    table = torch.full((len(c.lens), max(c.width, tokens // c.page)), -7, dtype=torch.int32, device="cuda")
     table[:, :c.width] = c.table
     return table
 
@@ -98,7 +99,7 @@ def test_decode_of_short_and_of_wide_tables(case, kind):
     c = Cache(lens, H_kv, d, page, kind, seed=case)
     h, q = c.handle(), _q(len(lens), H_q, d)
     want = _decode_want(c, q, 1.0 / math.sqrt(d))
-    for table in (c.table, _table(c, True)):
+    for table in (c.table, _table(c, 100000)):
         o, lse = binding.paged_decode(h, q, table, c.kv_lens)
         assert_attention(o, lse, *want, what=tuple(table.shape))
         again = binding.paged_decode(h, q, table, c.kv_lens)
@@ -181,7 +182,7 @@ def test_decode_large_query_values_over_e4m3():
         assert_attention(o, lse, *_decode_want(c, q, scale), what=factor)
 
 
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_chunk_large_query_values_over_e4m3(wide):
     """The same in the tensor-core kernel's fp16 queries, and given buffers."""
     c = Cache([300, 200], 2, 128, 16, "e4m3")
@@ -195,7 +196,7 @@ def test_chunk_large_query_values_over_e4m3(wide):
 
 
 @pytest.mark.parametrize("n", [1, 130])
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_small_weights_over_e4m3(wide, n):
     """A key with weight 1 and no value next to 199 with weights of 2^-19: they keep the
     accuracy of larger ones (as fp16 numbers of their own they would have 5 bits)."""
@@ -288,7 +289,7 @@ MANY = [
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("case", range(len(MANY)))
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_chunk_of_many(wide, case, kind):
     new, lens, H_q, H_kv, d, page = MANY[case]
     c = Cache(lens, H_kv, d, page, kind, seed=case)
@@ -356,7 +357,7 @@ def _offsets(new):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("case", range(len(CHUNK)))
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 16000, 100000])
 def test_chunk(wide, case, kind, causal):
     new, lens, H_q, H_kv, d, page = CHUNK[case]
     c = Cache(lens, H_kv, d, page, kind, seed=case)
@@ -368,7 +369,7 @@ def test_chunk(wide, case, kind, causal):
 
 
 @pytest.mark.parametrize("n", [3, 200])
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_chunk_leaves_rows_behind_the_last_sequence(wide, n):
     new = [n, 2 * n]
     c = Cache([n, 500], 2, 128, 16)
@@ -382,7 +383,7 @@ def test_chunk_leaves_rows_behind_the_last_sequence(wide, n):
 
 
 @pytest.mark.parametrize("n", [2, 300])
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_chunk_captured(wide, n):
     """A captured call replays over other lengths in the same buffers."""
     c = Cache([1000, 400], 2, 64, 16, width=70)
@@ -401,7 +402,7 @@ def test_chunk_captured(wide, n):
         assert_attention(o, lse, *_chunk_want(c, q, new, 1.0 / 8.0, True))
 
 
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 100000])
 def test_chunk_agrees_with_the_packed_forward(wide):
     """A fresh prompt through the cache gives what attn_fwd gives on its rows: both
     within bf16's rounding of P and of O of the same value."""
