@@ -35,13 +35,14 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 }
 // x / s, rounded to nearest, from the rounded inverse of s: the product's residual
 // corrects it (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990). For infinities and NaN the residual is NaN, and the
-// product stands. The inverse alone would now and then land on the other side of a
-// rounding border of e4m3; a division per value cost a sixth of the kernel's time
-// over an e4m3 cache.
+// System/6000 processor", 1990). The product stands where the residual is no number to
+// correct with: NaN for an infinite or NaN x, an infinity where x is finite and the product
+// passes 32 bits (3e38 by 0.5), whose correction would be the NaN inf - inf. The inverse
+// alone would now and then land on the other side of a rounding border of e4m3; a division
+// per value cost a sixth of the kernel's time over an e4m3 cache.
 __device__ __forceinline__ float quotient(float x, float s, float inverse) {
   const float q = x * inverse, r = __fmaf_rn(-q, s, x);
-  return r == r ? __fmaf_rn(r, inverse, q) : q;
+  return fabsf(r) < INFINITY ? __fmaf_rn(r, inverse, q) : q;
 }
 __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale, float inverse) {
   float y[8];
