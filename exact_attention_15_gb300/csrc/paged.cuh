@@ -92,10 +92,10 @@ cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream
 // A power of two that brings a row whose largest magnitude is `top` to [1, 2) when
 // it divides the row; its inverse is in `down`. fp16 then holds bf16 values exactly
 // but for what lies below 2^-25 of the largest, whatever their range was.
-// Infinities stay infinities.
+// Infinities stay infinities; a row of zeros is left alone (its power would be 2^-126).
 __device__ __forceinline__ float row_power(float top, float& down) {
   int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-  ex = ex > 127 ? 0 : max(-126, min(126, ex));
+  ex = ex > 127 || top == 0.0f ? 0 : max(-126, min(126, ex));
   down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 }

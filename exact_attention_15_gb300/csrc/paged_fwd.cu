@@ -594,10 +594,15 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // keys that this row sees: one comparison per score covers both masks
       const int see = p.causal ? min(t.len, see0 + tok_r + 1) : t.len;
       float c = p.scale_log2;
+      if constexpr (E4M3) c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
+      // the same in every lane: softmax_row_max votes within either branch
+      const bool pos = c > 0.0f;
       if constexpr (E4M3) {
-        c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
         if (tok_r < p.tok_tile && tok < t.n_new)
           c *= p.q_up[(static_cast<size_t>(t.row0) + tok) * p.H_q + t.h * p.group + head_r];
+        // A row of tiny queries can bring c to 0, and -inf of a masked score times 0 is NaN:
+        // the smallest normal number in its place moves no score by more than 2^-108.
+        if (pos) c = fmaxf(c, 1.17549435e-38f);
       }
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
@@ -616,7 +621,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t pk[64];
         bool rescale_warp;
         float factor;
-        const bool pos = c > 0.0f;
         const float mb = pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
                                                      rescale_warp, factor)
                              : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,

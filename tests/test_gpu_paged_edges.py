@@ -1,5 +1,7 @@
 """The paged key-value cache at the ends of its range."""
 
+import math
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -7,7 +9,9 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from exact_attention_15_gb300 import binding  # noqa: E402
-from paged_common import E4M3_MAX, Cache  # noqa: E402
+from paged_common import E4M3_MAX, Cache, assert_attention, attention  # noqa: E402
+
+WIDE = 100000  # tokens that a page table can hold: a chunk call then takes the tensor-core kernel
 
 
 @pytest.fixture(autouse=True)
@@ -17,8 +21,33 @@ def _clean():
     assert binding.attn_check(None) == 0
 
 
+def _q(n, H, d, seed=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(n, H, d, generator=g, device="cuda").to(torch.bfloat16)
+
+
 def _offsets(new):
     return torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32, device="cuda")
+
+
+def _table(c, tokens):
+    """The page table, or one that could hold that many tokens a sequence."""
+    table = torch.full((len(c.lens), max(c.width, tokens // c.page)), -7, dtype=torch.int32, device="cuda")
+    table[:, :c.width] = c.table
+    return table
+
+
+def _want(c, q, new, scale, causal=True):
+    o, a, lse, t0 = [], [], [], 0
+    for b, n in enumerate(new):
+        L = c.lens[b]
+        last = torch.full((n,), L, device="cuda")
+        if causal:
+            last = torch.clamp(L - n + 1 + torch.arange(n, device="cuda"), min=0)
+        r = attention(q[t0:t0 + n], c.keys[b], c.values[b], scale, last)
+        o.append(r[0]), a.append(r[1]), lse.append(r[2])
+        t0 += n
+    return torch.cat(o), torch.cat(a), torch.cat(lse, 1)
 
 
 @pytest.mark.parametrize("x, scale", [(3e38, 0.5), (3.3e38, 0.9375), (1e37, 0.01), (1e30, 1e-9), (1e20, 1e-20), (1e10, 1e-29),
@@ -38,3 +67,22 @@ def test_append_finite_values_past_the_range(x, scale):
     want = torch.where(k == 0, torch.zeros_like(k), torch.copysign(torch.full_like(k, E4M3_MAX), k)).float()
     for cache in (c.k, c.v):
         assert torch.equal(c.get(cache, 0, 0, 2).float(), want)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("wide", [0, WIDE])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_rows_of_zeros_and_tiny_rows_over_e4m3(d, wide, causal):
+    """Rows of zeros and of tiny values between rows of large ones, whose scale is small: the
+    product of the scales and a row's power of two passes below 32 bits in some rows of a
+    warp and not in others."""
+    new = [150, 200]
+    c = Cache([300, 200], 2, d, 16, "e4m3")
+    q = _q(350, 8, d).float() * 2.0 ** 40
+    q[::3] = 0.0
+    q[1::5] *= 2.0 ** -150
+    q[7, :4] = 0.0
+    q = q.to(torch.bfloat16)
+    for scale in (2.0 ** -40 / math.sqrt(d), -(2.0 ** -40) / math.sqrt(d), 1e-36):
+        o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new), scale=scale, causal=causal)
+        assert_attention(o, lse, *_want(c, q, new, scale, causal), what=scale)
