@@ -604,7 +604,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // the smallest normal number in its place moves no score by more than 2^-108.
         if (pos) c = fmaxf(c, 1.17549435e-38f);
       }
-      float m_used = -INFINITY, l = 0.0f;
+      // Rows of the tile that are no query row of this sequence (what an earlier call left
+      // behind the last whole token, the next sequence's rows) have no part in the warp's
+      // votes: a bias of +inf never moves, and their P is 0 or NaN in their own rows of O,
+      // which are not written.
+      float m_used = tok_r < p.tok_tile && tok < t.n_new ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
         if (!mbar_wait(smem_addr(&bars->s_full[i]), sw & 1, lim)) { ok = false; break; }
         ++sw;

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from exact_attention_15_gb300 import binding  # noqa: E402
-from paged_common import E4M3_MAX, Cache, assert_attention, attention  # noqa: E402
+from paged_common import E4M3_MAX, Cache, as_int, assert_attention, attention  # noqa: E402
 
 WIDE = 100000  # tokens that a page table can hold: a chunk call then takes the tensor-core kernel
 
@@ -86,3 +86,50 @@ def test_chunk_rows_of_zeros_and_tiny_rows_over_e4m3(d, wide, causal):
     for scale in (2.0 ** -40 / math.sqrt(d), -(2.0 ** -40) / math.sqrt(d), 1e-36):
         o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new), scale=scale, causal=causal)
         assert_attention(o, lse, *_want(c, q, new, scale, causal), what=scale)
+
+
+def _fill_query_tiles(d, kind, factor):
+    """A chunk call that fills every row of the query tiles of all CTAs."""
+    c = Cache([10300], 4, d, 64, kind, seed=5)
+    q = (_q(10300, 4, d, seed=6).float() * factor).to(torch.bfloat16)
+    binding.paged_forward(c.handle(), q, c.table, c.kv_lens, _offsets([10300]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 7, 24])
+def test_chunk_does_not_depend_on_the_call_before(group, d, kind):
+    """Groups that do not divide a tile's 128 rows leave rows that no copy writes: what an
+    earlier call left there changes no bit of a result."""
+    new = [200, 50]
+    c = Cache([2000, 1500], 2, d, 64, kind, seed=2)
+    h, q, table, cu = c.handle(), _q(250, 2 * group, d), _table(c, WIDE), _offsets(new)
+    got = []
+    for factor in (0.0, 40.0, 0.01, -40.0):
+        _fill_query_tiles(d, kind, factor)
+        got.append(binding.paged_forward(h, q, table, c.kv_lens, cu))
+    assert_attention(*got[0], *_want(c, q, new, 1.0 / math.sqrt(d)))
+    for o, lse in got[1:]:
+        assert torch.equal(as_int(o), as_int(got[0][0])) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [1, 5, 8])
+def test_chunk_does_not_depend_on_rows_of_others(group, kind):
+    """The rows of q behind the last sequence, and the next sequence's, lie in the last
+    tile of one: they change no bit of it."""
+    d, new = 128, [190, 30]
+    c = Cache([2000, 1500], 2, d, 64, kind, seed=3)
+    h, table, cu = c.handle(), _table(c, WIDE), _offsets(new)
+    q = _q(300, 2 * group, d)
+    got = []
+    for factor in (1.0, 40.0):
+        x = q.clone()
+        x[220:] *= factor
+        got.append([t for t in binding.paged_forward(h, x, table, c.kv_lens, cu)])
+    assert torch.equal(as_int(got[0][0][:220]), as_int(got[1][0][:220]))
+    assert torch.equal(got[0][1][:, :220], got[1][1][:, :220])
+    x = q.clone()
+    x[190:220] *= 40.0
+    o, lse = binding.paged_forward(h, x, table, c.kv_lens, cu)
+    assert torch.equal(as_int(o[:190]), as_int(got[0][0][:190])) and torch.equal(lse[:, :190], got[0][1][:, :190])
