@@ -71,6 +71,7 @@ KERNEL_NAMES = {1: "attn_fwd_kernel", 2: "attn_bwd_pre_kernel", 3: "attn_bwd_mai
                 16: "queries_f16_kernel"}
 FAULT_NONE = 0
 FAULT_SKIP_DQ_RELEASE = 1
+FAULT_LEAVE_WARP = 2
 BWD_ONE_CTA = 0
 BWD_CTA_PAIR = 1
 FWD_ONE_CTA = 0

@@ -513,6 +513,7 @@ int host_setup(HostDevice* out) {
   out->n_sm = sm_count(out->dev);
   out->encode = g_encode;
   out->wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+  out->fault = g_fault.load(std::memory_order_relaxed);
   return out->n_sm > 0 ? ATTN_OK : ATTN_ERR_CUDA;
 }
 int prof_begin(int kernel, cudaStream_t stream) {
@@ -916,7 +917,8 @@ int attn_debug_fwd_plan(int B, int H_q, int H_kv, int N_q, int N_k, int d_qk, in
 }
 
 int attn_debug_inject(int fault) {
-  if (fault != ATTN_FAULT_NONE && fault != ATTN_FAULT_SKIP_DQ_RELEASE) return ATTN_ERR_BAD_SHAPE;
+  if (fault != ATTN_FAULT_NONE && fault != ATTN_FAULT_SKIP_DQ_RELEASE && fault != ATTN_FAULT_LEAVE_WARP)
+    return ATTN_ERR_BAD_SHAPE;
   std::lock_guard<std::mutex> lock(g_mu);
   g_fault.store(fault);
   return ATTN_OK;

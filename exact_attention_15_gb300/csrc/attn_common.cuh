@@ -35,7 +35,7 @@ constexpr float kTau = ATTN_TAU;
 // table or a cache length points outside the paged cache.
 enum DevErr : int { kErrNone = 0, kErrTimeout = 1, kErrSeqlens = 2, kErrPages = 3 };
 // Host-injected faults (attn_debug_inject); none of them can fault or hang the GPU.
-enum Fault : int { kFaultNone = 0, kFaultSkipDqRelease = 1 };
+enum Fault : int { kFaultNone = 0, kFaultSkipDqRelease = 1, kFaultLeaveWarp = 2 };
 
 struct FwdParams {
   void* o;              // bf16

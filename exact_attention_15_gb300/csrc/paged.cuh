@@ -142,6 +142,7 @@ struct StreamParams {
   int cluster;        // CTAs of a cluster, 0: the units are dealt out
   long long items;    // clusters
   int grid, cluster_shift;  // set by the launch
+  int fault;
   long long wait_limit;
 };
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,

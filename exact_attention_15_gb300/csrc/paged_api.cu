@@ -246,6 +246,7 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.part_ml = reinterpret_cast<float*>(ws + plan.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
   p.wait_limit = dev.wait_limit;
+  p.fault = dev.fault;
   p.cluster = shape.cluster;
   p.items = shape.items;
   return launch_paged_stream(tk, tv, p, c->d, shape.rows, c->type == ATTN_CACHE_E4M3, dev.n_sm, cs) == cudaSuccess

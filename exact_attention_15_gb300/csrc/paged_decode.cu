@@ -47,7 +47,7 @@ struct StreamCfg {
   static constexpr int kMlOff = kMergeOff + kMergeBytes;
   static constexpr int kRingOff = kMlOff + kWarps * 16 * 2 * 4;
   static constexpr int kBarOff = kRingOff + kRing * 48;
-  static constexpr int kPieceOff = kBarOff + (2 * kStages + 2 * kRing + 1) * 8;  // clusters: [16][2]
+  static constexpr int kPieceOff = kBarOff + (2 * kStages + 2 * kRing + 2) * 8;  // clusters: [16][2]
   static constexpr int kSmemBytes = kPieceOff + 16 * 2 * 4;
   // the CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
   static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory of an SM");
@@ -240,6 +240,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const uint32_t full = smem_addr(smem + Cfg::kBarOff), empty = full + 8 * Cfg::kStages;
   const uint32_t given = empty + 8 * Cfg::kStages, taken = given + 8 * kRing;  // of the ring
   const uint32_t merge_free = taken + 8 * kRing;  // the merge buffer has been read
+  const uint32_t merge_full = merge_free + 8;     // the four warps have written it
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long lim = p.wait_limit;
 
@@ -253,6 +254,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       mbar_init(taken + 8 * i, kWarps);
     }
     mbar_init(merge_free, kWarps);
+    mbar_init(merge_full, kWarps);
     fence_barrier_init();
   }
   float* piece_o = reinterpret_cast<float*>(smem);  // clusters: [R][D], once the tiles are read
@@ -443,7 +445,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   int nth = 0;  // pieces taken
   auto take = [&]() {  // the next piece, in every lane
     const int at = nth % kRing;
-    if (!mbar_wait_warp(given + 8 * at, (nth / kRing) & 1, lim)) {
+    if (!mbar_wait_warp(given + 8 * at, (nth / kRing) & 1, lim) || (p.fault == kFaultLeaveWarp && warp == 1)) {
       if (lane == 0) record_error(p.s.err, kErrTimeout);
       return false;
     }
@@ -512,8 +514,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     for (int t = x.t0; t < x.t1; ++t) {
       if (ok && !mbar_wait_warp(full + 8 * stage, phase, lim)) {
         // the copies may still be on their way: one more bounded wait, then the
-        // rest of the work is walked without waiting so that every warp reaches
-        // the same barriers
+        // rest of the work is walked without waiting
         if (lane == 0) record_error(p.s.err, kErrTimeout);
         mbar_wait_warp(full + 8 * stage, phase, lim);
         ok = false;
@@ -696,7 +697,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
           }
         }
-      named_bar_sync(1, 32 * kWarps);
+      // A warp whose wait for a piece ran out has left, so the others may wait for it here
+      // in vain: not a counted barrier, which would hold them for ever.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merge_full);
+      if (!mbar_wait_warp(merge_full, (merges - 1) & 1, ok ? lim : 0)) {
+        if (lane == 0) record_error(p.s.err, kErrTimeout);
+        ok = false;
+      }
       if (r < rows) {
         float2 w[kWarps];
         float top = -INFINITY, sum = 0.0f;

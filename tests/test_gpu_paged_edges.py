@@ -133,3 +133,34 @@ def test_chunk_does_not_depend_on_rows_of_others(group, kind):
     x[190:220] *= 40.0
     o, lse = binding.paged_forward(h, x, table, c.kv_lens, cu)
     assert torch.equal(as_int(o[:190]), as_int(got[0][0][:190])) and torch.equal(lse[:, :190], got[0][1][:, :190])
+
+
+SHORT_LIMIT = 2_000_000  # cycles, about a millisecond
+
+
+def _with_a_warp_that_leaves(call):
+    """The call's status when one warp of each CTA leaves as if its wait had run out, and the
+    outputs of the same call before and after it."""
+    before = [t.clone() for t in call()]
+    assert binding.attn_check(None) == 0
+    old = binding.attn_set_wait_limit(SHORT_LIMIT)
+    try:
+        assert binding.attn_debug_inject(binding.FAULT_LEAVE_WARP) == 0
+        call()
+        status = binding.attn_check(None)
+    finally:
+        assert binding.attn_debug_inject(binding.FAULT_NONE) == 0
+        binding.attn_set_wait_limit(old)
+    after = call()
+    assert all(torch.equal(a, b) for a, b in zip(before, after))
+    return status
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_a_warp_that_leaves_ends_one_token_attention(wide, kind):
+    """The other warps give up where they wait for it: the call ends, reports the time-out,
+    and the next one is right."""
+    c = Cache([2000, 700], 2, 128, 16, kind)
+    h, q, table = c.handle(), _q(2, 8, 128), _table(c, wide)
+    assert _with_a_warp_that_leaves(lambda: binding.paged_decode(h, q, table, c.kv_lens)) == 9  # ATTN_ERR_TIMEOUT
