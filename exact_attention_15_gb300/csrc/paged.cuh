@@ -174,11 +174,11 @@ struct PagedFwdParams {
   float* part_ml;    // workspace, split: [2 grid, 2, 128, 2]
   float* part_o;     // workspace, split: [2 grid, 2, 128, d]
   int grid;
+  int fault;
   long long wait_limit;
 };
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& to, const PagedFwdParams& p, int d, bool e4m3,
-                             cudaStream_t stream);
+                             const PagedFwdParams& p, int d, bool e4m3, cudaStream_t stream);
 // Queries as fp16 for products with an e4m3 cache: each row divided by a power of
 // two (kept in q_up) that brings its largest value to [1, 2).
 cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,

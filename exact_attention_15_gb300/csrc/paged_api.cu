@@ -89,10 +89,10 @@ int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cac
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 3-D map over q or o, [T, H_q, d] bf16 (or fp16): boxes of 64 columns, the heads of a group
+// 3-D map over q, [T, H_q, d] bf16 (or fp16): boxes of 64 columns, the heads of a group
 // and `tokens` tokens, 128-byte swizzle.
 int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int d, int H_q, int T,
-                    int group, int tokens, bool f16 = false) {
+                    int group, int tokens, bool f16) {
   const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(T)};
   cuuint64_t strides[2] = {row, row * H_q};
@@ -261,11 +261,10 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d, e4m3);
   const int box = e4m3 ? kTileN / 2 : kTileN;  // rows that land together
   const unsigned rows = c->page_size < box ? c->page_size : box;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv;
   int st;
   const void* queries = e4m3 ? ws + plan.q16_off : q;
   if ((st = encode_rows_map(dev, &tq, queries, c->d, H_q, seqs.T, group, plan.tok_tile, e4m3)) != ATTN_OK ||
-      (st = encode_rows_map(dev, &to, o, c->d, H_q, seqs.T, group, plan.tok_tile)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
     return st;
@@ -299,10 +298,11 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   const int sms = dev.n_sm < kFwdSms ? dev.n_sm : kFwdSms;
   p.grid = plan.split ? sms : dev.n_sm < p.max_work ? dev.n_sm : p.max_work;
   p.wait_limit = dev.wait_limit;
+  p.fault = dev.fault;
   if (e4m3 && launch_queries_f16(q, ws + plan.q16_off, reinterpret_cast<float*>(ws + plan.up_off),
                                  static_cast<long long>(seqs.T) * H_q, c->d, cs) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  return launch_paged_fwd(tq, tk, tv, to, p, c->d, e4m3, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_paged_fwd(tq, tk, tv, p, c->d, e4m3, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Both attention calls, after the checks they share.

@@ -248,8 +248,7 @@ struct TileSource {
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(384, 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                 const PagedFwdParams p) {
+                 const __grid_constant__ CUtensorMap tm_v, const PagedFwdParams p) {
   using Cfg = PagedFwdCfg<D, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -610,7 +609,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // which are not written.
       float m_used = tok_r < p.tok_tile && tok < t.n_new ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
-        if (!mbar_wait(smem_addr(&bars->s_full[i]), sw & 1, lim)) { ok = false; break; }
+        if (!mbar_wait_warp(smem_addr(&bars->s_full[i]), sw & 1, lim)) { ok = false; break; }
         ++sw;
         tc_fence_after();
         float s[128];
@@ -657,7 +656,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // for this warpgroup's next p_full arrival, i.e. after these loads.
       if (q0 >= t.n_new) continue;
       if (my_n > 0) {
-        if (!mbar_wait(smem_addr(&bars->pv_done[i]), pvw & 1, lim)) { ok = false; break; }
+        if (!mbar_wait_warp(smem_addr(&bars->pv_done[i]), pvw & 1, lim) ||
+            (p.fault == kFaultLeaveWarp && (warp & 3) == 1)) {
+          ok = false;
+          break;
+        }
         ++pvw;
         tc_fence_after();
       }
@@ -687,8 +690,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const size_t slot = (static_cast<size_t>(t.slot) * 2 + i) * kTileM;
         if (row_ok) *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m_used - lift, l);
         if (my_n > 0) {
-          if (r == 0) bulk_wait_group_read<0>();
-          named_bar_sync(2 + i, 128);
           const int row0 = r & ~31;
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -715,44 +716,38 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // a row with a NaN score has l = NaN and keeps it
       const float inv_l = l == 0.0f ? 0.0f : v_scale / l;
       const size_t row = static_cast<size_t>(t.row0) + tok;
-      // O leaves through shared memory, 64 columns at a time: by one TMA store of
-      // whole rows where the tile ends inside the sequence, else (the store's box
-      // would reach into the next sequence) by 128-byte runs of the rows it has
-      const bool box = q0 + p.tok_tile <= t.n_new;
+      // O leaves through the warp's part of the staging block, 64 columns at a time, in
+      // 128-byte runs: a row's place in o comes from the lane that holds it. The warps of a
+      // tile do not wait for one another anywhere, so that one whose wait runs out leaves
+      // alone (a TMA store of whole tiles, with two barriers of the four warps for each 64
+      // columns, took as long: 8 prompts 236 us either way).
+      const uint32_t to = row_ok ? static_cast<uint32_t>(row * p.H_q + hq) : 0xffffffffu;
 #pragma unroll
       for (int hf = 0; hf < Cfg::kBlocks; ++hf) {
-        uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(ov[hf * 64 + 2 * e]) * inv_l,
-                             __uint_as_float(ov[hf * 64 + 2 * e + 1]) * inv_l);
-        if (r == 0) bulk_wait_group_read<0>();
-        named_bar_sync(2 + i, 128);
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t w[4];
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(buf + sw128_offset(r, ch)) =
-              make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-        if (box) fence_async_shared();
-        named_bar_sync(2 + i, 128);
-        if (box) {
-          if (r == 0) {
-            tma_store_3d(&tm_o, smem_addr(buf), hf * 64, t.h * p.group, t.row0 + q0);
-            bulk_commit_group();
-          }
-        } else {
-          for (int x = r; x < rows * 8; x += 128) {
-            const int rr = x >> 3, tk = rr / p.group;
-            const size_t at = (static_cast<size_t>(t.row0 + q0 + tk) * p.H_q + t.h * p.group + rr - tk * p.group) * D;
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at + hf * 64 + (x & 7) * 8) =
-                *reinterpret_cast<const uint4*>(buf + sw128_offset(rr, x & 7));
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(ov[hf * 64 + 8 * ch + 2 * e]) * inv_l,
+                               __uint_as_float(ov[hf * 64 + 8 * ch + 2 * e + 1]) * inv_l);
+          *reinterpret_cast<uint4*>(buf + sw128_offset(r, ch)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int in = x * 4 + (lane >> 3);
+          const uint32_t at = __shfl_sync(0xffffffffu, to, in);
+          if (at != 0xffffffffu)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + static_cast<size_t>(at) * D + hf * 64 +
+                                      (lane & 7) * 8) =
+                *reinterpret_cast<const uint4*>(buf + sw128_offset((r & ~31) + in, lane & 7));
+        }
+        __syncwarp();
       }
       if (row_ok)
         p.lse[static_cast<size_t>(hq) * p.s.T + row] = l == 0.0f ? -INFINITY : (m_used - lift) * kLn2 + logf(l);
     }
-    // the O stores have read the staging buffer before the CTA's shared memory goes
-    if (r == 0) bulk_wait_group<0>();
     if (!ok) record_error(p.s.err, kErrTimeout);
   }
   tc_fence_before();
@@ -1049,7 +1044,7 @@ queries_f16_kernel(const uint2* q, uint2* q16, float* q_up, long long rows) {
 
 template <int D, bool E4M3>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& to, const PagedFwdParams& p, cudaStream_t stream) {
+                   const PagedFwdParams& p, cudaStream_t stream) {
   // sorting compares every pair of sequences and keeps them in shared memory
   const int sort = p.s.B <= 1024;
   int slot = prof_begin(kKPagedPlan, stream);
@@ -1059,7 +1054,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
   e = launch_chained<paged_fwd_kernel<D, E4M3>>(dim3(p.grid), 384, PagedFwdCfg<D, E4M3>::kSmemBytes, stream, tq, tk,
-                     tv, to, p);
+                     tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
   slot = prof_begin(kKPagedJoin, stream);
@@ -1071,10 +1066,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 }  // namespace
 
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const CUtensorMap& to, const PagedFwdParams& p, int d, bool e4m3,
-                             cudaStream_t stream) {
-  if (e4m3) return d == 128 ? launch<128, true>(tq, tk, tv, to, p, stream) : launch<64, true>(tq, tk, tv, to, p, stream);
-  return d == 128 ? launch<128, false>(tq, tk, tv, to, p, stream) : launch<64, false>(tq, tk, tv, to, p, stream);
+                             const PagedFwdParams& p, int d, bool e4m3, cudaStream_t stream) {
+  if (e4m3) return d == 128 ? launch<128, true>(tq, tk, tv, p, stream) : launch<64, true>(tq, tk, tv, p, stream);
+  return d == 128 ? launch<128, false>(tq, tk, tv, p, stream) : launch<64, false>(tq, tk, tv, p, stream);
 }
 
 cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,

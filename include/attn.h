@@ -407,9 +407,10 @@ int attn_debug_rescale_stats(unsigned long long* out, int reset);
  * ordering semaphores, so the key tiles after it give up waiting once the wait
  * limit is spent and the call ends with ATTN_ERR_TIMEOUT recorded (its gradients
  * are then not valid); ATTN_FAULT_LEAVE_WARP makes one warp of every streaming
- * attention CTA (attn_paged_decode and short attn_paged_fwd) leave as if its wait for
- * work had run out, so that the others give up theirs one after the other (outputs not
- * valid). Returns ATTN_ERR_BAD_SHAPE for an unknown fault.
+ * attention CTA (attn_paged_decode and short attn_paged_fwd), or one of each query tile's
+ * in the tensor-core kernel, leave as if a wait had run out, so that the others give up
+ * theirs one after the other (outputs not valid). Returns ATTN_ERR_BAD_SHAPE for an unknown
+ * fault.
  *
  * attn_debug_stall(stream) launches one CTA that waits on an mbarrier nothing
  * arrives at; the wait gives up after the wait limit and records

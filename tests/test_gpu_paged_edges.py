@@ -164,3 +164,13 @@ def test_a_warp_that_leaves_ends_one_token_attention(wide, kind):
     c = Cache([2000, 700], 2, 128, 16, kind)
     h, q, table = c.handle(), _q(2, 8, 128), _table(c, wide)
     assert _with_a_warp_that_leaves(lambda: binding.paged_decode(h, q, table, c.kv_lens)) == 9  # ATTN_ERR_TIMEOUT
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [[300, 200], [1024]])
+def test_a_warp_that_leaves_ends_chunk_attention(new, d, kind):
+    """The same in the tensor-core kernel, where a warp leaves before the tile's epilogue."""
+    c = Cache([n + 900 for n in new], 2, d, 16, kind)
+    h, q, table, cu = c.handle(), _q(sum(new), 8, d), _table(c, WIDE), _offsets(new)
+    assert _with_a_warp_that_leaves(lambda: binding.paged_forward(h, q, table, c.kv_lens, cu)) == 9
