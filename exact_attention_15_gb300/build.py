@@ -5,6 +5,10 @@ arch=compute_103a,code=sm_103a``), in parallel, and linked with the static CUDA
 runtime, so the library needs nothing at load time but the C++ runtime (the
 driver is reached lazily at the first call). Run ``python -m
 exact_attention_15_gb300.build`` or call ``build()``.
+
+Beside it a small CPython module is built that makes the paged cache's common calls
+(``csrc/paged_call.c``). It needs Python's headers; where they are missing the build says
+so and goes on, and ``paged.py`` makes every call by itself.
 """
 
 from __future__ import annotations
@@ -40,10 +44,14 @@ def _nvcc():
     return cand
 
 
-def _newest_dep_mtime():
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [CALLS]]
+def _newest_dep_mtime(files):
+    paths = [os.path.join(CSRC, f) for f in files]
     paths.append(os.path.join(ROOT, "include", "attn.h"))
     return max(os.path.getmtime(p) for p in paths if os.path.exists(p))
+
+
+def _fresh(target, files):
+    return os.path.exists(target) and os.path.getmtime(target) >= _newest_dep_mtime(files)
 
 
 def _compile(src, extra):
@@ -55,31 +63,39 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
-def _compile_calls():
-    """gcc for the CPython module (it includes no torch or CUDA header)."""
+def _build_calls():
+    """The CPython module, by the host's C compiler (it includes no torch or CUDA header).
+    Where it cannot be built none is left, so that none of an older source is loaded."""
     tmp = CALLS_LIB + ".tmp"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC",
            "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, CALLS), "-o", tmp, "-lm"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for {CALLS}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_LIB)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        said = None if r.returncode == 0 else r.stderr
+    except OSError as e:
+        said = str(e)
+    if said is None:
+        os.replace(tmp, CALLS_LIB)
+        return
+    if os.path.exists(CALLS_LIB):
+        os.remove(CALLS_LIB)
+    sys.stderr.write(f"{CALLS} was not built, the paged cache's calls are made from Python:\n{said}\n")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compiles and links the library if any source is newer than it. Returns its path."""
+    """Compiles and links the library, and the CPython module, where a source is newer.
+    Returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
-    if (not force and os.path.exists(LIB) and os.path.exists(CALLS_LIB)
-            and os.path.getmtime(LIB) >= _newest_dep_mtime()):
+    if force or not _fresh(CALLS_LIB, [CALLS]):
+        _build_calls()
+    if not force and _fresh(LIB, SOURCES + HEADERS):
         return LIB
     extra = list(extra_flags)
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(lambda s: _compile(s, extra), SOURCES))
-    calls.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

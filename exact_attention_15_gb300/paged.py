@@ -4,8 +4,8 @@ Checks of arguments, allocation of the outputs and of the workspace, and the
 C calls on torch's current stream; the computation runs in the library's CUDA
 kernels. One call costs the host several microseconds, as much as the GPU needs
 for a small one: ``csrc/paged_call.c`` makes the common calls (no given outputs,
-the cache on the current device), and what it does not take goes through the
-checks here.
+the cache on the current device), and what it does not take, or everything where it
+has not been built, goes through the checks here.
 """
 
 from __future__ import annotations
@@ -35,14 +35,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _calls = None
 
 
+class _PythonCalls:
+    """Stands in for the compiled calls where they have not been built: takes none."""
+
+    @staticmethod
+    def append(*args):
+        return NotImplemented
+
+    decode = forward = append
+
+
 def _load_calls():
-    """The compiled calls, bound to the library and torch (once). Raises if they
-    have not been built."""
+    """The compiled calls, bound to the library and torch (once), or their stand-in."""
     global _calls
     if _calls is None:
         path = os.path.join(os.path.dirname(library_path()), "_paged_call.so")
         if not os.path.exists(path):
-            raise ImportError(f"not built: {path} is missing (run `python -c 'import __graft_entry__ as g; g.build()'`)")
+            _calls = _PythonCalls
+            return _calls
         spec = importlib.util.spec_from_file_location(
             "_paged_call", path, loader=importlib.machinery.ExtensionFileLoader("_paged_call", path))
         module = importlib.util.module_from_spec(spec)
