@@ -26,7 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libattn_gb300.so")
-CALLS_LIB = os.path.join(LIBDIR, "_paged_call.so")
+# (named for the Python it was built for: another one builds its own)
+CALLS_LIB = os.path.join(LIBDIR, "_paged_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_fwd_pair.cu", "attn_bwd.cu", "attn_bwd_pair.cu",
            "noalloc.cu", "paged_api.cu", "paged_append.cu", "paged_decode.cu", "paged_fwd.cu"]

@@ -19,6 +19,7 @@ import os
 import torch
 
 from .binding import _check, _check_tensor, library_path, load
+from .build import CALLS_LIB
 
 CACHE_BF16 = 0
 CACHE_E4M3 = 1
@@ -49,7 +50,7 @@ def _load_calls():
     """The compiled calls, bound to the library and torch (once), or their stand-in."""
     global _calls
     if _calls is None:
-        path = os.path.join(os.path.dirname(library_path()), "_paged_call.so")
+        path = os.path.join(os.path.dirname(library_path()), os.path.basename(CALLS_LIB))
         if not os.path.exists(path):
             _calls = _PythonCalls
             return _calls

@@ -3,6 +3,7 @@ them the library builds, and the calls go through Python's own checks."""
 
 import ctypes
 import os
+import sysconfig
 
 import pytest
 
@@ -38,6 +39,18 @@ def test_compiled_calls_are_built_where_they_can_be():
     build.build()
     assert os.path.exists(build.CALLS_LIB)
     paged._load_calls()
+
+
+def test_a_module_for_another_python_is_not_loaded(monkeypatch, tmp_path):
+    """Its name carries the interpreter's tag, so that one left by another version is neither
+    found fresh nor loaded."""
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert suffix != ".so" and build.CALLS_LIB.endswith(suffix)
+    for name in ("_paged_call.so", "_paged_call.cpython-39-other.so"):
+        (tmp_path / name).write_bytes(b"not this interpreter's")
+    monkeypatch.setattr(paged, "_calls", None)
+    monkeypatch.setattr(paged, "library_path", lambda: str(tmp_path / "libattn_gb300.so"))
+    assert paged._load_calls() is paged._PythonCalls
 
 
 def test_calls_go_through_python_without_the_module(monkeypatch, tmp_path):
