@@ -1,4 +1,6 @@
-"""The paged key-value cache at the ends of its range."""
+"""The paged key-value cache at the ends of its range: quotients past 32 bits, rows of a
+tile that belong to no token, query rows of zeros, waits that run out, small weights and
+small steps over an e4m3 cache, chunks of very unequal lengths."""
 
 import math
 
@@ -10,6 +12,7 @@ torch = pytest.importorskip("torch")
 
 from exact_attention_15_gb300 import binding  # noqa: E402
 from paged_common import E4M3_MAX, Cache, as_int, assert_attention, attention  # noqa: E402
+from paged_weights import SMALL, bound, small_weights  # noqa: E402
 
 WIDE = 100000  # tokens that a page table can hold: a chunk call then takes the tensor-core kernel
 
@@ -174,3 +177,84 @@ def test_a_warp_that_leaves_ends_chunk_attention(new, d, kind):
     c = Cache([n + 900 for n in new], 2, d, 16, kind)
     h, q, table, cu = c.handle(), _q(sum(new), 8, d), _table(c, WIDE), _offsets(new)
     assert _with_a_warp_that_leaves(lambda: binding.paged_forward(h, q, table, c.kv_lens, cu)) == 9
+
+
+def _lost(q, k, v, scale, last):
+    """Of q [n, H_q, d] over k, v [L, H_kv, d]: the sum of |v_j| over the keys whose weight
+    is below 2^-21 of the row's largest, by the sum of weights [n, H_q, d]."""
+    g = q.shape[1] // k.shape[1]
+    k, v = k.repeat_interleave(g, 1).transpose(0, 1), v.repeat_interleave(g, 1).transpose(0, 1)
+    s = q.double().transpose(0, 1) @ k.transpose(1, 2) * scale
+    s = s.masked_fill(torch.arange(k.shape[1], device=q.device)[None] >= last[:, None], -math.inf)
+    w = torch.exp(s - s.amax(-1, keepdim=True))
+    small = (w < 2.0 ** -21) & (s > -math.inf)
+    return ((small.double() @ v.abs()) / w.sum(-1, keepdim=True)).transpose(0, 1)
+
+
+def _assert_e4m3(o, c, q, new, scale, causal):
+    want, size, _ = _want(c, q, new, scale, causal)
+    lost, t0 = [], 0
+    for b, n in enumerate(new):
+        L = c.lens[b]
+        last = torch.full((n,), L, device="cuda")
+        if causal:
+            last = L - n + 1 + torch.arange(n, device="cuda")
+        lost.append(_lost(q[t0:t0 + n], c.keys[b], c.values[b], scale, last))
+        t0 += n
+    err, most = (o.double() - want).abs(), bound(want, size, torch.cat(lost))
+    assert bool((err <= most).all()), float((err / most).max())
+
+
+@pytest.mark.parametrize("wide", [0, WIDE])
+@pytest.mark.parametrize("n", [1, 3, 130])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("exponent", SMALL)
+def test_small_weights_keep_eleven_bits_over_e4m3(exponent, d, n, wide):
+    """Weights that bf16, or fp16 without the factor of 2^7, would round past the bound (as
+    the planted mistakes show on the CPU), next to weights of 1."""
+    c = Cache([200], 1, d, 16, "e4m3")
+    c.k_scale.fill_(0.25)
+    c.v_scale.fill_(0.5)
+    w, v = small_weights(exponent, d)
+    k = torch.zeros(200, 1, d, device="cuda")
+    k[::16, 0, 0] = 4.0
+    v = v.cuda()[:, None] / 0.5
+    for cache, x in ((c.k, k), (c.v, v)):
+        c.put(cache, 0, 0, x.to(torch.float8_e4m3fn))
+    c.keys, c.values = [k.double() * 0.25], [v * 0.5]
+    q = torch.zeros(n, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    scale = float(torch.tensor(exponent * math.log(2.0)))
+    if n == 1:
+        o, _ = binding.paged_decode(c.handle(), q, _table(c, wide), c.kv_lens, scale=scale)
+    else:
+        o, _ = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets([n]), scale=scale, causal=False)
+    _assert_e4m3(o, c, q, [n], scale, False)
+
+
+@pytest.mark.parametrize("wide", [0, WIDE])
+@pytest.mark.parametrize("new, lens, H_q, H_kv, d, page", [
+    ([1, 1, 1], [1, 700, 3000], 8, 2, 128, 16), ([1], [9000], 5, 1, 64, 32), ([4, 2], [500, 64], 16, 4, 128, 64),
+    ([300, 40], [300, 900], 8, 2, 128, 16), ([129, 65], [2000, 65], 10, 2, 64, 32)])
+def test_attention_over_e4m3_keeps_fp16_weights(new, lens, H_q, H_kv, d, page, wide):
+    """Random sequences within the bound of fp16 weights, not bf16's."""
+    c = Cache(lens, H_kv, d, page, "e4m3", seed=7)
+    q, scale = _q(sum(new), H_q, d), 1.0 / math.sqrt(d)
+    if max(new) == 1:
+        o, _ = binding.paged_decode(c.handle(), q, _table(c, wide), c.kv_lens)
+    else:
+        o, _ = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new))
+    _assert_e4m3(o, c, q, new, scale, max(new) > 1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("wide", [0, 3000, WIDE])
+def test_one_prompt_among_many_single_tokens(wide, kind):
+    """The host knows the mean of the chunks only: a prompt of 700 tokens, in the middle of 255
+    sequences of one token each, and one without any."""
+    new = [1] * 100 + [700, 0] + [1] * 155
+    lens = [17 + 3 * i for i in range(100)] + [900, 40] + [5 + 2 * i for i in range(155)]
+    c = Cache(lens, 2, 64, 16, kind, seed=8)
+    q = _q(sum(new), 8, 64)
+    o, lse = binding.paged_forward(c.handle(), q, _table(c, wide), c.kv_lens, _offsets(new))
+    assert_attention(o, lse, *_want(c, q, new, 1.0 / 8.0))
