@@ -90,8 +90,9 @@ cudaError_t launch_chained(dim3 grid, int threads, int smem, cudaStream_t stream
 }
 
 // A power of two that brings a row whose largest magnitude is `top` to [1, 2) when
-// it divides the row; its inverse is in `down`. fp16 then holds bf16 values exactly
-// but for what lies below 2^-25 of the largest, whatever their range was.
+// it divides the row; its inverse is in `down`. fp16 then holds bf16 values exactly from
+// 2^-17 on, those below to half a step of 2^-24, whatever the row's range was: an element
+// moves by 2^-25 of the largest at most.
 // Infinities stay infinities; a row of zeros is left alone (its power would be 2^-126).
 __device__ __forceinline__ float row_power(float top, float& down) {
   int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;

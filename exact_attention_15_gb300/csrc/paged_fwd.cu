@@ -6,7 +6,10 @@
 // covers floor(128 / group) tokens and every key that it loads meets all the
 // heads that use it. A work tile is two such tiles in a row; the CTA that owns it
 // streams the keys and values that they see, 128 at a time, from the pages.
-// Roles, TMEM plan and pipeline are those of the packed forward kernel:
+// Roles, TMEM plan and pipeline are those of the packed forward kernel at d = 128: P
+// takes the place of S, so that softmax(j), P V(j) and S(j + 1) of a query tile follow one
+// another, and two query tiles take turns. (At 64 that kernel keeps P in columns of its
+// own; this one does not.)
 //   warp 0      TMA producer: both Q tiles, then K_j / V_j into a ring; the lanes
 //               look up the pages of a tile and issue one box each.
 //   warp 1      TMEM owner and MMA issuer: S_i = Q_i K_j^T, O_i += P_i V_j.

@@ -269,7 +269,8 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  *               of q. Rows behind the last sequence are left as they were. NULL
  *               (attn_paged_append): one token per sequence, T = B.
  * New token i of the n of sequence b stands at position kv_lens[b] - n + i. A
- * negative position is padding: nothing is appended for it and it sees no key.
+ * negative position is padding: nothing is appended for it, and with the causal mask it
+ * sees no key (without, every row of a chunk sees every key of its sequence).
  * B * max_pages * page_size may be anything the arrays can hold, up to 2^30 tokens
  * a sequence. The kernels clamp lengths into [0, max_pages * page_size] and take page 0
  * for an index outside [0, num_pages) (an append there is skipped), so nothing
@@ -297,8 +298,8 @@ typedef struct {
  * and key head turn by the angle position * inv_freq[i] (device double array of
  * rotary_dim / 2 entries, radians per position, e.g. base^(-2 i / rotary_dim)).
  * Pair i is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved.
- * The angles are exact to about 2^-24 turns at any position. Turned in 32 bits and
- * rounded once. rotary_dim is a multiple of 16, at most d; 0 appends keys as
+ * The angles are exact to about 2^-24 turns at any position (for inv_freq up to pi in
+ * magnitude; half a turn per position). Turned in 32 bits and rounded once. rotary_dim is a multiple of 16, at most d; 0 appends keys as
  * they are.
  * q (bf16 [T, H_q, d], tokens q_stride apart) is turned likewise into q_out (same
  * shape, q_out_stride apart; q_out == q with the same stride turns in place).
@@ -338,6 +339,8 @@ size_t attn_paged_call_workspace_bytes(const attn_paged_cache* cache, int T, int
  * over the GPU whatever the lengths (behind a short page table, over clusters of CTAs for
  * each sequence and KV head), and the parts are joined in a fixed order: equal inputs
  * and sizes give equal bits on the same device. Allocates nothing; can be captured.
+ * Over an e4m3 cache the products run in fp16, the query rows divided by powers of two:
+ * a row's elements are exact from 2^-17 of its largest on, smaller ones to 2^-25 of it.
  */
 int attn_paged_decode(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
                       const int* kv_lens, const int* page_table, int max_pages,
