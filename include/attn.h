@@ -299,8 +299,8 @@ typedef struct {
  * rotary_dim / 2 entries, radians per position, e.g. base^(-2 i / rotary_dim)).
  * Pair i is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved.
  * The angles are exact to about 2^-24 turns at any position (for inv_freq up to pi in
- * magnitude; half a turn per position). Turned in 32 bits and rounded once. rotary_dim is a multiple of 16, at most d; 0 appends keys as
- * they are.
+ * magnitude; half a turn per position). Turned in 32 bits and rounded once. rotary_dim
+ * is a multiple of 16, at most d; 0 appends keys as they are.
  * q (bf16 [T, H_q, d], tokens q_stride apart) is turned likewise into q_out (same
  * shape, q_out_stride apart; q_out == q with the same stride turns in place).
  * H_q = 0 leaves queries out (q and q_out may be NULL). For e4m3, k / k_scale[h]
