@@ -202,7 +202,7 @@ def _inputs(case, seed):
     s["cu"] = None
     if "new_lo" in case and (op == "attend" or case["new_hi"] > 1):
         s["cu"] = torch.tensor([sum(new[:i]) for i in range(B + 1)], dtype=torch.int32, device=dev)
-    s["most_new"] = max(new)  # a program that packs its batch knows its longest piece
+    s["tokens"], s["most_new"] = T, max(new)  # a program that packs its batch knows its tokens and its longest piece
     return s
 
 
@@ -227,7 +227,7 @@ def run(s):
                                  inv_freq=s["inv_freq"], interleaved=c["interleaved"])
         return {"q": q, "k": s["k"], "v": s["v"], "k_exp": s["k_exp"], "v_exp": s["v_exp"]}
     if op == "bounds":
-        return binding.paged_bounds(s["cache"], s["bounds"], s["table"], s["lens"], cu_seqlens=s["cu"])
+        return binding.paged_bounds(s["cache"], s["bounds"], s["table"], s["lens"], cu_seqlens=s["cu"], tokens=s["tokens"])
     if op == "select":
         pages, lens = binding.paged_select(s["cache"], s["q"], s["bounds"], s["table"], s["lens"], c["count"], cu_seqlens=s["cu"],
                                            keep_first=c["first"], keep_last=c["last"])
