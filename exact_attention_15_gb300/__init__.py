@@ -13,7 +13,7 @@ binding function does, and it fails loudly when the library is missing.
 __all__ = ["attn_fwd", "attn_fwd_dims", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_workspace_bytes",
            "attn_status_string", "attn_check", "attn_set_wait_limit", "attn_set_fwd_variant",
            "attn_set_bwd_variant", "forward", "backward", "PagedCache", "paged_append", "paged_decode",
-           "paged_forward", "paged_workspace_bytes"]
+           "paged_forward", "paged_workspace_bytes", "paged_bounds", "paged_select"]
 
 
 def __getattr__(name):

@@ -48,6 +48,9 @@ _SIGS = {
     "attn_paged_fwd_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
     "attn_paged_call_workspace_bytes": (_Z, [_P, _I, _I, _I, _I, _I]),
     "attn_paged_decode": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _I, _L, _F, _P, _Z, _P]),
+    "attn_paged_decode_lists": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _I, _L, _L, _F, _P, _Z, _P]),
+    "attn_paged_bounds": (_I, [_P, _P, _I, _I, _P, _P, _P, _I, _L, _P]),
+    "attn_paged_select": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _L, _I, _I, _I, _P]),
     "attn_paged_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _L, _I, _F, _P, _Z, _P]),
     "attn_check": (_I, [_P]),
     "attn_status_string": (ctypes.c_char_p, [_I]),
@@ -68,7 +71,7 @@ KERNEL_NAMES = {1: "attn_fwd_kernel", 2: "attn_bwd_pre_kernel", 3: "attn_bwd_mai
                 7: "fwd_plan_kernel", 8: "attn_fwd_pair_kernel", 9: "attn_bwd_main_kernel_pass2",
                 10: "bwd_plan_kernel", 11: "paged_append_kernel", 12: "paged_stream_kernel",
                 13: "paged_join_kernel", 14: "paged_fwd_kernel", 15: "paged_plan_kernel",
-                16: "queries_f16_kernel"}
+                16: "queries_f16_kernel", 17: "paged_bounds_kernel", 18: "paged_select_kernel"}
 FAULT_NONE = 0
 FAULT_SKIP_DQ_RELEASE = 1
 FAULT_LEAVE_WARP = 2
@@ -377,7 +380,8 @@ def backward(q, k, v, o, lse, dout, scale=None, causal=False, cu_seqlens=None,
 
 # ------------------------------------------------------------------ paged key-value cache
 
-_PAGED = ("PagedCache", "paged_append", "paged_decode", "paged_forward", "paged_workspace_bytes")
+_PAGED = ("PagedCache", "paged_append", "paged_decode", "paged_forward", "paged_workspace_bytes", "paged_bounds",
+          "paged_select")
 
 
 def __getattr__(name):

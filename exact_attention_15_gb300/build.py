@@ -30,9 +30,10 @@ LIB = os.path.join(LIBDIR, "libattn_gb300.so")
 CALLS_LIB = os.path.join(LIBDIR, "_paged_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_fwd_pair.cu", "attn_bwd.cu", "attn_bwd_pair.cu",
-           "noalloc.cu", "paged_api.cu", "paged_append.cu", "paged_decode.cu", "paged_fwd.cu"]
+           "noalloc.cu", "paged_api.cu", "paged_append.cu", "paged_append_pages.cu", "paged_decode.cu", "paged_fwd.cu",
+           "paged_select.cu"]
 CALLS = "paged_call.c"  # a CPython module: the paged cache's torch calls
-HEADERS = ["ptx.cuh", "attn_common.cuh", "fwd_softmax.cuh", "host.h", "paged.cuh"]
+HEADERS = ["ptx.cuh", "attn_common.cuh", "fwd_softmax.cuh", "host.h", "paged.cuh", "append.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

@@ -95,7 +95,8 @@ struct BwdParams {
 enum KernelId : int { kKFwd = 1, kKBwdPre = 2, kKBwdMain = 3, kKBwdPost = 4, kKExp2 = 5,
                       kKStall = 6, kKFwdPlan = 7, kKFwdPair = 8, kKBwdMain2 = 9,
                       kKBwdPlan = 10, kKPagedAppend = 11, kKPagedDecode = 12, kKPagedJoin = 13,
-                      kKPagedFwd = 14, kKPagedPlan = 15, kKPagedQueries = 16 };
+                      kKPagedFwd = 14, kKPagedPlan = 15, kKPagedQueries = 16,
+                      kKPagedBounds = 17, kKPagedSelect = 18 };
 int prof_begin(int kernel, cudaStream_t stream);
 void prof_end(int slot, cudaStream_t stream);
 

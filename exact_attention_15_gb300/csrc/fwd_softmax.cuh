@@ -88,6 +88,41 @@ __device__ __forceinline__ void softmax_row_exp(const float (&s)[128], float c, 
   }
 }
 
+// Keys whose values have a power of two each, one for 16 keys: entry g of `of_page` holds
+// 2^ek, ev and 2^-ev for the stored keys and values of group g. The scores become
+// x = s c 2^ek + ev, so that p = 2^(x - m) is the weight of the stored value, and m bounds it
+// however the groups differ; softmax_row_exp_pages takes 2^ev out of the sum again.
+__device__ __forceinline__ void softmax_row_pages(float (&s)[128], float c, const float4* of_page) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const float2 x = *reinterpret_cast<const float2*>(of_page + g);
+    // (finite, so that a score of 0 stays 0)
+    const float a = fminf(fmaxf(c * x.x, -3.402823466e38f), 3.402823466e38f);
+    const uint64_t a2 = f32x2(a, a), b2 = f32x2(x.y, x.y);
+#pragma unroll
+    for (int i = 8 * g; i < 8 * g + 8; ++i)
+      f32x2_split(fma_f32x2(f32x2(s[2 * i], s[2 * i + 1]), a2, b2), s[2 * i], s[2 * i + 1]);
+  }
+}
+// The fp16 P row of such scores (softmax_row_max has masked them), and its sum.
+__device__ __forceinline__ void softmax_row_exp_pages(const float (&s)[128], float mb, const float4* of_page,
+                                                      uint32_t (&pk)[64], uint64_t (&sum2)[2]) {
+  const uint64_t nb2 = f32x2(-mb, -mb);
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const float down = of_page[g].z;
+    const uint64_t d2 = f32x2(down, down);
+#pragma unroll
+    for (int i = 8 * g; i < 8 * g + 8; ++i) {
+      float x0, x1;
+      f32x2_split(add_f32x2(f32x2(s[2 * i], s[2 * i + 1]), nb2), x0, x1);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      sum2[i & 1] = fma_f32x2(f32x2(p0, p1), d2, sum2[i & 1]);
+      pk[i] = pack_f16x2(p0, p1);
+    }
+  }
+}
+
 // Row sum of the two packed pair accumulators.
 __device__ __forceinline__ float softmax_row_sum(const uint64_t (&sum2)[2]) {
   float a, b, c, d;

@@ -3,11 +3,30 @@
 // access leaves the cache or the page table whatever the device arrays hold.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <atomic>
 
 #include "attn_common.cuh"
 
 namespace attn {
+
+// What the cache holds (the values of ATTN_CACHE_*): bf16; e4m3 with an fp32 scale for each
+// KV head; e4m3 with a power of two for each page and KV head.
+constexpr int kBf16 = 0, kE4m3 = 1, kE4m3Pages = 3;
+
+// Exponents of the powers of two: within +-kMaxExp, so that sums of weights divided by them
+// stay far inside 32 bits (2^20 keys, a bias of 2^15 and 2^64).
+constexpr int kMaxExp = 64;
+__device__ __forceinline__ int page_exponent(const uint8_t* exps, int page, int H_kv, int h) {
+  const int e = static_cast<int>(__ldg(exps + static_cast<size_t>(page) * H_kv + h)) - 127;
+  return max(-kMaxExp, min(kMaxExp, e));
+}
+// 2^e, e from -126 to 127.
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Two fp16 values, widened.
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
 // Sequences, their lengths in the cache and their pages.
 struct PagedSeqs {
@@ -17,6 +36,7 @@ struct PagedSeqs {
   int B, T;               // sequences; rows of q
   int max_pages, num_pages;
   long long table_stride;  // entries between rows of page_table
+  long long head_stride;   // entries between the KV heads of a row, 0: they share their pages
   int page_shift;         // log2(page_size)
   int* err;               // device error word
 };
@@ -30,13 +50,52 @@ __device__ __forceinline__ int kv_len(const PagedSeqs& s, int b) {
 __device__ __forceinline__ SeqSpan new_span(const PagedSeqs& s, int b) {
   return s.cu_seqlens ? seq_span(s.cu_seqlens, b, s.T, 0) : SeqSpan{b, b < s.T ? 1 : 0};
 }
-// The page that holds place `i` of sequence b's page table row (i < max_pages).
-// An index outside the cache is recorded and page 0 taken for it.
-__device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int i) {
-  const int id = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + i);
+// The page that holds place `i` of sequence b's page table row (i < max_pages), for KV head h
+// where the heads have pages of their own. An index outside the cache is recorded and page 0
+// taken for it.
+__device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int i, int h = 0) {
+  const int id = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + h * s.head_stride + i);
   if (static_cast<unsigned>(id) < static_cast<unsigned>(s.num_pages)) return id;
   record_error(s.err, kErrPages);
   return 0;
+}
+// A page that new tokens of a sequence go to.
+struct TouchedPage {
+  int b, at;   // sequence, place in its page table row
+  int lo, hi;  // positions of the new tokens in it
+  int row;     // row of q, k and v of the first
+  int len;     // keys of the sequence
+};
+// The pages that new tokens touch are numbered sequence by sequence: sequence b's numbers
+// begin at cu[b] / page_size + 2 b, which leaves it floor(n / page_size) + 2, and n tokens touch
+// floor((n - 2) / page_size) + 2 at most. So no sum over the sequences is needed; some numbers
+// stay without a page. One token for each sequence: number b is its page.
+__host__ __device__ __forceinline__ long long touched_numbers(int T, int B, int page_shift, bool packed) {
+  return packed ? (T >> page_shift) + 2ll * B : B;
+}
+__device__ __forceinline__ bool touched_page(const PagedSeqs& s, long long number, TouchedPage& x) {
+  x.b = static_cast<int>(number);
+  long long first = number;
+  if (s.cu_seqlens) {
+    auto base = [&](int b) { return (min(max(__ldg(s.cu_seqlens + b), 0), s.T) >> s.page_shift) + 2ll * b; };
+    int lo = 0, hi = s.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (base(mid) <= number) lo = mid; else hi = mid;
+    }
+    x.b = lo;
+    first = base(lo);
+  }
+  const SeqSpan span = new_span(s, x.b);
+  x.len = kv_len(s, x.b);
+  const int before = x.len - span.len, begin = max(before, 0);  // before < 0: padding
+  const long long at = (begin >> s.page_shift) + (number - first);
+  if (span.len == 0 || x.len == 0 || number < first || at > (x.len - 1) >> s.page_shift) return false;
+  x.at = static_cast<int>(at);
+  x.lo = max(begin, x.at << s.page_shift);
+  x.hi = min(x.len, (x.at + 1) << s.page_shift);
+  x.row = span.start + (x.lo - before);
+  return true;
 }
 // Records lengths that the clamps above would change: thread `tid` of
 // `nthreads` checks its share. Rows of q behind the last sequence are allowed.
@@ -52,22 +111,29 @@ __device__ __forceinline__ void check_paged_seqs(const PagedSeqs& s, int tid, in
   }
 }
 
+// Allows a kernel that much shared memory, once per device: the most that it is launched with.
+template <auto Kernel>
+cudaError_t allow_smem(int most) {
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Launches a kernel that calls grid_wait() in every thread before it touches
-// memory: its launch and set-up overlap the end of the grid before it. The
-// shared-memory size is set once per device. Clusters of `cluster` CTAs.
+// memory: its launch and set-up overlap the end of the grid before it. Clusters of
+// `cluster` CTAs. (A kernel whose shared memory differs from call to call calls allow_smem with
+// the most before.)
 template <auto Kernel, typename... Args>
 cudaError_t launch_clusters(int cluster, dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
   if (smem > 48 * 1024) {
-    static std::atomic<unsigned long long> ready{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem<Kernel>(smem);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-      ready.fetch_or(bit, std::memory_order_relaxed);
-    }
   }
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -116,9 +182,37 @@ struct AppendParams {
   long long k_page, v_page;  // elements between pages
   const float* k_scale; const float* v_scale;  // e4m3: [H_kv] or nullptr
   const double* inv_freq;    // [rotary_dim / 2] radians per position, or nullptr
+  uint8_t* k_exp; uint8_t* v_exp;  // a scale for each page: [num_pages, H_kv]
   int H_q, H_kv, d, rotary_dim, interleaved, e4m3;
 };
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
+// Over a cache with a scale for each page.
+cudaError_t launch_paged_append_pages(const AppendParams& p, cudaStream_t stream);
+
+// ---- choosing pages by bounds of their keys
+struct BoundsParams {
+  PagedSeqs s;
+  const void* k;  // the cache's keys
+  long long k_page;  // elements between pages
+  const float* k_scale;  // e4m3: [H_kv] or nullptr
+  const uint8_t* k_exp;  // a scale for each page
+  void* bounds;  // bf16 [num_pages, H_kv, 2, d]: minimum, maximum
+  int H_kv;
+};
+cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStream_t stream);
+
+struct SelectParams {
+  PagedSeqs s;
+  const void* q;       // bf16 [T, H_q, d]
+  const void* bounds;
+  int* pages;          // [T, H_kv, count]
+  int* lens;           // [T]
+  int H_q, H_kv, group, count, first, last;
+  int cluster_shift, slice;  // set by the launch: CTAs of a token and KV head, pages of each at most
+};
+// Pages that a row of a page table may have: eight CTAs keep 8192 scores each.
+constexpr int kSelectSlice = 8192, kSelectCluster = 8, kSelectPages = kSelectSlice * kSelectCluster;
+cudaError_t launch_paged_select(const SelectParams& p, int d, int n_sm, cudaStream_t stream);
 
 // ---- streaming attention: few query rows per sequence
 constexpr int kStreamCtas = 456;  // CTAs the workspace holds partial results for
@@ -135,6 +229,7 @@ struct StreamParams {
   float* lse;
   long long lse_row, lse_head;  // elements between rows and between heads of lse
   const float* k_scale; const float* v_scale;
+  const uint8_t* k_exp; const uint8_t* v_exp;  // kE4m3Pages: [num_pages, H_kv]
   int H_q, H_kv, group, causal;
   float scale_log2;
   int4* heads;            // workspace: [kStreamCtas, 2] where the pieces of a split item begin
@@ -147,7 +242,7 @@ struct StreamParams {
   long long wait_limit;
 };
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
-                                int d, int rows, bool e4m3, int n_sm, cudaStream_t stream);
+                                int d, int rows, int kind, int n_sm, cudaStream_t stream);
 
 // ---- tensor-core attention: many query rows per sequence
 constexpr int kFwdSms = 152;               // SMs that calls and workspaces are planned for
@@ -163,6 +258,7 @@ struct PagedFwdParams {
   int max_work;      // work tiles that the host expects at most
   float scale_log2;
   const float* k_scale; const float* v_scale;  // e4m3: [H_kv] or nullptr
+  const uint8_t* k_exp; const uint8_t* v_exp;  // kE4m3Pages: [num_pages, H_kv]
   const float* q_up;  // e4m3, workspace: what each row of the fp16 queries was divided by [T, H_q]
   int* seq_order;    // workspace: sequences, longest first [B]
   int* tile_start;   // workspace: first work tile of each of them [B + 1]
@@ -179,7 +275,7 @@ struct PagedFwdParams {
   long long wait_limit;
 };
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedFwdParams& p, int d, bool e4m3, cudaStream_t stream);
+                             const PagedFwdParams& p, int d, int kind, cudaStream_t stream);
 // Queries as fp16 for products with an e4m3 cache: each row divided by a power of
 // two (kept in q_up) that brings its largest value to [1, 2).
 cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,

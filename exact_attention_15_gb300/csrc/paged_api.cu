@@ -15,21 +15,25 @@ using namespace attn;
 
 namespace {
 
+static_assert(kBf16 == ATTN_CACHE_BF16 && kE4m3 == ATTN_CACHE_E4M3 && kE4m3Pages == ATTN_CACHE_E4M3_PAGES, "types");
+bool in_bytes(const attn_paged_cache* c) { return c->type != kBf16; }
+
 bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 int check_cache(const attn_paged_cache* c) {
   if (!c) return ATTN_ERR_NULL_PTR;
   if (c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED_HEADDIM;
-  if (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3) return ATTN_ERR_BAD_SHAPE;
+  if (c->type != kBf16 && c->type != kE4m3 && c->type != kE4m3Pages) return ATTN_ERR_BAD_SHAPE;
   if (c->num_pages < 1 || c->H_kv < 1 || c->H_kv > 65535) return ATTN_ERR_BAD_SHAPE;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return ATTN_ERR_BAD_SHAPE;
   if (!c->k || !c->v) return ATTN_ERR_NULL_PTR;
+  if (c->type == kE4m3Pages && (!c->k_exp || !c->v_exp)) return ATTN_ERR_NULL_PTR;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
     return ATTN_ERR_ALIGNMENT;
   const long long page = static_cast<long long>(c->H_kv) * c->page_size * c->d;
-  const long long es = c->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  const long long es = in_bytes(c) ? 1 : 2;
   // tensor maps hold strides below 2^40 bytes
   for (long long stride : {c->k_page_stride, c->v_page_stride}) {
     if (stride < page || stride >= (1ll << 39)) return ATTN_ERR_BAD_SHAPE;
@@ -62,6 +66,7 @@ PagedSeqs seqs_of(const attn_paged_cache* c, int T, int B, const int* seqlens, c
   s.T = T;
   s.max_pages = max_pages;
   s.table_stride = table_stride;
+  s.head_stride = 0;
   s.num_pages = c->num_pages;
   s.page_shift = 0;
   while ((1 << s.page_shift) < c->page_size) ++s.page_shift;
@@ -73,7 +78,7 @@ PagedSeqs seqs_of(const attn_paged_cache* c, int T, int B, const int* seqlens, c
 // page, at most 128 bytes of each, swizzled over the box's row width.
 int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cache* c, const void* base,
                      long long page_stride, unsigned rows) {
-  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  const bool e4m3 = in_bytes(c);
   const cuuint64_t es = e4m3 ? 1 : 2, d = static_cast<cuuint64_t>(c->d);
   const cuuint64_t page = static_cast<cuuint64_t>(c->page_size);
   cuuint64_t dims[4] = {d, page, static_cast<cuuint64_t>(c->H_kv), static_cast<cuuint64_t>(c->num_pages)};
@@ -163,7 +168,7 @@ bool few_rows(int T, int B, int group) {
 bool little_work(const attn_paged_cache* c, int T, int B, int group, int max_pages) {
   const long long items = ((static_cast<long long>(T) * group + 15) / 16 + B) * c->H_kv;
   const long long keys = static_cast<long long>(max_pages) * c->page_size;
-  const long long bytes = keys * c->d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2);
+  const long long bytes = keys * c->d * (in_bytes(c) ? 1 : 2);
   return items * (bytes / (kStreamTile * 256) + 10) <= 8000;
 }
 
@@ -194,7 +199,7 @@ StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, boo
                                   : static_cast<long long>(B) * ((group + s.rows - 1) / s.rows);
   s.items = chunks * c->H_kv;
   const long long tiles = (static_cast<long long>(max_pages) * c->page_size + kStreamTile - 1) / kStreamTile;
-  const long long grid = static_cast<long long>(stream_ctas(s.rows, c->d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2))) * n_sm;
+  const long long grid = static_cast<long long>(stream_ctas(s.rows, c->d * (in_bytes(c) ? 1 : 2))) * n_sm;
   s.cluster = 1;
   while (2 * s.cluster <= kStreamCluster && 8 * s.items * 2 * s.cluster <= 7 * grid) {
     const long long per_sm = (s.items * 2 * s.cluster + n_sm - 1) / n_sm;
@@ -215,7 +220,7 @@ size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
 }
 size_t workspace_of_call(const attn_paged_cache* c, int T, int B, int group, bool packed, const StreamShape& shape) {
   if (shape.cluster > 0) return 0;
-  return packed ? workspace_bytes_of(T, B, group, c->H_kv, c->d, c->type == ATTN_CACHE_E4M3) : stream_plan(c->d).total;
+  return packed ? workspace_bytes_of(T, B, group, c->H_kv, c->d, in_bytes(c)) : stream_plan(c->d).total;
 }
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
@@ -235,8 +240,10 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.lse = lse;
   p.lse_row = lse_row;
   p.lse_head = lse_head;
-  p.k_scale = c->type == ATTN_CACHE_E4M3 ? c->k_scale : nullptr;
-  p.v_scale = c->type == ATTN_CACHE_E4M3 ? c->v_scale : nullptr;
+  p.k_scale = c->type == kE4m3 ? c->k_scale : nullptr;
+  p.v_scale = c->type == kE4m3 ? c->v_scale : nullptr;
+  p.k_exp = c->type == kE4m3Pages ? c->k_exp : nullptr;
+  p.v_exp = c->type == kE4m3Pages ? c->v_exp : nullptr;
   p.H_q = H_q;
   p.H_kv = c->H_kv;
   p.group = H_q / c->H_kv;
@@ -249,7 +256,7 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
   p.fault = dev.fault;
   p.cluster = shape.cluster;
   p.items = shape.items;
-  return launch_paged_stream(tk, tv, p, c->d, shape.rows, c->type == ATTN_CACHE_E4M3, dev.n_sm, cs) == cudaSuccess
+  return launch_paged_stream(tk, tv, p, c->d, shape.rows, c->type, dev.n_sm, cs) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }
@@ -257,7 +264,7 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
 int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q, void* o,
                float* lse, int H_q, int causal, float scale, uint8_t* ws, cudaStream_t cs) {
   const int group = H_q / c->H_kv;
-  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  const bool e4m3 = in_bytes(c);
   const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d, e4m3);
   const int box = e4m3 ? kTileN / 2 : kTileN;  // rows that land together
   const unsigned rows = c->page_size < box ? c->page_size : box;
@@ -282,8 +289,10 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   p.split = plan.split ? 1 : 0;
   p.max_work = static_cast<int>(plan.tiles);
   p.scale_log2 = scale * kLog2e;
-  p.k_scale = e4m3 ? c->k_scale : nullptr;
-  p.v_scale = e4m3 ? c->v_scale : nullptr;
+  p.k_scale = c->type == kE4m3 ? c->k_scale : nullptr;
+  p.v_scale = c->type == kE4m3 ? c->v_scale : nullptr;
+  p.k_exp = c->type == kE4m3Pages ? c->k_exp : nullptr;
+  p.v_exp = c->type == kE4m3Pages ? c->v_exp : nullptr;
   p.q_up = reinterpret_cast<const float*>(ws + plan.up_off);
   p.seq_order = reinterpret_cast<int*>(ws);
   p.tile_start = p.seq_order + seqs.B;
@@ -302,14 +311,15 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   if (e4m3 && launch_queries_f16(q, ws + plan.q16_off, reinterpret_cast<float*>(ws + plan.up_off),
                                  static_cast<long long>(seqs.T) * H_q, c->d, cs) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  return launch_paged_fwd(tq, tk, tv, p, c->d, e4m3, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_paged_fwd(tq, tk, tv, p, c->d, c->type, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Both attention calls, after the checks they share.
 int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* lse, int T, int B, int H_q,
                     const int* seqlens, const int* kv_lens, const int* page_table, int max_pages,
                     long long table_stride, int causal, float scale, void* workspace,
-                    size_t workspace_bytes, long long lse_row, long long lse_head, cudaStream_t cs) {
+                    size_t workspace_bytes, long long lse_row, long long lse_head, cudaStream_t cs,
+                    long long head_stride = 0) {
   int st = check_cache(c);
   if (st != ATTN_OK) return st;
   if ((st = check_seqs(c, T, B, H_q, seqlens, kv_lens, page_table, max_pages, table_stride)) != ATTN_OK)
@@ -325,7 +335,8 @@ int paged_attention(const attn_paged_cache* c, const void* q, void* o, float* ls
   if (!aligned(workspace, 256)) return ATTN_ERR_ALIGNMENT;
   HostDevice dev;
   if ((st = host_setup(&dev)) != ATTN_OK) return st;
-  const PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  PagedSeqs seqs = seqs_of(c, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  seqs.head_stride = head_stride;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (!seqlens || few_rows(T, B, group) || shape.cluster > 0 ||
       little_work(c, T, B, group, max_pages))
@@ -365,24 +376,27 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
   p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride; p.q_out_stride = q_out_stride;
   p.k_cache = cache->k; p.v_cache = cache->v;
   p.k_page = cache->k_page_stride; p.v_page = cache->v_page_stride;
-  p.e4m3 = cache->type == ATTN_CACHE_E4M3 ? 1 : 0;
+  p.e4m3 = cache->type == kE4m3 ? 1 : 0;
   p.k_scale = p.e4m3 ? cache->k_scale : nullptr;
   p.v_scale = p.e4m3 ? cache->v_scale : nullptr;
+  p.k_exp = cache->type == kE4m3Pages ? cache->k_exp : nullptr;
+  p.v_exp = cache->type == kE4m3Pages ? cache->v_exp : nullptr;
   p.inv_freq = inv_freq;
   p.H_q = H_q; p.H_kv = cache->H_kv; p.d = d;
   p.rotary_dim = rotary_dim;
   p.interleaved = interleaved ? 1 : 0;
-  return launch_paged_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
-                                                                                       : ATTN_ERR_CUDA;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->type == kE4m3Pages ? launch_paged_append_pages(p, cs) : launch_paged_append(p, cs);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 size_t attn_paged_decode_workspace_bytes(int d) { return d == 64 || d == 128 ? stream_plan(d).total : 0; }
 
 size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, int type) {
   if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
-      (type != ATTN_CACHE_BF16 && type != ATTN_CACHE_E4M3))
+      (type != kBf16 && type != kE4m3 && type != kE4m3Pages))
     return 0;
-  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type == ATTN_CACHE_E4M3);
+  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type != kBf16);
 }
 
 size_t attn_paged_call_workspace_bytes(const attn_paged_cache* cache, int T, int B, int H_q, int packed, int max_pages) {
@@ -410,6 +424,74 @@ int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float*
   return paged_attention(cache, q, o, lse, T, B, H_q, seqlens, kv_lens, page_table, max_pages,
                          table_stride, causal, scale, workspace, workspace_bytes, 1, T,
                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_paged_decode_lists(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
+                            const int* kv_lens, const int* lists, int max_pages, long long list_stride,
+                            long long head_stride, float scale, void* workspace, size_t workspace_bytes,
+                            attn_stream_t stream) {
+  if (max_pages > 0 && head_stride < max_pages) return ATTN_ERR_BAD_SHAPE;
+  return paged_attention(cache, q, o, lse, B, B, H_q, nullptr, kv_lens, lists, max_pages, list_stride, 0, scale,
+                         workspace, workspace_bytes, H_q, 1, reinterpret_cast<cudaStream_t>(stream), head_stride);
+}
+
+int attn_paged_bounds(const attn_paged_cache* cache, void* bounds, int T, int B, const int* seqlens,
+                      const int* kv_lens, const int* page_table, int max_pages, long long table_stride,
+                      attn_stream_t stream) {
+  int st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  if ((st = check_seqs(cache, T, B, 0, seqlens, kv_lens, page_table, max_pages, table_stride)) != ATTN_OK) return st;
+  if (T == 0) return ATTN_OK;
+  if (!bounds) return ATTN_ERR_NULL_PTR;
+  if (!aligned(bounds, 16)) return ATTN_ERR_ALIGNMENT;
+  HostDevice dev;
+  if ((st = host_setup(&dev)) != ATTN_OK) return st;
+  BoundsParams p;
+  p.s = seqs_of(cache, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  p.k = cache->k;
+  p.k_page = cache->k_page_stride;
+  p.k_scale = cache->type == kE4m3 ? cache->k_scale : nullptr;
+  p.k_exp = cache->type == kE4m3Pages ? cache->k_exp : nullptr;
+  p.bounds = bounds;
+  p.H_kv = cache->H_kv;
+  return launch_paged_bounds(p, cache->d, cache->type, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+int attn_paged_select(const attn_paged_cache* cache, const void* q, const void* bounds, int* pages, int* lens,
+                      int T, int B, int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
+                      int max_pages, long long table_stride, int count, int keep_first, int keep_last,
+                      attn_stream_t stream) {
+  int st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  if ((st = check_seqs(cache, T, B, H_q, seqlens, kv_lens, page_table, max_pages, table_stride)) != ATTN_OK)
+    return st;
+  if (H_q < 1 || count < 1 || keep_first < 0 || keep_last < 1 ||
+      static_cast<long long>(keep_first) + keep_last > count || max_pages > kSelectPages ||
+      static_cast<long long>(count) * cache->page_size > (1ll << 30))
+    return ATTN_ERR_BAD_SHAPE;
+  if (H_q / cache->H_kv > kTileM) return ATTN_ERR_GQA_RATIO;
+  if (T == 0) return ATTN_OK;
+  if (!q || !bounds || !pages || !lens) return ATTN_ERR_NULL_PTR;
+  if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(pages, 4) || !aligned(lens, 4)) return ATTN_ERR_ALIGNMENT;
+  HostDevice dev;
+  if ((st = host_setup(&dev)) != ATTN_OK) return st;
+  SelectParams p;
+  p.s = seqs_of(cache, T, B, seqlens, kv_lens, page_table, max_pages, table_stride, dev.err);
+  p.q = q;
+  p.bounds = bounds;
+  p.pages = pages;
+  p.lens = lens;
+  p.H_q = H_q;
+  p.H_kv = cache->H_kv;
+  p.group = H_q / cache->H_kv;
+  p.count = count;
+  p.first = keep_first;
+  p.last = keep_last;
+  return launch_paged_select(p, cache->d, dev.n_sm, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

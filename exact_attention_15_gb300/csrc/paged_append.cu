@@ -1,13 +1,6 @@
 // Appends new tokens to a paged key-value cache, with the rotary position
 // embedding of queries and keys applied on the way.
-//
-// A pair (a, b) of a query or key at position p turns into
-// (a cos t - b sin t, a sin t + b cos t) with t = p * inv_freq[i]. Far positions
-// make t large (10^6 radians at a million tokens), where 32-bit products lose
-// the angle: the turn count p * inv_freq / 2 pi is kept as a 64-bit binary
-// fraction, whose integer product with p drops whole turns exactly; its top 24
-// bits after that are the angle.
-#include "paged.cuh"
+#include "append.cuh"
 
 namespace attn {
 
@@ -15,24 +8,6 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 
-__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo_to_f32(u[i]);
-    x[2 * i + 1] = bf16hi_to_f32(u[i]);
-  }
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-// Two values to e4m3, nearest-even, what lies beyond 448 to 448 (NaN stays NaN).
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // x / s, rounded to nearest, from the rounded inverse of s: the product's residual
 // corrects it (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990). The product stands where the residual is no number to
@@ -59,10 +34,6 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], flo
                                             pack_e4m3x2(y[4], y[5]) | pack_e4m3x2(y[6], y[7]) << 16);
 }
 
-// 16 elements of a head: two runs of 8.
-struct Part {
-  uint4 a, b;
-};
 // Which 16 elements part i of a token is: the threads of a head take a pair of
 // 8-element runs half the rotated width apart (so that each holds whole pairs), or
 // 16 elements in a row.
@@ -145,15 +116,7 @@ paged_append_kernel(const AppendParams p) {
   if (live) {
     page = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + (pos >> s.page_shift));
     for (int i = tid; i < p.rotary_dim >> 1; i += W) {
-      double turns = __ldg(p.inv_freq + i) * 0.15915494309189533577;  // 1 / 2 pi
-      turns -= floor(turns);
-      const unsigned long long f = static_cast<unsigned long long>(turns * 18446744073709551616.0);
-      const long long whole = static_cast<long long>(f * static_cast<unsigned long long>(pos));
-      // half turns in [-1, 1)
-      const float half = static_cast<float>(static_cast<int>(whole >> 32)) * (1.0f / 2147483648.0f);
-      float sn, c;
-      sincospif(half, &sn, &c);
-      cs[(i & 7) * (p.rotary_dim >> 4) + (i >> 3)] = make_float2(c, sn);
+      cs[(i & 7) * (p.rotary_dim >> 4) + (i >> 3)] = turn_at(turn_fraction(__ldg(p.inv_freq + i)), pos);
     }
   }
   if (W <= 32) __syncwarp(); else __syncthreads();
@@ -178,25 +141,8 @@ paged_append_kernel(const AppendParams p) {
     float x0[8], x1[8];
     widen8(w.a, x0);
     widen8(w.b, x1);
-    if (x.split) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 r = turn[e];
-        const float a = x0[e], c = x1[e];
-        x0[e] = a * r.x - c * r.y;
-        x1[e] = a * r.y + c * r.x;
-      }
-    } else if (x.turn) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 r = turn[e], u = turn[4 + e];
-        const float a = x0[2 * e], c = x0[2 * e + 1], a1 = x1[2 * e], c1 = x1[2 * e + 1];
-        x0[2 * e] = a * r.x - c * r.y;
-        x0[2 * e + 1] = a * r.y + c * r.x;
-        x1[2 * e] = a1 * u.x - c1 * u.y;
-        x1[2 * e + 1] = a1 * u.y + c1 * u.x;
-      }
-    }
+    if (x.split) turn_halves(x0, x1, turn);
+    else if (x.turn) turn_neighbours(x0, x1, turn);
     if (x.kind == 0) {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + x.h * p.d;
       store8(dst + x.e0, x0);

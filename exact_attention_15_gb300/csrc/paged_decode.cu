@@ -21,6 +21,8 @@
 // (tcgen05 wants 128 rows; here there are 16 at most, and the tensor work is
 // small against the tile's bytes); warp 4 walks the work, hands its pieces to the
 // others through a ring and loads the tiles with TMA.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace attn {
@@ -32,8 +34,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRing = 4;  // pieces that the loading warp can be ahead
 
-template <int D, int R, bool FP8>
+template <int D, int R, int KIND>
 struct StreamCfg {
+  static constexpr bool FP8 = KIND != kBf16;
   static constexpr int kEs = FP8 ? 1 : 2;
   static constexpr int kCtas = stream_ctas(R, D * kEs);
   // a tile is kept as blocks of 64 rows x (at most) 128 bytes, swizzled
@@ -48,6 +51,11 @@ struct StreamCfg {
   static constexpr int kRingOff = kMlOff + kWarps * 16 * 2 * 4;
   static constexpr int kBarOff = kRingOff + kRing * 48;
   static constexpr int kPieceOff = kBarOff + (2 * kStages + 2 * kRing + 2) * 8;  // clusters: [16][2]
+  // A scale for each page: the exponents, plus 127, of K and V for the four warps' 16 keys in
+  // every stage. They share the place of a cluster's sums, which are written when every warp has
+  // done its tiles: two CTAs with 16 query rows leave 16 bytes of an SM's shared memory.
+  static constexpr int kExpOff = kPieceOff;
+  static_assert(kStages * kWarps * 2 <= 16 * 2 * 4, "exponents");
   static constexpr int kSmemBytes = kPieceOff + 16 * 2 * 4;
   // the CTAs share an SM's 228 KB, of which each takes 1 KB besides its own
   static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory of an SM");
@@ -228,12 +236,14 @@ __device__ __forceinline__ void write_empty(const StreamParams& p, SeqSpan rows,
 
 // CLUSTER: the CTAs of a cluster share one item and join their pieces through each
 // other's shared memory.
-template <int D, int R, bool FP8, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, StreamCfg<D, R, FP8>::kCtas)
+template <int D, int R, int KIND, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, StreamCfg<D, R, KIND>::kCtas)
 paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const StreamParams p) {
-  using Cfg = StreamCfg<D, R, FP8>;
+  using Cfg = StreamCfg<D, R, KIND>;
+  constexpr bool FP8 = Cfg::FP8, PAGES = KIND == kE4m3Pages;
   extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* exponents = smem + Cfg::kExpOff;  // [stage][warp][K, V]
   float* merge = reinterpret_cast<float*>(smem + Cfg::kMergeOff);
   float* ml = reinterpret_cast<float*>(smem + Cfg::kMlOff);  // [warp][16][2]
   Piece* ring = reinterpret_cast<Piece*>(smem + Cfg::kRingOff);
@@ -348,14 +358,37 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       auto page_at = [&](int t) {
         const int key = t * kTile + box_row;
-        return has_box && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift) : 0;
+        return has_box && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
       };
       int id = page_at(x.t0);
+      // A scale for each page: lane w < 4 looks up that of K, lane 4 + w that of V of warp w's
+      // 16 keys (they share a page), the page two tiles ahead and its exponent one.
+      auto exp_page_at = [&](int t) {
+        const int key = t * kTile + (lane & 3) * 16;
+        return lane < 8 && t < x.t1 && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
+      };
+      auto exp_at = [&](int page) {
+        return lane < 8 ? page_exponent(lane < 4 ? p.k_exp : p.v_exp, page, p.H_kv, x.h) : 0;
+      };
+      int ex = 0, ex_page = 0;
+      if constexpr (PAGES) {
+        ex = exp_at(exp_page_at(x.t0));
+        ex_page = exp_page_at(x.t0 + 1);
+      }
       for (int t = x.t0; t < x.t1; ++t) {
         const int key0 = t * kTile;
         const int here = id;
         if (t + 1 < x.t1) id = page_at(t + 1);
+        const int ex_here = ex;
+        if constexpr (PAGES) {
+          ex = exp_at(ex_page);
+          ex_page = exp_page_at(t + 2);
+        }
         if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1, lim)) { ok = false; break; }
+        if constexpr (PAGES) {
+          if (lane < 8) exponents[(stage * kWarps + (lane & 3)) * 2 + (lane >> 2)] = static_cast<uint8_t>(ex_here + 127);
+          __syncwarp();
+        }
         // boxes that hold a key; the rows of the others keep what they held
         const int boxes = min(n_box, (x.len - key0 + (1 << box_shift) - 1) >> box_shift);
         if (lane == 0)
@@ -556,7 +589,17 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int nb = 0; nb < NB; ++nb) mma16816<false>(sc[nb][kk % kChains], f, qb[nb][kk][0], qb[nb][kk][1]);
           }
         }
-        // scaled scores s[nb][e]: key ar + 8 (e >> 1), query row 2 qd + (e & 1)
+        // scaled scores s[nb][e]: key ar + 8 (e >> 1), query row 2 qd + (e & 1). With scales
+        // 2^ek and 2^ev of the page they carry that of V too, so that P is the weight of the
+        // stored V and stays at most 2^tau however the pages' scales differ; the sum takes
+        // it out again.
+        float k_up = 1.0f, v_exp = 0.0f, v_down = 1.0f;  // 2^ek, ev, 2^-ev
+        if constexpr (PAGES) {
+          const uint32_t x = *reinterpret_cast<const uint16_t*>(exponents + (stage * kWarps + warp) * 2);
+          k_up = __uint_as_float((x & 255u) << 23);
+          v_exp = static_cast<float>(static_cast<int>(x >> 8) - 127);
+          v_down = __uint_as_float((254u - (x >> 8)) << 23);
+        }
         float sv[NB][4];
         bool grew = false;
 #pragma unroll
@@ -564,7 +607,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + ar + 8 * (e >> 1);
-            const float v = (kChains == 2 ? sc[nb][0][e] + sc[nb][kChains - 1][e] : sc[nb][0][e]) * c[nb][e & 1];
+            const float raw = kChains == 2 ? sc[nb][0][e] + sc[nb][kChains - 1][e] : sc[nb][0][e];
+            const float v = PAGES ? fmaf(raw * c[nb][e & 1], k_up, v_exp) : raw * c[nb][e & 1];
             sv[nb][e] = key < last[nb][e & 1] ? v : -INFINITY;
             grew |= sv[nb][e] - m[nb][e & 1] > kTau;
           }
@@ -600,7 +644,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               pv[e] = ex2_approx(sv[nb][2 * h + e] - (m[nb][e] == -INFINITY ? 0.0f : m[nb][e] - lift));
-              l[nb][e] += pv[e];
+              l[nb][e] = PAGES ? fmaf(pv[e], v_down, l[nb][e]) : l[nb][e] + pv[e];
             }
             pb[nb][h] = transpose8x8(FP8 ? pack_f16x2(pv[0], pv[1]) : pack_bf16x2(pv[0], pv[1]));
           }
@@ -913,21 +957,21 @@ paged_join_kernel(const StreamParams p) {
   if (lane == 0) p.lse[row * p.lse_row + head * p.lse_head] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-template <int D, int R, bool FP8>
+template <int D, int R, int KIND>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p, int n_sm,
                    cudaStream_t stream) {
-  using Cfg = StreamCfg<D, R, FP8>;
+  using Cfg = StreamCfg<D, R, KIND>;
   p.grid = min(Cfg::kCtas * n_sm, kStreamCtas);
   int slot = prof_begin(kKPagedDecode, stream);
   cudaError_t e;
   if (p.cluster > 0) {
     for (p.cluster_shift = 0; 1 << p.cluster_shift < p.cluster;) ++p.cluster_shift;
-    e = launch_clusters<paged_stream_kernel<D, R, FP8, true>>(
+    e = launch_clusters<paged_stream_kernel<D, R, KIND, true>>(
         p.cluster, dim3(static_cast<unsigned>(p.items * p.cluster)), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
     prof_end(slot, stream);
     return e;
   }
-  e = launch_chained<paged_stream_kernel<D, R, FP8, false>>(dim3(p.grid), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
+  e = launch_chained<paged_stream_kernel<D, R, KIND, false>>(dim3(p.grid), kThreads, Cfg::kSmemBytes, stream, tk, tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedJoin, stream);
@@ -942,13 +986,15 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, StreamParams p,
 }  // namespace
 
 cudaError_t launch_paged_stream(const CUtensorMap& tk, const CUtensorMap& tv, const StreamParams& p,
-                                int d, int rows, bool e4m3, int n_sm, cudaStream_t stream) {
-  if (d == 128) {
-    if (rows == 8) return e4m3 ? launch<128, 8, true>(tk, tv, p, n_sm, stream) : launch<128, 8, false>(tk, tv, p, n_sm, stream);
-    return e4m3 ? launch<128, 16, true>(tk, tv, p, n_sm, stream) : launch<128, 16, false>(tk, tv, p, n_sm, stream);
-  }
-  if (rows == 8) return e4m3 ? launch<64, 8, true>(tk, tv, p, n_sm, stream) : launch<64, 8, false>(tk, tv, p, n_sm, stream);
-  return e4m3 ? launch<64, 16, true>(tk, tv, p, n_sm, stream) : launch<64, 16, false>(tk, tv, p, n_sm, stream);
+                                int d, int rows, int kind, int n_sm, cudaStream_t stream) {
+  auto of_kind = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if (d == 128) return rows == 8 ? launch<128, 8, K>(tk, tv, p, n_sm, stream) : launch<128, 16, K>(tk, tv, p, n_sm, stream);
+    return rows == 8 ? launch<64, 8, K>(tk, tv, p, n_sm, stream) : launch<64, 16, K>(tk, tv, p, n_sm, stream);
+  };
+  if (kind == kBf16) return of_kind(std::integral_constant<int, kBf16>{});
+  if (kind == kE4m3) return of_kind(std::integral_constant<int, kE4m3>{});
+  return of_kind(std::integral_constant<int, kE4m3Pages>{});
 }
 
 }  // namespace attn

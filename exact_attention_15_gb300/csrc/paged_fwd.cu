@@ -43,8 +43,16 @@ namespace attn {
 
 namespace {
 
-template <int D, bool E4M3>
+// Key tiles whose pages' scales are kept. The producer writes those of tile j when it has a place
+// for the first half of K_j in the small ring; the halves before it there have been widened then,
+// K_(j - 2) or a later tile among them, into places of the K / V ring that V_(j - 6) or a later
+// tile had left. V_i leaves its place when its products are done, which come after both softmax
+// warpgroups have finished with tile i: of eight places none is overwritten that is still read.
+constexpr int kScaleSlots = 8;
+
+template <int D, int KIND>
 struct PagedFwdCfg {
+  static constexpr bool E4M3 = KIND != kBf16;
   static constexpr int kBlocks = D / 64;                // 64-column blocks of a tile
   static constexpr int kBlockBytes = kTileM * 64 * 2;   // 16 KB
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
@@ -57,7 +65,9 @@ struct PagedFwdCfg {
   static constexpr int kKVOff = 2 * kTileBytes;
   static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + (E4M3 ? kRawStages * kRawBytes : 0);
-  static constexpr int kEpiOff = kBarOff + 1024;        // one staging block per warpgroup
+  // a scale for each page: what the softmax needs of the 16-key groups of a key tile
+  static constexpr int kScaleOff = kBarOff + 1024;
+  static constexpr int kEpiOff = kScaleOff + (KIND == kE4m3Pages ? kScaleSlots * 8 * 16 : 0);  // one staging block per warpgroup
   static constexpr int kSmemBytes = kEpiOff + 2 * kBlockBytes + 1024;
   static constexpr uint32_t kColS = 2 * D;
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -248,16 +258,18 @@ struct TileSource {
   }
 };
 
-template <int D, bool E4M3>
+template <int D, int KIND>
 __global__ void __launch_bounds__(384, 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedFwdParams p) {
-  using Cfg = PagedFwdCfg<D, E4M3>;
+  using Cfg = PagedFwdCfg<D, KIND>;
+  constexpr bool E4M3 = Cfg::E4M3, PAGES = KIND == kE4m3Pages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   PagedBars* bars = reinterpret_cast<PagedBars*>(smem + Cfg::kBarOff);
   static_assert(sizeof(PagedBars) <= 1024, "barrier block");
+  float4* page_scales = reinterpret_cast<float4*>(smem + Cfg::kScaleOff);  // [kScaleSlots][8]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -327,6 +339,22 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           return j < n_kv && j_box < n_box && key < t.len ? page_of(p.s, t.b, key >> p.s.page_shift) : 0;
         };
         int id = page_at(0);
+        // A scale for each page: lane g < 8 looks up those of keys 16 g .. 16 g + 15 of a tile
+        // (they share a page), the page two tiles ahead and its exponents one.
+        auto scale_page_at = [&](int j) {
+          const int key = (t.kt0 + j) * kTileN + lane * 16;
+          return lane < 8 && j < n_kv && key < t.len ? page_of(p.s, t.b, key >> p.s.page_shift) : 0;
+        };
+        auto scales_at = [&](int page) {
+          return lane < 8 ? make_int2(page_exponent(p.k_exp, page, p.H_kv, t.h), page_exponent(p.v_exp, page, p.H_kv, t.h))
+                          : make_int2(0, 0);
+        };
+        int2 ex = make_int2(0, 0);
+        int ex_page = 0;
+        if constexpr (PAGES) {
+          ex = scales_at(scale_page_at(0));
+          ex_page = scale_page_at(1);
+        }
         // Q goes in once the previous tile's last S MMA has read its buffer
         if (qk > 0 && !mbar_wait_warp(smem_addr(&bars->q_empty), (qk - 1) & 1, lim)) {
           ok = false;
@@ -346,6 +374,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int j = 0; ok && j < n_kv; ++j) {
           const int here = id;
           id = page_at(j + 1);
+          const int2 ex_here = ex;
+          if constexpr (PAGES) {
+            ex = scales_at(ex_page);
+            ex_page = scale_page_at(j + 2);
+          }
           const int key0 = (t.kt0 + j) * kTileN;
           // boxes that hold a key; the rows of the others keep what they held
           const int boxes = min(n_box, (t.len - key0 + (1 << box_shift) - 1) >> box_shift);
@@ -360,6 +393,12 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint32_t stage = ld % Cfg::kRawStages, round = ld / Cfg::kRawStages;
                 if (!mbar_wait_warp(smem_addr(&bars->raw_empty[stage]), (round & 1) ^ 1, lim)) { ok = false; break; }
                 const uint32_t fbar = smem_addr(&bars->raw_full[stage]);
+                if (PAGES && kv == 0 && half == 0) {
+                  if (lane < 8)
+                    page_scales[((ld >> 2) % kScaleSlots) * 8 + lane] = make_float4(
+                        power_of_two(ex_here.x), static_cast<float>(ex_here.y), power_of_two(-ex_here.y), 0.0f);
+                  __syncwarp();
+                }
                 if (lane == 0)
                   mbar_arrive_expect_tx(fbar, max(0, min(per, boxes - half * per)) * (D << box_shift));
                 __syncwarp();
@@ -586,9 +625,12 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     int sw = 0, pvw = 0;  // s_full and pv_done waits so far
     constexpr float lift = E4M3 ? kLift : 0.0f;
     bool ok = true;
+    uint32_t tiles_before = 0;  // key tiles of the work tiles before this one
     for (int k = 0; ok; ++k) {
       PagedTile t;
       if (!take_tile(bars, k, t, lim, ok)) break;
+      const uint32_t tile0 = tiles_before;
+      tiles_before += max(t.n[0], t.n[1]);
       const int my_n = i ? t.n[1] : t.n[0];
       const int q0 = t.q0 + i * p.tok_tile;           // first token of this query tile
       const int see0 = t.len - t.n_new + q0;          // the last key that it sees (causal)
@@ -627,12 +669,17 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t pk[64];
         bool rescale_warp;
         float factor;
-        const float mb = pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
-                                                     rescale_warp, factor)
-                             : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
-                                                      rescale_warp, factor);
+        const float4* of_page = page_scales + ((tile0 + j) % kScaleSlots) * 8;
+        if constexpr (PAGES) softmax_row_pages(s, c, of_page);
+        const float mb = PAGES ? softmax_row_max<true>(s, 1.0f, m_used, l, kv0, 0, see, need_mask, 0,
+                                                       rescale_warp, factor)
+                         : pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                       rescale_warp, factor)
+                               : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                        rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
-        if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
+        if constexpr (PAGES) softmax_row_exp_pages(s, mb - lift, of_page, pk, sum2);
+        else if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
         else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
         if (rescale_warp && j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
           // O is complete: the commit that signalled S_j came after PV_{j-1}
@@ -1046,7 +1093,7 @@ queries_f16_kernel(const uint2* q, uint2* q16, float* q_up, long long rows) {
   if (lane == 0) q_up[row] = up;
 }
 
-template <int D, bool E4M3>
+template <int D, int KIND>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const PagedFwdParams& p, cudaStream_t stream) {
   // sorting compares every pair of sequences and keeps them in shared memory
@@ -1057,7 +1104,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  e = launch_chained<paged_fwd_kernel<D, E4M3>>(dim3(p.grid), 384, PagedFwdCfg<D, E4M3>::kSmemBytes, stream, tq, tk,
+  e = launch_chained<paged_fwd_kernel<D, KIND>>(dim3(p.grid), 384, PagedFwdCfg<D, KIND>::kSmemBytes, stream, tq, tk,
                      tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
@@ -1070,9 +1117,11 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 }  // namespace
 
 cudaError_t launch_paged_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedFwdParams& p, int d, bool e4m3, cudaStream_t stream) {
-  if (e4m3) return d == 128 ? launch<128, true>(tq, tk, tv, p, stream) : launch<64, true>(tq, tk, tv, p, stream);
-  return d == 128 ? launch<128, false>(tq, tk, tv, p, stream) : launch<64, false>(tq, tk, tv, p, stream);
+                             const PagedFwdParams& p, int d, int kind, cudaStream_t stream) {
+  if (kind == kE4m3Pages)
+    return d == 128 ? launch<128, kE4m3Pages>(tq, tk, tv, p, stream) : launch<64, kE4m3Pages>(tq, tk, tv, p, stream);
+  if (kind == kE4m3) return d == 128 ? launch<128, kE4m3>(tq, tk, tv, p, stream) : launch<64, kE4m3>(tq, tk, tv, p, stream);
+  return d == 128 ? launch<128, kBf16>(tq, tk, tv, p, stream) : launch<64, kBf16>(tq, tk, tv, p, stream);
 }
 
 cudaError_t launch_queries_f16(const void* q, void* q16, float* q_up, long long rows, int d,

@@ -23,6 +23,7 @@ from .build import CALLS_LIB
 
 CACHE_BF16 = 0
 CACHE_E4M3 = 1
+CACHE_E4M3_PAGES = 3  # a power of two for each page and KV head
 _KINDS = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -68,7 +69,7 @@ def _load_calls():
 class _PagedCacheStruct(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("k_page_stride", _L),
                 ("v_page_stride", _L), ("num_pages", _I), ("page_size", _I), ("H_kv", _I), ("d", _I),
-                ("type", _I)]
+                ("type", _I), ("k_exp", _P), ("v_exp", _P)]
 
 
 class PagedCache:
@@ -77,8 +78,10 @@ class PagedCache:
     k and v: [num_pages, H_kv, page_size, d], bf16 or float8_e4m3fn, on the GPU,
     contiguous within a page (pages may be further apart, as in the halves of one
     [num_pages, 2, ...] tensor). k_scale and v_scale (e4m3): fp32 [H_kv], the
-    factor a head's stored values stand for; None for 1. Keeps the tensors; their
-    contents may change between calls."""
+    factor a head's stored values stand for; None for 1. Both scales as contiguous
+    float8_e8m0fnu [num_pages, H_kv] give each page and head a power of two of its own, which
+    paged_append finds and writes (exponents from -64 to 64; others count as the nearest of
+    these). Keeps the tensors; their contents may change between calls."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         for name, t in (("k", k), ("v", v)):
@@ -91,22 +94,29 @@ class PagedCache:
         for name, t in (("k", k), ("v", v)):
             if num_pages > 0 and not t[0].is_contiguous():
                 raise ValueError(f"{name} must be contiguous within a page")
+        of_pages = any(t is not None and t.dtype == torch.float8_e8m0fnu for t in (k_scale, v_scale))
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is None:
+                if of_pages:
+                    raise ValueError(f"{name}: pages with scales need those of k and of v")
                 continue
             if k.dtype == _bf16:
                 raise ValueError(f"{name}: a bf16 cache has no scales")
-            _check_tensor(name, t, (H_kv,), torch.float32, k.device)
+            if of_pages:
+                _check_tensor(name, t, (num_pages, H_kv), torch.float8_e8m0fnu, k.device)
+            else:
+                _check_tensor(name, t, (H_kv,), torch.float32, k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.H_kv, self.page_size, self.d = num_pages, H_kv, page_size, d
         self.device = k.device
         self._index = k.get_device()
-        self._kind = _KINDS[k.dtype]
+        self._kind = CACHE_E4M3_PAGES if of_pages else _KINDS[k.dtype]
         page = H_kv * page_size * d
         self._struct = _PagedCacheStruct(
-            k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+            k.data_ptr(), v.data_ptr(), None if of_pages else _ptr(k_scale), None if of_pages else _ptr(v_scale),
             k.stride(0) if num_pages > 1 else page, v.stride(0) if num_pages > 1 else page,
-            num_pages, page_size, H_kv, d, self._kind)
+            num_pages, page_size, H_kv, d, self._kind, _ptr(k_scale) if of_pages else None,
+            _ptr(v_scale) if of_pages else None)
         self._ref = ctypes.addressof(self._struct)
         self._lib = load()
         self._calls = _load_calls()
@@ -117,21 +127,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_seqs(cache, page_table, kv_lens, cu_seqlens, tokens):
+def _check_seqs(cache, page_table, kv_lens, cu_seqlens, tokens, lists=False):
     """Checks the arrays that describe the sequences. Returns their number and the
-    page table's pointer, columns and row stride (one row may have any)."""
+    page table's pointer, columns and row stride (one row may have any). With `lists`
+    the page table has a row for each KV head, and two strides come back."""
     index = cache._index
     if (kv_lens.dtype is not _i32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous()
             or kv_lens.get_device() != index):
         raise ValueError(f"kv_lens must be a contiguous 1-D int32 tensor on {cache.device}")
     B = kv_lens.numel()
-    if page_table.dtype is not _i32 or page_table.dim() != 2 or page_table.get_device() != index:
+    if page_table.dtype is not _i32 or page_table.dim() != (3 if lists else 2) or page_table.get_device() != index:
         raise ValueError(f"page_table must be a [{B}, max_pages] int32 tensor on {cache.device}")
-    rows, cols = page_table.shape
+    rows, cols = page_table.shape[0], page_table.shape[-1]
     stride = cols
     if rows != B:
         raise ValueError(f"page_table has {rows} rows for {B} sequences")
-    if not page_table.is_contiguous():
+    if lists:
+        if page_table.shape[1] != cache.H_kv:
+            raise ValueError(f"page_table has lists of {page_table.shape[1]} KV heads, the cache {cache.H_kv}")
+        if cols > 1 and page_table.stride(2) != 1:
+            raise ValueError("page_table must have contiguous rows")
+        stride = (page_table.stride(0) if rows > 1 else cache.H_kv * cols,
+                  page_table.stride(1) if cache.H_kv > 1 else cols)
+    elif not page_table.is_contiguous():
         stride = page_table.stride(0) if rows > 1 else cols
         if cols > 1 and page_table.stride(1) != 1:
             raise ValueError("page_table must have contiguous rows")
@@ -262,6 +280,8 @@ def _workspace(cache, workspace, size):
 def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, workspace=None):
     """Attention of one new token per sequence over the cache: q [B, H_q, d] bf16.
     Returns (o [B, H_q, d], lse [B, H_q]); a sequence without keys gives 0 and -inf.
+    page_table is [B, max_pages], or [B, H_kv, max_pages] where each KV head has a list of pages
+    of its own (paged_select's; kv_lens then counts the keys of each list).
     The default scale is 1/sqrt(d). The workspace (paged_workspace_bytes) is
     allocated with torch unless given."""
     if out is None and lse is None and workspace is None:
@@ -271,12 +291,14 @@ def paged_decode(cache, q, page_table, kv_lens, scale=None, out=None, lse=None, 
                 _check(r, "attn_paged_decode")
             return r
     T, H_q, _ = _tokens("q", q, cache)
-    B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, None, T)
+    lists = page_table.dim() == 3
+    B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, None, T, lists)
     o, lse = _outputs(cache, q, (B, H_q), out, lse)
     lib = cache._lib
     ws, size = _workspace(cache, workspace, cache._decode_bytes)
-    status = _call(cache._index, lib.attn_paged_decode, cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                   B, H_q, kv_lens.data_ptr(), table, cols, stride,
+    status = _call(cache._index, lib.attn_paged_decode_lists if lists else lib.attn_paged_decode, cache._ref, q.data_ptr(),
+                   o.data_ptr(), lse.data_ptr(), B, H_q, kv_lens.data_ptr(), table, cols,
+                   *(stride if lists else (stride,)),
                    1.0 / math.sqrt(cache.d) if scale is None else scale, ws.data_ptr(), size)
     if status:
         _check(status, "attn_paged_decode")
@@ -310,3 +332,56 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
     if status:
         _check(status, "attn_paged_fwd")
     return o, lse
+
+
+def paged_bounds(cache, bounds, page_table, kv_lens, cu_seqlens=None, tokens=None):
+    """Brings the bounds of the keys up to date after paged_append: bounds
+    [num_pages, H_kv, 2, d] bf16, the elementwise minimum and maximum of each page's keys in
+    use. Writes those of the pages that the new tokens lie in (kv_lens and cu_seqlens as in the
+    append; with cu_seqlens `tokens` is their number, that of the append's rows). Returns
+    bounds."""
+    _check_tensor("bounds", bounds, (cache.num_pages, cache.H_kv, 2, cache.d), _bf16, cache.device)
+    if tokens is None:
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens needs the number of tokens that it packs")
+        tokens = kv_lens.numel()
+    T = tokens
+    B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
+    status = _call(cache._index, cache._lib.attn_paged_bounds, cache._ref, bounds.data_ptr(), T, B,
+                   None if cu_seqlens is None else cu_seqlens.data_ptr(), kv_lens.data_ptr(), table, cols, stride)
+    if status:
+        _check(status, "attn_paged_bounds")
+    return bounds
+
+
+def paged_select(cache, q, bounds, page_table, kv_lens, count, cu_seqlens=None, keep_first=0, keep_last=1,
+                 pages=None, lens=None):
+    """Chooses `count` pages for each new token and KV head to attend to: the keep_first first
+    and keep_last last of those that hold the token's keys, and the ones with the largest bound of
+    q . k over the KV head's query heads. q [T, H_q, d] bf16 (turned), bounds as kept by
+    paged_bounds; kv_lens and cu_seqlens as in paged_append (None: one token per sequence).
+    Returns (pages [T, H_kv, count] int32, -1 behind the last one, lens [T] int32), a page table
+    and lengths for paged_decode."""
+    _check_tensor("bounds", bounds, (cache.num_pages, cache.H_kv, 2, cache.d), _bf16, cache.device)
+    T, H_q, _ = _tokens("q", q, cache)
+    if H_q < 1 or H_q % cache.H_kv:
+        raise ValueError(f"q has {H_q} heads, not a multiple of the cache's {cache.H_kv}")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if keep_first < 0 or keep_last < 1 or keep_first + keep_last > count:
+        raise ValueError(f"of {count} pages the first {keep_first} and the last {keep_last} cannot be kept")
+    B, table, cols, stride = _check_seqs(cache, page_table, kv_lens, cu_seqlens, T)
+    if pages is None:
+        pages = _empty((T, cache.H_kv, count), dtype=_i32, device=cache.device)
+    else:
+        _check_tensor("pages", pages, (T, cache.H_kv, count), _i32, cache.device)
+    if lens is None:
+        lens = _empty((T,), dtype=_i32, device=cache.device)
+    else:
+        _check_tensor("lens", lens, (T,), _i32, cache.device)
+    status = _call(cache._index, cache._lib.attn_paged_select, cache._ref, q.data_ptr(), bounds.data_ptr(),
+                   pages.data_ptr(), lens.data_ptr(), T, B, H_q, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                   kv_lens.data_ptr(), table, cols, stride, count, keep_first, keep_last)
+    if status:
+        _check(status, "attn_paged_select")
+    return pages, lens

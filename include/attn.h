@@ -259,6 +259,12 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  * H_kv entries, NULL for 1, and not read with bf16. d is 64 or 128; page_size is
  * 16, 32, 64, 128 or 256; k and v are 16-byte aligned.
  *
+ * ATTN_CACHE_E4M3_PAGES: e4m3 with a power of two for each page and head. k_exp and v_exp are
+ * device arrays of num_pages * H_kv bytes (the E8M0 format of scales): an x of page p and
+ * head h stands for x * 2^(k_exp[p * H_kv + h] - 127). attn_paged_append finds them and writes
+ * exponents from -64 to 64; others count as the nearest of these. The scale arrays are not
+ * read.
+ *
  * Sequences are described by device arrays that the host does not read:
  *   kv_lens     int32 [B]: keys of each sequence, its new tokens among them
  *   page_table  int32 [B, max_pages], rows table_stride entries apart: token t
@@ -281,6 +287,7 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  */
 #define ATTN_CACHE_BF16 0
 #define ATTN_CACHE_E4M3 1
+#define ATTN_CACHE_E4M3_PAGES 3
 typedef struct {
   void* k;
   void* v;
@@ -289,6 +296,8 @@ typedef struct {
   long long k_page_stride, v_page_stride; /* elements */
   int num_pages, page_size, H_kv, d;
   int type;
+  unsigned char* k_exp; /* ATTN_CACHE_E4M3_PAGES alone */
+  unsigned char* v_exp;
 } attn_paged_cache;
 
 /*
@@ -308,6 +317,12 @@ typedef struct {
  * Strides are multiples of 8 elements, tensor pointers 16-byte aligned. The pages that
  * a call writes must not be shared with another of its sequences. Rows of q_out
  * at padding positions are left as they were.
+ * With a scale for each page, a page that begins with a new token takes for each head the
+ * smallest exponent e (from -64 to 64) with which 448 * 2^e is at least the largest finite
+ * magnitude of its new values; a page that holds rows already takes the larger of that and what it
+ * had, and where it grows those rows are encoded again. Values x / 2^e are rounded to nearest,
+ * those past +-448 (infinities among them) to +-448. With rotary_dim > 0 keys count with 1.5
+ * times their magnitude before the turn, which no turned element exceeds.
  */
 int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* k, const void* v,
                       void* q_out, long long q_stride, long long k_stride, long long v_stride,
@@ -364,6 +379,49 @@ int attn_paged_fwd(const attn_paged_cache* cache, const void* q, void* o, float*
                    int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
                    int max_pages, long long table_stride, int causal, float scale, void* workspace,
                    size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_paged_decode with pages of its own for each KV head: lists int32 [B, H_kv, max_pages], the
+ * lists of a sequence head_stride entries apart, those of sequences list_stride (both at
+ * least max_pages). Key t of KV head h is row t % page_size of page lists[b][h][t / page_size],
+ * and kv_lens[b] counts the keys of each of a sequence's lists: what attn_paged_select writes. The
+ * workspace is that of attn_paged_decode.
+ */
+int attn_paged_decode_lists(const attn_paged_cache* cache, const void* q, void* o, float* lse, int B, int H_q,
+                            const int* kv_lens, const int* lists, int max_pages, long long list_stride,
+                            long long head_stride, float scale, void* workspace, size_t workspace_bytes,
+                            attn_stream_t stream);
+
+/*
+ * Bounds of the keys: bounds is bf16 [num_pages, H_kv, 2, d] (contiguous, 16-byte aligned), the
+ * elementwise minimum and then the maximum of a page's keys in use. A call writes those of
+ * the pages that the T new tokens lie in (as appended: seqlens, or NULL for one token per
+ * sequence), from all rows that are in use there; call it after attn_paged_append. Exact for
+ * bf16 and ATTN_CACHE_E4M3_PAGES, for ATTN_CACHE_E4M3 rounded to nearest. A NaN among the keys makes
+ * its column's bounds NaN.
+ */
+int attn_paged_bounds(const attn_paged_cache* cache, void* bounds, int T, int B, const int* seqlens,
+                      const int* kv_lens, const int* page_table, int max_pages, long long table_stride,
+                      attn_stream_t stream);
+
+/*
+ * Chooses `count` pages for each new token and KV head to attend to. Token i of the n of
+ * sequence b (rows of q, bf16 [T, H_q, d]; seqlens, or NULL for one token per sequence) sees
+ * its kv_lens[b] - n + i + 1 first keys. Of the pages that hold them the keep_first (>= 0) first and
+ * the keep_last (>= 1) last are taken, and of the others those with the largest
+ *   max over the query heads of the KV head of  sum_i max(q_i, 0) hi_i + min(q_i, 0) lo_i
+ * with lo and hi from `bounds` (attn_paged_bounds): no key of a page has a larger product with
+ * any of these queries. Decided as in 64 bits; equal values go to the lower page, a NaN is
+ * above all numbers. pages (int32 [T, H_kv, count]) gets their page indices in the order of the
+ * keys, -1 behind the last one; lens (int32 [T]) how many keys they hold (the last page is always
+ * chosen, so the lists are attn_paged_decode_lists' for B = T sequences). A token that sees no key
+ * gets no page and length 0; rows of tokens behind the last sequence are left as they were.
+ * keep_first + keep_last <= count, max_pages <= 65536, H_q / H_kv <= 128. Needs no workspace.
+ */
+int attn_paged_select(const attn_paged_cache* cache, const void* q, const void* bounds, int* pages, int* lens,
+                      int T, int B, int H_q, const int* seqlens, const int* kv_lens, const int* page_table,
+                      int max_pages, long long table_stride, int count, int keep_first, int keep_last,
+                      attn_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns the first failure a kernel of this library
