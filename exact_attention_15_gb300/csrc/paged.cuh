@@ -125,6 +125,20 @@ cudaError_t allow_smem(int most) {
   return e;
 }
 
+// Allows a kernel clusters of 16 CTAs, once per device.
+template <auto Kernel>
+cudaError_t allow_wide_clusters() {
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Launches a kernel that calls grid_wait() in every thread before it touches
 // memory: its launch and set-up overlap the end of the grid before it. Clusters of
 // `cluster` CTAs. (A kernel whose shared memory differs from call to call calls allow_smem with
@@ -208,10 +222,13 @@ struct SelectParams {
   int* pages;          // [T, H_kv, count]
   int* lens;           // [T]
   int H_q, H_kv, group, count, first, last;
-  int cluster_shift, slice;  // set by the launch: CTAs of a token and KV head, pages of each at most
+  // set by the launch: CTAs of a token and KV head, whether the first of them has all the scores, and
+  // how many a CTA can have
+  int cluster_shift, gather, slice;
+  long long wait_limit;
 };
-// Pages that a row of a page table may have: eight CTAs keep 8192 scores each.
-constexpr int kSelectSlice = 8192, kSelectCluster = 8, kSelectPages = kSelectSlice * kSelectCluster;
+// Pages that a row of a page table may have: 16 CTAs keep 4096 scores each.
+constexpr int kSelectSlice = 4096, kSelectCluster = 16, kSelectPages = kSelectSlice * kSelectCluster;
 cudaError_t launch_paged_select(const SelectParams& p, int d, int n_sm, cudaStream_t stream);
 
 // ---- streaming attention: few query rows per sequence

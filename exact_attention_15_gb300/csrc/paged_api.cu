@@ -489,6 +489,7 @@ int attn_paged_select(const attn_paged_cache* cache, const void* q, const void* 
   p.count = count;
   p.first = keep_first;
   p.last = keep_last;
+  p.wait_limit = dev.wait_limit;
   return launch_paged_select(p, cache->d, dev.n_sm, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;

@@ -113,29 +113,37 @@ paged_bounds_kernel(const BoundsParams p) {
 }
 
 // ---------------------------------------------------------------- selection
-// One cluster of 1 to 8 CTAs for each token and KV head; each takes a run of the pages.
+// One cluster of 1 to 16 CTAs for each token and KV head; each scores a run of the pages. Where
+// the first CTA's shared memory holds all scores it does the rest alone; behind wider tables
+// (10,000 pages or so) every CTA keeps its own, and they count together. (Each step that
+// a cluster takes together costs a barrier and reads of the others' shared memory: with 4096 pages on 8
+// CTAs the steps behind the scores took 18 us together, 11 in one.)
 //
 // 1. Bounds as products on mma.sync m16n8k16: 16 pages in M, the heads of the group in N,
-//    (lo, hi) and (min(q, 0), max(q, 0)) side by side in K. A lane's fragment of A is 16 bytes of
-//    a page's bounds at a time (the order of K does not matter as long as B has the same), so
-//    they go from memory to the registers, each byte once: the bytes bound this part.
+//    (lo, hi) and (min(q, 0), max(q, 0)) side by side in K, whose order does not matter as long as
+//    both operands have the same: a lane reads 16 bytes of a row at a time. The bytes bound
+//    this part: every warp has a ring of its own of 16 pages' bounds, filled by bulk copies.
+//    (With loads to registers, four 128-register CTAs' worth of which fit no SM, 4096 pages of
+//    8 heads took 9.7 us on 64 SMs.)
 // 2. A histogram of the scores over their range finds the interval that the last chosen
 //    score lies in.
 // 3. The products are exact, their sums are not: with eps a bound on the sums' error, pages
 //    more than 2 eps above the interval are chosen for certain, pages more than 2 eps below it are
-//    not, and the few between are scored again in 64 bits, where ties go to the lower page. So
-//    the choice is that of 64-bit scores, whatever the order of the sums.
+//    not, and the few between are scored again: as 64-bit integers, in units of 2^-61 of what
+//    the sums can be, so that they do not depend on an order (in 64-bit floating point where
+//    the inputs are no such numbers). Ties go to the lower page.
 // 4. The chosen pages are written in their order.
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32, kBins = 2048;
+constexpr int kBins = 1024;
 // Up to this many pages to be ranked in 64 bits are compared pair by pair, more by digits:
 // 256 threads of a CTA compare 512 with 512 in the time of about two of the ten digits.
 constexpr int kPairs = 512;
-// Error of a sum relative to the sum of the magnitudes: 2 d / 16 = 16 instructions, each of which
-// adds 17 terms, each to 2^-23 of the largest at least, is below 2^-14.9.
-constexpr float kSumError = 6.103515625e-05f;  // 2^-14
-// Sums below this stay finite, so that no score is an infinity or a NaN; above its inverse, what
-// products below the normal numbers lose (256 times 2^-126 at most) is less than the bound.
-constexpr float kLargest = 1.2676506e30f;  // 2^100
+// Error of a sum relative to the sum of the magnitudes: two chains of d / 16 = 8 instructions,
+// each of which adds 17 terms, each to 2^-23 of the largest at least, and the chains' sum to 2^-24,
+// is below 136 * 2^-23 + 2^-24 = 1.63e-5.
+constexpr float kSumError = 1.75e-5f;
+// Sums below this stay finite, so that no score is an infinity or a NaN; above the other, what
+// products below the normal numbers lose (256 times 2^-126 at most) is less than 2^-77 of it.
+constexpr float kLargest = 1.2676506e30f, kSmallest = 9.0949470e-13f;  // 2^100, 2^-40
 
 // An order of floats as unsigned numbers; NaN above all.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -145,15 +153,29 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xffffffffu));
 }
-__device__ __forceinline__ unsigned long long ordered(double x) {
-  if (x != x) return ~0ull;
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));  // (-0 as 0)
-  return b ^ (static_cast<unsigned long long>(static_cast<long long>(b) >> 63) | 0x8000000000000000ull);
+__device__ __forceinline__ long long ordered(double x) {  // (signed)
+  if (x != x) return 0x7fffffffffffffffll;
+  const long long b = __double_as_longlong(x + 0.0);  // (-0 as 0)
+  return b ^ static_cast<long long>(static_cast<unsigned long long>(b >> 63) >> 1);
+}
+constexpr long long kNoKey = -0x7fffffffffffffffll - 1;  // below them all
+// x (below 2^61 in magnitude) rounded to an integer, by two conversions to 32 bits: one to 64
+// runs at a fraction of their rate.
+__device__ __forceinline__ long long in_units(float x) {
+  const int high = __float2int_rn(x * 4.656612873e-10f);  // 2^-31
+  const int low = __float2int_rn(fmaf(static_cast<float>(high), -2147483648.0f, x));
+  return (static_cast<long long>(high) << 31) + low;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void max_cluster_u32(uint32_t addr, uint32_t x) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) { return static_cast<uint32_t>(ld_cluster_s32(addr)); }
-__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ long long ld_cluster_s64(uint32_t addr) {
+  long long v;
+  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -163,39 +185,40 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Where score i is kept: runs of 16 or 32 scores begin in different banks.
+__host__ __device__ __forceinline__ int spread(int i) { return i + (i >> 5); }
+__host__ __device__ __forceinline__ int spread_size(int n) { return (spread(n) + 3) & ~3; }
+
 // What a CTA shows the others of its cluster.
+template <int THREADS>
 struct SelectShared {
   uint32_t hist[kBins];
   uint32_t l1, k_most;       // largest sum of a query row's magnitudes; largest magnitude of the bounds
-  uint32_t least, most;      // scores, ordered
+  uint32_t least, most;      // scores, ordered (the least as its complement)
   uint32_t sure, unsure, chosen;
   uint32_t bin, above;       // the bin that was looked for, and what lies above it
-  uint32_t warp_sum[kSelWarps];
+  uint32_t warp_sum[THREADS / 32];
+  uint64_t full[THREADS / 32];
 };
 
 // Finds the bin from the top that holds the k-th of the clusters' numbers (k >= 1 and at most as
 // many as there are): sh.bin, and how many lie above it, sh.above. kPer bins a thread.
-template <int kPer>
-__device__ __forceinline__ void find_bin(SelectShared& sh, int cluster, uint32_t k) {
+template <int kPer, int THREADS>
+__device__ __forceinline__ void find_bin(SelectShared<THREADS>& sh, int cluster, uint32_t k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t v[kPer];
-  uint32_t mine = 0;
+  uint32_t v[kPer], mine = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = 0;
-  const uint32_t at = smem_addr(sh.hist + tid * kPer);
-  for (int r = 0; r < cluster; ++r) {
-    const uint32_t from = cluster_map(at, r);
-    if constexpr (kPer == 8) {
+  for (int i = 0; i < kPer; ++i) v[i] = sh.hist[tid * kPer + i];
+  if (cluster > 1) {
+    const int rank = cluster_ctarank();
+    const uint32_t at = smem_addr(sh.hist + tid * kPer);
+    for (int r = 1; r < cluster; ++r) {
+      const uint32_t from = cluster_map(at, (rank + r) & (cluster - 1));
+      uint32_t w[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        uint32_t w[4];
-        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + 4 * i) : "memory");
+      for (int i = 0; i < kPer; ++i) w[i] = ld_cluster_u32(from + 4 * i);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[i + u] += w[u];
-      }
-    } else {
-      v[0] += ld_cluster_u32(from);
+      for (int i = 0; i < kPer; ++i) v[i] += w[i];
     }
   }
 #pragma unroll
@@ -209,50 +232,68 @@ __device__ __forceinline__ void find_bin(SelectShared& sh, int cluster, uint32_t
   }
   if (lane == 0) sh.warp_sum[warp] = from_here;
   __syncthreads();
-  for (int w = warp + 1; w < kSelWarps; ++w) from_here += sh.warp_sum[w];
+  for (int w = warp + 1; w < THREADS / 32; ++w) from_here += sh.warp_sum[w];
   uint32_t above = from_here - mine;
   if (above < k && k <= from_here) {
+    bool found = false;
 #pragma unroll
     for (int i = kPer - 1; i >= 0; --i) {
-      if (above < k && k <= above + v[i]) {
+      if (!found && k <= above + v[i]) {
         sh.bin = tid * kPer + i;
         sh.above = above;
-        above = 0xffffffffu;  // found
-      } else if (above != 0xffffffffu) {
-        above += v[i];
+        found = true;
       }
+      above += v[i];
     }
   }
   __syncthreads();
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads, 2)
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
 paged_select_kernel(const SelectParams p) {
+  constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ SelectShared sh;
-  constexpr int kQStride = 4 * D + 64;  // bytes of a query row (the gap spreads rows over the banks)
+  __shared__ SelectShared<THREADS> sh;
+  constexpr int kStride = 4 * D + 64;  // bytes of a row of queries or bounds (the gap spreads rows over the banks)
   const PagedSeqs& s = p.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cluster = 1 << p.cluster_shift, rank = blockIdx.x & (cluster - 1);
+  const int ctas = 1 << p.cluster_shift, rank = blockIdx.x & (ctas - 1);
   const long long item = blockIdx.x >> p.cluster_shift;
   const int t = static_cast<int>(item / p.H_kv), h = static_cast<int>(item % p.H_kv);
   const int q_tiles = (p.group + 7) / 8;
   uint8_t* qs = smem;
-  unsigned long long* list_key = reinterpret_cast<unsigned long long*>(smem + q_tiles * 8 * kQStride);
-  float* score = reinterpret_cast<float*>(list_key + p.slice);
-  uint32_t* list = reinterpret_cast<uint32_t*>(score + p.slice);
-  auto sync = [&]() {
-    if (cluster > 1) cluster_sync_all(); else __syncthreads();
-  };
-  auto total = [&](const uint32_t& x) {
-    uint32_t sum = 0;
-    for (int r = 0; r < cluster; ++r) sum += ld_cluster_u32(cluster_map(smem_addr(&x), r));
-    return sum;
-  };
+  float* score = reinterpret_cast<float*>(qs + q_tiles * 8 * kStride);
+  // 16 pages' bounds for each warp, and when every page has its score those to be scored again
+  uint8_t* bounds_at = reinterpret_cast<uint8_t*>(score + spread_size(p.slice));
+  uint8_t* tile = bounds_at + warp * 16 * kStride;
+  long long* list_key = reinterpret_cast<long long*>(bounds_at);
+  uint32_t* list = reinterpret_cast<uint32_t*>(list_key + p.slice);
+  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  if (tid == 0) {
+    sh.l1 = sh.k_most = sh.most = sh.least = 0;
+    sh.sure = sh.unsure = sh.chosen = 0;
+  }
+  const uint32_t full = smem_addr(&sh.full[warp]);
+  if (lane == 0) {
+    mbar_init(full, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
   grid_wait();
   grid_release();
   if (blockIdx.x == 0) check_paged_seqs(s, tid, kSelThreads);
+
+  // ---- queries: a warp for each row, loaded before the token's sequence is looked up
+  constexpr int kPairs32 = D / 64;  // words of a lane
+  auto query_word = [&](int r, int i) {
+    return r < p.group ? __ldg(reinterpret_cast<const uint32_t*>(p.q) +
+                               (static_cast<size_t>(t) * p.H_q + h * p.group + r) * (D / 2) + i * 32 + lane)
+                       : 0u;
+  };
+  uint32_t first_row[kPairs32];
+#pragma unroll
+  for (int i = 0; i < kPairs32; ++i) first_row[i] = query_word(warp, i);
 
   // ---- the token's sequence and what it sees
   int b = t;
@@ -273,66 +314,83 @@ paged_select_kernel(const SelectParams p) {
   if (h == 0 && rank == 0 && tid == 0)
     p.lens[t] = len - (max(0, pages - p.count) << s.page_shift);
   if (pages <= p.count) {  // all of them
-    for (int i = rank * kSelThreads + tid; i < p.count; i += cluster * kSelThreads)
+    for (int i = rank * kSelThreads + tid; i < p.count; i += ctas * kSelThreads)
       out[i] = i < pages ? page_of(s, b, i) : -1;
     return;
   }
   const int room = p.count - p.first - p.last;  // pages to choose
   const int n_all = pages - p.first - p.last;   // pages to choose from
-  if (rank == 0) {
+  if (rank == ctas - 1) {
     for (int i = tid; i < p.first; i += kSelThreads) out[i] = page_of(s, b, i);
     for (int i = tid; i < p.last; i += kSelThreads) out[p.count - p.last + i] = page_of(s, b, pages - p.last + i);
   }
   if (room == 0) return;
-  const int per = ((n_all + cluster - 1) / cluster + 15) & ~15;
-  const int begin = min(n_all, rank * per), n = min(n_all, begin + per) - begin;
+  const int per = ((n_all + ctas - 1) / ctas + 15) & ~15;
+  int begin = min(n_all, rank * per), n = min(n_all, begin + per) - begin;
 
-  // ---- queries: a warp for each row
-  if (tid == 0) {
-    sh.l1 = sh.k_most = 0;
-    sh.least = 0xffffffffu;
-    sh.most = 0;
-    sh.sure = sh.unsure = sh.chosen = 0;
+  // ---- scores of 16 pages a warp
+  const int qd = lane & 3, ar = lane >> 2;
+  constexpr int kSteps = 2 * D / 32;  // 16-byte pieces of a lane in a row
+  const int tiles = (n + 15) / 16, my_tiles = tiles > warp ? (tiles - warp + kSelWarps - 1) / kSelWarps : 0;
+  // lane i < 16 copies page i of a tile (behind the last page that again); the table's entries are
+  // checked where they are used, so that their loads do not wait for one another
+  const int* table = s.page_table + static_cast<size_t>(b) * s.table_stride + p.first;
+  auto entry_at = [&](int k) {
+    return lane < 16 ? __ldg(table + begin + min((warp + k * kSelWarps) * 16 + lane, n - 1)) : 0;
+  };
+  auto checked = [&](int id) {
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(s.num_pages)) return id;
+    record_error(s.err, kErrPages);
+    return 0;
+  };
+  auto copy = [&](int entry) {
+    const int id = checked(entry);
+    if (lane == 0) mbar_arrive_expect_tx(full, 16 * 4 * D);
+    __syncwarp();
+    if (lane < 16)
+      bulk_load(smem_addr(tile + lane * kStride),
+                static_cast<const uint8_t*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * (4 * D), 4 * D, full);
+  };
+  int next = my_tiles > 0 ? entry_at(0) : 0;
+  if (ctas > 1) cluster_arrive();  // (this CTA's shared memory is ready for the others)
+  if (my_tiles > 0) {
+    copy(next);
+    if (my_tiles > 1) next = entry_at(1);
   }
-  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
-  __syncthreads();
   for (int r = warp; r < q_tiles * 8; r += kSelWarps) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.q) +
-                                                            ((static_cast<size_t>(t) * p.H_q + h * p.group + r) * D) * 2);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(qs + r * kQStride);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(qs + r * kStride);
     float sum = 0.0f;
 #pragma unroll
-    for (int i = lane; i < D / 2; i += 32) {
-      const uint32_t w = r < p.group ? src[i] : 0u;
+    for (int i = 0; i < kPairs32; ++i) {
+      const uint32_t w = r == warp ? first_row[i] : query_word(r, i);
       sum += fabsf(bf16lo_to_f32(w)) + fabsf(bf16hi_to_f32(w));
-      dst[i] = min2(w, 0u, false);
-      dst[D / 2 + i] = max2(w, 0u, false);
+      dst[i * 32 + lane] = min2(w, 0u, false);
+      dst[D / 2 + i * 32 + lane] = max2(w, 0u, false);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) atomicMax(&sh.l1, __float_as_uint(sum) & 0x7fffffffu);
   }
   __syncthreads();
-
-  // ---- scores of 16 pages a warp
-  const int qd = lane & 3, ar = lane >> 2;
-  constexpr int kSteps = 2 * D / 32;  // 16-byte pieces of a lane in a row
-  const uint4* bounds = static_cast<const uint4*>(p.bounds);
+  if (ctas > 1) cluster_wait();
+  const uint32_t scores_to = p.gather ? cluster_map(smem_addr(score), 0) : smem_addr(score);
+  const int score0 = p.gather ? begin : 0;
   uint32_t k_most = 0;
   float least = INFINITY, most = -INFINITY;
-  for (int tile = warp; tile * 16 < n; tile += kSelWarps) {
-    const int i0 = tile * 16 + ar;
-    uint4 a[2][kSteps];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int id = page_of(s, b, p.first + begin + min(i0 + 8 * u, n - 1));
-      const uint4* src = bounds + (static_cast<size_t>(id) * p.H_kv + h) * (2 * D / 8) + qd;
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) a[u][c] = __ldg(src + 4 * c);
+  bool ok = true;
+  for (int k = 0; k < my_tiles; ++k) {
+    const int i0 = (warp + k * kSelWarps) * 16 + ar;
+    // After a wait that ran out nothing more is copied, what is on its way is waited for once
+    // more, and the pages that are left count as 0.
+    if (ok && !mbar_wait_warp(full, k & 1, p.wait_limit)) {
+      if (lane == 0) record_error(s.err, kErrTimeout);
+      mbar_wait_warp(full, k & 1, p.wait_limit);
+      ok = false;
     }
+    const uint8_t* pages_at = tile + ar * kStride + qd * 16;
     float best[2] = {-INFINITY, -INFINITY};
     for (int nt = 0; nt < q_tiles; ++nt) {
-      const uint8_t* rows = qs + (nt * 8 + ar) * kQStride + qd * 16;
+      const uint8_t* rows = qs + (nt * 8 + ar) * kStride + qd * 16;
       float acc[2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -340,29 +398,38 @@ paged_select_kernel(const SelectParams p) {
         for (int e = 0; e < 4; ++e) acc[u][e] = 0.0f;
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
+        uint4 a[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) a[u] = *reinterpret_cast<const uint4*>(pages_at + 8 * u * kStride + c * 64);
         const uint4 w = *reinterpret_cast<const uint4*>(rows + c * 64);
-        mma_bf16(acc[0], a[0][c].x, a[1][c].x, a[0][c].y, a[1][c].y, w.x, w.y);
-        mma_bf16(acc[1], a[0][c].z, a[1][c].z, a[0][c].w, a[1][c].w, w.z, w.w);
+        mma_bf16(acc[0], a[0].x, a[1].x, a[0].y, a[1].y, w.x, w.y);
+        mma_bf16(acc[1], a[0].z, a[1].z, a[0].w, a[1].w, w.z, w.w);
+        if (nt == 0) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = __vmaxu2(a[u].x & 0x7fff7fffu, a[u].y & 0x7fff7fffu);
+            const uint32_t y = __vmaxu2(a[u].z & 0x7fff7fffu, a[u].w & 0x7fff7fffu);
+            k_most = __vmaxu2(k_most, __vmaxu2(x, y));
+          }
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (nt * 8 + 2 * qd + (e & 1) < p.group) best[e >> 1] = fmaxf(best[e >> 1], acc[0][e] + acc[1][e]);
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) {
-        const uint32_t x = __vmaxu2(a[u][c].x & 0x7fff7fffu, a[u][c].y & 0x7fff7fffu);
-        const uint32_t y = __vmaxu2(a[u][c].z & 0x7fff7fffu, a[u][c].w & 0x7fff7fffu);
-        k_most = __vmaxu2(k_most, __vmaxu2(x, y));
-      }
+    __syncwarp();
+    if (ok && k + 1 < my_tiles) {
+      copy(next);
+      if (k + 2 < my_tiles) next = entry_at(k + 2);
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], 1));
       best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], 2));
+      if (!ok) best[u] = 0.0f;
       const int i = i0 + 8 * u;
       if (i < n) {
-        if (qd == 0) score[i] = best[u];
+        if (qd == 0) st_cluster_f32(scores_to + 4 * spread(score0 + i), best[u]);
         least = fminf(least, best[u]);
         most = fmaxf(most, best[u]);
       }
@@ -375,35 +442,49 @@ paged_select_kernel(const SelectParams p) {
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
   if (lane == 0) {
-    atomicMax(&sh.k_most, max(k_most & 0xffffu, k_most >> 16) << 16);
-    atomicMin(&sh.least, ordered(least));
-    atomicMax(&sh.most, ordered(most));
+    // (the least as the most of what is opposite to it; every CTA gets every other's, or the first all)
+    const uint32_t x = max(k_most & 0xffffu, k_most >> 16) << 16, y = ~ordered(least), z = ordered(most);
+    for (int r = 0; r < (p.gather ? 1 : ctas); ++r) {
+      max_cluster_u32(cluster_map(smem_addr(&sh.k_most), r), x);
+      max_cluster_u32(cluster_map(smem_addr(&sh.least), r), y);
+      max_cluster_u32(cluster_map(smem_addr(&sh.most), r), z);
+    }
   }
-  sync();
+  if (ctas > 1) cluster_sync_all(); else __syncthreads();
+  if (p.gather) {
+    if (rank > 0) return;
+    begin = 0;
+    n = n_all;
+  }
+  // the CTAs that share the rest
+  const int cluster = p.gather ? 1 : ctas;
+  auto sync = [&]() {
+    if (cluster > 1) cluster_sync_all(); else __syncthreads();
+  };
+  auto total = [&](uint32_t& x) {
+    if (cluster == 1) return x;
+    uint32_t sum = 0;
+    for (int r = 0; r < cluster; ++r) sum += ld_cluster_u32(cluster_map(smem_addr(&x), r));
+    return sum;
+  };
 
   // ---- the interval [lo, hi] of the last score to be chosen
-  uint32_t k_bits = 0, lo_bits = 0xffffffffu, hi_bits = 0;
-  for (int r = 0; r < cluster; ++r) {
-    k_bits = max(k_bits, ld_cluster_u32(cluster_map(smem_addr(&sh.k_most), r)));
-    lo_bits = min(lo_bits, ld_cluster_u32(cluster_map(smem_addr(&sh.least), r)));
-    hi_bits = max(hi_bits, ld_cluster_u32(cluster_map(smem_addr(&sh.most), r)));
-  }
-  const float size = __uint_as_float(sh.l1) * __uint_as_float(k_bits);  // of the products' sums at most
-  // every product is zero; else sums outside these bounds are taken in 64 bits alone
-  const bool zero = sh.l1 == 0 || k_bits == 0;
-  const bool finite = zero || (size < kLargest && size > 1.0f / kLargest);
+  const float size = __uint_as_float(sh.l1) * __uint_as_float(sh.k_most);  // of the products' sums at most
+  // every product is zero; else sums outside these bounds are taken in floating point alone
+  const bool zero = sh.l1 == 0 || sh.k_most == 0;
+  const bool finite = zero || (size < kLargest && size > kSmallest);
   const float eps = size * kSumError;
-  float lo = unordered(lo_bits), hi = unordered(hi_bits);
+  float lo = unordered(~sh.least), hi = unordered(sh.most);
   const float range = hi - lo;
   if (finite && range > eps) {
     // (bins by the same rounded expression for every page, so their order is that of the scores)
     const float low = lo, inv = kBins / range;
     auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((x - low) * inv)); };
-    for (int i = tid; i < n; i += kSelThreads) atomicAdd(&sh.hist[bin_of(score[i])], 1u);
+    for (int i = tid; i < n; i += kSelThreads) atomicAdd(&sh.hist[bin_of(score[spread(i)])], 1u);
     sync();
     find_bin<kBins / kSelThreads>(sh, cluster, room);
     const int bin = sh.bin;
-    uint32_t above = sh.above;
+    const uint32_t above = sh.above;
     lo = low + bin * (range / kBins);
     hi = low + (bin + 1) * (range / kBins);
     // a bin far wider than eps (a few scores far from the rest): its own pages again
@@ -414,7 +495,7 @@ paged_select_kernel(const SelectParams p) {
       for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
       __syncthreads();
       for (int i = tid; i < n; i += kSelThreads)
-        if (bin_of(score[i]) == bin) atomicAdd(&sh.hist[bin2_of(score[i])], 1u);
+        if (bin_of(score[spread(i)]) == bin) atomicAdd(&sh.hist[bin2_of(score[spread(i)])], 1u);
       sync();
       find_bin<kBins / kSelThreads>(sh, cluster, room - above);
       const float w2 = range / kBins / kBins;
@@ -426,79 +507,107 @@ paged_select_kernel(const SelectParams p) {
   const float margin = 2.5f * eps + range * 1.9073486e-06f;
   const float low_cut = lo - margin, high_cut = hi + margin;
 
-  // ---- pages chosen for certain, and those to be scored again
-  for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + lane;
-    const float x = i < n ? score[i] : -INFINITY;
-    const bool sure = finite && i < n && x > high_cut, unsure = i < n && !sure && !(finite && x < low_cut);
-    const uint32_t a = __ballot_sync(0xffffffffu, sure), u = __ballot_sync(0xffffffffu, unsure);
-    uint32_t at = 0;
-    if (lane == 0) {
-      if (a) atomicAdd(&sh.sure, __popc(a));
-      if (u) at = atomicAdd(&sh.unsure, __popc(u));
-    }
-    at = __shfl_sync(0xffffffffu, at, 0);
-    if (unsure) list[at + __popc(u & ((1u << lane) - 1))] = i;
+  // ---- pages chosen for certain, and those to be scored again: a run of up to 32 a thread
+  const int run = (n + kSelThreads - 1) / kSelThreads, run0 = tid * run, run_n = max(0, min(run, n - run0));
+  uint32_t chosen = 0, unsure = 0;  // of the run, a bit each
+#pragma unroll 4
+  for (int i = 0; i < run_n; ++i) {
+    const float x = score[spread(run0 + i)];
+    const bool sure = finite && x > high_cut;
+    chosen |= static_cast<uint32_t>(sure) << i;
+    unsure |= static_cast<uint32_t>(!sure && !(finite && x < low_cut)) << i;
   }
+  for (uint32_t left = unsure; left; left &= left - 1) {
+    const uint32_t at = atomicAdd(&sh.unsure, 1u);
+    list[at] = run0 + __ffs(left) - 1;
+    list_key[at] = kNoKey;
+  }
+  const uint32_t sures = __reduce_add_sync(0xffffffffu, __popc(chosen));
+  if (lane == 0 && sures) atomicAdd(&sh.sure, sures);
   sync();
   const uint32_t n_unsure = total(sh.unsure), need = room - total(sh.sure);
   const int mine = sh.unsure;
   if (n_unsure == need) {
-    for (int e = tid; e < mine; e += kSelThreads) score[list[e]] = INFINITY;
+    for (int e = tid; e < mine; e += kSelThreads) score[spread(list[e])] = INFINITY;
     if (tid == 0) sh.chosen = mine;
   } else {
-    for (int e = warp; e < mine; e += kSelWarps) {
-      unsigned long long key = 0;
-      if (zero) {
-        key = ordered(0.0);
-      } else {
-        const int id = page_of(s, b, p.first + begin + list[e]);
-        const uint32_t* src = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * D;
-        for (int r = 0; r < p.group; ++r) {
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(qs + r * kQStride);
-          double sum = 0.0;
+    if (!zero) {
+      // 2^62 over a power of two that the sums' magnitudes stay below
+      const int top = static_cast<int>(__float_as_uint(size) >> 23) - 126;
+      const float unit = power_of_two(max(-126, min(126, 61 - top)));
+      // a warp for each page and four query rows
+      const int quads = (p.group + 3) / 4;
+      for (int x = warp; x < mine * quads; x += kSelWarps) {
+        const int e = x / quads, r0 = (x - e * quads) * 4;
+        const int page = page_of(s, b, p.first + begin + list[e]);
+        const uint32_t* src = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(page) * p.H_kv + h) * D;
+        uint32_t y[D / 32];
 #pragma unroll
-          for (int i = lane; i < D; i += 32) {  // pairs of (lo, hi)
-            const uint32_t x = q[i], y = __ldg(src + i);
-            sum = fma(static_cast<double>(bf16lo_to_f32(x)), static_cast<double>(bf16lo_to_f32(y)), sum);
-            sum = fma(static_cast<double>(bf16hi_to_f32(x)), static_cast<double>(bf16hi_to_f32(y)), sum);
+        for (int i = 0; i < D / 32; ++i) y[i] = __ldg(src + i * 32 + lane);
+        long long key = kNoKey;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (r0 + u >= p.group) break;
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(qs + (r0 + u) * kStride);
+          long long of_row = 0;
+          if (finite) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint32_t w = q[i * 32 + lane];
+              of_row += in_units(bf16lo_to_f32(w) * bf16lo_to_f32(y[i]) * unit);
+              of_row += in_units(bf16hi_to_f32(w) * bf16hi_to_f32(y[i]) * unit);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) of_row += __shfl_xor_sync(0xffffffffu, of_row, o);
+          } else {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint32_t w = q[i * 32 + lane];
+              sum = fma(static_cast<double>(bf16lo_to_f32(w)), static_cast<double>(bf16lo_to_f32(y[i])), sum);
+              sum = fma(static_cast<double>(bf16hi_to_f32(w)), static_cast<double>(bf16hi_to_f32(y[i])), sum);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            of_row = ordered(sum);
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          key = max(key, ordered(sum));
+          key = max(key, of_row);
         }
+        if (lane == 0) atomicMax(list_key + e, key);
       }
-      if (lane == 0) list_key[e] = key;
     }
     sync();
     if (n_unsure <= kPairs) {
       for (int e = tid; e < mine; e += kSelThreads) {
-        const unsigned long long key = list_key[e];
+        const long long key = list_key[e];
         const int place = begin + list[e];
         uint32_t better = 0;
         for (int r = 0; r < cluster; ++r) {
-          const uint32_t theirs = ld_cluster_u32(cluster_map(smem_addr(&sh.unsure), r));
-          const uint32_t keys = cluster_map(smem_addr(list_key), r), places = cluster_map(smem_addr(list), r);
+          const uint32_t theirs = cluster == 1 ? mine : ld_cluster_u32(cluster_map(smem_addr(&sh.unsure), r));
+          // (its own shared memory by an address of the same kind)
+          const uint32_t keys = cluster == 1 ? smem_addr(list_key) : cluster_map(smem_addr(list_key), r);
+          const uint32_t places = cluster == 1 ? smem_addr(list) : cluster_map(smem_addr(list), r);
 #pragma unroll 4
           for (uint32_t i = 0; i < theirs; ++i) {
-            const unsigned long long other = ld_cluster_u64(keys + 8 * i);
+            const long long other = ld_cluster_s64(keys + 8 * i);
             better += other > key || (other == key && static_cast<int>(ld_cluster_u32(places + 4 * i)) + r * per < place);
           }
         }
         if (better < need) atomicAdd(&sh.chosen, 1u);
         // (the list's scores are not read by others)
-        score[list[e]] = better < need ? INFINITY : -INFINITY;
+        score[spread(list[e])] = better < need ? INFINITY : -INFINITY;
       }
     } else {
       // By digits of 8 bits from the top: eight of the score, two of the place (lower ones first).
       unsigned long long key = 0;
       uint32_t place = 0, left = need;
+      auto key_of = [&](int e) { return static_cast<unsigned long long>(list_key[e]) ^ 0x8000000000000000ull; };
       auto place_of = [&](int e) { return 0xffffu - (begin + list[e]); };
       for (int digit = 0; digit < 10; ++digit) {
         for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
         for (int e = tid; e < mine; e += kSelThreads) {
-          const unsigned long long x = list_key[e];
+          const unsigned long long x = key_of(e);
           const uint32_t y = place_of(e);
           if (digit < 8) {
             if (digit == 0 || (x ^ key) >> (64 - 8 * digit) == 0) atomicAdd(&sh.hist[(x >> (56 - 8 * digit)) & 255], 1u);
@@ -507,63 +616,79 @@ paged_select_kernel(const SelectParams p) {
           }
         }
         sync();
-        find_bin<1>(sh, cluster, left);
+        find_bin<256 / kSelThreads>(sh, cluster, left);
         left -= sh.above;
         if (digit < 8) key |= static_cast<unsigned long long>(sh.bin) << (56 - 8 * digit);
         else place |= sh.bin << (8 * (9 - digit));
         sync();
       }
       for (int e = tid; e < mine; e += kSelThreads) {
-        const unsigned long long x = list_key[e];
+        const unsigned long long x = key_of(e);
         const bool in = x > key || (x == key && place_of(e) >= place);
         if (in) atomicAdd(&sh.chosen, 1u);
-        score[list[e]] = in ? INFINITY : -INFINITY;
+        score[spread(list[e])] = in ? INFINITY : -INFINITY;
       }
     }
   }
   sync();
 
-  // ---- the chosen pages in their order: a run of them for each warp
-  uint32_t at = p.first;
-  for (int r = 0; r < rank; ++r)
+  // ---- the chosen pages in their order
+  int at = p.first;
+  for (int r = 0; r < (cluster == 1 ? 0 : rank); ++r)
     at += ld_cluster_u32(cluster_map(smem_addr(&sh.sure), r)) + ld_cluster_u32(cluster_map(smem_addr(&sh.chosen), r));
-  const float cut = finite ? high_cut : 0.0f;
-  const int run = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
-  uint32_t before = 0;
-  for (int i = i0; i < i1; i += 32) before += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && score[i + lane] > cut));
-  if (lane == 0) sh.warp_sum[warp] = before;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) at += sh.warp_sum[w];
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1 && score[i + lane] > cut;
-    const uint32_t all = __ballot_sync(0xffffffffu, in);
-    if (in) out[at + __popc(all & ((1u << lane) - 1))] = page_of(s, b, p.first + begin + i + lane);
-    at += __popc(all);
+  for (uint32_t left = unsure; left; left &= left - 1) {
+    const int i = __ffs(left) - 1;
+    chosen |= static_cast<uint32_t>(score[spread(run0 + i)] == INFINITY) << i;
   }
+  int before = __popc(chosen);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sh.warp_sum[warp] = before;
+  __syncthreads();
+  at += before - __popc(chosen);
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) at += w < warp ? sh.warp_sum[w] : 0;
+  for (uint32_t left = chosen; left; left &= left - 1)
+    out[at++] = page_of(s, b, p.first + begin + run0 + __ffs(left) - 1);
   if (cluster > 1) cluster_sync_all();  // no CTA leaves while another one reads its counts
 }
 
+template <int D, int THREADS>
+cudaError_t launch_select(const SelectParams& p, int cluster, long long ctas, int smem, int most, cudaStream_t stream) {
+  cudaError_t e = allow_smem<paged_select_kernel<D, THREADS>>(most);
+  if (e == cudaSuccess) e = allow_wide_clusters<paged_select_kernel<D, THREADS>>();
+  if (e != cudaSuccess) return e;
+  return launch_clusters<paged_select_kernel<D, THREADS>>(cluster, dim3(static_cast<unsigned>(ctas)), THREADS, smem, stream, p);
+}
+
 template <int D>
-cudaError_t launch_select(SelectParams p, int n_sm, cudaStream_t stream) {
-  // More CTAs of a cluster while they find places at once (two on an SM) and each has a full
+cudaError_t plan_select(SelectParams p, int n_sm, cudaStream_t stream) {
+  constexpr int kStride = 4 * D + 64, kMost = 218 * 1024;  // (beside the static shared memory)
+  // More CTAs of a cluster while they find places at once (two on an SM) and each has a
   // round of its warps.
   const long long items = static_cast<long long>(p.s.T) * p.H_kv;
   int cluster = 1;
   p.cluster_shift = 0;
   while (cluster < kSelectCluster &&
          (p.s.max_pages > kSelectSlice * cluster ||
-          (items * 2 * cluster <= 2ll * n_sm && p.s.max_pages >= 2 * cluster * 16 * kSelWarps))) {
+          (items * 2 * cluster <= 2ll * n_sm && p.s.max_pages >= 2 * cluster * 128))) {
     cluster *= 2;
     ++p.cluster_shift;
   }
-  p.slice = ((p.s.max_pages + cluster - 1) / cluster + 15) & ~15;
-  if (items * cluster > 0x7fffffffll) return cudaErrorInvalidValue;
-  const int smem = (p.group + 7) / 8 * 8 * (4 * D + 64) + p.slice * 16;
-  const cudaError_t e = allow_smem<paged_select_kernel<D>>(kTileM * (4 * D + 64) + kSelectSlice * 16);
-  if (e != cudaSuccess) return e;
-  return launch_clusters<paged_select_kernel<D>>(cluster, dim3(static_cast<unsigned>(items * cluster)), kSelThreads, smem,
-                                                 stream, p);
+  const long long ctas = items * cluster;
+  const int warps = cluster > 1 ? 8 : 4;
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  auto bytes = [&](int share) {
+    p.slice = ((p.s.max_pages + share - 1) / share + 15) & ~15;
+    return (p.group + 7) / 8 * 8 * kStride + spread_size(p.slice) * 4 + max(warps * 16 * kStride, p.slice * 12);
+  };
+  p.gather = cluster > 1 && p.s.max_pages <= 32 * 256 && bytes(1) <= kMost;
+  const int smem = bytes(p.gather ? 1 : cluster);
+  return cluster > 1 ? launch_select<D, 256>(p, cluster, ctas, smem, kMost, stream)
+                     : launch_select<D, 128>(p, cluster, ctas, smem, kMost, stream);
 }
 
 }  // namespace
@@ -587,7 +712,7 @@ cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStre
 
 cudaError_t launch_paged_select(const SelectParams& p, int d, int n_sm, cudaStream_t stream) {
   const int slot = prof_begin(kKPagedSelect, stream);
-  const cudaError_t e = d == 128 ? launch_select<128>(p, n_sm, stream) : launch_select<64>(p, n_sm, stream);
+  const cudaError_t e = d == 128 ? plan_select<128>(p, n_sm, stream) : plan_select<64>(p, n_sm, stream);
   prof_end(slot, stream);
   return e;
 }
