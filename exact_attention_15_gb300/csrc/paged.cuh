@@ -73,15 +73,22 @@ struct TouchedPage {
 __host__ __device__ __forceinline__ long long touched_numbers(int T, int B, int page_shift, bool packed) {
   return packed ? (T >> page_shift) + 2ll * B : B;
 }
+// (The same number in every lane of a warp, which look for the sequence together: 32 places of the
+// offsets at a time, so that up to 1024 sequences take two dependent loads and not ten.)
 __device__ __forceinline__ bool touched_page(const PagedSeqs& s, long long number, TouchedPage& x) {
   x.b = static_cast<int>(number);
   long long first = number;
   if (s.cu_seqlens) {
     auto base = [&](int b) { return (min(max(__ldg(s.cu_seqlens + b), 0), s.T) >> s.page_shift) + 2ll * b; };
-    int lo = 0, hi = s.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (base(mid) <= number) lo = mid; else hi = mid;
+    const int lane = threadIdx.x & 31;
+    // the last sequence whose numbers begin at or before it lies in [lo, lo + n)
+    int lo = 0, n = s.B;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lo + lane * step;
+      const bool below = lane * step < n && base(at) <= number;
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+      n = min(step, n - last * step);
+      lo += last * step;
     }
     x.b = lo;
     first = base(lo);
@@ -199,6 +206,7 @@ struct AppendParams {
   uint8_t* k_exp; uint8_t* v_exp;  // a scale for each page: [num_pages, H_kv]
   int H_q, H_kv, d, rotary_dim, interleaved, e4m3;
 };
+// (over a cache with a scale for each page: when the exponents are there)
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
 // Over a cache with a scale for each page.
 cudaError_t launch_paged_append_pages(const AppendParams& p, cudaStream_t stream);
