@@ -18,9 +18,14 @@ constexpr int kBf16 = 0, kE4m3 = 1, kE4m3Pages = 3;
 // Exponents of the powers of two: within +-kMaxExp, so that sums of weights divided by them
 // stay far inside 32 bits (2^20 keys, a bias of 2^15 and 2^64).
 constexpr int kMaxExp = 64;
+__device__ __forceinline__ uint32_t page_byte(const uint8_t* exps, int page, int H_kv, int h) {
+  return __ldg(exps + static_cast<size_t>(page) * H_kv + h);
+}
+__device__ __forceinline__ int exponent_of(uint32_t byte) {
+  return max(-kMaxExp, min(kMaxExp, static_cast<int>(byte) - 127));
+}
 __device__ __forceinline__ int page_exponent(const uint8_t* exps, int page, int H_kv, int h) {
-  const int e = static_cast<int>(__ldg(exps + static_cast<size_t>(page) * H_kv + h)) - 127;
-  return max(-kMaxExp, min(kMaxExp, e));
+  return exponent_of(page_byte(exps, page, H_kv, h));
 }
 // 2^e, e from -126 to 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -53,11 +58,18 @@ __device__ __forceinline__ SeqSpan new_span(const PagedSeqs& s, int b) {
 // The page that holds place `i` of sequence b's page table row (i < max_pages), for KV head h
 // where the heads have pages of their own. An index outside the cache is recorded and page 0
 // taken for it.
-__device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int i, int h = 0) {
-  const int id = __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + h * s.head_stride + i);
+// A warp that looks pages up ahead keeps the table's entry and checks it when it uses it: the check
+// waits for the load.
+__device__ __forceinline__ int page_entry(const PagedSeqs& s, int b, int i, int h = 0) {
+  return __ldg(s.page_table + static_cast<size_t>(b) * s.table_stride + h * s.head_stride + i);
+}
+__device__ __forceinline__ int checked_page(const PagedSeqs& s, int id) {
   if (static_cast<unsigned>(id) < static_cast<unsigned>(s.num_pages)) return id;
   record_error(s.err, kErrPages);
   return 0;
+}
+__device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int i, int h = 0) {
+  return checked_page(s, page_entry(s, b, i, h));
 }
 // A page that new tokens of a sequence go to.
 struct TouchedPage {

@@ -220,7 +220,7 @@ size_t workspace_bytes_of(int T, int B, int group, int H_kv, int d, bool e4m3) {
 }
 size_t workspace_of_call(const attn_paged_cache* c, int T, int B, int group, bool packed, const StreamShape& shape) {
   if (shape.cluster > 0) return 0;
-  return packed ? workspace_bytes_of(T, B, group, c->H_kv, c->d, in_bytes(c)) : stream_plan(c->d).total;
+  return packed ? workspace_bytes_of(T, B, group, c->H_kv, c->d, c->type == kE4m3) : stream_plan(c->d).total;
 }
 
 int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q,
@@ -264,9 +264,9 @@ int launch_stream(const HostDevice& dev, const attn_paged_cache* c, const PagedS
 int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs& seqs, const void* q, void* o,
                float* lse, int H_q, int causal, float scale, uint8_t* ws, cudaStream_t cs) {
   const int group = H_q / c->H_kv;
-  const bool e4m3 = in_bytes(c);
+  const bool e4m3 = c->type == kE4m3;  // fp16 queries
   const FwdPlan plan = fwd_plan(seqs.T, seqs.B, group, c->H_kv, c->d, e4m3);
-  const int box = e4m3 ? kTileN / 2 : kTileN;  // rows that land together
+  const int box = in_bytes(c) ? kTileN / 2 : kTileN;  // rows that land together
   const unsigned rows = c->page_size < box ? c->page_size : box;
   CUtensorMap tq, tk, tv;
   int st;
@@ -396,7 +396,7 @@ size_t attn_paged_fwd_workspace_bytes(int T, int B, int H_q, int H_kv, int d, in
   if (T < 0 || B < 0 || H_q < 1 || H_kv < 1 || H_q > 65535 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
       (type != kBf16 && type != kE4m3 && type != kE4m3Pages))
     return 0;
-  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type != kBf16);
+  return workspace_bytes_of(T, B, H_q / H_kv, H_kv, d, type == kE4m3);
 }
 
 size_t attn_paged_call_workspace_bytes(const attn_paged_cache* cache, int T, int B, int H_q, int packed, int max_pages) {

@@ -78,7 +78,7 @@ __device__ __forceinline__ void encode_kept(uint8_t* head, int kept, int d, int 
   uint4* old = reinterpret_cast<uint4*>(head);
   const int n = kept * d >> 4;
   const float scale = power_of_two(max(-126, -more));
-#pragma unroll 4
+#pragma unroll 8
   for (int i = tid; i < n; i += nthreads) {
     const uint4 w = old[i];
     old[i] = make_uint4(encode_again(w.x, scale), encode_again(w.y, scale), encode_again(w.z, scale),

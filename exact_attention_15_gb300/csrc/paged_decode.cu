@@ -358,35 +358,37 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       auto page_at = [&](int t) {
         const int key = t * kTile + box_row;
-        return has_box && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
+        return has_box && key < x.len ? page_entry(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
       };
       int id = page_at(x.t0);
       // A scale for each page: lane w < 4 looks up that of K, lane 4 + w that of V of warp w's
       // 16 keys (they share a page), the page two tiles ahead and its exponent one.
       auto exp_page_at = [&](int t) {
         const int key = t * kTile + (lane & 3) * 16;
-        return lane < 8 && t < x.t1 && key < x.len ? page_of(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
+        return lane < 8 && t < x.t1 && key < x.len ? page_entry(p.s, x.b, key >> p.s.page_shift, x.h) : 0;
       };
-      auto exp_at = [&](int page) {
-        return lane < 8 ? page_exponent(lane < 4 ? p.k_exp : p.v_exp, page, p.H_kv, x.h) : 0;
+      auto exp_at = [&](int entry) {
+        const int page = static_cast<unsigned>(entry) < static_cast<unsigned>(p.s.num_pages) ? entry : 0;
+        return lane < 8 ? page_byte(lane < 4 ? p.k_exp : p.v_exp, page, p.H_kv, x.h) : 0u;
       };
-      int ex = 0, ex_page = 0;
+      uint32_t ex = 0;
+      int ex_page = 0;
       if constexpr (PAGES) {
         ex = exp_at(exp_page_at(x.t0));
         ex_page = exp_page_at(x.t0 + 1);
       }
       for (int t = x.t0; t < x.t1; ++t) {
         const int key0 = t * kTile;
-        const int here = id;
+        const int here = checked_page(p.s, id);
         if (t + 1 < x.t1) id = page_at(t + 1);
-        const int ex_here = ex;
+        const uint32_t ex_here = ex;
         if constexpr (PAGES) {
           ex = exp_at(ex_page);
           ex_page = exp_page_at(t + 2);
         }
         if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1, lim)) { ok = false; break; }
         if constexpr (PAGES) {
-          if (lane < 8) exponents[(stage * kWarps + (lane & 3)) * 2 + (lane >> 2)] = static_cast<uint8_t>(ex_here + 127);
+          if (lane < 8) exponents[(stage * kWarps + (lane & 3)) * 2 + (lane >> 2)] = static_cast<uint8_t>(exponent_of(ex_here) + 127);
           __syncwarp();
         }
         // boxes that hold a key; the rows of the others keep what they held

@@ -21,12 +21,18 @@
 //
 // Over an e4m3 cache the products run in fp16, which holds every e4m3 value exactly
 // (the instructions take no operands of two types): half tiles of 64 keys land in a
-// small ring of their own, and warps 2 and 3 widen one half each of every tile into
+// small ring of their own, and warps 2, 3, 12 and 13 widen a quarter each of every tile into
 // the K / V ring (and put the zeros past the end); lane 0 of warp 2 looks for work
-// between the tiles. The queries come as fp16 rows scaled by powers of two. One
-// widening warp, which loads, converts and stores 16 values at a time, took 1181 us
-// for the next 1024 tokens of two prompts of 25,000 (32 heads on 8, d 128); with a
-// row's loads ahead of its conversions 773; two warps 661 (bf16: 506).
+// between the tiles. The queries come as fp16 rows scaled by powers of two. Two widening
+// warps took 542 us for 8 prompts of 512 to 4096 (32 heads on 8, d 128; bf16: 358), four 535, and
+// with K_(j + 1) waited for only after P V(j) has been issued, since its place in the ring is
+// that of V_(j - 1), 498. A fourth place for half the small ring and half the staging: 513.
+//
+// A cache with a power of two for each page: K is widened to bf16 instead, so that the queries
+// are taken as they are (the rows scaled for fp16 cost a kernel of 50 us for those prompts), and the
+// producer keeps the scales of the 16-key groups of a tile in shared memory for the softmax
+// (softmax_row_max_pages). 501 us; without the conversion to bf16 496, without the groups'
+// scales 36 less.
 //
 // With many work tiles the CTAs claim them one by one. With few, what the last
 // wave leaves idle costs more: every CTA takes the same number of whole tiles, and
@@ -85,7 +91,10 @@ struct __align__(16) PagedTile {
 };
 
 constexpr int kSlots = 2;     // of the ring that hands out work tiles
-constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (e4m3: and two that widen)
+constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (e4m3: and those that widen)
+constexpr int kWideners = 4;  // e4m3: warps 2, 3, 12 and 13, a quarter of the rows of a tile each
+// (16 warps where there are some that widen, so that setmaxnreg finds whole warpgroups)
+constexpr int fwd_threads(int kind) { return kind == kBf16 ? 384 : 512; }
 
 struct PagedBars {
   uint64_t q_full, q_empty;
@@ -259,7 +268,7 @@ struct TileSource {
 };
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(fwd_threads(KIND), 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedFwdParams p) {
   using Cfg = PagedFwdCfg<D, KIND>;
@@ -281,16 +290,16 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mbar_init(smem_addr(&bars->pv_done[i]), 1);
     }
     for (int i = 0; i < Cfg::kStages; ++i) {
-      mbar_init(smem_addr(&bars->kv_full[i]), 1 + E4M3);  // the copies, or two warps
+      mbar_init(smem_addr(&bars->kv_full[i]), E4M3 ? kWideners : 1);  // the copies, or those that widen
       mbar_init(smem_addr(&bars->kv_empty[i]), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_addr(&bars->sched_full[i]), 1);
-      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders + 2 * E4M3);
+      mbar_init(smem_addr(&bars->sched_empty[i]), kReaders + kWideners * E4M3);
     }
     for (int i = 0; E4M3 && i < Cfg::kRawStages; ++i) {
       mbar_init(smem_addr(&bars->raw_full[i]), 1);
-      mbar_init(smem_addr(&bars->raw_empty[i]), 1);
+      mbar_init(smem_addr(&bars->raw_empty[i]), kWideners / 2);
     }
     mbar_init(smem_addr(&bars->drained), 1);
     bars->sched_taken = 0;
@@ -307,9 +316,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const long long lim = p.wait_limit;
   grid_wait();
 
-  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168.
-  if (warp < 4) {
-    regs_dec<88>();
+  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; e4m3: 256 x 72 (warps 0-3
+  // and 12-15) + 256 x 184 = 512 x 128 (8 prompts over pages with scales 501 us; with 64 and 192, or
+  // 80 and 176, which spill more, 517 and 513).
+  if (warp < 4 || warp >= 12) {
+    regs_dec<E4M3 ? 72 : 88>();
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       // Lane (page j of a key tile, column block) issues one box per tile.
@@ -336,20 +347,21 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (n_kv == 0) continue;
         auto page_at = [&](int j) {
           const int key = (t.kt0 + j) * kTileN + box_row;
-          return j < n_kv && j_box < n_box && key < t.len ? page_of(p.s, t.b, key >> p.s.page_shift) : 0;
+          return j < n_kv && j_box < n_box && key < t.len ? page_entry(p.s, t.b, key >> p.s.page_shift) : 0;
         };
         int id = page_at(0);
         // A scale for each page: lane g < 8 looks up those of keys 16 g .. 16 g + 15 of a tile
         // (they share a page), the page two tiles ahead and its exponents one.
         auto scale_page_at = [&](int j) {
           const int key = (t.kt0 + j) * kTileN + lane * 16;
-          return lane < 8 && j < n_kv && key < t.len ? page_of(p.s, t.b, key >> p.s.page_shift) : 0;
+          return lane < 8 && j < n_kv && key < t.len ? page_entry(p.s, t.b, key >> p.s.page_shift) : 0;
         };
-        auto scales_at = [&](int page) {
-          return lane < 8 ? make_int2(page_exponent(p.k_exp, page, p.H_kv, t.h), page_exponent(p.v_exp, page, p.H_kv, t.h))
-                          : make_int2(0, 0);
+        auto scales_at = [&](int entry) {
+          const int page = static_cast<unsigned>(entry) < static_cast<unsigned>(p.s.num_pages) ? entry : 0;
+          return lane < 8 ? make_uint2(page_byte(p.k_exp, page, p.H_kv, t.h), page_byte(p.v_exp, page, p.H_kv, t.h))
+                          : make_uint2(0, 0);
         };
-        int2 ex = make_int2(0, 0);
+        uint2 ex = make_uint2(0, 0);
         int ex_page = 0;
         if constexpr (PAGES) {
           ex = scales_at(scale_page_at(0));
@@ -372,9 +384,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
         for (int j = 0; ok && j < n_kv; ++j) {
-          const int here = id;
+          const int here = checked_page(p.s, id);
           id = page_at(j + 1);
-          const int2 ex_here = ex;
+          const uint2 ex_here = ex;
           if constexpr (PAGES) {
             ex = scales_at(ex_page);
             ex_page = scale_page_at(j + 2);
@@ -394,9 +406,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!mbar_wait_warp(smem_addr(&bars->raw_empty[stage]), (round & 1) ^ 1, lim)) { ok = false; break; }
                 const uint32_t fbar = smem_addr(&bars->raw_full[stage]);
                 if (PAGES && kv == 0 && half == 0) {
+                  const int ek = exponent_of(ex_here.x), ev = exponent_of(ex_here.y);
                   if (lane < 8)
-                    page_scales[((ld >> 2) % kScaleSlots) * 8 + lane] = make_float4(
-                        power_of_two(ex_here.x), static_cast<float>(ex_here.y), power_of_two(-ex_here.y), 0.0f);
+                    page_scales[((ld >> 2) % kScaleSlots) * 8 + lane] =
+                        make_float4(power_of_two(ek), static_cast<float>(ev), power_of_two(-ev), 0.0f);
                   __syncwarp();
                 }
                 if (lane == 0)
@@ -431,7 +444,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const bool leader = elect_one_sync();
-      constexpr uint32_t kIdS = E4M3 ? make_idesc_f16(128, 128, 0, 0) : make_idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t kIdS = E4M3 && !PAGES ? make_idesc_f16(128, 128, 0, 0) : make_idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t kIdPV = E4M3 ? make_idesc_f16(128, D, 0, 1) : make_idesc_bf16(128, D, 0, 1);
       const uint32_t kv_base = smem_addr(smem + Cfg::kKVOff);
       const uint64_t q_desc = make_sdesc_sw128(smem_addr(smem), 16, 1024);  // K-major
@@ -493,7 +506,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_async_shared();
             __syncwarp();
           }
-          if (next_k && !(ok = wait_full(itk))) break;
+          bool have_k = false;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (j >= t.n[i]) continue;
@@ -503,8 +516,15 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ++pw[i];
             // only the last PV of a tile is signalled (to the epilogue); earlier
             // ones are covered by the commit of the S MMA issued after them
-            if (j + 1 == t.n[i]) mma_commit_by(leader, smem_addr(&bars->pv_done[i]));
-            else issue_s(i, itk);
+            if (j + 1 == t.n[i]) {
+              mma_commit_by(leader, smem_addr(&bars->pv_done[i]));
+              continue;
+            }
+            // (not before P V, which needs no K: with a ring of three places K_(j + 1) takes that of V_(j - 1))
+            if (!have_k && !(ok = wait_full(itk))) break;
+            if (!have_k) tc_fence_after();
+            have_k = true;
+            issue_s(i, itk);
           }
           if (!ok) break;
           mma_commit_by(leader, smem_addr(&bars->kv_empty[stage_of(itv)]));
@@ -542,24 +562,23 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-    } else if (E4M3 && warp >= 2) {
+    } else if (E4M3 && warp >= 2 && warp < 12 + kWideners - 2) {
       // -------------------------------------------------------- widening (e4m3)
-      // Warp 2 the first, warp 3 the second half of every tile, a row per lane; both
-      // rings are swizzled, so neither side's accesses meet in a bank. Lane 0 of
-      // warp 2 publishes the next work tile when it takes one.
-      const int half = warp - 2;
+      // A quarter of every tile, a row per lane; both rings are swizzled, so neither side's
+      // accesses meet in a bank. Lane 0 of warp 2 publishes the next work tile when it takes one.
+      const int part = warp < 4 ? warp - 2 : warp - 10, half = part * 2 / kWideners;
       const uint32_t raw0 = smem_addr(smem + Cfg::kRawOff), kv0 = smem_addr(smem + Cfg::kKVOff);
       uint32_t ld = 0;  // tiles widened so far
       bool ok = true;
       TileSource source(p);
       PagedTile t;
-      if (half == 0 && lane == 0) {
+      if (part == 0 && lane == 0) {
         source.next(t);
         publish_tile(bars, 0, t, p);
       }
       __syncwarp();
       for (int k = 0; ok && take_tile(bars, k, t, lim, ok); ++k) {
-        if (half == 0 && lane == 0) {
+        if (part == 0 && lane == 0) {
           PagedTile next;
           source.next(next);
           publish_tile(bars, k + 1, next, p);
@@ -577,45 +596,55 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           // rows of V past the end become zeros
           const int live = (it & 1) ? t.len - (t.kt0 + (it >> 1)) * kTileN : kTileN;
           const uint32_t src = raw0 + rs * Cfg::kRawBytes, dst = kv0 + ks * Cfg::kTileBytes;
-#pragma unroll 1
-          for (int in = lane; in < Cfg::kHalf; in += 32) {
-            const int row = half * Cfg::kHalf + in;
+          {
+            const int row = part * (kTileN / kWideners) + lane, in = row & (Cfg::kHalf - 1);
             const uint32_t from = src + in * D;
             const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
             const bool keep = row < live;
-            // all loads of the row first: one latency for them
-            uint32_t w[D / 16][4];
+            // 64 columns at a time, all their loads first: one latency for them
+#pragma unroll 1
+            for (int blk = 0; blk < Cfg::kBlocks; ++blk) {
+              uint32_t w[4][4];
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
-                           : "r"(from + ((c ^ sw) << 4)));
+              for (int c = 0; c < 4; ++c)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                             : "r"(from + (((blk * 4 + c) ^ sw) << 4)) : "memory");
+              if (blk == Cfg::kBlocks - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&bars->raw_empty[rs]));
+              }
+              const uint32_t to = dst + blk * Cfg::kBlockBytes;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint32_t to = dst + (c >> 2) * Cfg::kBlockBytes;
+              for (int c = 0; c < 4; ++c) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a = keep ? w[c][2 * h] : 0u, b = keep ? w[c][2 * h + 1] : 0u;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 to + sw128_offset(row, 2 * (c & 3) + h)),
-                             "r"(e4m3x2_to_f16x2(a)), "r"(e4m3x2_to_f16x2(a >> 16)), "r"(e4m3x2_to_f16x2(b)),
-                             "r"(e4m3x2_to_f16x2(b >> 16)));
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t a = keep ? w[c][2 * h] : 0u, b = keep ? w[c][2 * h + 1] : 0u;
+                  uint32_t y[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b),
+                                   e4m3x2_to_f16x2(b >> 16)};
+                  if (PAGES && !(it & 1)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const float2 f = f16x2_to_f32(y[e]);
+                      y[e] = pack_bf16x2(f.x, f.y);
+                    }
+                  }
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + sw128_offset(row, 2 * c + h)),
+                               "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]));
+                }
               }
             }
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(&bars->kv_full[ks]));
-            mbar_arrive(smem_addr(&bars->raw_empty[rs]));
-          }
+          if (lane == 0) mbar_arrive(smem_addr(&bars->kv_full[ks]));
         }
       }
       if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
     }
     __syncwarp();
   } else {
-    regs_inc<208>();
+    regs_inc<E4M3 ? 184 : 208>();
     // ---------------------------------------------------------- softmax + epilogue
     const int i = (warp - 4) >> 2;      // query tile of this warpgroup
     const int r = tid - 128 * (1 + i);  // row of the tile == TMEM lane
@@ -641,7 +670,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if constexpr (E4M3) c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
       // the same in every lane: softmax_row_max votes within either branch
       const bool pos = c > 0.0f;
-      if constexpr (E4M3) {
+      const float c_pages = fabsf(c);
+      if constexpr (E4M3 && !PAGES) {
         if (tok_r < p.tok_tile && tok < t.n_new)
           c *= p.q_up[(static_cast<size_t>(t.row0) + tok) * p.H_q + t.h * p.group + head_r];
         // A row of tiny queries can bring c to 0, and -inf of a masked score times 0 is NaN:
@@ -670,15 +700,20 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool rescale_warp;
         float factor;
         const float4* of_page = page_scales + ((tile0 + j) % kScaleSlots) * 8;
-        if constexpr (PAGES) softmax_row_pages(s, c, of_page);
-        const float mb = PAGES ? softmax_row_max<true>(s, 1.0f, m_used, l, kv0, 0, see, need_mask, 0,
+        if constexpr (PAGES) {
+          if (!pos) {  // (a scale of 0 or below: the scores take its sign first)
+#pragma unroll
+            for (int e = 0; e < 128; ++e) s[e] = c == 0.0f ? 0.0f : -s[e];
+          }
+        }
+        const float mb = PAGES ? softmax_row_max_pages(s, c_pages, of_page, m_used, l, kv0, see, need_mask,
                                                        rescale_warp, factor)
                          : pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
                                                        rescale_warp, factor)
                                : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
                                                         rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
-        if constexpr (PAGES) softmax_row_exp_pages(s, mb - lift, of_page, pk, sum2);
+        if constexpr (PAGES) softmax_row_exp_pages(s, c_pages, mb - lift, of_page, pk, sum2);
         else if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
         else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
         if (rescale_warp && j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
@@ -1104,7 +1139,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  e = launch_chained<paged_fwd_kernel<D, KIND>>(dim3(p.grid), 384, PagedFwdCfg<D, KIND>::kSmemBytes, stream, tq, tk,
+  e = launch_chained<paged_fwd_kernel<D, KIND>>(dim3(p.grid), fwd_threads(KIND), PagedFwdCfg<D, KIND>::kSmemBytes, stream, tq, tk,
                      tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;

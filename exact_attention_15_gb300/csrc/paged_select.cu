@@ -338,13 +338,8 @@ paged_select_kernel(const SelectParams p) {
   auto entry_at = [&](int k) {
     return lane < 16 ? __ldg(table + begin + min((warp + k * kSelWarps) * 16 + lane, n - 1)) : 0;
   };
-  auto checked = [&](int id) {
-    if (static_cast<unsigned>(id) < static_cast<unsigned>(s.num_pages)) return id;
-    record_error(s.err, kErrPages);
-    return 0;
-  };
   auto copy = [&](int entry) {
-    const int id = checked(entry);
+    const int id = checked_page(s, entry);
     if (lane == 0) mbar_arrive_expect_tx(full, 16 * 4 * D);
     __syncwarp();
     if (lane < 16)

@@ -91,7 +91,7 @@ def test_lists_refusals(lib):
 
 def test_sizes_of_workspaces(lib):
     for T, B in ((5, 5), (1000, 3)):
-        assert lib.attn_paged_fwd_workspace_bytes(T, B, 8, 2, 128, 3) == lib.attn_paged_fwd_workspace_bytes(T, B, 8, 2, 128, 1)
+        assert lib.attn_paged_fwd_workspace_bytes(T, B, 8, 2, 128, 3) == lib.attn_paged_fwd_workspace_bytes(T, B, 8, 2, 128, 0)
     assert lib.attn_paged_fwd_workspace_bytes(5, 5, 8, 2, 128, 2) == 0
 
 
