@@ -233,7 +233,7 @@ struct BoundsParams {
   void* bounds;  // bf16 [num_pages, H_kv, 2, d]: minimum, maximum
   int H_kv;
 };
-cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStream_t stream);
+cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, int n_sm, cudaStream_t stream);
 
 struct SelectParams {
   PagedSeqs s;

@@ -454,7 +454,7 @@ int attn_paged_bounds(const attn_paged_cache* cache, void* bounds, int T, int B,
   p.k_exp = cache->type == kE4m3Pages ? cache->k_exp : nullptr;
   p.bounds = bounds;
   p.H_kv = cache->H_kv;
-  return launch_paged_bounds(p, cache->d, cache->type, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_paged_bounds(p, cache->d, cache->type, dev.n_sm, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }

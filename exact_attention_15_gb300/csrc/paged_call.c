@@ -24,12 +24,21 @@ typedef int (*decode_fn)(const attn_paged_cache*, const void*, void*, float*, in
                          const int*, int, long long, float, void*, size_t, attn_stream_t);
 typedef int (*fwd_fn)(const attn_paged_cache*, const void*, void*, float*, int, int, int, const int*,
                       const int*, const int*, int, long long, int, float, void*, size_t, attn_stream_t);
+typedef int (*lists_fn)(const attn_paged_cache*, const void*, void*, float*, int, int, const int*, const int*, int,
+                        long long, long long, float, void*, size_t, attn_stream_t);
+typedef int (*bounds_fn)(const attn_paged_cache*, void*, int, int, const int*, const int*, const int*, int, long long,
+                         attn_stream_t);
+typedef int (*select_fn)(const attn_paged_cache*, const void*, const void*, int*, int*, int, int, int, const int*,
+                         const int*, const int*, int, long long, int, int, int, attn_stream_t);
 typedef size_t (*bytes_fn)(const attn_paged_cache*, int, int, int, int, int);
 
 static append_fn c_append;
 static decode_fn c_decode;
 static fwd_fn c_fwd;
 static bytes_fn c_bytes;
+static lists_fn c_lists;
+static bounds_fn c_bounds;
+static select_fn c_select;
 /* from torch */
 static PyObject *t_bf16, *t_f32, *t_f64, *t_i32, *t_u8, *f_empty, *f_empty_like, *f_device, *f_stream, *o_contiguous;
 /* names */
@@ -37,8 +46,9 @@ static PyObject *n_dtype, *n_shape, *n_get_device, *n_is_contiguous, *n_stride, 
 static PyObject *kw_dtype_device, *kw_memory_format;
 
 /* What a call knows of a tensor. */
+enum { kDims = 4 };
 typedef struct {
-  long long size[3], stride[3];
+  long long size[kDims], stride[kDims];
   int dims, contiguous;
   void* ptr;
 } view;
@@ -54,7 +64,7 @@ static int integers(PyObject* tuple, long long* out, int most) {
   return (int)n;
 }
 
-/* 1 when t is a tensor of that dtype on device `index` with at most 3 dimensions. */
+/* 1 when t is a tensor of that dtype on device `index` with at most kDims dimensions. */
 static int look(PyObject* t, PyObject* dtype, long index, view* v) {
   PyObject* x = PyObject_GetAttr(t, n_dtype);
   if (!x) return 0;
@@ -66,7 +76,7 @@ static int look(PyObject* t, PyObject* dtype, long index, view* v) {
   Py_DECREF(x);
   if (dev != index) return 0;
   x = PyObject_GetAttr(t, n_shape);
-  v->dims = integers(x, v->size, 3);
+  v->dims = integers(x, v->size, kDims);
   Py_XDECREF(x);
   if (v->dims < 0) return 0;
   x = PyObject_CallMethodNoArgs(t, n_is_contiguous);
@@ -75,7 +85,7 @@ static int look(PyObject* t, PyObject* dtype, long index, view* v) {
   Py_DECREF(x);
   if (!v->contiguous) {
     x = PyObject_CallMethodNoArgs(t, n_stride);
-    const int n = integers(x, v->stride, 3);
+    const int n = integers(x, v->stride, kDims);
     Py_XDECREF(x);
     if (n != v->dims) return 0;
   }
@@ -102,21 +112,27 @@ static int tokens_of(PyObject* t, long index, long long d, view* v, long long* a
 typedef struct {
   const int *lens, *table, *cu;
   int B, cols;
-  long long stride;
+  long long stride, head; /* head: entries between the lists of KV heads, 0 where they share a row */
 } seqs;
 
-static int seqs_of(PyObject* table, PyObject* lens, PyObject* cu, long index, long long tokens, seqs* s) {
+/* lists: the page table may have a row for each of that many KV heads (0: it may not). */
+static int seqs_of(PyObject* table, PyObject* lens, PyObject* cu, long index, long long tokens, int lists, seqs* s) {
   view v;
   if (!look(lens, t_i32, index, &v) || v.dims != 1 || !v.contiguous || v.size[0] >= INT_MAX) return 0;
   s->B = (int)v.size[0];
   s->lens = (const int*)v.ptr;
-  if (!look(table, t_i32, index, &v) || v.dims != 2 || v.size[0] != s->B || v.size[1] > INT_MAX) return 0;
-  s->cols = (int)v.size[1];
-  s->stride = v.size[1];
+  if (!look(table, t_i32, index, &v) || (v.dims != 2 && (v.dims != 3 || !lists)) || v.size[0] != s->B) return 0;
+  const int last = v.dims - 1;
+  if (v.size[last] > INT_MAX || (last == 2 && v.size[1] != lists)) return 0;
+  s->cols = (int)v.size[last];
+  s->stride = last == 2 ? lists * v.size[2] : v.size[1];
+  s->head = last == 2 ? v.size[2] : 0;
   if (!v.contiguous) {
-    if (s->cols > 1 && v.stride[1] != 1) return 0;
+    if (s->cols > 1 && v.stride[last] != 1) return 0;
     if (s->B > 1) s->stride = v.stride[0];
+    if (last == 2 && lists > 1) s->head = v.stride[1];
   }
+  if (last == 2 && s->head < 1) return 0; /* (paged.py says what is wrong) */
   s->table = (const int*)v.ptr;
   s->cu = NULL;
   if (cu == Py_None) return tokens == s->B;
@@ -172,7 +188,7 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   long long ks, vs, qs = 0, os = 0;
   seqs s;
   if (!tokens_of(a[3], index, c->d, &k, &ks) || k.size[1] != c->H_kv || !tokens_of(a[4], index, c->d, &v, &vs) ||
-      v.size[1] != c->H_kv || v.size[0] != k.size[0] || !seqs_of(a[5], a[6], a[7], index, k.size[0], &s))
+      v.size[1] != c->H_kv || v.size[0] != k.size[0] || !seqs_of(a[5], a[6], a[7], index, k.size[0], 0, &s))
     return not_taken();
   const double* freq = NULL;
   int rotary = 0, H_q = 0;
@@ -269,7 +285,7 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   float scale;
   attn_stream_t stream;
   if (!tokens_of(a[3], index, c->d, &q, &apart) || !q.contiguous || q.size[1] < 1 || q.size[1] % c->H_kv ||
-      !seqs_of(a[4], a[5], Py_None, index, q.size[0], &s) || !scale_of(a[6], c->d, &scale) ||
+      !seqs_of(a[4], a[5], Py_None, index, q.size[0], c->H_kv, &s) || !scale_of(a[6], c->d, &scale) ||
       !stream_of(a[1], index, &stream))
     return not_taken();
   const size_t bytes = c_bytes(c, s.B, s.B, (int)q.size[1], 0, s.cols);
@@ -278,8 +294,10 @@ static PyObject* decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!outputs(a[3], s.B, q.size[1], bytes, a[2], &o, &lse, &ws, ptr)) return not_taken();
   int status;
   Py_BEGIN_ALLOW_THREADS
-  status = c_decode(c, q.ptr, ptr[0], (float*)ptr[1], s.B, (int)q.size[1], s.lens, s.table, s.cols, s.stride, scale,
-                    ptr[2], bytes, stream);
+  status = s.head ? c_lists(c, q.ptr, ptr[0], (float*)ptr[1], s.B, (int)q.size[1], s.lens, s.table, s.cols, s.stride,
+                            s.head, scale, ptr[2], bytes, stream)
+                  : c_decode(c, q.ptr, ptr[0], (float*)ptr[1], s.B, (int)q.size[1], s.lens, s.table, s.cols, s.stride,
+                             scale, ptr[2], bytes, stream);
   Py_END_ALLOW_THREADS
   return answer(status, o, lse, ws);
 }
@@ -296,7 +314,7 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   float scale;
   attn_stream_t stream;
   if (!tokens_of(a[3], index, c->d, &q, &apart) || !q.contiguous || q.size[1] < 1 || q.size[1] % c->H_kv ||
-      !seqs_of(a[4], a[5], a[6], index, q.size[0], &s) || !scale_of(a[7], c->d, &scale) ||
+      !seqs_of(a[4], a[5], a[6], index, q.size[0], 0, &s) || !scale_of(a[7], c->d, &scale) ||
       !stream_of(a[1], index, &stream))
     return not_taken();
   const int causal = PyObject_IsTrue(a[8]), T = (int)q.size[0], H_q = (int)q.size[1];
@@ -313,15 +331,98 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return answer(status, o, lse, ws);
 }
 
-/* setup(addresses of the four C functions, torch module) */
+/* A contiguous tensor of bounds for that cache. */
+static int bounds_of(PyObject* t, const attn_paged_cache* c, long index, view* v) {
+  return look(t, t_bf16, index, v) && v->dims == 4 && v->contiguous && v->size[0] == c->num_pages &&
+         v->size[1] == c->H_kv && v->size[2] == 2 && v->size[3] == c->d;
+}
+
+/* bounds(cache struct, index, bounds, page_table, kv_lens, cu_seqlens, tokens) */
+static PyObject* bounds(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) return not_taken();
+  const attn_paged_cache* c = (const attn_paged_cache*)PyLong_AsVoidPtr(a[0]);
+  const long index = PyLong_AsLong(a[1]);
+  if (!c || PyErr_Occurred()) return not_taken();
+  view v, lens;
+  seqs s;
+  attn_stream_t stream;
+  if (!look(a[4], t_i32, index, &lens) || lens.dims != 1) return not_taken();
+  long long T = lens.size[0];
+  if (a[6] != Py_None) {
+    T = PyLong_AsLongLong(a[6]);
+    if (PyErr_Occurred() || T < 0 || T > INT_MAX) return not_taken();
+  } else if (a[5] != Py_None) {
+    return not_taken();
+  }
+  if (!bounds_of(a[2], c, index, &v) || !seqs_of(a[3], a[4], a[5], index, T, 0, &s) || !stream_of(a[1], index, &stream))
+    return not_taken();
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = c_bounds(c, v.ptr, (int)T, s.B, s.cu, s.lens, s.table, s.cols, s.stride, stream);
+  Py_END_ALLOW_THREADS
+  return status ? PyLong_FromLong(status) : Py_NewRef(a[2]);
+}
+
+/* select(cache struct, index, device, q, bounds, page_table, kv_lens, count, cu_seqlens, keep_first, keep_last) */
+static PyObject* select_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (n != 11) return not_taken();
+  const attn_paged_cache* c = (const attn_paged_cache*)PyLong_AsVoidPtr(a[0]);
+  const long index = PyLong_AsLong(a[1]);
+  if (!c || PyErr_Occurred()) return not_taken();
+  view q, v;
+  long long apart;
+  seqs s;
+  attn_stream_t stream;
+  const long long count = PyLong_AsLongLong(a[7]), first = PyLong_AsLongLong(a[9]), last = PyLong_AsLongLong(a[10]);
+  if (PyErr_Occurred() || count < 1 || count > INT_MAX || first < 0 || last < 1 || first > count || last > count - first)
+    return not_taken();
+  if (!tokens_of(a[3], index, c->d, &q, &apart) || !q.contiguous || q.size[1] < 1 || q.size[1] % c->H_kv ||
+      !bounds_of(a[4], c, index, &v) || !seqs_of(a[5], a[6], a[8], index, q.size[0], 0, &s) ||
+      !stream_of(a[1], index, &stream))
+    return not_taken();
+  PyObject* shape = Py_BuildValue("(LiL)", q.size[0], c->H_kv, count);
+  PyObject* rows = Py_BuildValue("(L)", q.size[0]);
+  PyObject* pages = new_tensor(shape, t_i32, a[2]);
+  PyObject* lens = new_tensor(rows, t_i32, a[2]);
+  Py_XDECREF(shape);
+  Py_XDECREF(rows);
+  PyObject* both[2] = {pages, lens};
+  void* ptr[2] = {NULL, NULL};
+  int ok = pages && lens;
+  for (int i = 0; ok && i < 2; ++i) {
+    PyObject* x = PyObject_CallMethodNoArgs(both[i], n_data_ptr);
+    ptr[i] = x ? PyLong_AsVoidPtr(x) : NULL;
+    ok = x != NULL;
+    Py_XDECREF(x);
+  }
+  if (!ok || PyErr_Occurred()) {
+    Py_XDECREF(pages);
+    Py_XDECREF(lens);
+    return not_taken();
+  }
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = c_select(c, q.ptr, v.ptr, (int*)ptr[0], (int*)ptr[1], (int)q.size[0], s.B, (int)q.size[1], s.cu, s.lens, s.table,
+                    s.cols, s.stride, (int)count, (int)first, (int)last, stream);
+  Py_END_ALLOW_THREADS
+  PyObject* r = status ? PyLong_FromLong(status) : PyTuple_Pack(2, pages, lens);
+  Py_DECREF(pages);
+  Py_DECREF(lens);
+  return r;
+}
+
+/* setup(addresses of the seven C functions, torch module) */
 static PyObject* setup(PyObject* self, PyObject* args) {
-  unsigned long long f[4];
+  unsigned long long f[7];
   PyObject* torch;
-  if (!PyArg_ParseTuple(args, "KKKKO", &f[0], &f[1], &f[2], &f[3], &torch)) return NULL;
+  if (!PyArg_ParseTuple(args, "KKKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &torch)) return NULL;
   c_append = (append_fn)(size_t)f[0];
   c_decode = (decode_fn)(size_t)f[1];
   c_fwd = (fwd_fn)(size_t)f[2];
   c_bytes = (bytes_fn)(size_t)f[3];
+  c_lists = (lists_fn)(size_t)f[4];
+  c_bounds = (bounds_fn)(size_t)f[5];
+  c_select = (select_fn)(size_t)f[6];
   PyObject* low = PyObject_GetAttrString(torch, "_C");
   PyObject* cuda = PyObject_GetAttrString(torch, "cuda");
   if (!low || !cuda) return NULL;
@@ -343,6 +444,8 @@ static PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, NULL},
     {"forward", (PyCFunction)(void (*)(void))forward, METH_FASTCALL, NULL},
+    {"bounds", (PyCFunction)(void (*)(void))bounds, METH_FASTCALL, NULL},
+    {"select", (PyCFunction)(void (*)(void))select_pages, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -14,10 +14,12 @@ namespace attn {
 namespace {
 
 // ---------------------------------------------------------------- bounds
-// A CTA for each touched page and KV head, four rows or more at a time: thread (row, 16-byte
+// A warp, or four, for each touched page and KV head, two rows or more at a time: lane (row, 16-byte
 // column) keeps the minimum and maximum of its column's elements, packed as the cache's values
 // are (bf16, or e4m3 widened to fp16, both exact), NaN before anything else. Every byte of
-// the pages is read once; they bound it.
+// the pages is read once; they bound it where there are many pages, and a row's latency where
+// there are few, for which four warps share a page (64 pages of 8 heads: XX, with one YY; 40,000
+// tokens' in pages of 32: XX, with four YY).
 constexpr int kBoundsThreads = 128;
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b, bool f16) {
@@ -33,83 +35,118 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, bool f16) {
   return r;
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int WARPS>
 __global__ void __launch_bounds__(kBoundsThreads)
 paged_bounds_kernel(const BoundsParams p) {
   constexpr bool F16 = KIND != kBf16;
-  constexpr int kRowChunks = D * (F16 ? 1 : 2) / 16;   // 16-byte pieces of a row
-  constexpr int kRows = kBoundsThreads / kRowChunks;   // rows at a time
-  constexpr int kWords = F16 ? 8 : 4;                  // packed pairs of a piece
-  constexpr int kWarpLanes = kRowChunks < 32 ? 32 / kRowChunks : 1;  // lanes of a warp with the same column
-  __shared__ uint32_t part[kBoundsThreads / 32][2][kRowChunks][kWords];
+  constexpr int kCols = D * (F16 ? 1 : 2) / 16;  // 16-byte pieces of a row
+  constexpr int kWarpRows = 32 / kCols;          // rows of a warp at a time
+  constexpr int kWords = F16 ? 8 : 4;            // packed pairs of a piece
+  __shared__ uint32_t part[WARPS > 1 ? WARPS : 1][2][kWords][kCols];
   const PagedSeqs& s = p.s;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   grid_wait();
   grid_release();
   if (blockIdx.x == 0) check_paged_seqs(s, threadIdx.x, kBoundsThreads);
-  const int h = static_cast<int>(blockIdx.x % p.H_kv);
+  constexpr int kUnits = kBoundsThreads / 32 / WARPS;  // of a CTA
+  const long long unit = static_cast<long long>(blockIdx.x) * kUnits + (kUnits > 1 ? warp : 0);
+  const long long number = unit / p.H_kv;
+  const int h = static_cast<int>(unit - number * p.H_kv);
   TouchedPage x;
-  if (!touched_page(s, blockIdx.x / p.H_kv, x)) return;
-  const int id = __ldg(s.page_table + static_cast<size_t>(x.b) * s.table_stride + x.at);
+  if (number >= touched_numbers(s.T, s.B, s.page_shift, s.cu_seqlens != nullptr) || !touched_page(s, number, x)) return;
+  const int id = page_entry(s, x.b, x.at);
   if (static_cast<unsigned>(id) >= static_cast<unsigned>(s.num_pages)) {
-    if (threadIdx.x == 0) record_error(s.err, kErrPages);
+    if (lane == 0) record_error(s.err, kErrPages);
     return;
   }
   const int rows = min(1 << s.page_shift, x.len - (x.at << s.page_shift));
-  const int col = threadIdx.x % kRowChunks, row0 = threadIdx.x / kRowChunks;
+  const int col = lane % kCols;
   const uint4* keys = reinterpret_cast<const uint4*>(
       static_cast<const uint8_t*>(p.k) +
-      (static_cast<long long>(id) * p.k_page + (static_cast<long long>(h) << s.page_shift) * D) * (F16 ? 1 : 2));
+      (static_cast<long long>(id) * p.k_page + (static_cast<long long>(h) << s.page_shift) * D) * (F16 ? 1 : 2)) + col;
   constexpr uint32_t kPlusInf = F16 ? 0x7c007c00u : 0x7f807f80u, kMinusInf = kPlusInf | 0x80008000u;
   uint32_t lo[kWords], hi[kWords];
 #pragma unroll
   for (int i = 0; i < kWords; ++i) { lo[i] = kPlusInf; hi[i] = kMinusInf; }
-#pragma unroll 8
-  for (int r = row0; r < rows; r += kRows) {
-    const uint4 v = keys[r * kRowChunks + col];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  constexpr int kStep = kWarpRows * WARPS, kAtOnce = WARPS > 1 ? 4 : 8;  // (all loads before the first is used)
+  for (int first = (WARPS > 1 ? warp : 0) * kWarpRows; first < rows; first += kAtOnce * kStep) {
+    uint4 v[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const uint32_t y = F16 ? e4m3x2_to_f16x2(w[(i / 2) & 3] >> (16 * (i & 1))) : w[i & 3];
-      lo[i] = min2(lo[i], y, F16);
-      hi[i] = max2(hi[i], y, F16);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int r = min(first + k * kStep + lane / kCols, rows - 1);  // (behind the last row that again)
+      if (first + k * kStep < rows)
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "l"(keys + r * kCols));
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (first + k * kStep >= rows) break;
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t y = F16 ? e4m3x2_to_f16x2(w[(i / 2) & 3] >> (16 * (i & 1))) : w[i & 3];
+        lo[i] = min2(lo[i], y, F16);
+        hi[i] = max2(hi[i], y, F16);
+      }
     }
   }
-  // lanes with the same column lie kRowChunks apart
+  // lanes with the same column lie kCols apart
 #pragma unroll
   for (int i = 0; i < kWords; ++i)
 #pragma unroll
-    for (int o = kRowChunks; o < kRowChunks * kWarpLanes; o <<= 1) {
+    for (int o = kCols; o < 32; o <<= 1) {
       lo[i] = min2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o), F16);
       hi[i] = max2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o), F16);
     }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (lane < kRowChunks) {
+  if constexpr (WARPS > 1) {
+    if (lane < kCols) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      part[warp][0][col][i] = lo[i];
-      part[warp][1][col][i] = hi[i];
+      for (int i = 0; i < kWords; ++i) {
+        part[warp][0][i][col] = lo[i];
+        part[warp][1][i][col] = hi[i];
+      }
     }
-  }
-  __syncthreads();
-  // thread: a pair of columns of the minimum or of the maximum
-  if (threadIdx.x >= D) return;
-  const int side = threadIdx.x / (D / 2), at = threadIdx.x % (D / 2);
-  uint32_t y = part[0][side][at / kWords][at % kWords];
+    __syncthreads();
+    if (warp > 0) return;
 #pragma unroll
-  for (int w = 1; w < kBoundsThreads / 32; ++w) {
-    const uint32_t z = part[w][side][at / kWords][at % kWords];
-    y = side ? max2(y, z, F16) : min2(y, z, F16);
+    for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        lo[i] = min2(lo[i], part[w][0][i][col], F16);
+        hi[i] = max2(hi[i], part[w][1][i][col], F16);
+      }
   }
-  int to = side;
+  if (lane >= kCols) return;
+  bool turned = false;
   if constexpr (F16) {
     float scale = 1.0f;
     if constexpr (KIND == kE4m3Pages) scale = power_of_two(page_exponent(p.k_exp, id, p.H_kv, h));
     else if (p.k_scale) scale = __ldg(p.k_scale + h);
-    const float2 f = f16x2_to_f32(y);
-    y = pack_bf16x2(f.x * scale, f.y * scale);
-    if (scale < 0.0f) to = 1 - side;  // turns the order round
+    turned = scale < 0.0f;  // turns the order round
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const float2 a = f16x2_to_f32(lo[i]), b = f16x2_to_f32(hi[i]);
+      lo[i] = pack_bf16x2(a.x * scale, a.y * scale);
+      hi[i] = pack_bf16x2(b.x * scale, b.y * scale);
+    }
   }
-  reinterpret_cast<uint32_t*>(p.bounds)[((static_cast<size_t>(id) * p.H_kv + h) * 2 + to) * (D / 2) + at] = y;
+  uint4* out = reinterpret_cast<uint4*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * (D / 4);
+#pragma unroll
+  for (int i = 0; i < kWords; i += 4) {
+    out[(turned ? D / 8 : 0) + col * (kWords / 4) + i / 4] = make_uint4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+    out[(turned ? 0 : D / 8) + col * (kWords / 4) + i / 4] = make_uint4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+  }
+}
+
+template <int D, int KIND>
+cudaError_t launch_bounds(const BoundsParams& p, int n_sm, cudaStream_t stream) {
+  const long long units = touched_numbers(p.s.T, p.s.B, p.s.page_shift, p.s.cu_seqlens != nullptr) * p.H_kv;
+  if (units > 0x7fffffffll) return cudaErrorInvalidValue;
+  // four warps while those of all pages find places at once
+  if (units <= 16ll * n_sm)
+    return launch_chained<paged_bounds_kernel<D, KIND, 4>>(dim3(static_cast<unsigned>(units)), kBoundsThreads, 0, stream, p);
+  return launch_chained<paged_bounds_kernel<D, KIND, 1>>(dim3(static_cast<unsigned>((units + 3) / 4)), kBoundsThreads, 0,
+                                                         stream, p);
 }
 
 // ---------------------------------------------------------------- selection
@@ -688,15 +725,11 @@ cudaError_t plan_select(SelectParams p, int n_sm, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStream_t stream) {
-  const long long blocks = touched_numbers(p.s.T, p.s.B, p.s.page_shift, p.s.cu_seqlens != nullptr) * p.H_kv;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
+cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, int n_sm, cudaStream_t stream) {
   const int slot = prof_begin(kKPagedBounds, stream);
   auto of_kind = [&](auto k) {
     constexpr int K = decltype(k)::value;
-    return d == 128 ? launch_chained<paged_bounds_kernel<128, K>>(grid, kBoundsThreads, 0, stream, p)
-                    : launch_chained<paged_bounds_kernel<64, K>>(grid, kBoundsThreads, 0, stream, p);
+    return d == 128 ? launch_bounds<128, K>(p, n_sm, stream) : launch_bounds<64, K>(p, n_sm, stream);
   };
   const cudaError_t e = kind == kBf16   ? of_kind(std::integral_constant<int, kBf16>{})
                         : kind == kE4m3 ? of_kind(std::integral_constant<int, kE4m3>{})

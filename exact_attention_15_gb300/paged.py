@@ -44,7 +44,7 @@ class _PythonCalls:
     def append(*args):
         return NotImplemented
 
-    decode = forward = append
+    decode = forward = bounds = select = append
 
 
 def _load_calls():
@@ -61,7 +61,8 @@ def _load_calls():
         spec.loader.exec_module(module)
         lib = load()
         module.setup(*(ctypes.cast(getattr(lib, name), _P).value for name in (
-            "attn_paged_append", "attn_paged_decode", "attn_paged_fwd", "attn_paged_call_workspace_bytes")), torch)
+            "attn_paged_append", "attn_paged_decode", "attn_paged_fwd", "attn_paged_call_workspace_bytes",
+            "attn_paged_decode_lists", "attn_paged_bounds", "attn_paged_select")), torch)
         _calls = module
     return _calls
 
@@ -340,6 +341,11 @@ def paged_bounds(cache, bounds, page_table, kv_lens, cu_seqlens=None, tokens=Non
     use. Writes those of the pages that the new tokens lie in (kv_lens and cu_seqlens as in the
     append; with cu_seqlens `tokens` is their number, that of the append's rows). Returns
     bounds."""
+    r = cache._calls.bounds(cache._ref, cache._index, bounds, page_table, kv_lens, cu_seqlens, tokens)
+    if r is not NotImplemented:
+        if type(r) is int:
+            _check(r, "attn_paged_bounds")
+        return r
     _check_tensor("bounds", bounds, (cache.num_pages, cache.H_kv, 2, cache.d), _bf16, cache.device)
     if tokens is None:
         if cu_seqlens is not None:
@@ -362,6 +368,13 @@ def paged_select(cache, q, bounds, page_table, kv_lens, count, cu_seqlens=None, 
     paged_bounds; kv_lens and cu_seqlens as in paged_append (None: one token per sequence).
     Returns (pages [T, H_kv, count] int32, -1 behind the last one, lens [T] int32), a page table
     and lengths for paged_decode."""
+    if pages is None and lens is None:
+        r = cache._calls.select(cache._ref, cache._index, cache.device, q, bounds, page_table, kv_lens, count, cu_seqlens,
+                                keep_first, keep_last)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r, "attn_paged_select")
+            return r
     _check_tensor("bounds", bounds, (cache.num_pages, cache.H_kv, 2, cache.d), _bf16, cache.device)
     T, H_q, _ = _tokens("q", q, cache)
     if H_q < 1 or H_q % cache.H_kv:
