@@ -218,10 +218,14 @@ struct AppendParams {
   uint8_t* k_exp; uint8_t* v_exp;  // a scale for each page: [num_pages, H_kv]
   int H_q, H_kv, d, rotary_dim, interleaved, e4m3;
 };
-// (over a cache with a scale for each page: when the exponents are there)
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
-// Over a cache with a scale for each page.
-cudaError_t launch_paged_append_pages(const AppendParams& p, cudaStream_t stream);
+// Over a cache with a scale for each page; where many tokens are appended by rows, with maps of k
+// and v in boxes of kAppendRows tokens and append_box_heads heads.
+constexpr int kAppendRows = 16;
+bool append_by_rows(const PagedSeqs& s);
+int append_box_heads(int H_kv, int d);
+cudaError_t launch_paged_append_pages(const AppendParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                      long long wait_limit, cudaStream_t stream);
 
 // ---- choosing pages by bounds of their keys
 struct BoundsParams {
@@ -233,7 +237,7 @@ struct BoundsParams {
   void* bounds;  // bf16 [num_pages, H_kv, 2, d]: minimum, maximum
   int H_kv;
 };
-cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, int n_sm, cudaStream_t stream);
+cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStream_t stream);
 
 struct SelectParams {
   PagedSeqs s;

@@ -94,17 +94,17 @@ int encode_pages_map(const HostDevice& dev, CUtensorMap* m, const attn_paged_cac
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// 3-D map over q, [T, H_q, d] bf16 (or fp16): boxes of 64 columns, the heads of a group
-// and `tokens` tokens, 128-byte swizzle.
-int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int d, int H_q, int T,
-                    int group, int tokens, bool f16) {
-  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(T)};
-  cuuint64_t strides[2] = {row, row * H_q};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
+// 3-D map over q, k or v, [T, H, d] bf16 (or fp16), tokens `stride` elements apart: boxes of `width`
+// columns, `heads` heads and `tokens` tokens, with a 128-byte swizzle or none.
+int encode_rows_map(const HostDevice& dev, CUtensorMap* m, const void* base, int d, int H, int T, long long stride,
+                    int width, int heads, int tokens, bool f16, bool swizzle) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
   cuuint32_t step[3] = {1, 1, 1};
   const CUresult r = dev.encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                                const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -271,7 +271,8 @@ int launch_fwd(const HostDevice& dev, const attn_paged_cache* c, const PagedSeqs
   CUtensorMap tq, tk, tv;
   int st;
   const void* queries = e4m3 ? ws + plan.q16_off : q;
-  if ((st = encode_rows_map(dev, &tq, queries, c->d, H_q, seqs.T, group, plan.tok_tile, e4m3)) != ATTN_OK ||
+  if ((st = encode_rows_map(dev, &tq, queries, c->d, H_q, seqs.T, static_cast<long long>(H_q) * c->d, 64, group,
+                            plan.tok_tile, e4m3, true)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tk, c, c->k, c->k_page_stride, rows)) != ATTN_OK ||
       (st = encode_pages_map(dev, &tv, c, c->v, c->v_page_stride, rows)) != ATTN_OK)
     return st;
@@ -386,7 +387,21 @@ int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* 
   p.rotary_dim = rotary_dim;
   p.interleaved = interleaved ? 1 : 0;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->type == kE4m3Pages ? launch_paged_append_pages(p, cs) : launch_paged_append(p, cs);
+  cudaError_t e;
+  if (cache->type == kE4m3Pages) {
+    CUtensorMap tk, tv;
+    if (append_by_rows(p.s)) {
+      // tensor maps hold strides below 2^40 bytes
+      if (k_stride >= (1ll << 39) || v_stride >= (1ll << 39)) return ATTN_ERR_BAD_SHAPE;
+      const int heads = append_box_heads(p.H_kv, d);
+      if ((st = encode_rows_map(dev, &tk, k, d, p.H_kv, T, k_stride, d, heads, kAppendRows, false, false)) != ATTN_OK ||
+          (st = encode_rows_map(dev, &tv, v, d, p.H_kv, T, v_stride, d, heads, kAppendRows, false, false)) != ATTN_OK)
+        return st;
+    }
+    e = launch_paged_append_pages(p, tk, tv, dev.wait_limit, cs);
+  } else {
+    e = launch_paged_append(p, cs);
+  }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -454,7 +469,7 @@ int attn_paged_bounds(const attn_paged_cache* cache, void* bounds, int T, int B,
   p.k_exp = cache->type == kE4m3Pages ? cache->k_exp : nullptr;
   p.bounds = bounds;
   p.H_kv = cache->H_kv;
-  return launch_paged_bounds(p, cache->d, cache->type, dev.n_sm, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_paged_bounds(p, cache->d, cache->type, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK
              : ATTN_ERR_CUDA;
 }

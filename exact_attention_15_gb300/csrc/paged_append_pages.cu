@@ -13,11 +13,17 @@
 // holds the new rows in registers, finds their largest magnitude, looks up what the page has, and turns,
 // scales and stores; the last CTAs of the grid turn the queries, a token on 8 to 128 threads.
 //
-// More: the exponents first (paged_append_exps_kernel), which reads the new keys and values once more
-// than there is need, then the tokens as over the other caches (paged_append.cu). 40,000 tokens of 16
-// prompts (32 query and 8 KV heads of 128): 31 us and 153, where a plain copy of all bytes takes 133; with
-// the rows of a page in shared memory between both, which reads them once, 189 to 216 (the angles are
-// then computed for every few heads, and what waits for a page's largest value keeps few CTAs busy).
+// More (paged_append_rows_kernel): a cluster for each page and 8 KV heads of 128 (16 of 64), a CTA for
+// 16 rows of the page. They come to shared memory in two copies while the CTA turns its tokens'
+// queries; then each tells the others its rows' largest magnitudes, and encodes them. Every byte is
+// moved once; 40,000 tokens of 16 prompts (32 query and 8 KV heads of 128) take 171 us, where a copy of
+// all bytes takes 133. What is left are the steps of a CTA one after the other, of which three find
+// place on an SM (31 us: 15 the queries, 4 to 7 until the page is known and the copies are
+// issued, 8 the rest). Measured beside it: exponents in a kernel of their own, which reads K and V
+// twice, 185 (33 of them, 40 with eight loads of a thread at once, which leaves fewer CTAs on an SM);
+// a copy for each row instead of a tensor map's box, and the magnitudes read from the other
+// CTAs, 178; pages in registers, a warp or 128 threads for a KV head's, 218, as the angles are then
+// computed for every head.
 #include <type_traits>
 
 #include "append.cuh"
@@ -257,76 +263,202 @@ paged_append_few_kernel(const AppendParams p, int kv_blocks, int q_shift) {
   for (int i = tid + KP * 32; i < parts; i += 32) put(load(i), i);
 }
 
-// The exponents alone, for calls of many tokens: a CTA for each page, 2^heads_shift KV heads and K or
-// V reads the new rows, a 16-byte column a thread, and encodes the page's other rows again.
-constexpr int kExpThreads = 256, kExpHeads = 32;
-__global__ void __launch_bounds__(kExpThreads)
-paged_append_exps_kernel(const AppendParams p, int heads_shift) {
-  __shared__ uint32_t most_of[kExpHeads];
+// Many tokens: a cluster for each page and up to 64 KB / 16 rows of KV heads, a CTA for 16 rows. The
+// rows of K and V are copied to shared memory while the CTA turns its tokens' queries; then the
+// CTAs find the page's largest magnitudes together and each encodes its rows.
+constexpr int kRows = kAppendRows, kRowBytes = 64 * 1024;
+struct RowsShared {
+  uint32_t most[64];  // of the page's new rows: the KV heads' keys, then their values
+  int before[64], e[64];
+  uint64_t full;
+  int4 found;  // position of the page's first new token, new tokens, sequence, place in its table row
+  int row;     // of the first
+};
+
+template <int kRowThreads>
+__global__ void __launch_bounds__(kRowThreads, 768 / kRowThreads)
+paged_append_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const AppendParams p, int cluster_shift, int heads, int groups, int q_shift, long long wait_limit) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ RowsShared sh;
   const PagedSeqs& s = p.s;
-  const int tid = threadIdx.x, heads = 1 << heads_shift, groups = (p.H_kv + heads - 1) >> heads_shift;
-  const int col_shift = p.d == 128 ? 4 : 3;  // log2(16-byte columns of a head)
-  if (tid < kExpHeads) most_of[tid] = 0;
+  const int tid = threadIdx.x, cluster = 1 << cluster_shift, rank = blockIdx.x & (cluster - 1);
+  const int block = blockIdx.x >> cluster_shift, number = block / groups, group = block - number * groups;
+  const int h0 = group * heads, n_heads = min(heads, p.H_kv - h0);
+  const int head_shift = p.d == 128 ? 3 : 2;  // log2(16-element parts of a head)
+  const uint32_t bar = smem_addr(&sh.full);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (tid < 64) sh.most[tid] = 0;
+  __syncthreads();
+  if (cluster > 1) cluster_arrive();  // (ready for the others' magnitudes)
   grid_wait();
   grid_release();
-  if (blockIdx.x == 0) check_paged_seqs(s, tid, kExpThreads);
-  // K and V, then the groups of heads innermost: neighbours read neighbouring columns
-  const int number = blockIdx.x / (2 * groups), which = blockIdx.x - number * 2 * groups;
-  const bool is_v = which >= groups;
-  const int h0 = (is_v ? which - groups : which) << heads_shift, n_heads = min(heads, p.H_kv - h0);
-  TouchedPage x;
-  if (!touched_page(s, number, x)) return;
-  const int page = __ldg(s.page_table + static_cast<size_t>(x.b) * s.table_stride + x.at);
-  const int cols = heads << col_shift, col = tid & (cols - 1), step = kExpThreads / cols;
-  const int col_head = col >> col_shift, rows = x.hi - x.lo, row0 = tid / cols;
-  const long long stride = is_v ? p.v_stride : p.k_stride;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) + x.row * stride + h0 * p.d + col * 8;
-  uint32_t most = 0;
-  auto look = [&](auto finite) {
-    most = 0;
-    if (col_head < n_heads) {
-      constexpr int kAtOnce = 8;  // (all loads before the first is used)
-      for (int r0 = row0; r0 < rows; r0 += kAtOnce * step) {
-        uint4 w[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          w[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (r0 + k * step < rows)
-            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w) : "l"(src + (r0 + k * step) * stride));
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) most = larger<decltype(finite)::value>(most, w[k]);
+  if (blockIdx.x == 0) check_paged_seqs(s, tid, kRowThreads);
+  // ---- the page, and copies of this CTA's rows of `heads` heads, K and then V (what lies behind
+  // the page's rows or the heads comes along and is not used)
+  const uint32_t row_bytes = static_cast<uint32_t>(heads) * p.d * 2, v_off = kRows * row_bytes;
+  if (tid < 32) {
+    TouchedPage x;
+    const bool some = touched_page(s, number, x);
+    const int n = some ? max(0, min(kRows, x.hi - x.lo - rank * kRows)) : 0;
+    if (tid == 0) {
+      sh.found = make_int4(x.lo, some ? x.hi - x.lo : 0, x.b, x.at);
+      sh.row = x.row;
+      if (n > 0) {
+        mbar_arrive_expect_tx(bar, 2 * v_off);
+        tma_load_3d(smem_addr(smem), &tm_k, bar, 0, h0, x.row + rank * kRows);
+        tma_load_3d(smem_addr(smem) + v_off, &tm_v, bar, 0, h0, x.row + rank * kRows);
       }
     }
-  };
-  look(std::false_type{});
-  if (__vcmpgeu2(most, kInfinities)) look(std::true_type{});
-  for (int o = 1; o < 1 << col_shift; o <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
-  __syncthreads();
-  if ((col & ((1 << col_shift) - 1)) == 0 && col_head < n_heads)
-    atomicMax(&most_of[col_head], max(most & 0xffffu, most >> 16) << 16);
-  __syncthreads();
-  // (a bad index is recorded where the tokens are written)
-  if (static_cast<unsigned>(page) >= static_cast<unsigned>(s.num_pages)) return;
-  const bool turned = !is_v && p.rotary_dim > 0;
-  const int kept = x.lo & ((1 << s.page_shift) - 1);
-  uint8_t* exps = is_v ? p.v_exp : p.k_exp;
-  int before = -kMaxExp;
-  if (kept) {
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
-                   static_cast<long long>(page) * (is_v ? p.v_page : p.k_page) +
-                   (static_cast<long long>(h0) << s.page_shift) * p.d;
-    for (int h = 0; h < n_heads; ++h) {
-      const int was = plain_exponent(exps, page, p.H_kv, h0 + h), is = max(was, exponent_for(counted(most_of[h], turned)));
-      if (is > was) encode_kept(dst + (h * p.d << s.page_shift), kept, p.d, is - was, tid, kExpThreads);
-    }
-    if (tid < n_heads) before = plain_exponent(exps, page, p.H_kv, h0 + tid);
-    __syncthreads();  // (everyone has read the exponents)
   }
-  if (tid < n_heads) {
-    const int e = max(before, exponent_for(counted(most_of[tid], turned)));
-    if (!kept || e != before) exps[static_cast<size_t>(page) * p.H_kv + h0 + tid] = static_cast<uint8_t>(e + 127);
+  __syncthreads();
+  if (sh.found.y == 0) {  // no page of that number: the whole cluster leaves
+    if (cluster > 1) cluster_wait();
+    return;
+  }
+  const int lo = sh.found.x + rank * kRows, n = max(0, min(kRows, sh.found.y - rank * kRows));
+  const int kept = sh.found.x & ((1 << s.page_shift) - 1);  // rows that the page holds already
+  const int page = page_entry(s, sh.found.z, sh.found.w);
+  const bool page_ok = static_cast<unsigned>(page) < static_cast<unsigned>(s.num_pages);
+  if (!page_ok && tid == 0) record_error(s.err, kErrPages);
+  if (tid < 2 * n_heads)
+    sh.before[tid] = kept && page_ok ? plain_exponent(tid < n_heads ? p.k_exp : p.v_exp, page, p.H_kv,
+                                                      h0 + (tid < n_heads ? tid : tid - n_heads))
+                                     : -kMaxExp;
+  // ---- angles
+  const int pairs = p.rotary_dim >> 1, j_count = p.rotary_dim >> 4;
+  float2* angles = reinterpret_cast<float2*>(smem + 2 * v_off);  // [row][e][part]
+  if (pairs) {  // (a thread has one frequency and every so many rows)
+    const int step = kRowThreads / pairs, r0 = tid / pairs, place = tid - r0 * pairs, e = place / j_count;
+    if (r0 < step) {
+      const unsigned long long f = turn_fraction(__ldg(p.inv_freq + 8 * (place - e * j_count) + e));
+      for (int r = r0; r < n; r += step) angles[r * pairs + place] = turn_at(f, lo + r);
+    }
+  }
+  __syncthreads();
+  // ---- queries: 2^q_shift threads a token, this group's share of the heads
+  if (p.H_q > 0) {
+    const int W = 1 << q_shift, i0 = tid & (W - 1), j = i0 & ((1 << head_shift) - 1);
+    const bool turn = 16 * j < p.rotary_dim, split = turn && !p.interleaved;
+    const int e0 = split ? 8 * j : 16 * j, e1 = split ? 8 * j + (p.rotary_dim >> 1) : 16 * j + 8;
+    const int share = (p.H_q + groups - 1) / groups, h_end = min(p.H_q, (group + 1) * share);
+    const long long t0 = sh.row + rank * kRows;
+    // four tokens' parts are loaded before the first is stored (q_out may be q)
+    constexpr int kAhead = 4;
+    const int step = kRowThreads >> q_shift;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + t0 * p.q_stride;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t0 * p.q_out_stride;
+    for (int h = group * share + (i0 >> head_shift); h < h_end; h += W >> head_shift)
+      for (int r0 = tid >> q_shift; r0 < n; r0 += kAhead * step) {
+        Part w[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const __nv_bfloat16* at = src + min(r0 + k * step, n - 1) * p.q_stride + h * p.d;
+          w[k] = Part{*reinterpret_cast<const uint4*>(at + e0), *reinterpret_cast<const uint4*>(at + e1)};
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = r0 + k * step;
+          if (r >= n) break;
+          float x0[8], x1[8];
+          widen8(w[k].a, x0);
+          widen8(w[k].b, x1);
+          if (turn) {
+            float2 of[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) of[e] = angles[r * pairs + e * j_count + j];
+            if (split) turn_halves(x0, x1, of);
+            else turn_neighbours(x0, x1, of);
+          }
+          __nv_bfloat16* to = dst + r * p.q_out_stride + h * p.d;
+          store8(to + e0, x0);
+          store8(to + e1, x1);
+        }
+      }
+  }
+  // ---- the largest magnitudes: a thread has a 16-byte column of the rows
+  bool ok = n == 0 || mbar_wait(bar, 0, wait_limit);
+  if (!ok) {
+    // the copies may still be on their way: once more, then the rows are not written
+    record_error(s.err, kErrTimeout);
+    mbar_wait(bar, 0, wait_limit);
+  }
+  ok = !__syncthreads_or(!ok);
+  if (cluster > 1) cluster_wait();
+  const int cols = n_heads << (head_shift + 2);  // of K and of V
+  for (int col0 = 0; col0 < cols; col0 += kRowThreads) {
+    const int col = col0 + tid, in_half = col >= cols >> 1 ? col - (cols >> 1) : col;
+    const uint8_t* at = smem + (col >= cols >> 1 ? v_off : 0) + in_half * 16;
+    uint32_t most = 0;
+    auto look = [&](auto finite) {
+      most = 0;
+      if (col < cols) {
+#pragma unroll 4
+        for (int r = 0; r < n; ++r)
+          most = larger<decltype(finite)::value>(most, *reinterpret_cast<const uint4*>(at + r * row_bytes));
+      }
+    };
+    look(std::false_type{});
+    if (__vcmpgeu2(most, kInfinities)) look(std::true_type{});
+    // (a head's columns are 8 or 16 lanes of a warp)
+    for (int o = 1; o < 2 << head_shift; o <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // each of its lanes tells one CTA of the cluster, so that nobody has to ask
+    const int to = col & ((2 << head_shift) - 1);
+    if (col < cols && n > 0)
+      for (int r = to; r < cluster; r += 2 << head_shift)
+        max_cluster_u32(cluster_map(smem_addr(&sh.most[col >> (head_shift + 1)]), r), max(most & 0xffffu, most >> 16) << 16);
+  }
+  if (cluster > 1) cluster_sync_all(); else __syncthreads();
+  // ---- exponents
+  if (tid < 2 * n_heads) {
+    const bool is_v = tid >= n_heads;
+    sh.e[tid] = max(sh.before[tid], exponent_for(counted(sh.most[tid], !is_v && p.rotary_dim > 0)));
+    if (rank == 0 && page_ok && (!kept || sh.e[tid] != sh.before[tid]))
+      (is_v ? p.v_exp : p.k_exp)[static_cast<size_t>(page) * p.H_kv + h0 + (is_v ? tid - n_heads : tid)] =
+          static_cast<uint8_t>(sh.e[tid] + 127);
+  }
+  __syncthreads();
+  if (page_ok && ok) {
+    const long long k_at = static_cast<long long>(page) * p.k_page + (static_cast<long long>(h0) << s.page_shift) * p.d;
+    const long long v_at = static_cast<long long>(page) * p.v_page + (static_cast<long long>(h0) << s.page_shift) * p.d;
+    const int head_bytes = p.d << s.page_shift;
+    if (kept && rank == 0) {
+      for (int i = 0; i < 2 * n_heads; ++i)
+        if (sh.e[i] > sh.before[i])
+          encode_kept(i < n_heads ? static_cast<uint8_t*>(p.k_cache) + k_at + i * head_bytes
+                                  : static_cast<uint8_t*>(p.v_cache) + v_at + (i - n_heads) * head_bytes,
+                      kept, p.d, sh.e[i] - sh.before[i], tid, kRowThreads);
+    }
+    // ---- the new rows: a thread has a part of 16 elements of every so many
+    const int parts = 2 * n_heads << head_shift, at_once = kRowThreads / parts;  // (128 parts at most)
+    const int r0 = tid / parts, part = tid - r0 * parts, head = part >> head_shift, j = part & ((1 << head_shift) - 1);
+    const bool is_v = head >= n_heads;
+    const bool turn = !is_v && 16 * j < p.rotary_dim, split = turn && !p.interleaved;
+    const int e0 = split ? 8 * j : 16 * j, e1 = split ? 8 * j + (p.rotary_dim >> 1) : 16 * j + 8;
+    const uint8_t* from = smem + (is_v ? v_off + (head - n_heads) * p.d * 2 : head * p.d * 2);
+    uint8_t* to = (is_v ? static_cast<uint8_t*>(p.v_cache) + v_at + (head - n_heads) * head_bytes
+                        : static_cast<uint8_t*>(p.k_cache) + k_at + head * head_bytes) +
+                  (kept + rank * kRows) * p.d;
+    const float scale = r0 < at_once ? power_of_two(-sh.e[head]) : 0.0f;
+#pragma unroll 2
+    for (int r = r0; r0 < at_once && r < n; r += at_once) {
+      float x0[8], x1[8];
+      widen8(*reinterpret_cast<const uint4*>(from + r * row_bytes + e0 * 2), x0);
+      widen8(*reinterpret_cast<const uint4*>(from + r * row_bytes + e1 * 2), x1);
+      if (turn) {
+        float2 of[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) of[e] = angles[r * pairs + e * j_count + j];
+        if (split) turn_halves(x0, x1, of);
+        else turn_neighbours(x0, x1, of);
+      }
+      store16_e4m3(to + r * p.d, e0, e1, x0, x1, scale);
+    }
   }
 }
 
@@ -353,26 +485,51 @@ cudaError_t launch_few(const AppendParams& p, cudaStream_t stream) {
   return e;
 }
 
-cudaError_t launch_many(const AppendParams& p, cudaStream_t stream) {
-  // heads for a quarter of the threads: 4 of 128, 8 of 64
-  int shift = 0;
-  while ((1 << shift) < p.H_kv && (2 << shift) * p.d <= kExpThreads * 2) ++shift;
-  const int groups = (p.H_kv + (1 << shift) - 1) >> shift;
-  const long long blocks = touched_numbers(p.s.T, p.s.B, p.s.page_shift, true) * 2 * groups;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+cudaError_t launch_rows(const AppendParams& p, const CUtensorMap& tk, const CUtensorMap& tv, long long wait_limit,
+                        cudaStream_t stream) {
+  const int heads = append_box_heads(p.H_kv, p.d), groups = (p.H_kv + heads - 1) / heads;
+  const int cluster_shift = p.s.page_shift - 4;  // a CTA for 16 rows
+  const long long ctas = touched_numbers(p.s.T, p.s.B, p.s.page_shift, true) * groups << cluster_shift;
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  const int smem = kRows * heads * p.d * 4 + kRows * (p.rotary_dim / 2) * 8;
   const int slot = prof_begin(kKPagedAppend, stream);
-  const cudaError_t e =
-      launch_chained<paged_append_exps_kernel>(dim3(static_cast<unsigned>(blocks)), kExpThreads, 0, stream, p, shift);
+  auto with = [&](auto threads) {
+    constexpr int kThreadsOf = decltype(threads)::value;
+    // a token's query parts of a group, one or a few a thread
+    const int parts = (p.H_q + groups - 1) / groups * (p.d >> 4);
+    int q_shift = 3;
+    while ((2 << q_shift) <= kThreadsOf && (2 << q_shift) <= parts) ++q_shift;
+    cudaError_t e = allow_smem<paged_append_rows_kernel<kThreadsOf>>(kRowBytes + kRows * 64 * 8);
+    if (e == cudaSuccess) e = allow_wide_clusters<paged_append_rows_kernel<kThreadsOf>>();
+    if (e != cudaSuccess) return e;
+    return launch_clusters<paged_append_rows_kernel<kThreadsOf>>(1 << cluster_shift, dim3(static_cast<unsigned>(ctas)),
+                                                                 kThreadsOf, smem, stream, tk, tv, p, cluster_shift, heads,
+                                                                 groups, q_shift, wait_limit);
+  };
+  // 12 parts of 16 elements a thread at least (25,000 tokens with 2 query and 2 KV heads of 128, 768
+  // parts: 27.1 us with 256 threads, 23.8 with 64; 750 with 8 and 4, 2048 parts: 5.2 us with 256,
+  // 6.3 with 128), and a thread at least for each part of a row of K and V.
+  const int row = 2 * heads * (p.d >> 4), all = kRows * ((p.H_q + groups - 1) / groups * (p.d >> 4) + row);
+  const cudaError_t e = all <= 12 * 64 && row <= 64     ? with(std::integral_constant<int, 64>{})
+                        : all <= 12 * 128 && row <= 128 ? with(std::integral_constant<int, 128>{})
+                                                        : with(std::integral_constant<int, 256>{});
   prof_end(slot, stream);
-  return e == cudaSuccess ? launch_paged_append(p, stream) : e;
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_paged_append_pages(const AppendParams& p, cudaStream_t stream) {
-  // Up to 16 new tokens of each sequence on the mean a warp has them in registers.
-  if (!p.s.cu_seqlens) return launch_few<1>(p, stream);
-  return p.s.T <= 16ll * p.s.B ? launch_few<4>(p, stream) : launch_many(p, stream);
+// Up to 16 new tokens of each sequence on the mean a warp has them in registers.
+bool append_by_rows(const PagedSeqs& s) { return s.cu_seqlens && s.T > 16ll * s.B; }
+int append_box_heads(int H_kv, int d) {
+  const int most = kRowBytes / (kRows * 4 * d), groups = (H_kv + most - 1) / most;  // 8 of 128, 16 of 64
+  return (H_kv + groups - 1) / groups;
+}
+
+cudaError_t launch_paged_append_pages(const AppendParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                      long long wait_limit, cudaStream_t stream) {
+  if (append_by_rows(p.s)) return launch_rows(p, tk, tv, wait_limit, stream);
+  return p.s.cu_seqlens ? launch_few<4>(p, stream) : launch_few<1>(p, stream);
 }
 
 }  // namespace attn

@@ -14,12 +14,13 @@ namespace attn {
 namespace {
 
 // ---------------------------------------------------------------- bounds
-// A warp, or four, for each touched page and KV head, two rows or more at a time: lane (row, 16-byte
+// A warp for each touched page and KV head, two rows or more at a time: lane (row, 16-byte
 // column) keeps the minimum and maximum of its column's elements, packed as the cache's values
 // are (bf16, or e4m3 widened to fp16, both exact), NaN before anything else. Every byte of
-// the pages is read once; they bound it where there are many pages, and a row's latency where
-// there are few, for which four warps share a page (64 pages of 8 heads: XX, with one YY; 40,000
-// tokens' in pages of 32: XX, with four YY).
+// the pages is read once; they bound it where there are many pages (40,000 tokens of 8 KV heads of 128 in
+// pages of 32, bf16: 12.8 us, 73% of a copy's rate), and the latency of the lookups and a page's
+// rows where there are few (64 pages of 64: 2.8 us). Four warps for a page were 0.3 us faster or
+// slower for few pages (by their size) and 3 us slower for many.
 constexpr int kBoundsThreads = 128;
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b, bool f16) {
@@ -35,21 +36,19 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, bool f16) {
   return r;
 }
 
-template <int D, int KIND, int WARPS>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kBoundsThreads)
 paged_bounds_kernel(const BoundsParams p) {
   constexpr bool F16 = KIND != kBf16;
   constexpr int kCols = D * (F16 ? 1 : 2) / 16;  // 16-byte pieces of a row
   constexpr int kWarpRows = 32 / kCols;          // rows of a warp at a time
   constexpr int kWords = F16 ? 8 : 4;            // packed pairs of a piece
-  __shared__ uint32_t part[WARPS > 1 ? WARPS : 1][2][kWords][kCols];
   const PagedSeqs& s = p.s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   grid_wait();
   grid_release();
   if (blockIdx.x == 0) check_paged_seqs(s, threadIdx.x, kBoundsThreads);
-  constexpr int kUnits = kBoundsThreads / 32 / WARPS;  // of a CTA
-  const long long unit = static_cast<long long>(blockIdx.x) * kUnits + (kUnits > 1 ? warp : 0);
+  const long long unit = static_cast<long long>(blockIdx.x) * (kBoundsThreads / 32) + warp;
   const long long number = unit / p.H_kv;
   const int h = static_cast<int>(unit - number * p.H_kv);
   TouchedPage x;
@@ -68,19 +67,19 @@ paged_bounds_kernel(const BoundsParams p) {
   uint32_t lo[kWords], hi[kWords];
 #pragma unroll
   for (int i = 0; i < kWords; ++i) { lo[i] = kPlusInf; hi[i] = kMinusInf; }
-  constexpr int kStep = kWarpRows * WARPS, kAtOnce = WARPS > 1 ? 4 : 8;  // (all loads before the first is used)
-  for (int first = (WARPS > 1 ? warp : 0) * kWarpRows; first < rows; first += kAtOnce * kStep) {
+  constexpr int kAtOnce = 8;  // (all loads before the first is used)
+  for (int first = 0; first < rows; first += kAtOnce * kWarpRows) {
     uint4 v[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int r = min(first + k * kStep + lane / kCols, rows - 1);  // (behind the last row that again)
-      if (first + k * kStep < rows)
+      const int r = min(first + k * kWarpRows + lane / kCols, rows - 1);  // (behind the last row that again)
+      if (first + k * kWarpRows < rows)
         asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "l"(keys + r * kCols));
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      if (first + k * kStep >= rows) break;
+      if (first + k * kWarpRows >= rows) break;
       const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -98,24 +97,6 @@ paged_bounds_kernel(const BoundsParams p) {
       lo[i] = min2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o), F16);
       hi[i] = max2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o), F16);
     }
-  if constexpr (WARPS > 1) {
-    if (lane < kCols) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        part[warp][0][i][col] = lo[i];
-        part[warp][1][i][col] = hi[i];
-      }
-    }
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w)
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        lo[i] = min2(lo[i], part[w][0][i][col], F16);
-        hi[i] = max2(hi[i], part[w][1][i][col], F16);
-      }
-  }
   if (lane >= kCols) return;
   bool turned = false;
   if constexpr (F16) {
@@ -139,14 +120,11 @@ paged_bounds_kernel(const BoundsParams p) {
 }
 
 template <int D, int KIND>
-cudaError_t launch_bounds(const BoundsParams& p, int n_sm, cudaStream_t stream) {
+cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
   const long long units = touched_numbers(p.s.T, p.s.B, p.s.page_shift, p.s.cu_seqlens != nullptr) * p.H_kv;
-  if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-  // four warps while those of all pages find places at once
-  if (units <= 16ll * n_sm)
-    return launch_chained<paged_bounds_kernel<D, KIND, 4>>(dim3(static_cast<unsigned>(units)), kBoundsThreads, 0, stream, p);
-  return launch_chained<paged_bounds_kernel<D, KIND, 1>>(dim3(static_cast<unsigned>((units + 3) / 4)), kBoundsThreads, 0,
-                                                         stream, p);
+  const long long blocks = (units + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  return launch_chained<paged_bounds_kernel<D, KIND>>(dim3(static_cast<unsigned>(blocks)), kBoundsThreads, 0, stream, p);
 }
 
 // ---------------------------------------------------------------- selection
@@ -205,9 +183,6 @@ __device__ __forceinline__ long long in_units(float x) {
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
-__device__ __forceinline__ void max_cluster_u32(uint32_t addr, uint32_t x) {
-  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) { return static_cast<uint32_t>(ld_cluster_s32(addr)); }
 __device__ __forceinline__ long long ld_cluster_s64(uint32_t addr) {
@@ -725,11 +700,11 @@ cudaError_t plan_select(SelectParams p, int n_sm, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, int n_sm, cudaStream_t stream) {
+cudaError_t launch_paged_bounds(const BoundsParams& p, int d, int kind, cudaStream_t stream) {
   const int slot = prof_begin(kKPagedBounds, stream);
   auto of_kind = [&](auto k) {
     constexpr int K = decltype(k)::value;
-    return d == 128 ? launch_bounds<128, K>(p, n_sm, stream) : launch_bounds<64, K>(p, n_sm, stream);
+    return d == 128 ? launch_bounds<128, K>(p, stream) : launch_bounds<64, K>(p, stream);
   };
   const cudaError_t e = kind == kBf16   ? of_kind(std::integral_constant<int, kBf16>{})
                         : kind == kE4m3 ? of_kind(std::integral_constant<int, kE4m3>{})

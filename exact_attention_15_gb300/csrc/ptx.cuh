@@ -572,6 +572,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
 __device__ __forceinline__ void fence_async_shared_cluster() {
   asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
+__device__ __forceinline__ void max_cluster_u32(uint32_t addr, uint32_t x) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");

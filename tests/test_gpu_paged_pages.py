@@ -221,7 +221,8 @@ def _append(c, new, H_q, rotary, interleaved, x=None, fused=True, seed=1):
 
 @pytest.mark.parametrize("H_q,H_kv,d,page,rotary,interleaved", [
     (8, 2, 128, 16, 128, False), (6, 3, 64, 32, 32, True), (4, 4, 64, 16, 0, False), (0, 1, 128, 256, 64, False),
-    (16, 1, 128, 64, 128, True), (32, 8, 128, 128, 64, False)])
+    (16, 1, 128, 64, 128, True), (32, 8, 128, 128, 64, False), (20, 10, 128, 64, 48, False), (3, 3, 64, 256, 16, True),
+    (34, 17, 64, 32, 64, False)])
 @pytest.mark.parametrize("new,ctx", [
     ([1], [0]), ([1, 1, 1, 1, 1], [0, 15, 16, 17, 300]), ([5, 1, 40, 0, 33], [0, 31, 100, 9, 7]), ([700, 129], [0, 63]),
     ([300], [1])])
@@ -239,25 +240,26 @@ def test_append(new, ctx, H_q, H_kv, d, page, rotary, interleaved):
     assert bool((err <= (BF16 * y.abs() + 2.0 ** -20 * pair if rotary else 0 * err)).all())
 
 
-def test_append_values_of_every_size():
+@pytest.mark.parametrize("middle,page", [(40, 16), (80, 16), (80, 64)])  # (few and many tokens of a sequence)
+def test_append_values_of_every_size(middle, page):
     """Zeros, the smallest and largest numbers, infinities and NaN among the new values."""
-    c = Pages([5, 40, 1], 2, 64, 16, seed=9)
-    x = torch.randn(46, 4, 64, device="cuda", dtype=torch.bfloat16)
+    c = Pages([5, middle, 1], 2, 64, page, seed=9)
+    x = torch.randn(6 + middle, 4, 64, device="cuda", dtype=torch.bfloat16)
     x[0] = 0                       # first token of a sequence: zeros
     x[5:12] *= 2.0 ** -100         # a page of numbers below 2^-64: the exponent's lower end
     x[5:21, 2] = 2.0 ** -90
     x[21:37, 1] = 3e38             # above 448 2^64
     x[22:30, 3, 5] = math.inf
     x[23, 2, 7], x[24, 2, 8] = math.nan, -math.inf
-    x[45, 0] = 448.0 * 2.0 ** -5   # the border of an exponent, and one step above it
-    x[45, 1] = 450.0 * 2.0 ** -5
+    x[-1, 0] = 448.0 * 2.0 ** -5   # the border of an exponent, and one step above it
+    x[-1, 1] = 450.0 * 2.0 ** -5
     B = _binding()
-    B.paged_append(c.handle(), None, x[:, :2].contiguous(), x[:, 2:].contiguous(), c.table, c.kv_lens, cu_seqlens=_cu([5, 40, 1]))
+    B.paged_append(c.handle(), None, x[:, :2].contiguous(), x[:, 2:].contiguous(), c.table, c.kv_lens, cu_seqlens=_cu([5, middle, 1]))
     _ok()
     t0 = 0
     for b, n in enumerate(c.lens):
-        for i in range(-(-n // 16)):
-            p, rows = c.ids[b][i], slice(t0 + 16 * i, t0 + min(n, 16 * i + 16))
+        for i in range(-(-n // page)):
+            p, rows = c.ids[b][i], slice(t0 + page * i, t0 + min(n, page * i + page))
             for h in range(4):
                 name, hh = ("k", h) if h < 2 else ("v", h - 2)
                 y = x[rows, h].double()
@@ -300,18 +302,18 @@ def test_append_token_by_token_grows_pages():
 def test_append_bad_pages_and_lengths():
     """Page indices and lengths outside the cache write nothing and are recorded."""
     B = _binding()
-    for bad in (-1, 10 ** 6):
-        c = Pages([20, 20], 2, 64, 16, seed=1)
+    for bad, n in ((-1, 10), (10 ** 6, 10), (-1, 40), (10 ** 6, 40)):
+        c = Pages([n + 10, n + 10], 2, 64, 16, seed=1)
         c.table[0, 1] = bad
-        before = {n: getattr(c, n).clone() for n in ("k", "v", "k_exp", "v_exp")}
-        x = torch.randn(20, 2, 64, device="cuda", dtype=torch.bfloat16)
-        B.paged_append(c.handle(), None, x, x, c.table, c.kv_lens, cu_seqlens=_cu([10, 10]))
+        before = {m: getattr(c, m).clone() for m in ("k", "v", "k_exp", "v_exp")}
+        x = torch.randn(2 * n, 2, 64, device="cuda", dtype=torch.bfloat16)
+        B.paged_append(c.handle(), None, x, x, c.table, c.kv_lens, cu_seqlens=_cu([n, n]))
         assert B.attn_check(None) == 13
-        ids = set(c.ids[0][:1] + c.ids[1])
+        ids = set(c.ids[0][:1] + c.ids[0][2:] + c.ids[1])
         for p in range(c.k.shape[0]):
             if p not in ids:
-                for n, t in before.items():
-                    assert torch.equal(as_int(getattr(c, n)[p]), as_int(t[p])), (n, p)
+                for m, t in before.items():
+                    assert torch.equal(as_int(getattr(c, m)[p]), as_int(t[p])), (m, p)
     c = Pages([20], 1, 64, 16, seed=1, width=2)
     before = c.k.clone()
     x = torch.randn(4, 1, 64, device="cuda", dtype=torch.bfloat16)
@@ -321,16 +323,18 @@ def test_append_bad_pages_and_lengths():
     assert torch.equal(as_int(c.k), as_int(before))
 
 
-def test_append_padding_rows():
+@pytest.mark.parametrize("n", [8, 50])  # (few and many tokens of a sequence)
+def test_append_padding_rows(n):
     """A sequence that is shorter than its rows: only the rows at positions from 0 on."""
-    c = Pages([3, 20], 1, 64, 16, seed=6)
-    x = torch.randn(17, 4, 64, device="cuda", dtype=torch.bfloat16)
-    q_out = torch.full((17, 2, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    c = Pages([3, n + 12], 1, 64, 16, seed=6)
+    x = torch.randn(n + 9, 4, 64, device="cuda", dtype=torch.bfloat16)
+    q_out = torch.full((n + 9, 2, 64), 7.0, device="cuda", dtype=torch.bfloat16)
     freq = _inv_freq(64)
-    _binding().paged_append(c.handle(), x[:, :2], x[:, 2:3], x[:, 3:], c.table, c.kv_lens, cu_seqlens=_cu([8, 8]), inv_freq=freq,
+    _binding().paged_append(c.handle(), x[:, :2], x[:, 2:3], x[:, 3:], c.table, c.kv_lens, cu_seqlens=_cu([8, n]), inv_freq=freq,
                             q_out=q_out)
     _ok()
-    assert bool((q_out[:5] == 7).all()) and bool((q_out[16:] == 7).all()) and not bool((q_out[5:16] == 7).all(dim=2).any())
+    assert bool((q_out[:5] == 7).all()) and bool((q_out[8 + n:] == 7).all())
+    assert not bool((q_out[5:8 + n] == 7).all(dim=2).any())
     e = exponent(float(x[5:8, 3].abs().max()))
     assert int(c.v_exp[c.ids[0][0], 0]) == e + 127
     assert torch.equal(as_int(c.v[c.ids[0][0], 0, :3]), as_int(encoded(x[5:8, 3].double(), e)))
