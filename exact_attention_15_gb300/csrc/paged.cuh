@@ -15,14 +15,16 @@ namespace attn {
 // KV head; e4m3 with a power of two for each page and KV head.
 constexpr int kBf16 = 0, kE4m3 = 1, kE4m3Pages = 3;
 
-// Exponents of the powers of two: within +-kMaxExp, so that sums of weights divided by them
-// stay far inside 32 bits (2^20 keys, a bias of 2^15 and 2^64).
-constexpr int kMaxExp = 64;
+// Exponents of the powers of two. Attention works with the weights times the values' 2^ev, in
+// 32 bits, and takes 2^ev out of their sum again: a weight w of a page beside one whose ev is higher
+// by s is lost below 2^-126 2^s, with 88 powers between the ends below 2^-38 of the largest. (448
+// 2^24 is 7.5e9; a page of zeros has the lowest.)
+constexpr int kMinExp = -64, kMaxExp = 24;
 __device__ __forceinline__ uint32_t page_byte(const uint8_t* exps, int page, int H_kv, int h) {
   return __ldg(exps + static_cast<size_t>(page) * H_kv + h);
 }
 __device__ __forceinline__ int exponent_of(uint32_t byte) {
-  return max(-kMaxExp, min(kMaxExp, static_cast<int>(byte) - 127));
+  return max(kMinExp, min(kMaxExp, static_cast<int>(byte) - 127));
 }
 __device__ __forceinline__ int page_exponent(const uint8_t* exps, int page, int H_kv, int h) {
   return exponent_of(page_byte(exps, page, H_kv, h));

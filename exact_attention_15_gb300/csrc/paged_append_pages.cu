@@ -49,11 +49,11 @@ template <bool FINITE>
 __device__ __forceinline__ uint32_t larger(uint32_t most, const Part& x) {
   return larger<FINITE>(larger<FINITE>(most, x.a), x.b);
 }
-// The smallest e from -kMaxExp to kMaxExp with most <= 448 2^e = 1.75 2^(e + 8).
+// The smallest e from kMinExp to kMaxExp with most <= 448 2^e = 1.75 2^(e + 8).
 __device__ __forceinline__ int exponent_for(float most) {
   const uint32_t bits = __float_as_uint(most);
   const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-  return max(-kMaxExp, min(kMaxExp, e));
+  return max(kMinExp, min(kMaxExp, e));
 }
 // 16 elements of a row: two runs of 8, or one of 16.
 __device__ __forceinline__ void store16_e4m3(uint8_t* row, int e0, int e1, const float (&x0)[8], const float (&x1)[8],
@@ -75,8 +75,7 @@ __device__ __forceinline__ uint32_t encode_again(uint32_t w, float scale) {
 
 // page_exponent() of an exponent that this kernel may write.
 __device__ __forceinline__ int plain_exponent(const uint8_t* exps, int page, int H_kv, int h) {
-  const int e = static_cast<int>(exps[static_cast<size_t>(page) * H_kv + h]) - 127;
-  return max(-kMaxExp, min(kMaxExp, e));
+  return exponent_of(exps[static_cast<size_t>(page) * H_kv + h]);
 }
 // Re-encodes the `kept` rows of a head of a page, which are contiguous, for an exponent that is
 // larger by `more`; thread `tid` of `nthreads`.
@@ -193,7 +192,7 @@ paged_append_few_kernel(const AppendParams p, int kv_blocks, int q_shift) {
   const int head_shift = p.d == 128 ? 3 : 2, j = tid & ((1 << head_shift) - 1);  // the same in every row
   const bool turn = !is_v && 16 * j < p.rotary_dim, split = turn && !p.interleaved;
   const int e0 = split ? 8 * j : 16 * j, e1 = split ? 8 * j + (p.rotary_dim >> 1) : 16 * j + 8;
-  int page = 0, e = -kMaxExp, kept = 0;
+  int page = 0, e = kMinExp, kept = 0;
   Part held[KP];
   uint32_t most = 0;
   const __nv_bfloat16* src = nullptr;
@@ -329,7 +328,7 @@ paged_append_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_
   if (tid < 2 * n_heads)
     sh.before[tid] = kept && page_ok ? plain_exponent(tid < n_heads ? p.k_exp : p.v_exp, page, p.H_kv,
                                                       h0 + (tid < n_heads ? tid : tid - n_heads))
-                                     : -kMaxExp;
+                                     : kMinExp;
   // ---- angles
   const int pairs = p.rotary_dim >> 1, j_count = p.rotary_dim >> 4;
   float2* angles = reinterpret_cast<float2*>(smem + 2 * v_off);  // [row][e][part]

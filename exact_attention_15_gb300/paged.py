@@ -81,7 +81,7 @@ class PagedCache:
     [num_pages, 2, ...] tensor). k_scale and v_scale (e4m3): fp32 [H_kv], the
     factor a head's stored values stand for; None for 1. Both scales as contiguous
     float8_e8m0fnu [num_pages, H_kv] give each page and head a power of two of its own, which
-    paged_append finds and writes (exponents from -64 to 64; others count as the nearest of
+    paged_append finds and writes (exponents from -64 to 24; others count as the nearest of
     these). Keeps the tensors; their contents may change between calls."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):

@@ -262,7 +262,7 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  * ATTN_CACHE_E4M3_PAGES: e4m3 with a power of two for each page and head. k_exp and v_exp are
  * device arrays of num_pages * H_kv bytes (the E8M0 format of scales): an x of page p and
  * head h stands for x * 2^(k_exp[p * H_kv + h] - 127). attn_paged_append finds them and writes
- * exponents from -64 to 64; others count as the nearest of these. The scale arrays are not
+ * exponents from -64 to 24; others count as the nearest of these. The scale arrays are not
  * read.
  *
  * Sequences are described by device arrays that the host does not read:
@@ -318,11 +318,12 @@ typedef struct {
  * a call writes must not be shared with another of its sequences. Rows of q_out
  * at padding positions are left as they were.
  * With a scale for each page, a page that begins with a new token takes for each head the
- * smallest exponent e (from -64 to 64) with which 448 * 2^e is at least the largest finite
+ * smallest exponent e (from -64 to 24) with which 448 * 2^e is at least the largest finite
  * magnitude of its new values; a page that holds rows already takes the larger of that and what it
  * had, and where it grows those rows are encoded again. Values x / 2^e are rounded to nearest,
  * those past +-448 (infinities among them) to +-448. With rotary_dim > 0 keys count with 1.5
- * times their magnitude before the turn, which no turned element exceeds.
+ * times their magnitude before the turn, which no turned element exceeds. As the rows that a page holds
+ * may be encoded again, a page that is appended to must not be shared with any other sequence.
  */
 int attn_paged_append(const attn_paged_cache* cache, const void* q, const void* k, const void* v,
                       void* q_out, long long q_stride, long long k_stride, long long v_stride,
@@ -566,7 +567,9 @@ long long attn_set_wait_limit(long long cycles);
  * pass at d_qk = 192), 4 backward post (dQ conversion), 5 exp2 test hook, 6 stall
  * test hook, 7 forward planning kernel (packed inputs), 8 forward on CTA pairs
  * (ATTN_FWD_CTA_PAIR), 9 second pass of the backward main kernel (d_qk = 192),
- * 10 backward planning kernel (packed inputs).
+ * 10 backward planning kernel (packed inputs). Over a paged cache: 11 appending,
+ * 12 streaming attention, 13 the joins of both attention kernels, 14 chunk attention, 15 its
+ * planning kernel, 16 queries as fp16, 17 page bounds, 18 page selection.
  */
 typedef struct {
   int kernel;  /* kernel id, see above */

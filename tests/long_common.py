@@ -63,11 +63,11 @@ class Pages:
 
 
 def exponent(most):
-    """The smallest e from -64 to 64 with most <= 448 2^e."""
+    """The smallest e from -64 to 24 with most <= 448 2^e (24 if there is none)."""
     if not most > 0:
         return -64
     m, x = math.frexp(most)
-    return max(-64, min(64, x - 9 + (m > 0.875)))
+    return max(-64, min(24, x - 9 + (m > 0.875)))
 
 
 def encoded(x, e):

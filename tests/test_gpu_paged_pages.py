@@ -33,7 +33,7 @@ def _cu(new):
 
 EXPS = {
     "near": ((-8, -4), (-8, -4)),
-    "far": ((-12, -3), (-40, 30)),   # the values' sizes differ by 2^70
+    "far": ((-12, -3), (-46, 24)),   # the values' sizes differ by 2^70
     "tiny": ((-50, -40), (-64, -60)),
 }
 
@@ -129,7 +129,7 @@ def test_exponents_outside_the_range_count_as_its_ends(new):
     assert torch.equal(as_int(call()), as_int(o))
     c.v_exp.fill_(255)
     o = call()
-    c.v_exp.fill_(127 + 64)
+    c.v_exp.fill_(127 + 24)
     assert torch.equal(as_int(call()), as_int(o))
     _ok()
 
@@ -145,6 +145,31 @@ def test_pages_of_zeros():
         o, lse = _binding().paged_forward(c.handle(), q, c.table, c.kv_lens, _cu([n]), causal=False)
         want, want_abs, want_lse = attention(q, c.sequence("k", 0), c.sequence("v", 0), 0.125, torch.full((n,), 256, device="cuda"))
         assert_attention(o, lse, want, want_abs, want_lse, n)
+    _ok()
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_weights_across_the_whole_range(n):
+    """Equal keys, so equal weights: pages of the smallest and of the largest scale share the sum,
+    and with -inf-like scores on the large ones the small ones' values come out."""
+    c = Pages([512], 1, 64, 64, (-6, -6), (-64, -64), seed=8)
+    for i in (1, 4):
+        c.v_exp[c.ids[0][i]] = 127 + 24
+    as_int(c.k)[:] = as_int(c.k)[c.ids[0][0], :, :1]
+    q = torch.randn(n, 2, 64, device="cuda", dtype=torch.bfloat16)
+    call = lambda: _binding().paged_forward(c.handle(), q, c.table, c.kv_lens, _cu([n]), causal=False)  # noqa: E731
+    o, lse = call()
+    want, want_abs, want_lse = attention(q, c.sequence("k", 0), c.sequence("v", 0), 0.125, torch.full((n,), 512, device="cuda"))
+    assert_attention(o, lse, want, want_abs, want_lse, n)
+    # scores 256 below: weights of 0
+    q = torch.full_like(q, 4.0)
+    as_int(c.k)[:] = as_int(torch.ones(1, device="cuda").to(c.k.dtype))
+    for i in (1, 4):
+        as_int(c.k)[c.ids[0][i]] = as_int(torch.full((1,), -64.0, device="cuda").to(c.k.dtype))
+    c.k_exp.fill_(127)
+    o, lse = call()
+    want, want_abs, want_lse = attention(q, c.sequence("k", 0), c.sequence("v", 0), 0.125, torch.full((n,), 512, device="cuda"))
+    assert_attention(o, lse, want, want_abs, want_lse, n)
     _ok()
 
 
@@ -191,7 +216,7 @@ def _append(c, new, H_q, rotary, interleaved, x=None, fused=True, seed=1):
                     most = float(size[size < math.inf].max()) if bool((size < math.inf).any()) else 0.0
                     e = exponent(most * (1.5 if name == "k" and rotary else 1.0))
                     if r0:
-                        old = max(-64, min(64, int(before[name + "_exp"][p, h]) - 127))
+                        old = max(-64, min(24, int(before[name + "_exp"][p, h]) - 127))
                         e = max(e, old)
                         if e > old:
                             kept = encoded(before[name][p, h, :r0].double(), e - old)
@@ -248,7 +273,7 @@ def test_append_values_of_every_size(middle, page):
     x[0] = 0                       # first token of a sequence: zeros
     x[5:12] *= 2.0 ** -100         # a page of numbers below 2^-64: the exponent's lower end
     x[5:21, 2] = 2.0 ** -90
-    x[21:37, 1] = 3e38             # above 448 2^64
+    x[21:37, 1] = 3e38             # above 448 2^24
     x[22:30, 3, 5] = math.inf
     x[23, 2, 7], x[24, 2, 8] = math.nan, -math.inf
     x[-1, 0] = 448.0 * 2.0 ** -5   # the border of an exponent, and one step above it

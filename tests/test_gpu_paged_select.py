@@ -402,3 +402,130 @@ def test_decoding_with_selected_pages(kind, drafted):
         for i, p in enumerate(c.ids[b]):
             want = bounds_of(_keys(c, kind, p), min(page, total - i * page)).float().to(torch.bfloat16)
             assert torch.equal(bounds[p], want), (b, i)
+
+
+def test_prompts_and_steps_captured_on_two_streams():
+    """Whole prompts (the appending kernel by rows, chunk attention) and a selecting step over long tables
+    (clusters), captured and replayed on two streams at once: the bits of eager calls."""
+    B_ = _binding()
+    H_kv, group, d, page = 2, 4, 128, 32
+    new = [300, 70, 500]
+    freq = 10000.0 ** (-torch.arange(d // 2, dtype=torch.float64, device="cuda") * 2 / d)
+
+    def world(seed):
+        c = Pages([n + 1 for n in new], H_kv, d, page, seed=seed)
+        cache = c.handle()
+        c.kv_lens.sub_(1)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn(sum(new), H_kv * (group + 2), d, generator=g, device="cuda", dtype=torch.bfloat16)
+        y = torch.randn(len(new), H_kv * (group + 2), d, generator=g, device="cuda", dtype=torch.bfloat16)
+        bounds = torch.zeros(c.k.shape[0], H_kv, 2, d, device="cuda", dtype=torch.bfloat16)
+        wide = torch.zeros(len(new), 3000, dtype=torch.int32, device="cuda")
+        wide[:, :c.table.shape[1]] = c.table
+        after, cu = c.kv_lens + 1, _cu(new)
+
+        def work():
+            q = B_.paged_append(cache, x[:, :-2 * H_kv], x[:, -2 * H_kv:-H_kv], x[:, -H_kv:], c.table, c.kv_lens, cu_seqlens=cu,
+                                inv_freq=freq)
+            B_.paged_bounds(cache, bounds, c.table, c.kv_lens, cu_seqlens=cu, tokens=sum(new))
+            o, lse = B_.paged_forward(cache, q, c.table, c.kv_lens, cu)
+            q1 = B_.paged_append(cache, y[:, :-2 * H_kv], y[:, -2 * H_kv:-H_kv], y[:, -H_kv:], wide, after, inv_freq=freq)
+            B_.paged_bounds(cache, bounds, wide, after)
+            pages, lens = B_.paged_select(cache, q1, bounds, wide, after, 5, keep_first=1)
+            return (q, o, lse, q1, pages, lens, *B_.paged_decode(cache, q1, pages, lens))
+
+        keep = (c, cache, x, y, bounds, wide, after, cu)
+        return work, (c.k, c.v, c.k_exp, c.v_exp, bounds), keep
+
+    worlds = [world(1), world(2)]
+    eager = []
+    for work, state, _ in worlds:
+        out = work()
+        eager.append([as_int(t).clone() if t.element_size() < 4 else t.clone() for t in (*out, *state)])
+    _ok()
+    streams = [torch.cuda.Stream() for _ in worlds]
+    graphs, outs = [], []
+    for (work, _, _), stream in zip(worlds, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs.append(work())
+        graphs.append(graph)
+    for _ in range(5):
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    _ok()
+    for out, (_, state, _), want in zip(outs, worlds, eager):
+        for t, w in zip((*out, *state), want):
+            assert torch.equal(as_int(t) if t.element_size() < 4 else t, w)
+
+
+def test_pages_behind_2_31_elements():
+    """Pages, lists and bounds whose places pass 32 bits."""
+    B_ = _binding()
+    H_kv, d, page = 8, 128, 256
+    n_pages = (1 << 31) // (H_kv * page * d) + 6
+    k = torch.empty(n_pages, H_kv, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v = torch.empty_like(k)
+    exps = [torch.empty(n_pages, H_kv, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache = B_.PagedCache(k, v, k_scale=exps[0].view(torch.float8_e8m0fnu), v_scale=exps[1].view(torch.float8_e8m0fnu))
+    bounds = torch.empty(n_pages, H_kv, 2, d, dtype=torch.bfloat16, device="cuda")
+    ids = [n_pages - 1, 3, n_pages - 2, n_pages - 3]
+    table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    n = 3 * page + 40
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    x = torch.randn(n, 2 * H_kv, d, device="cuda", dtype=torch.bfloat16)
+    B_.paged_append(cache, None, x[:, :H_kv], x[:, H_kv:], table, lens, cu_seqlens=_cu([n]))
+    B_.paged_bounds(cache, bounds, table, lens, cu_seqlens=_cu([n]), tokens=n)
+    q = torch.randn(1, 2 * H_kv, d, device="cuda", dtype=torch.bfloat16)
+    pages, chosen = B_.paged_select(cache, q, bounds, table, lens, 3, keep_first=1)
+    o, lse = B_.paged_decode(cache, q, pages, chosen)
+    full, full_lse = B_.paged_decode(cache, q, table, lens)
+    _ok()
+    values = [values_of(t[ids], e[ids]) for t, e in ((k, exps[0]), (v, exps[1]))]  # [4, H_kv, page, d]
+    for i in range(4):
+        rows = min(page, n - i * page)
+        assert torch.equal(bounds[ids[i]], bounds_of(values[0][i], rows).float().to(torch.bfloat16))
+    want, keys = selected(q[0].view(H_kv, 2, d), bounds, ids, n, page, 3, 1, 1)
+    assert torch.equal(pages[0].cpu(), want) and int(chosen) == keys
+    place = {p: i for i, p in enumerate(ids)}
+    for lists, length, got, got_lse in ((pages, keys, o, lse), (table[:, None].expand(-1, H_kv, -1), n, full, full_lse)):
+        kv = [torch.stack([torch.cat([t[place[int(p)], h] for p in lists[0, h]])[:length] for h in range(H_kv)], 1) for t in values]
+        want, want_abs, want_lse = attention(q, *kv, 1 / math.sqrt(d), torch.tensor([length], device="cuda"))
+        assert_attention(got, got_lse[0][:, None], want, want_abs, want_lse, length)
+
+
+def test_selection_is_the_same_again_and_on_another_stream():
+    c = Boxes([50000] * 3, 4, 128, 16, seed=5)
+    q = torch.randn(3, 16, 128, device="cuda", dtype=torch.bfloat16)
+    pages, lens = _binding().paged_select(c.handle, q, c.bounds, c.table, c.kv_lens, 100)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    out = []
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 3]):
+            out.append(_binding().paged_select(c.handle, q, c.bounds, c.table, c.kv_lens, 100))
+    torch.cuda.synchronize()
+    for p, n in out:
+        assert torch.equal(p, pages) and torch.equal(n, lens)
+    _ok()
+
+
+def test_offsets_that_are_no_offsets_stay_inside():
+    """Decreasing, overlapping and negative offsets write nothing outside and are recorded."""
+    B_ = _binding()
+    c = Pages([200, 300, 100], 2, 64, 16, seed=3)
+    guard = torch.randint(0, 255, (64, 2, 16, 64), dtype=torch.uint8, device="cuda")
+    before = guard.clone()
+    bounds = torch.zeros(c.k.shape[0], 2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(120, 2, 64, device="cuda", dtype=torch.bfloat16)
+    for bad in ([0, 90, 40, 120], [5, 60, 90, 120], [0, -7, 60, 500], [100, 50, 20, 10]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        q = torch.randn(120, 4, 64, device="cuda", dtype=torch.bfloat16)
+        B_.paged_append(c.handle(), q, x, x, c.table, c.kv_lens, cu_seqlens=cu)
+        B_.paged_bounds(c.handle(), bounds, c.table, c.kv_lens, cu_seqlens=cu, tokens=120)
+        pages, _ = B_.paged_select(c.handle(), q, bounds, c.table, c.kv_lens, 4, cu_seqlens=cu)
+        assert B_.attn_check(None) == 12
+        assert torch.equal(guard, before)
