@@ -506,7 +506,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_async_shared();
             __syncwarp();
           }
-          bool have_k = false;
+          // e4m3, whose ring has three places: not before P V, which needs no K, since K_(j + 1) takes the
+          // place of V_(j - 1)
+          bool have_k = !E4M3;
+          if (!E4M3 && next_k && !(ok = wait_full(itk))) break;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (j >= t.n[i]) continue;
@@ -520,7 +523,6 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               mma_commit_by(leader, smem_addr(&bars->pv_done[i]));
               continue;
             }
-            // (not before P V, which needs no K: with a ring of three places K_(j + 1) takes that of V_(j - 1))
             if (!have_k && !(ok = wait_full(itk))) break;
             if (!have_k) tc_fence_after();
             have_k = true;

@@ -131,15 +131,17 @@ cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
 // One cluster of 1 to 16 CTAs for each token and KV head; each scores a run of the pages. Where
 // the first CTA's shared memory holds all scores it does the rest alone; behind wider tables
 // (10,000 pages or so) every CTA keeps its own, and they count together. (Each step that
-// a cluster takes together costs a barrier and reads of the others' shared memory: with 4096 pages on 8
-// CTAs the steps behind the scores took 18 us together, 11 in one.)
+// a cluster takes together costs a barrier and reads of the others' shared memory: of 4096 pages
+// on 8 CTAs the steps behind the scores took 19 of 26 us. With 16 CTAs and all scores in one of them
+// they take 7 of 13.)
 //
 // 1. Bounds as products on mma.sync m16n8k16: 16 pages in M, the heads of the group in N,
 //    (lo, hi) and (min(q, 0), max(q, 0)) side by side in K, whose order does not matter as long as
 //    both operands have the same: a lane reads 16 bytes of a row at a time. The bytes bound
-//    this part: every warp has a ring of its own of 16 pages' bounds, filled by bulk copies.
-//    (With loads to registers, four 128-register CTAs' worth of which fit no SM, 4096 pages of
-//    8 heads took 9.7 us on 64 SMs.)
+//    this part: every warp has a place of its own for 16 pages' bounds, filled by bulk copies while
+//    other warps compute. (With loads to registers, 64 of a thread, too few CTAs find place on an
+//    SM: 64 sequences of 64 to 512 pages took 34 us in all, with copies 24; two places for a warp, and
+//    so half the CTAs, 35.)
 // 2. A histogram of the scores over their range finds the interval that the last chosen
 //    score lies in.
 // 3. The products are exact, their sums are not: with eps a bound on the sums' error, pages
@@ -149,12 +151,13 @@ cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
 //    the inputs are no such numbers). Ties go to the lower page.
 // 4. The chosen pages are written in their order.
 constexpr int kBins = 1024;
-// Up to this many pages to be ranked in 64 bits are compared pair by pair, more by digits:
-// 256 threads of a CTA compare 512 with 512 in the time of about two of the ten digits.
-constexpr int kPairs = 512;
+// Up to this many pages to be ranked in 64 bits are compared pair by pair, more by digits (8
+// tokens and heads with 100 equal pages take 43 us either way, with 512 163 and 109).
+constexpr int kPairs = 64;
 // Error of a sum relative to the sum of the magnitudes: two chains of d / 16 = 8 instructions,
 // each of which adds 17 terms, each to 2^-23 of the largest at least, and the chains' sum to 2^-24,
-// is below 136 * 2^-23 + 2^-24 = 1.63e-5.
+// is below 136 * 2^-23 + 2^-24 = 1.63e-5. (On random products, some a thousand times the others, the
+// largest seen was 2.3e-6 after eight instructions.)
 constexpr float kSumError = 1.75e-5f;
 // Sums below this stay finite, so that no score is an infinity or a NaN; above the other, what
 // products below the normal numbers lose (256 times 2^-126 at most) is less than 2^-77 of it.
@@ -542,15 +545,22 @@ paged_select_kernel(const SelectParams p) {
       // 2^62 over a power of two that the sums' magnitudes stay below
       const int top = static_cast<int>(__float_as_uint(size) >> 23) - 126;
       const float unit = power_of_two(max(-126, min(126, 61 - top)));
-      // a warp for each page and four query rows
+      // a warp for each page and four query rows; the next page's bounds are loaded before
       const int quads = (p.group + 3) / 4;
+      uint32_t next[D / 32];
+      auto load = [&](int x) {
+        const int page = page_of(s, b, p.first + begin + list[x / quads]);
+        const uint32_t* src = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(page) * p.H_kv + h) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) next[i] = __ldg(src + i * 32 + lane);
+      };
+      if (warp < mine * quads) load(warp);
       for (int x = warp; x < mine * quads; x += kSelWarps) {
         const int e = x / quads, r0 = (x - e * quads) * 4;
-        const int page = page_of(s, b, p.first + begin + list[e]);
-        const uint32_t* src = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(page) * p.H_kv + h) * D;
         uint32_t y[D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) y[i] = __ldg(src + i * 32 + lane);
+        for (int i = 0; i < D / 32; ++i) y[i] = next[i];
+        if (x + kSelWarps < mine * quads) load(x + kSelWarps);
         long long key = kNoKey;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -589,15 +599,17 @@ paged_select_kernel(const SelectParams p) {
         const long long key = list_key[e];
         const int place = begin + list[e];
         uint32_t better = 0;
-        for (int r = 0; r < cluster; ++r) {
-          const uint32_t theirs = cluster == 1 ? mine : ld_cluster_u32(cluster_map(smem_addr(&sh.unsure), r));
-          // (its own shared memory by an address of the same kind)
-          const uint32_t keys = cluster == 1 ? smem_addr(list_key) : cluster_map(smem_addr(list_key), r);
-          const uint32_t places = cluster == 1 ? smem_addr(list) : cluster_map(smem_addr(list), r);
-#pragma unroll 4
-          for (uint32_t i = 0; i < theirs; ++i) {
-            const long long other = ld_cluster_s64(keys + 8 * i);
-            better += other > key || (other == key && static_cast<int>(ld_cluster_u32(places + 4 * i)) + r * per < place);
+        if (cluster == 1) {
+          for (int i = 0; i < mine; ++i)
+            better += list_key[i] > key || (list_key[i] == key && static_cast<int>(list[i]) < place);
+        } else {
+          for (int r = 0; r < cluster; ++r) {
+            const uint32_t theirs = ld_cluster_u32(cluster_map(smem_addr(&sh.unsure), r));
+            const uint32_t keys = cluster_map(smem_addr(list_key), r), places = cluster_map(smem_addr(list), r);
+            for (uint32_t i = 0; i < theirs; ++i) {
+              const long long other = ld_cluster_s64(keys + 8 * i);
+              better += other > key || (other == key && static_cast<int>(ld_cluster_u32(places + 4 * i)) + r * per < place);
+            }
           }
         }
         if (better < need) atomicAdd(&sh.chosen, 1u);
