@@ -262,8 +262,12 @@ constexpr int kStreamCtas = 456;  // CTAs the workspace holds partial results fo
 constexpr int kStreamTile = 64;   // keys per tile
 constexpr int kStreamCluster = 8;  // CTAs of a cluster at most
 // CTAs on an SM: three where the registers (8 query rows) and shorter tiles (rows of
-// `row_bytes` of K or V) allow it.
-constexpr int stream_ctas(int rows, int row_bytes) { return rows == 8 && row_bytes <= 128 ? 3 : 2; }
+// `row_bytes` of K or V) allow it, and over pages with scales with 16 query rows of 64 (4 drafted tokens
+// behind 4000 to 32,000 keys, 8 sequences, 32 heads on 8: 41.5 us with two, 38.1 with three; rows of
+// 128 spill: 35.3 and 49.6).
+constexpr int stream_ctas(int rows, int row_bytes, bool pages) {
+  return (rows == 8 && row_bytes <= 128) || (pages && row_bytes <= 64) ? 3 : 2;
+}
 
 struct StreamParams {
   PagedSeqs s;

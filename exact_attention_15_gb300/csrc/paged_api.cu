@@ -199,7 +199,7 @@ StreamShape stream_shape(const attn_paged_cache* c, int T, int B, int group, boo
                                   : static_cast<long long>(B) * ((group + s.rows - 1) / s.rows);
   s.items = chunks * c->H_kv;
   const long long tiles = (static_cast<long long>(max_pages) * c->page_size + kStreamTile - 1) / kStreamTile;
-  const long long grid = static_cast<long long>(stream_ctas(s.rows, c->d * (in_bytes(c) ? 1 : 2))) * n_sm;
+  const long long grid = static_cast<long long>(stream_ctas(s.rows, c->d * (in_bytes(c) ? 1 : 2), c->type == kE4m3Pages)) * n_sm;
   s.cluster = 1;
   while (2 * s.cluster <= kStreamCluster && 8 * s.items * 2 * s.cluster <= 7 * grid) {
     const long long per_sm = (s.items * 2 * s.cluster + n_sm - 1) / n_sm;

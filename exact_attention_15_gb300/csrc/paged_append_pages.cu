@@ -182,13 +182,12 @@ paged_append_few_kernel(const AppendParams p, int kv_blocks, int q_shift) {
   }
   if (blockIdx.x == 0) check_paged_seqs(s, threadIdx.x, kThreads);
   const int tid = threadIdx.x % 32;
-  const long long at = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / 32;
-  const int which = static_cast<int>(at % (2 * p.H_kv));
-  const int h = which >> 1;
+  // (64-bit divisions took 0.3 us of 6.2)
+  const uint32_t at = blockIdx.x * kGroups + threadIdx.x / 32, per = 2u * p.H_kv, number = at / per;
+  const int which = static_cast<int>(at - number * per), h = which >> 1;
   const bool is_v = which & 1;
   TouchedPage x;
-  bool live = at / (2 * p.H_kv) < touched_numbers(s.T, s.B, s.page_shift, s.cu_seqlens != nullptr) &&
-              touched_page(s, at / (2 * p.H_kv), x);
+  bool live = number < touched_numbers(s.T, s.B, s.page_shift, s.cu_seqlens != nullptr) && touched_page(s, number, x);
   const int head_shift = p.d == 128 ? 3 : 2, j = tid & ((1 << head_shift) - 1);  // the same in every row
   const bool turn = !is_v && 16 * j < p.rotary_dim, split = turn && !p.interleaved;
   const int e0 = split ? 8 * j : 16 * j, e1 = split ? 8 * j + (p.rotary_dim >> 1) : 16 * j + 8;
@@ -476,7 +475,7 @@ cudaError_t launch_few(const AppendParams& p, cudaStream_t stream) {
   const long long kv_blocks = (units * 32 + kThreads - 1) / kThreads;
   const int q_shift = query_shift(p), tokens = kThreads >> q_shift;
   const long long q_blocks = p.H_q > 0 ? (p.s.T + tokens - 1) / tokens : 0;
-  if (kv_blocks + q_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (units > 0x7fffffffll || kv_blocks + q_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   const int slot = prof_begin(kKPagedAppend, stream);
   const cudaError_t e = launch_chained<paged_append_few_kernel<KP>>(
       dim3(static_cast<unsigned>(kv_blocks + q_blocks)), kThreads, 0, stream, p, static_cast<int>(kv_blocks), q_shift);

@@ -38,7 +38,7 @@ template <int D, int R, int KIND>
 struct StreamCfg {
   static constexpr bool FP8 = KIND != kBf16;
   static constexpr int kEs = FP8 ? 1 : 2;
-  static constexpr int kCtas = stream_ctas(R, D * kEs);
+  static constexpr int kCtas = stream_ctas(R, D * kEs, KIND == kE4m3Pages);
   // a tile is kept as blocks of 64 rows x (at most) 128 bytes, swizzled
   static constexpr int kRowBytes = D * kEs < 128 ? D * kEs : 128;
   static constexpr int kBlocks = D * kEs / kRowBytes;

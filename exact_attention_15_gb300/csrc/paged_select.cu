@@ -48,8 +48,7 @@ paged_bounds_kernel(const BoundsParams p) {
   grid_wait();
   grid_release();
   if (blockIdx.x == 0) check_paged_seqs(s, threadIdx.x, kBoundsThreads);
-  const long long unit = static_cast<long long>(blockIdx.x) * (kBoundsThreads / 32) + warp;
-  const long long number = unit / p.H_kv;
+  const uint32_t unit = blockIdx.x * (kBoundsThreads / 32) + warp, number = unit / static_cast<uint32_t>(p.H_kv);
   const int h = static_cast<int>(unit - number * p.H_kv);
   TouchedPage x;
   if (number >= touched_numbers(s.T, s.B, s.page_shift, s.cu_seqlens != nullptr) || !touched_page(s, number, x)) return;
@@ -123,7 +122,7 @@ template <int D, int KIND>
 cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
   const long long units = touched_numbers(p.s.T, p.s.B, p.s.page_shift, p.s.cu_seqlens != nullptr) * p.H_kv;
   const long long blocks = (units + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (units > 0x7fffffffll) return cudaErrorInvalidValue;
   return launch_chained<paged_bounds_kernel<D, KIND>>(dim3(static_cast<unsigned>(blocks)), kBoundsThreads, 0, stream, p);
 }
 
@@ -274,8 +273,7 @@ paged_select_kernel(const SelectParams p) {
   const PagedSeqs& s = p.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = 1 << p.cluster_shift, rank = blockIdx.x & (ctas - 1);
-  const long long item = blockIdx.x >> p.cluster_shift;
-  const int t = static_cast<int>(item / p.H_kv), h = static_cast<int>(item % p.H_kv);
+  const int item = static_cast<int>(blockIdx.x >> p.cluster_shift), t = item / p.H_kv, h = item - t * p.H_kv;
   const int q_tiles = (p.group + 7) / 8;
   uint8_t* qs = smem;
   float* score = reinterpret_cast<float*>(qs + q_tiles * 8 * kStride);
@@ -325,7 +323,7 @@ paged_select_kernel(const SelectParams p) {
   }
   const int len = max(0, kv_len(s, b) - span.len + (t - span.start) + 1);
   const int pages = (len + (1 << s.page_shift) - 1) >> s.page_shift;
-  int* out = p.pages + item * p.count;
+  int* out = p.pages + static_cast<size_t>(item) * p.count;
   if (h == 0 && rank == 0 && tid == 0)
     p.lens[t] = len - (max(0, pages - p.count) << s.page_shift);
   if (pages <= p.count) {  // all of them
