@@ -31,8 +31,8 @@
 // A cache with a power of two for each page: K is widened to bf16 instead, so that the queries
 // are taken as they are (the rows scaled for fp16 cost a kernel of 50 us for those prompts), and the
 // producer keeps the scales of the 16-key groups of a tile in shared memory for the softmax
-// (softmax_row_max_pages). 501 us; without the conversion to bf16 496, without the groups'
-// scales 36 less.
+// (softmax_row_max_pages). 495 us for the prompts; the conversion of K to bf16 costs nothing, the groups'
+// scales about 30, the rest of the widening 70.
 //
 // With many work tiles the CTAs claim them one by one. With few, what the last
 // wave leaves idle costs more: every CTA takes the same number of whole tiles, and
@@ -317,8 +317,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   grid_wait();
 
   // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; e4m3: 256 x 72 (warps 0-3
-  // and 12-15) + 256 x 184 = 512 x 128 (8 prompts over pages with scales 501 us; with 64 and 192, or
-  // 80 and 176, which spill more, 517 and 513).
+  // and 12-15) + 256 x 184 = 512 x 128 (8 prompts over pages with scales 501 us; with 64 and 192
+  // 517, with 80 and 176 513).
   if (warp < 4 || warp >= 12) {
     regs_dec<E4M3 ? 72 : 88>();
     if (warp == 0) {
@@ -616,12 +616,16 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars->raw_empty[rs]));
               }
+              if (!keep) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+              }
               const uint32_t to = dst + blk * Cfg::kBlockBytes;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const uint32_t a = keep ? w[c][2 * h] : 0u, b = keep ? w[c][2 * h + 1] : 0u;
+                  const uint32_t a = w[c][2 * h], b = w[c][2 * h + 1];
                   uint32_t y[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b),
                                    e4m3x2_to_f16x2(b >> 16)};
                   if (PAGES && !(it & 1)) {
