@@ -8,7 +8,7 @@ import math
 
 import torch
 
-from paged_common import E4M3_MAX, as_int
+from paged_common import BF16, E4M3_MAX, as_int, attention
 
 E8M0 = torch.float8_e8m0fnu
 NAN8 = 0x7F
@@ -60,6 +60,30 @@ class Pages:
         x, e = getattr(self, name), getattr(self, name + "_exp")
         ids = torch.tensor(self.ids[b] or [0], device="cuda")
         return values_of(x[ids], e[ids]).transpose(1, 2).reshape(-1, self.H_kv, self.d)[:self.lens[b]]
+
+    def attention(self, q, b, scale, last):
+        """paged_common.attention over sequence b, its sum of w_j |v_j| with what the weights' fp16 adds.
+
+        The kernels hold p_j = w_j 2^ev_j, the weight of the stored value c_j, as fp16 at 2^7 times
+        p_j / 2^m or more, m being the largest log2 p so far (less 8 at most, which only raises the
+        factor). fp16 rounds to 11 bits, which 2^-12 of |w_j v_j| in assert_attention's bound covers, but
+        not below 2^-14: there it moves by half a step of 2^-24, 2^-25. That is 2^-32 of the largest p
+        (a later and larger m scales what was summed down, the error with it), so o moves by up to
+        2^-32 max_i p_i sum_j |c_j| more. It counts where the c of the largest p is 0 in a column and all the
+        other p lie 22 bits and more below."""
+        k, v = self.sequence("k", b), self.sequence("v", b)
+        o, o_abs, lse = attention(q, k, v, scale, last)
+        g, n = q.shape[1] // self.H_kv, k.shape[0]
+        if n == 0:
+            return o, o_abs, lse
+        ids = torch.tensor(self.ids[b], device="cuda")
+        ev = (self.v_exp[ids].double() - 127).repeat_interleave(self.page, 0)[:n].t()  # [H_kv, n]
+        stored = torch.ldexp(v, -ev.t()[..., None]).abs().sum(0)                         # [H_kv, d]
+        s = q.double().transpose(0, 1) @ k.repeat_interleave(g, 1).permute(1, 2, 0) * scale
+        s = s.masked_fill(torch.arange(n, device="cuda")[None] >= last[:, None], -math.inf)
+        p = (s + ev.repeat_interleave(g, 0)[:, None] * math.log(2)).amax(-1) - lse       # log p, [H_q, rows]
+        most = torch.exp(p.nan_to_num(nan=-math.inf)).t()                               # (no key seen: 0)
+        return o, o_abs + 2.0 ** -32 * most[..., None] * stored.repeat_interleave(g, 0) / (BF16 + 2.0 ** -12), lse
 
 
 def exponent(most):

@@ -47,8 +47,7 @@ def test_decode(lens, H_kv, group, d, page, exps):
     q = torch.randn(len(lens), H_kv * group, d, device="cuda", dtype=torch.bfloat16)
     o, lse = _binding().paged_decode(c.handle(), q, c.table, c.kv_lens)
     for b, n in enumerate(lens):
-        want, want_abs, want_lse = attention(q[b:b + 1], c.sequence("k", b), c.sequence("v", b), 1 / math.sqrt(d),
-                                             torch.tensor([n], device="cuda"))
+        want, want_abs, want_lse = c.attention(q[b:b + 1], b, 1 / math.sqrt(d), torch.tensor([n], device="cuda"))
         assert_attention(o[b:b + 1], lse[b][:, None], want, want_abs, want_lse, (b, n))
     _ok()
 
@@ -61,8 +60,7 @@ def test_decode_dealt_out(d, page, group):
     q = torch.randn(4, 2 * group, d, device="cuda", dtype=torch.bfloat16)
     o, lse = _binding().paged_decode(c.handle(), q, c.table, c.kv_lens)
     for b, n in enumerate(lens):
-        want, want_abs, want_lse = attention(q[b:b + 1], c.sequence("k", b), c.sequence("v", b), 1 / math.sqrt(d),
-                                             torch.tensor([n], device="cuda"))
+        want, want_abs, want_lse = c.attention(q[b:b + 1], b, 1 / math.sqrt(d), torch.tensor([n], device="cuda"))
         assert_attention(o[b:b + 1], lse[b][:, None], want, want_abs, want_lse, (b, n))
     again = _binding().paged_decode(c.handle(), q, c.table, c.kv_lens)
     assert torch.equal(as_int(again[0]), as_int(o)) and torch.equal(again[1], lse)
@@ -90,7 +88,7 @@ def test_chunks(new, ctx, H_kv, group, d, page, exps, causal):
         last = torch.full((n,), lens[b], device="cuda")
         if causal:
             last = last - n + 1 + torch.arange(n, device="cuda")
-        want, want_abs, want_lse = attention(q[t0:t0 + n], c.sequence("k", b), c.sequence("v", b), 1 / math.sqrt(d), last)
+        want, want_abs, want_lse = c.attention(q[t0:t0 + n], b, 1 / math.sqrt(d), last)
         assert_attention(out[t0:t0 + n], lse[:, t0:t0 + n], want, want_abs, want_lse, b)
         t0 += n
     assert bool((out[T:] == 7).all()) and bool((lse[:, T:] == 7).all())
