@@ -478,8 +478,9 @@ paged_select_kernel(const SelectParams p) {
 
   // ---- the interval [lo, hi] of the last score to be chosen
   const float size = __uint_as_float(sh.l1) * __uint_as_float(sh.k_most);  // of the products' sums at most
-  // every product is zero; else sums outside these bounds are taken in floating point alone
-  const bool zero = sh.l1 == 0 || sh.k_most == 0;
+  // every product is zero (none of 0 and an infinity or a NaN, which makes `size` NaN); else sums outside
+  // these bounds are taken in floating point alone
+  const bool zero = (sh.l1 == 0 || sh.k_most == 0) && size == 0.0f;
   const bool finite = zero || (size < kLargest && size > kSmallest);
   const float eps = size * kSumError;
   float lo = unordered(~sh.least), hi = unordered(sh.most);

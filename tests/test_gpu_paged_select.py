@@ -246,6 +246,17 @@ def test_select_of_zero_queries():
     _check(c, q, None, 30, 0, 1)
 
 
+@pytest.mark.parametrize("bound", [math.nan, math.inf])
+def test_select_of_zero_queries_and_infinite_bounds(bound):
+    """Zero times an infinity is NaN, and above all."""
+    def make(c):
+        c.bounds[c.ids[0][17], :, 1, 5] = bound
+    c = Boxes([5000], 2, 128, 16, make=make)
+    q = torch.zeros(1, 8, 128, device="cuda", dtype=torch.bfloat16)
+    pages = _check(c, q, None, 30, 0, 1)
+    assert bool((pages == c.ids[0][17]).any(-1).all())
+
+
 def test_select_many_equal_and_a_border_inside():
     """More than 512 pages at the border, equal in groups: ranked by digits."""
     def make(c):
