@@ -40,7 +40,7 @@ static lists_fn c_lists;
 static bounds_fn c_bounds;
 static select_fn c_select;
 /* from torch */
-static PyObject *t_bf16, *t_f32, *t_f64, *t_i32, *t_u8, *f_empty, *f_empty_like, *f_device, *f_stream, *o_contiguous;
+static PyObject *t_bf16, *t_f32, *t_f64, *t_i32, *t_u8, *f_empty, *f_zeros, *f_empty_like, *f_device, *f_stream, *o_contiguous;
 /* names */
 static PyObject *n_dtype, *n_shape, *n_get_device, *n_is_contiguous, *n_stride, *n_data_ptr;
 static PyObject *kw_dtype_device, *kw_memory_format;
@@ -160,9 +160,12 @@ static PyObject* not_taken(void) {
   Py_RETURN_NOTIMPLEMENTED;
 }
 
-static PyObject* new_tensor(PyObject* shape, PyObject* dtype, PyObject* device) {
+static PyObject* made(PyObject* by, PyObject* shape, PyObject* dtype, PyObject* device) {
   PyObject* a[3] = {shape, dtype, device};
-  return shape ? PyObject_Vectorcall(f_empty, a, 1, kw_dtype_device) : NULL;
+  return shape ? PyObject_Vectorcall(by, a, 1, kw_dtype_device) : NULL;
+}
+static PyObject* new_tensor(PyObject* shape, PyObject* dtype, PyObject* device) {
+  return made(f_empty, shape, dtype, device);
 }
 
 static int scale_of(PyObject* x, long long d, float* scale) {
@@ -383,7 +386,8 @@ static PyObject* select_pages(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   PyObject* shape = Py_BuildValue("(LiL)", q.size[0], c->H_kv, count);
   PyObject* rows = Py_BuildValue("(L)", q.size[0]);
   PyObject* pages = new_tensor(shape, t_i32, a[2]);
-  PyObject* lens = new_tensor(rows, t_i32, a[2]);
+  /* (rows behind the last sequence are not written: no keys for the attention that takes them) */
+  PyObject* lens = made(s.cu ? f_zeros : f_empty, rows, t_i32, a[2]);
   Py_XDECREF(shape);
   Py_XDECREF(rows);
   PyObject* both[2] = {pages, lens};
@@ -429,7 +433,7 @@ static PyObject* setup(PyObject* self, PyObject* args) {
   if (!(t_bf16 = PyObject_GetAttrString(torch, "bfloat16")) || !(t_f32 = PyObject_GetAttrString(torch, "float32")) ||
       !(t_f64 = PyObject_GetAttrString(torch, "float64")) || !(t_i32 = PyObject_GetAttrString(torch, "int32")) ||
       !(t_u8 = PyObject_GetAttrString(torch, "uint8")) || !(f_empty = PyObject_GetAttrString(torch, "empty")) ||
-      !(f_empty_like = PyObject_GetAttrString(torch, "empty_like")) ||
+      !(f_zeros = PyObject_GetAttrString(torch, "zeros")) || !(f_empty_like = PyObject_GetAttrString(torch, "empty_like")) ||
       !(o_contiguous = PyObject_GetAttrString(torch, "contiguous_format")) ||
       !(f_device = PyObject_GetAttrString(cuda, "current_device")) ||
       !(f_stream = PyObject_GetAttrString(low, "_cuda_getCurrentRawStream")))

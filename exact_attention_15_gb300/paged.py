@@ -367,7 +367,8 @@ def paged_select(cache, q, bounds, page_table, kv_lens, count, cu_seqlens=None, 
     q . k over the KV head's query heads. q [T, H_q, d] bf16 (turned), bounds as kept by
     paged_bounds; kv_lens and cu_seqlens as in paged_append (None: one token per sequence).
     Returns (pages [T, H_kv, count] int32, -1 behind the last one, lens [T] int32), a page table
-    and lengths for paged_decode."""
+    and lengths for paged_decode. Rows of tokens behind the last sequence are not written, but
+    lens that the call allocates are 0 there, so that paged_decode gives 0 and -inf for them."""
     if pages is None and lens is None:
         r = cache._calls.select(cache._ref, cache._index, cache.device, q, bounds, page_table, kv_lens, count, cu_seqlens,
                                 keep_first, keep_last)
@@ -389,7 +390,7 @@ def paged_select(cache, q, bounds, page_table, kv_lens, count, cu_seqlens=None, 
     else:
         _check_tensor("pages", pages, (T, cache.H_kv, count), _i32, cache.device)
     if lens is None:
-        lens = _empty((T,), dtype=_i32, device=cache.device)
+        lens = (_empty if cu_seqlens is None else torch.zeros)((T,), dtype=_i32, device=cache.device)
     else:
         _check_tensor("lens", lens, (T,), _i32, cache.device)
     status = _call(cache._index, cache._lib.attn_paged_select, cache._ref, q.data_ptr(), bounds.data_ptr(),

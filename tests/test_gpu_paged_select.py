@@ -257,6 +257,26 @@ def test_select_of_zero_queries_and_infinite_bounds(bound):
     assert bool((pages == c.ids[0][17]).any(-1).all())
 
 
+@pytest.mark.parametrize("explicit", [False, True])
+def test_attention_of_padding_tokens(explicit):
+    """Tokens behind the last sequence: a list that the call allocates holds no keys."""
+    c = Boxes([700, 300], 2, 64, 16)
+    q = torch.randn(40, 4, 64, device="cuda", dtype=torch.bfloat16)
+    cache = c.handle
+    cache.k.normal_()
+    for _ in range(3):   # what the allocator hands out again
+        x = [torch.full((40,), 1 << 28, device="cuda", dtype=torch.int32) for _ in range(8)]
+        del x
+        given = dict(lens=torch.zeros(40, device="cuda", dtype=torch.int32)) if explicit else {}
+        pages, lens = _binding().paged_select(cache, q, c.bounds, c.table, c.kv_lens, 9,
+                                              cu_seqlens=torch.tensor([0, 20, 30], device="cuda", dtype=torch.int32), **given)
+        assert bool((lens[30:] == 0).all()) and bool((lens[:30] > 0).all())
+        o, lse = _binding().paged_decode(cache, q, pages, lens)
+        assert bool((o[30:] == 0).all()) and bool((lse[30:] == -math.inf).all())
+        assert bool(torch.isfinite(o[:30].float()).all())
+    _ok()
+
+
 def test_select_many_equal_and_a_border_inside():
     """More than 512 pages at the border, equal in groups: ranked by digits."""
     def make(c):
