@@ -88,64 +88,6 @@ __device__ __forceinline__ void softmax_row_exp(const float (&s)[128], float c, 
   }
 }
 
-// Keys and values that have a power of two each, one for 16 keys: entry g of `of_page` holds
-// 2^ek, ev and 2^-ev for the stored keys and values of group g. The scores are
-// x = s c 2^ek + ev, so that p = 2^(x - m) is the weight of the stored value, and m bounds it
-// however the groups differ; the sum takes 2^ev out again. As with one scale (c > 0) no
-// score is scaled before the exponential: a group's largest is, 16 for one.
-__device__ __forceinline__ float page_factor(float c, float k_up) {
-  // (a row of tiny queries can bring it to 0 or, with large ones, to infinity, and -inf of a
-  // masked score times 0 is NaN, as is a score of 0 times infinity)
-  return fminf(fmaxf(c * k_up, 1.17549435e-38f), 3.402823466e38f);
-}
-__device__ __forceinline__ float softmax_row_max_pages(float (&s)[128], float c, const float4* of_page, float& m_used,
-                                                       float& l, int kv0, int Lk, bool need_mask, bool& rescale_warp,
-                                                       float& factor) {
-  if (need_mask) {
-#pragma unroll
-    for (int i = 0; i < 128; ++i) s[i] = kv0 + i < Lk ? s[i] : -INFINITY;
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    float mx = fmaxf(s[16 * g], s[16 * g + 1]);
-#pragma unroll
-    for (int i = 2; i < 16; i += 2) mx = max3f(mx, s[16 * g + i], s[16 * g + i + 1]);
-    const float2 x = *reinterpret_cast<const float2*>(of_page + g);
-    m = fmaxf(m, fmaf(mx, page_factor(c, x.x), x.y));
-  }
-  const float m_new = fmaxf(m_used, m);
-  const bool need = (m_new - m_used) > kTau;  // false when both are -inf (NaN compare)
-  rescale_warp = __any_sync(0xffffffffu, need);
-  factor = 1.0f;
-  if (rescale_warp) {
-    if (m_new > m_used) {
-      factor = ex2_approx(m_used - m_new);  // 0 when m_used = -inf
-      m_used = m_new;
-      l *= factor;
-    }
-  }
-  return (m_used == -INFINITY) ? 0.0f : m_used;
-}
-// The fp16 P row of such scores, and its sum.
-__device__ __forceinline__ void softmax_row_exp_pages(const float (&s)[128], float c, float mb, const float4* of_page,
-                                                      uint32_t (&pk)[64], uint64_t (&sum2)[2]) {
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    const float4 x = of_page[g];
-    const float a = page_factor(c, x.x), b = x.y - mb;
-    const uint64_t a2 = f32x2(a, a), b2 = f32x2(b, b), d2 = f32x2(x.z, x.z);
-#pragma unroll
-    for (int i = 8 * g; i < 8 * g + 8; ++i) {
-      float x0, x1;
-      f32x2_split(fma_f32x2(f32x2(s[2 * i], s[2 * i + 1]), a2, b2), x0, x1);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      sum2[i & 1] = fma_f32x2(f32x2(p0, p1), d2, sum2[i & 1]);
-      pk[i] = pack_f16x2(p0, p1);
-    }
-  }
-}
-
 // Row sum of the two packed pair accumulators.
 __device__ __forceinline__ float softmax_row_sum(const uint64_t (&sum2)[2]) {
   float a, b, c, d;

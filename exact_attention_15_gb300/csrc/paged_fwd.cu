@@ -28,11 +28,10 @@
 // with K_(j + 1) waited for only after P V(j) has been issued, since its place in the ring is
 // that of V_(j - 1), 498. A fourth place for half the small ring and half the staging: 513.
 //
-// A cache with a power of two for each page: K is widened to bf16 instead, so that the queries
-// are taken as they are (the rows scaled for fp16 cost a kernel of 50 us for those prompts), and the
-// producer keeps the scales of the 16-key groups of a tile in shared memory for the softmax
-// (softmax_row_max_pages). 495 us for the prompts; the conversion of K to bf16 costs nothing, the groups'
-// scales about 30, the rest of the widening 70.
+// A cache with a power of two for each page: both are widened to bf16 instead, which holds every
+// value with its page's scale exactly, so that the rest is as over a bf16 cache, queries as they are and
+// weights of 8 bits among it. With K widened to bf16, V to fp16 and the scales applied to scores and
+// weights 16 at a time the prompts took 495 us (now 454): eight scales for a row and tile in the softmax.
 //
 // With many work tiles the CTAs claim them one by one. With few, what the last
 // wave leaves idle costs more: every CTA takes the same number of whole tiles, and
@@ -49,16 +48,14 @@ namespace attn {
 
 namespace {
 
-// Key tiles whose pages' scales are kept. The producer writes those of tile j when it has a place
-// for the first half of K_j in the small ring; the halves before it there have been widened then,
-// K_(j - 2) or a later tile among them, into places of the K / V ring that V_(j - 6) or a later
-// tile had left. V_i leaves its place when its products are done, which come after both softmax
-// warpgroups have finished with tile i: of eight places none is overwritten that is still read.
-constexpr int kScaleSlots = 8;
+// Key tiles whose pages' exponents are kept. The producer writes those of tile j when it has a
+// place for the first half of K_j in the small ring, which holds one tile or two: V_(j - 3) and
+// all before it have been read by the widening warps then.
+constexpr int kExpSlots = 4;
 
 template <int D, int KIND>
 struct PagedFwdCfg {
-  static constexpr bool E4M3 = KIND != kBf16;
+  static constexpr bool E4M3 = KIND != kBf16, F16 = KIND == kE4m3;
   static constexpr int kBlocks = D / 64;                // 64-column blocks of a tile
   static constexpr int kBlockBytes = kTileM * 64 * 2;   // 16 KB
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
@@ -71,9 +68,9 @@ struct PagedFwdCfg {
   static constexpr int kKVOff = 2 * kTileBytes;
   static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + (E4M3 ? kRawStages * kRawBytes : 0);
-  // a scale for each page: what the softmax needs of the 16-key groups of a key tile
-  static constexpr int kScaleOff = kBarOff + 1024;
-  static constexpr int kEpiOff = kScaleOff + (KIND == kE4m3Pages ? kScaleSlots * 8 * 16 : 0);  // one staging block per warpgroup
+  // a scale for each page: exponents, plus 127, of K and V for the 16-key groups of a key tile
+  static constexpr int kExpOff = kBarOff + 1024 - kExpSlots * 8 * 2;
+  static constexpr int kEpiOff = kBarOff + 1024;        // one staging block per warpgroup
   static constexpr int kSmemBytes = kEpiOff + 2 * kBlockBytes + 1024;
   static constexpr uint32_t kColS = 2 * D;
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -272,13 +269,13 @@ __global__ void __launch_bounds__(fwd_threads(KIND), 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedFwdParams p) {
   using Cfg = PagedFwdCfg<D, KIND>;
-  constexpr bool E4M3 = Cfg::E4M3, PAGES = KIND == kE4m3Pages;
+  constexpr bool E4M3 = Cfg::E4M3, F16 = Cfg::F16, PAGES = KIND == kE4m3Pages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   PagedBars* bars = reinterpret_cast<PagedBars*>(smem + Cfg::kBarOff);
-  static_assert(sizeof(PagedBars) <= 1024, "barrier block");
-  float4* page_scales = reinterpret_cast<float4*>(smem + Cfg::kScaleOff);  // [kScaleSlots][8]
+  static_assert(Cfg::kBarOff + sizeof(PagedBars) <= Cfg::kExpOff, "barrier block");
+  uint8_t* exponents = smem + Cfg::kExpOff;  // [kExpSlots][8][K, V]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -316,11 +313,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const long long lim = p.wait_limit;
   grid_wait();
 
-  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; e4m3: 256 x 72 (warps 0-3
-  // and 12-15) + 256 x 184 = 512 x 128 (8 prompts over pages with scales 501 us; with 64 and 192
-  // 517, with 80 and 176 513).
+  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; e4m3: 256 x 88 (warps 0-3
+  // and 12-15) + 256 x 168 = 512 x 128 (8 prompts over pages with scales 454 us; with 80 and 176
+  // 455, with 72 and 184 465, with 64 and 192 485).
   if (warp < 4 || warp >= 12) {
-    regs_dec<E4M3 ? 72 : 88>();
+    regs_dec<88>();
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       // Lane (page j of a key tile, column block) issues one box per tile.
@@ -406,10 +403,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!mbar_wait_warp(smem_addr(&bars->raw_empty[stage]), (round & 1) ^ 1, lim)) { ok = false; break; }
                 const uint32_t fbar = smem_addr(&bars->raw_full[stage]);
                 if (PAGES && kv == 0 && half == 0) {
-                  const int ek = exponent_of(ex_here.x), ev = exponent_of(ex_here.y);
                   if (lane < 8)
-                    page_scales[((ld >> 2) % kScaleSlots) * 8 + lane] =
-                        make_float4(power_of_two(ek), static_cast<float>(ev), power_of_two(-ev), 0.0f);
+                    *reinterpret_cast<uchar2*>(exponents + ((ld >> 2) % kExpSlots * 8 + lane) * 2) =
+                        make_uchar2(exponent_of(ex_here.x) + 127, exponent_of(ex_here.y) + 127);
                   __syncwarp();
                 }
                 if (lane == 0)
@@ -444,8 +440,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const bool leader = elect_one_sync();
-      constexpr uint32_t kIdS = E4M3 && !PAGES ? make_idesc_f16(128, 128, 0, 0) : make_idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t kIdPV = E4M3 ? make_idesc_f16(128, D, 0, 1) : make_idesc_bf16(128, D, 0, 1);
+      constexpr uint32_t kIdS = F16 ? make_idesc_f16(128, 128, 0, 0) : make_idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t kIdPV = F16 ? make_idesc_f16(128, D, 0, 1) : make_idesc_bf16(128, D, 0, 1);
       const uint32_t kv_base = smem_addr(smem + Cfg::kKVOff);
       const uint64_t q_desc = make_sdesc_sw128(smem_addr(smem), 16, 1024);  // K-major
       const uint64_t k_desc = make_sdesc_sw128(kv_base, 16, 1024);          // K-major
@@ -603,6 +599,9 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const uint32_t from = src + in * D;
             const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
             const bool keep = row < live;
+            uint32_t up = 0;  // 2^e twice
+            if constexpr (PAGES)
+              up = exponents[((ld >> 1) % kExpSlots * 8 + (row >> 4)) * 2 + (it & 1)] * 0x00800080u;
             // 64 columns at a time, all their loads first: one latency for them
 #pragma unroll 1
             for (int blk = 0; blk < Cfg::kBlocks; ++blk) {
@@ -628,11 +627,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                   const uint32_t a = w[c][2 * h], b = w[c][2 * h + 1];
                   uint32_t y[4] = {e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b),
                                    e4m3x2_to_f16x2(b >> 16)};
-                  if (PAGES && !(it & 1)) {
+                  if constexpr (PAGES) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                       const float2 f = f16x2_to_f32(y[e]);
-                      y[e] = pack_bf16x2(f.x, f.y);
+                      y[e] = mul_bf16x2(pack_bf16x2(f.x, f.y), up);
                     }
                   }
                   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + sw128_offset(row, 2 * c + h)),
@@ -650,7 +649,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     __syncwarp();
   } else {
-    regs_inc<E4M3 ? 184 : 208>();
+    regs_inc<E4M3 ? 168 : 208>();
     // ---------------------------------------------------------- softmax + epilogue
     const int i = (warp - 4) >> 2;      // query tile of this warpgroup
     const int r = tid - 128 * (1 + i);  // row of the tile == TMEM lane
@@ -658,14 +657,11 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t col_s = Cfg::kColS + i * 128, col_o = i * D;
     const int tok_r = r / p.group, head_r = r - tok_r * p.group;
     int sw = 0, pvw = 0;  // s_full and pv_done waits so far
-    constexpr float lift = E4M3 ? kLift : 0.0f;
+    constexpr float lift = F16 ? kLift : 0.0f;
     bool ok = true;
-    uint32_t tiles_before = 0;  // key tiles of the work tiles before this one
     for (int k = 0; ok; ++k) {
       PagedTile t;
       if (!take_tile(bars, k, t, lim, ok)) break;
-      const uint32_t tile0 = tiles_before;
-      tiles_before += max(t.n[0], t.n[1]);
       const int my_n = i ? t.n[1] : t.n[0];
       const int q0 = t.q0 + i * p.tok_tile;           // first token of this query tile
       const int see0 = t.len - t.n_new + q0;          // the last key that it sees (causal)
@@ -673,11 +669,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // keys that this row sees: one comparison per score covers both masks
       const int see = p.causal ? min(t.len, see0 + tok_r + 1) : t.len;
       float c = p.scale_log2;
-      if constexpr (E4M3) c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
+      if constexpr (F16) c *= p.k_scale ? __ldg(p.k_scale + t.h) : 1.0f;
       // the same in every lane: softmax_row_max votes within either branch
       const bool pos = c > 0.0f;
-      const float c_pages = fabsf(c);
-      if constexpr (E4M3 && !PAGES) {
+      if constexpr (F16) {
         if (tok_r < p.tok_tile && tok < t.n_new)
           c *= p.q_up[(static_cast<size_t>(t.row0) + tok) * p.H_q + t.h * p.group + head_r];
         // A row of tiny queries can bring c to 0, and -inf of a masked score times 0 is NaN:
@@ -705,23 +700,13 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t pk[64];
         bool rescale_warp;
         float factor;
-        const float4* of_page = page_scales + ((tile0 + j) % kScaleSlots) * 8;
-        if constexpr (PAGES) {
-          if (!pos) {  // (a scale of 0 or below: the scores take its sign first)
-#pragma unroll
-            for (int e = 0; e < 128; ++e) s[e] = c == 0.0f ? 0.0f : -s[e];
-          }
-        }
-        const float mb = PAGES ? softmax_row_max_pages(s, c_pages, of_page, m_used, l, kv0, see, need_mask,
-                                                       rescale_warp, factor)
-                         : pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
-                                                       rescale_warp, factor)
-                               : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
-                                                        rescale_warp, factor);
+        const float mb = pos ? softmax_row_max<true>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                     rescale_warp, factor)
+                             : softmax_row_max<false>(s, c, m_used, l, kv0, 0, see, need_mask, 0,
+                                                      rescale_warp, factor);
         uint64_t sum2[2] = {0ull, 0ull};
-        if constexpr (PAGES) softmax_row_exp_pages(s, c_pages, mb - lift, of_page, pk, sum2);
-        else if (pos) softmax_row_exp<0, true, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
-        else softmax_row_exp<0, false, 0, 64, E4M3>(s, c, mb - lift, need_mask, pk, sum2);
+        if (pos) softmax_row_exp<0, true, 0, 64, F16>(s, c, mb - lift, need_mask, pk, sum2);
+        else softmax_row_exp<0, false, 0, 64, F16>(s, c, mb - lift, need_mask, pk, sum2);
         if (rescale_warp && j > 0 && __any_sync(0xffffffffu, factor != 1.0f)) {
           // O is complete: the commit that signalled S_j came after PV_{j-1}
 #pragma unroll
@@ -768,7 +753,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
         for (int e = 0; e < D; ++e) ov[e] = 0u;
       }
-      const float v_scale = E4M3 && p.v_scale ? __ldg(p.v_scale + t.h) : 1.0f;
+      const float v_scale = F16 && p.v_scale ? __ldg(p.v_scale + t.h) : 1.0f;
       uint32_t buf_off = Cfg::kEpiOff + i * Cfg::kBlockBytes;
       asm volatile("" : "+r"(buf_off));  // computed here, not kept across the key loop
       uint8_t* buf = smem + buf_off;

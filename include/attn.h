@@ -263,8 +263,9 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  * device arrays of num_pages * H_kv bytes (the E8M0 format of scales): an x of page p and
  * head h stands for x * 2^(k_exp[p * H_kv + h] - 127). attn_paged_append finds them and writes
  * exponents from -64 to 24; others count as the nearest of these. The scale arrays are not
- * read. The attention calls hold the weight of a stored value (what softmax gives its key, times its
- * page's power of two) to 11 bits, and those below 2^-21 of a row's largest to 2^-32 of that.
+ * read. For few tokens attention holds the weight of a stored value (what softmax gives its key,
+ * times its page's power of two) to 11 bits, and those below 2^-21 of a row's largest to 2^-32
+ * of that; for chunks, softmax's weight to 8 bits, as over a bf16 cache.
  *
  * Sequences are described by device arrays that the host does not read:
  *   kv_lens     int32 [B]: keys of each sequence, its new tokens among them

@@ -64,7 +64,7 @@ class Pages:
     def attention(self, q, b, scale, last):
         """paged_common.attention over sequence b, its sum of w_j |v_j| with what the weights' fp16 adds.
 
-        The kernels hold p_j = w_j 2^ev_j, the weight of the stored value c_j, as fp16 at 2^7 times
+        The kernel for few tokens holds p_j = w_j 2^ev_j, the weight of the stored value c_j, as fp16 at 2^7 times
         p_j / 2^m or more, m being the largest log2 p so far (less 8 at most, which only raises the
         factor). fp16 rounds to 11 bits, which 2^-12 of |w_j v_j| in assert_attention's bound covers, but
         not below 2^-14: there it moves by half a step of 2^-24, 2^-25. That is 2^-32 of the largest p
