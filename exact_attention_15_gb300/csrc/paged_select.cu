@@ -312,12 +312,16 @@ paged_select_kernel(const SelectParams p) {
   int b = t;
   SeqSpan span{t, 1};
   if (s.cu_seqlens) {
-    int lo = 0, hi = s.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(s.cu_seqlens + mid) <= t) lo = mid; else hi = mid;
+    // the last one that begins at or before it, found by each warp 32 places at a time: two
+    // dependent loads for up to 1024 sequences and not ten
+    int n = s.B;
+    for (b = 0; n > 1;) {
+      const int step = (n + 31) >> 5;
+      const bool below = lane * step < n && __ldg(s.cu_seqlens + b + lane * step) <= t;
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+      n = min(step, n - last * step);
+      b += last * step;
     }
-    b = lo;
     span = seq_span(s.cu_seqlens, b, s.T, 0);
     if (t < span.start || t >= span.start + span.len) return;  // behind the last sequence
   }
