@@ -149,7 +149,8 @@ cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
 //    the sums can be, so that they do not depend on an order (in 64-bit floating point where
 //    the inputs are no such numbers). Ties go to the lower page.
 // 4. The chosen pages are written in their order.
-constexpr int kBins = 1024;
+template <int THREADS>  // (one warp has 160 pages at most)
+constexpr int select_bins = THREADS == 32 ? 256 : 1024;
 // Up to this many pages to be ranked in 64 bits are compared pair by pair, more by digits (8
 // tokens and heads with 100 equal pages take 43 us either way, with 512 163 and 109).
 constexpr int kPairs = 64;
@@ -206,7 +207,7 @@ __host__ __device__ __forceinline__ int spread_size(int n) { return (spread(n) +
 // What a CTA shows the others of its cluster.
 template <int THREADS>
 struct SelectShared {
-  uint32_t hist[kBins];
+  uint32_t hist[select_bins<THREADS>];
   uint32_t l1, k_most;       // largest sum of a query row's magnitudes; largest magnitude of the bounds
   uint32_t least, most;      // scores, ordered (the least as its complement)
   uint32_t sure, unsure, chosen;
@@ -264,9 +265,9 @@ __device__ __forceinline__ void find_bin(SelectShared<THREADS>& sh, int cluster,
 }
 
 template <int D, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
+__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 12 : THREADS == 128 ? 5 : 2)
 paged_select_kernel(const SelectParams p) {
-  constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
+  constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32, kBins = select_bins<THREADS>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ SelectShared<THREADS> sh;
   constexpr int kStride = 4 * D + 64;  // bytes of a row of queries or bounds (the gap spreads rows over the banks)
@@ -304,9 +305,12 @@ paged_select_kernel(const SelectParams p) {
                                (static_cast<size_t>(t) * p.H_q + h * p.group + r) * (D / 2) + i * 32 + lane)
                        : 0u;
   };
-  uint32_t first_row[kPairs32];
+  constexpr int kFirst = kSelWarps < 8 ? 8 / kSelWarps : 1;  // rows of a warp among the first eight
+  uint32_t first_rows[kFirst][kPairs32];
 #pragma unroll
-  for (int i = 0; i < kPairs32; ++i) first_row[i] = query_word(warp, i);
+  for (int k = 0; k < kFirst; ++k)
+#pragma unroll
+    for (int i = 0; i < kPairs32; ++i) first_rows[k][i] = query_word(warp + k * kSelWarps, i);
 
   // ---- the token's sequence and what it sees
   int b = t;
@@ -369,12 +373,12 @@ paged_select_kernel(const SelectParams p) {
     copy(next);
     if (my_tiles > 1) next = entry_at(1);
   }
-  for (int r = warp; r < q_tiles * 8; r += kSelWarps) {
+  auto keep_row = [&](int r, const uint32_t (&row)[kPairs32]) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(qs + r * kStride);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPairs32; ++i) {
-      const uint32_t w = r == warp ? first_row[i] : query_word(r, i);
+      const uint32_t w = row[i];
       sum += fabsf(bf16lo_to_f32(w)) + fabsf(bf16hi_to_f32(w));
       dst[i * 32 + lane] = min2(w, 0u, false);
       dst[D / 2 + i * 32 + lane] = max2(w, 0u, false);
@@ -382,6 +386,14 @@ paged_select_kernel(const SelectParams p) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) atomicMax(&sh.l1, __float_as_uint(sum) & 0x7fffffffu);
+  };
+#pragma unroll
+  for (int k = 0; k < kFirst; ++k) keep_row(warp + k * kSelWarps, first_rows[k]);
+  for (int r = warp + kFirst * kSelWarps; r < q_tiles * 8; r += kSelWarps) {
+    uint32_t row[kPairs32];
+#pragma unroll
+    for (int i = 0; i < kPairs32; ++i) row[i] = query_word(r, i);
+    keep_row(r, row);
   }
   __syncthreads();
   if (ctas > 1) cluster_wait();
@@ -501,7 +513,7 @@ paged_select_kernel(const SelectParams p) {
     lo = low + bin * (range / kBins);
     hi = low + (bin + 1) * (range / kBins);
     // a bin far wider than eps (a few scores far from the rest): its own pages again
-    if (range > 64.0f * kBins * eps) {
+    if (range > 65536.0f * eps) {
       const float low2 = lo, inv2 = kBins / (range / kBins);
       auto bin2_of = [&](float x) { return max(0, min(kBins - 1, static_cast<int>((x - low2) * inv2))); };
       sync();
@@ -701,7 +713,12 @@ cudaError_t plan_select(SelectParams p, int n_sm, cudaStream_t stream) {
     ++p.cluster_shift;
   }
   const long long ctas = items * cluster;
-  const int warps = cluster > 1 ? 8 : 4;
+  // Few pages for each of many tokens and heads: a warp for each, of which twelve find place on an
+  // SM. Against four warps each, five on an SM (32 heads on 16 of 128, us): 200 tokens over 21 pages 22.2
+  // and 39.9, over 95 36.9 and 45.2, over 144 47.9 and 61.7, over 238 69.9 and 73.4, with heads of 64 60.5
+  // and 57.7; 800 tokens and heads, all at once on the SMs either way, 17.2 and 16.2, 1600 24.4 and 26.0.
+  const bool small = cluster == 1 && p.s.max_pages <= 160 && items > 10ll * n_sm;
+  const int warps = cluster > 1 ? 8 : small ? 1 : 4;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   auto bytes = [&](int share) {
     p.slice = ((p.s.max_pages + share - 1) / share + 15) & ~15;
@@ -710,6 +727,7 @@ cudaError_t plan_select(SelectParams p, int n_sm, cudaStream_t stream) {
   p.gather = cluster > 1 && p.s.max_pages <= 32 * 256 && bytes(1) <= kMost;
   const int smem = bytes(p.gather ? 1 : cluster);
   return cluster > 1 ? launch_select<D, 256>(p, cluster, ctas, smem, kMost, stream)
+         : small     ? launch_select<D, 32>(p, cluster, ctas, smem, kMost, stream)
                      : launch_select<D, 128>(p, cluster, ctas, smem, kMost, stream);
 }
 

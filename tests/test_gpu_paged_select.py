@@ -238,6 +238,25 @@ def test_select_of_special_bounds(make, n, tokens):
     _check(c, q.to(torch.bfloat16), None, 30, 1, 1)
 
 
+@pytest.mark.parametrize("make", [None, _same, _pairs, _zeros, _far, _close, _tiny, _huge, _infinite, _nan])
+@pytest.mark.parametrize("d,group,count", [(64, 3, 9), (128, 4, 70), (128, 11, 5)])
+def test_select_few_pages_for_many_tokens(make, d, group, count):
+    """More than 1520 tokens and heads behind a table of up to 160 pages."""
+    c = Boxes([1536, 1, 40, 700, 0, 1300, 1535, 160] * 26, 8, d, 16, make=make)
+    q = torch.randn(8 * 26, 8 * group, d, device="cuda", dtype=torch.bfloat16)
+    if make is _infinite:  # (no product of zero and infinity, which is NaN)
+        q = q.sign() * q.abs().clamp(min=0.1)
+    if make is _tiny:
+        q = q * 2.0 ** -50
+    _check(c, q.to(torch.bfloat16), None, count, 1, 1)
+
+
+def test_select_few_pages_for_many_tokens_of_chunks():
+    c = Boxes([900, 300, 1400, 50], 16, 64, 16)
+    q = torch.randn(127, 32, 64, device="cuda", dtype=torch.bfloat16)
+    _check(c, q, [60, 30, 30, 5], 8, 0, 2)
+
+
 def test_select_of_zero_queries():
     c = Boxes([5000], 2, 128, 16)
     q = torch.zeros(1, 8, 128, device="cuda", dtype=torch.bfloat16)
