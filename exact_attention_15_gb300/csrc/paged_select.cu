@@ -293,7 +293,9 @@ paged_select_kernel(const SelectParams p) {
     mbar_init(full, 1);
     fence_barrier_init();
   }
-  __syncwarp();
+  // The zeros stand before any warp adds to them: the queries' magnitudes (keep_row) come before the
+  // CTA's next barrier. (Here it overlaps the end of the grid before.)
+  __syncthreads();
   grid_wait();
   grid_release();
   if (blockIdx.x == 0) check_paged_seqs(s, tid, kSelThreads);
