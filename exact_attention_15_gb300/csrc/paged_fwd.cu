@@ -21,7 +21,7 @@
 //
 // Over an e4m3 cache the products run in fp16, which holds every e4m3 value exactly
 // (the instructions take no operands of two types): half tiles of 64 keys land in a
-// small ring of their own, and warps 2, 3, 12 and 13 widen a quarter each of every tile into
+// small ring of their own, and two or four warps widen an equal part each of every tile into
 // the K / V ring (and put the zeros past the end); lane 0 of warp 2 looks for work
 // between the tiles. The queries come as fp16 rows scaled by powers of two. Two widening
 // warps took 542 us for 8 prompts of 512 to 4096 (32 heads on 8, d 128; bf16: 358), four 535, and
@@ -89,9 +89,15 @@ struct __align__(16) PagedTile {
 
 constexpr int kSlots = 2;     // of the ring that hands out work tiles
 constexpr int kReaders = 10;  // producer warp, MMA warp, eight softmax warps (e4m3: and those that widen)
-constexpr int kWideners = 4;  // e4m3: warps 2, 3, 12 and 13, a quarter of the rows of a tile each
-// (16 warps where there are some that widen, so that setmaxnreg finds whole warpgroups)
-constexpr int fwd_threads(int kind) { return kind == kBf16 ? 384 : 512; }
+// e4m3: warps that widen an equal share of the rows of a tile each, 2 and 3, or 12 and 13 besides. With heads
+// of 64 and no scales to apply two keep up, and a third warpgroup would only cost the softmax its registers
+// (16 prompts of 33 to 1000 with 16 heads on 16: 72.5 us with two, 75.0 with four; 4 chunks of 700 to 1500
+// behind 4000 to 9000 with 32 heads on 8: 298 and 313). With heads of 64 over pages with scales the second
+// take 352 us with two and 313 with four; with heads of 128 and no scales 8 prompts took 364 with two, 338
+// with four.
+constexpr int wideners(int d, int kind) { return d == 128 || kind == kE4m3Pages ? 4 : 2; }
+// (16 warps where there are four that widen, so that setmaxnreg finds whole warpgroups)
+constexpr int fwd_threads(int d, int kind) { return kind != kBf16 && wideners(d, kind) == 4 ? 512 : 384; }
 
 struct PagedBars {
   uint64_t q_full, q_empty;
@@ -265,11 +271,13 @@ struct TileSource {
 };
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(fwd_threads(KIND), 1)
+__global__ void __launch_bounds__(fwd_threads(D, KIND), 1)
 paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedFwdParams p) {
   using Cfg = PagedFwdCfg<D, KIND>;
   constexpr bool E4M3 = Cfg::E4M3, F16 = Cfg::F16, PAGES = KIND == kE4m3Pages;
+  constexpr int kWideners = wideners(D, KIND);
+  constexpr bool kFour = E4M3 && kWideners == 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -313,8 +321,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const long long lim = p.wait_limit;
   grid_wait();
 
-  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; e4m3: 256 x 88 (warps 0-3
-  // and 12-15) + 256 x 168 = 512 x 128 (8 prompts over pages with scales 454 us; with 80 and 176
+  // Register split: 128 x 88 (warps 0-3) + 256 x 208 (softmax) = 384 x 168; with four widening warps 256 x 88
+  // (warps 0-3 and 12-15) + 256 x 168 = 512 x 128 (8 prompts over pages with scales 454 us; with 80 and 176
   // 455, with 72 and 184 465, with 64 and 192 485).
   if (warp < 4 || warp >= 12) {
     regs_dec<88>();
@@ -502,10 +510,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_async_shared();
             __syncwarp();
           }
-          // e4m3, whose ring has three places: not before P V, which needs no K, since K_(j + 1) takes the
-          // place of V_(j - 1)
-          bool have_k = !E4M3;
-          if (!E4M3 && next_k && !(ok = wait_full(itk))) break;
+          // where four warps widen: not before P V, which needs no K (with heads of 128 the ring has three places,
+          // and K_(j + 1) takes that of V_(j - 1))
+          bool have_k = !kFour;
+          if (have_k && next_k && !(ok = wait_full(itk))) break;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (j >= t.n[i]) continue;
@@ -562,7 +570,7 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     } else if (E4M3 && warp >= 2 && warp < 12 + kWideners - 2) {
       // -------------------------------------------------------- widening (e4m3)
-      // A quarter of every tile, a row per lane; both rings are swizzled, so neither side's
+      // A quarter or half of every tile, a row per lane; both rings are swizzled, so neither side's
       // accesses meet in a bank. Lane 0 of warp 2 publishes the next work tile when it takes one.
       const int part = warp < 4 ? warp - 2 : warp - 10, half = part * 2 / kWideners;
       const uint32_t raw0 = smem_addr(smem + Cfg::kRawOff), kv0 = smem_addr(smem + Cfg::kKVOff);
@@ -594,8 +602,10 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           // rows of V past the end become zeros
           const int live = (it & 1) ? t.len - (t.kt0 + (it >> 1)) * kTileN : kTileN;
           const uint32_t src = raw0 + rs * Cfg::kRawBytes, dst = kv0 + ks * Cfg::kTileBytes;
-          {
-            const int row = part * (kTileN / kWideners) + lane, in = row & (Cfg::kHalf - 1);
+          constexpr int kRows = kTileN / kWideners;
+#pragma unroll 1
+          for (int r0 = 0; r0 < kRows; r0 += 32) {  // (once where four warps widen)
+            const int row = part * kRows + r0 + lane, in = row & (Cfg::kHalf - 1);
             const uint32_t from = src + in * D;
             const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
             const bool keep = row < live;
@@ -611,7 +621,8 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
                              : "r"(from + (((blk * 4 + c) ^ sw) << 4)) : "memory");
-              if (blk == Cfg::kBlocks - 1) {
+              // (where two warps widen the place goes back with the tile: 298 us of the chunks above, here 302)
+              if (kFour && blk == Cfg::kBlocks - 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars->raw_empty[rs]));
               }
@@ -642,14 +653,17 @@ paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bars->kv_full[ks]));
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&bars->kv_full[ks]));
+            if (!kFour) mbar_arrive(smem_addr(&bars->raw_empty[rs]));
+          }
         }
       }
       if (!ok && lane == 0) record_error(p.s.err, kErrTimeout);
     }
     __syncwarp();
   } else {
-    regs_inc<E4M3 ? 168 : 208>();
+    regs_inc<kFour ? 168 : 208>();
     // ---------------------------------------------------------- softmax + epilogue
     const int i = (warp - 4) >> 2;      // query tile of this warpgroup
     const int r = tid - 128 * (1 + i);  // row of the tile == TMEM lane
@@ -1130,7 +1144,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   prof_end(slot, stream);
   if (e != cudaSuccess) return e;
   slot = prof_begin(kKPagedFwd, stream);
-  e = launch_chained<paged_fwd_kernel<D, KIND>>(dim3(p.grid), fwd_threads(KIND), PagedFwdCfg<D, KIND>::kSmemBytes, stream, tq, tk,
+  e = launch_chained<paged_fwd_kernel<D, KIND>>(dim3(p.grid), fwd_threads(D, KIND), PagedFwdCfg<D, KIND>::kSmemBytes, stream, tq, tk,
                      tv, p);
   prof_end(slot, stream);
   if (e != cudaSuccess || !p.split) return e;
