@@ -31,11 +31,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Eight values times `scale` (a power of two) as e4m3.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float scale) {
-  return make_uint2(pack_e4m3x2(x[0] * scale, x[1] * scale) | pack_e4m3x2(x[2] * scale, x[3] * scale) << 16,
-                    pack_e4m3x2(x[4] * scale, x[5] * scale) | pack_e4m3x2(x[6] * scale, x[7] * scale) << 16);
-}
 // 16 elements of a head: two runs of 8.
 struct Part {
   uint4 a, b;

@@ -78,7 +78,7 @@ __device__ __forceinline__ Part load_part(const AppendParams& p, const Place& x,
 // head; a CTA takes kAppendThreads / W tokens: with few heads a CTA per token would
 // leave most threads idle.
 constexpr int kAhead = 3;
-template <int W, bool PAGES>
+template <int W>
 __global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(const AppendParams p) {
   __shared__ float2 shared_cs[kAppendThreads / W][64];
@@ -151,12 +151,7 @@ paged_append_kernel(const AppendParams p) {
       const bool is_v = x.kind == 2;
       const size_t at = static_cast<size_t>(page) * (is_v ? p.v_page : p.k_page) +
                         ((static_cast<size_t>(x.h) << s.page_shift) + row) * p.d;
-      if constexpr (PAGES) {
-        const float scale = power_of_two(-page_exponent(is_v ? p.v_exp : p.k_exp, page, p.H_kv, x.h));
-        uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
-        *reinterpret_cast<uint2*>(dst + x.e0) = encode8(x0, scale);
-        *reinterpret_cast<uint2*>(dst + x.e1) = encode8(x1, scale);
-      } else if (p.e4m3) {
+      if (p.e4m3) {
         const float* sc = is_v ? p.v_scale : p.k_scale;
         const float scale = sc ? __ldg(sc + x.h) : 1.0f, inverse = __frcp_rn(scale);
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
@@ -174,9 +169,7 @@ paged_append_kernel(const AppendParams p) {
 template <int W>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   constexpr int kTokens = kAppendThreads / W;
-  const dim3 grid((p.s.T + kTokens - 1) / kTokens);
-  return p.k_exp ? launch_chained<paged_append_kernel<W, true>>(grid, kAppendThreads, 0, stream, p)
-                 : launch_chained<paged_append_kernel<W, false>>(grid, kAppendThreads, 0, stream, p);
+  return launch_chained<paged_append_kernel<W>>(dim3((p.s.T + kTokens - 1) / kTokens), kAppendThreads, 0, stream, p);
 }
 
 }  // namespace

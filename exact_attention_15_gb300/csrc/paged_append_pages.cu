@@ -55,6 +55,11 @@ __device__ __forceinline__ int exponent_for(float most) {
   const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
   return max(kMinExp, min(kMaxExp, e));
 }
+// Eight values times `scale` (a power of two) as e4m3.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float scale) {
+  return make_uint2(pack_e4m3x2(x[0] * scale, x[1] * scale) | pack_e4m3x2(x[2] * scale, x[3] * scale) << 16,
+                    pack_e4m3x2(x[4] * scale, x[5] * scale) | pack_e4m3x2(x[6] * scale, x[7] * scale) << 16);
+}
 // 16 elements of a row: two runs of 8, or one of 16.
 __device__ __forceinline__ void store16_e4m3(uint8_t* row, int e0, int e1, const float (&x0)[8], const float (&x1)[8],
                                              float scale) {
