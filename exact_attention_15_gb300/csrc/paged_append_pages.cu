@@ -1,7 +1,7 @@
 // Appends new tokens to a paged e4m3 cache that has a power of two for each page and KV head:
-// a stored value x stands for x 2^e. e is the smallest with which 448 2^e reaches the largest
-// finite magnitude that was written to the page and head, so nothing saturates and no value
-// loses bits for the size of another page's or head's. Where new tokens need a larger e than the
+// a stored value x stands for x 2^e. e is the smallest from kMinExp to kMaxExp with which 448 2^e reaches
+// the largest finite magnitude that was written to the page and head, so finite values saturate above
+// 448 2^24 = 7.5e9 alone, and none loses bits for the size of another page's or head's. Where new tokens need a larger e than the
 // page has, its rows are encoded again; a power of two costs them bits only below 2^-6 of the
 // stored range.
 //

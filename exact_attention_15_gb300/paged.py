@@ -312,7 +312,8 @@ def paged_forward(cache, q, page_table, kv_lens, cu_seqlens, scale=None, causal=
     them already: q [T, H_q, d] bf16, packed by cu_seqlens. With causal, the last new
     token sees all keys of its sequence and each one before sees one key less.
     Returns (o [T, H_q, d], lse [H_q, T]); rows behind the last sequence are not
-    written."""
+    written. Over pages with scales chunks of few rows or little work hold the weights to 11 bits
+    and larger ones to 8, as over a bf16 cache (attn_paged_fwd in include/attn.h says which)."""
     if out is None and lse is None and workspace is None:
         r = cache._calls.forward(cache._ref, cache._index, cache.device, q, page_table, kv_lens, cu_seqlens, scale,
                                  causal)

@@ -263,9 +263,12 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  * device arrays of num_pages * H_kv bytes (the E8M0 format of scales): an x of page p and
  * head h stands for x * 2^(k_exp[p * H_kv + h] - 127). attn_paged_append finds them and writes
  * exponents from -64 to 24; others count as the nearest of these. The scale arrays are not
- * read. For few tokens attention holds the weight of a stored value (what softmax gives its key,
- * times its page's power of two) to 11 bits, and those below 2^-21 of a row's largest to 2^-32
- * of that; for chunks, softmax's weight to 8 bits, as over a bf16 cache.
+ * read. How the weights enter their product with the values depends on the kernel that a call takes
+ * (attn_paged_fwd says which): the streaming kernel (attn_paged_decode, chunks of few rows or of little
+ * work) holds the weight of a stored value (what softmax gives its key, times its page's power of two)
+ * to 11 bits, and those below 2^-21 of a row's largest to 2^-32 of that, so that beside a page whose
+ * scale is 2^21 times larger small values lose bits; the tensor-core kernel (larger chunks) holds
+ * softmax's weight to 8 bits, as over a bf16 cache, however the pages' scales differ.
  *
  * Sequences are described by device arrays that the host does not read:
  *   kv_lens     int32 [B]: keys of each sequence, its new tokens among them
@@ -414,7 +417,8 @@ int attn_paged_bounds(const attn_paged_cache* cache, void* bounds, int T, int B,
  * the keep_last (>= 1) last are taken, and of the others those with the largest
  *   max over the query heads of the KV head of  sum_i max(q_i, 0) hi_i + min(q_i, 0) lo_i
  * with lo and hi from `bounds` (attn_paged_bounds): no key of a page has a larger product with
- * any of these queries. Decided as in 64 bits; equal values go to the lower page, a NaN is
+ * any of these queries where the bounds are exact (with ATTN_CACHE_E4M3, whose bounds are rounded to
+ * nearest, none larger by more than 2^-8 sum_i |q_i| max(|lo_i|, |hi_i|)). Decided as in 64 bits; equal values go to the lower page, a NaN is
  * above all numbers. pages (int32 [T, H_kv, count]) gets their page indices in the order of the
  * keys, -1 behind the last one; lens (int32 [T]) how many keys they hold (the last page is always
  * chosen, so the lists are attn_paged_decode_lists' for B = T sequences). A token that sees no key
