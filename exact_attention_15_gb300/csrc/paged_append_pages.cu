@@ -10,7 +10,7 @@
 // rounding of the angles, and known before a single angle is.
 //
 // Few new tokens per sequence (paged_append_few_kernel): a warp for each (page, KV head, K or V)
-// holds the new rows in registers, finds their largest magnitude, looks up what the page has, and turns,
+// holds the new rows (the first 16 of 128) in registers, finds their largest magnitude, looks up what the page has, and turns,
 // scales and stores; the last CTAs of the grid turn the queries, a token on 8 to 128 threads.
 //
 // More (paged_append_rows_kernel): a cluster for each page and 8 KV heads of 128 (16 of 64), a CTA for
@@ -522,8 +522,15 @@ cudaError_t launch_rows(const AppendParams& p, const CUtensorMap& tk, const CUte
 
 }  // namespace
 
-// Up to 16 new tokens of each sequence on the mean a warp has them in registers.
-bool append_by_rows(const PagedSeqs& s) { return s.cu_seqlens && s.T > 16ll * s.B; }
+// By rows where the sequences have more than 24 new tokens on the mean. By rows a sequence's pages cost
+// clusters that are mostly empty, with a warp for each page and head the angles are computed for every head and
+// rows beyond the 16 that it holds are read twice. us with few / by rows, 48 sequences, 32 query and 8 KV heads
+// of 128: 17 tokens in pages of 64 8.1 / 18.9, 24 in pages of 16 8.6 / 14.5, 32 in pages of 64 12.5 / 22.6 and
+// without queries 11.0 / 11.4, 64 21.7 / 26.1 and 19.9 / 12.4, 128 in pages of 256 51 / 70 and 40 / 34. One KV
+// head of 128 without queries, pages of 32: 17 tokens 6.3 / 6.0, 32 7.6 / 6.0; 4 sequences of 256 tokens in
+// pages of 128 30 / 14. So 24 is where neither costs more than 4%. A prompt of 4000 tokens beside 200 single
+// ones, which the mean sends the first way, 25 / 36; beside 100, which it sends the second, 26 / 27.
+bool append_by_rows(const PagedSeqs& s) { return s.cu_seqlens && s.T > 24ll * s.B; }
 int append_box_heads(int H_kv, int d) {
   const int most = kRowBytes / (kRows * 4 * d), groups = (H_kv + most - 1) / most;  // 8 of 128, 16 of 64
   return (H_kv + groups - 1) / groups;
