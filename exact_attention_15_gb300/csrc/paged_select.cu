@@ -146,8 +146,10 @@ cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
 // 3. The products are exact, their sums are not: with eps a bound on the sums' error, pages
 //    more than 2 eps above the interval are chosen for certain, pages more than 2 eps below it are
 //    not, and the few between are scored again: as 64-bit integers, in units of 2^-61 of what
-//    the sums can be, so that they do not depend on an order (in 64-bit floating point where
-//    the inputs are no such numbers). Ties go to the lower page.
+//    the sums can be, so that they do not depend on an order (in 64-bit floating point where the sums
+//    are outside [2^-40, 2^100] or a query has an infinity). Ties go to the lower page. A page with an
+//    infinity or a NaN among its bounds has a key of its own and leaves the others what they are (one of
+//    4096 pages: 14 us; 8700 while it sent all to the second scores).
 // 4. The chosen pages are written in their order.
 template <int THREADS>  // (one warp has 160 pages at most)
 constexpr int select_bins = THREADS == 32 ? 256 : 1024;
@@ -159,8 +161,8 @@ constexpr int kPairs = 64;
 // is below 136 * 2^-23 + 2^-24 = 1.63e-5. (On random products, some a thousand times the others, the
 // largest seen was 2.3e-6 after eight instructions.)
 constexpr float kSumError = 1.75e-5f;
-// Sums below this stay finite, so that no score is an infinity or a NaN; above the other, what
-// products below the normal numbers lose (256 times 2^-126 at most) is less than 2^-77 of it.
+// Sums of numbers below this stay finite; above the other, what products below the normal numbers lose (256
+// times 2^-126 at most) is less than 2^-77 of it.
 constexpr float kLargest = 1.2676506e30f, kSmallest = 9.0949470e-13f;  // 2^100, 2^-40
 
 // An order of floats as unsigned numbers; NaN above all.
@@ -177,6 +179,10 @@ __device__ __forceinline__ long long ordered(double x) {  // (signed)
   return b ^ static_cast<long long>(static_cast<unsigned long long>(b >> 63) >> 1);
 }
 constexpr long long kNoKey = -0x7fffffffffffffffll - 1;  // below them all
+// The key of a score that is no number, next to those in units of 2^-61 (below 2^62 in magnitude).
+__device__ __forceinline__ long long key_of_none(float x) {
+  return x != x ? 0x7fffffffffffffffll : x > 0.0f ? 0x7ffffffffffffffell : kNoKey;
+}
 // x (below 2^61 in magnitude) rounded to an integer, by two conversions to 32 bits: one to 64
 // runs at a fraction of their rate.
 __device__ __forceinline__ long long in_units(float x) {
@@ -184,6 +190,13 @@ __device__ __forceinline__ long long in_units(float x) {
   const int low = __float2int_rn(fmaf(static_cast<float>(high), -2147483648.0f, x));
   return (static_cast<long long>(high) << 31) + low;
 }
+// The larger, a NaN above all.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < INFINITY; }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
@@ -404,6 +417,17 @@ paged_select_kernel(const SelectParams p) {
   uint32_t k_most = 0;
   float least = INFINITY, most = -INFINITY;
   bool ok = true;
+  // The largest magnitude among the numbers of page i's bounds, this lane's quarter of them.
+  auto numbers_of = [&](int i) {
+    const int id = checked_page(s, __ldg(table + begin + min(i, n - 1)));
+    const uint32_t* at = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * D + qd * (D / 4);
+    uint32_t most = 0;
+    for (int x = 0; x < D / 4; ++x) {
+      const uint32_t w = __ldg(at + x) & 0x7fff7fffu;
+      most = __vmaxu2(most, w & ~__vcmpgeu2(w, 0x7f807f80u));
+    }
+    return most;
+  };
   for (int k = 0; k < my_tiles; ++k) {
     const int i0 = (warp + k * kSelWarps) * 16 + ar;
     // After a wait that ran out nothing more is copied, what is on its way is waited for once
@@ -415,6 +439,7 @@ paged_select_kernel(const SelectParams p) {
     }
     const uint8_t* pages_at = tile + ar * kStride + qd * 16;
     float best[2] = {-INFINITY, -INFINITY};
+    uint32_t page_most[2] = {0, 0};  // of this lane's columns
     for (int nt = 0; nt < q_tiles; ++nt) {
       const uint8_t* rows = qs + (nt * 8 + ar) * kStride + qd * 16;
       float acc[2][4];
@@ -435,13 +460,13 @@ paged_select_kernel(const SelectParams p) {
           for (int u = 0; u < 2; ++u) {
             const uint32_t x = __vmaxu2(a[u].x & 0x7fff7fffu, a[u].y & 0x7fff7fffu);
             const uint32_t y = __vmaxu2(a[u].z & 0x7fff7fffu, a[u].w & 0x7fff7fffu);
-            k_most = __vmaxu2(k_most, __vmaxu2(x, y));
+            page_most[u] = __vmaxu2(page_most[u], __vmaxu2(x, y));
           }
         }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (nt * 8 + 2 * qd + (e & 1) < p.group) best[e >> 1] = fmaxf(best[e >> 1], acc[0][e] + acc[1][e]);
+        if (nt * 8 + 2 * qd + (e & 1) < p.group) best[e >> 1] = max_nan(best[e >> 1], acc[0][e] + acc[1][e]);
     }
     __syncwarp();
     if (ok && k + 1 < my_tiles) {
@@ -450,14 +475,20 @@ paged_select_kernel(const SelectParams p) {
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], 1));
-      best[u] = fmaxf(best[u], __shfl_xor_sync(0xffffffffu, best[u], 2));
+      best[u] = max_nan(best[u], __shfl_xor_sync(0xffffffffu, best[u], 1));
+      best[u] = max_nan(best[u], __shfl_xor_sync(0xffffffffu, best[u], 2));
       if (!ok) best[u] = 0.0f;
       const int i = i0 + 8 * u;
+      // A page with an infinity or a NaN among its bounds has a score that is none either, whatever the
+      // queries: it is no part of the scores' range, and of its bounds those that are numbers count.
+      if (!is_finite(best[u])) page_most[u] = numbers_of(i);
+      k_most = __vmaxu2(k_most, page_most[u]);
       if (i < n) {
         if (qd == 0) st_cluster_f32(scores_to + 4 * spread(score0 + i), best[u]);
-        least = fminf(least, best[u]);
-        most = fmaxf(most, best[u]);
+        if (is_finite(best[u])) {
+          least = fminf(least, best[u]);
+          most = fmaxf(most, best[u]);
+        }
       }
     }
   }
@@ -495,18 +526,24 @@ paged_select_kernel(const SelectParams p) {
   };
 
   // ---- the interval [lo, hi] of the last score to be chosen
-  const float size = __uint_as_float(sh.l1) * __uint_as_float(sh.k_most);  // of the products' sums at most
-  // every product is zero (none of 0 and an infinity or a NaN, which makes `size` NaN); else sums outside
-  // these bounds are taken in floating point alone
-  const bool zero = (sh.l1 == 0 || sh.k_most == 0) && size == 0.0f;
-  const bool finite = zero || (size < kLargest && size > kSmallest);
+  // Every page whose bounds are numbers has a score of zero, or, where a query row has a NaN, every page one
+  // that is none; else sums outside these bounds are taken in floating point alone. With queries that are
+  // numbers and sums within the bounds a score is no number only for a page whose bounds are none, and then
+  // that of the exact sum: such pages are never chosen for certain, but by a key of their own.
+  const float l1 = __uint_as_float(sh.l1);
+  const float product = l1 * __uint_as_float(sh.k_most);  // of the products' sums at most
+  const bool same = l1 != l1 || (product == 0.0f && (sh.l1 == 0 || sh.k_most == 0));
+  const float size = same ? 0.0f : product;
+  const bool finite = same || (size < kLargest && size > kSmallest);
   const float eps = size * kSumError;
   float lo = unordered(~sh.least), hi = unordered(sh.most);
   const float range = hi - lo;
   if (finite && range > eps) {
     // (bins by the same rounded expression for every page, so their order is that of the scores)
     const float low = lo, inv = kBins / range;
-    auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((x - low) * inv)); };
+    // (plus infinity and NaN to the top, minus infinity to the bottom)
+    auto bin_at = [](float at) { return static_cast<int>(fmaxf(0.0f, fminf(at, kBins - 1.0f))); };
+    auto bin_of = [&](float x) { return bin_at((x - low) * inv); };
     for (int i = tid; i < n; i += kSelThreads) atomicAdd(&sh.hist[bin_of(score[spread(i)])], 1u);
     sync();
     find_bin<kBins / kSelThreads>(sh, cluster, room);
@@ -517,7 +554,7 @@ paged_select_kernel(const SelectParams p) {
     // a bin far wider than eps (a few scores far from the rest): its own pages again
     if (range > 65536.0f * eps) {
       const float low2 = lo, inv2 = kBins / (range / kBins);
-      auto bin2_of = [&](float x) { return max(0, min(kBins - 1, static_cast<int>((x - low2) * inv2))); };
+      auto bin2_of = [&](float x) { return bin_at((x - low2) * inv2); };
       sync();
       for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
       __syncthreads();
@@ -540,14 +577,16 @@ paged_select_kernel(const SelectParams p) {
 #pragma unroll 4
   for (int i = 0; i < run_n; ++i) {
     const float x = score[spread(run0 + i)];
-    const bool sure = finite && x > high_cut;
+    const bool number = finite && is_finite(x), sure = number && x > high_cut;
     chosen |= static_cast<uint32_t>(sure) << i;
-    unsure |= static_cast<uint32_t>(!sure && !(finite && x < low_cut)) << i;
+    unsure |= static_cast<uint32_t>(!sure && !(number && x < low_cut)) << i;
   }
   for (uint32_t left = unsure; left; left &= left - 1) {
     const uint32_t at = atomicAdd(&sh.unsure, 1u);
-    list[at] = run0 + __ffs(left) - 1;
-    list_key[at] = kNoKey;
+    const int i = run0 + __ffs(left) - 1;
+    const float x = score[spread(i)];
+    list[at] = i;
+    list_key[at] = finite && !is_finite(x) ? key_of_none(x) : same ? 0 : kNoKey;
   }
   const uint32_t sures = __reduce_add_sync(0xffffffffu, __popc(chosen));
   if (lane == 0 && sures) atomicAdd(&sh.sure, sures);
@@ -558,7 +597,7 @@ paged_select_kernel(const SelectParams p) {
     for (int e = tid; e < mine; e += kSelThreads) score[spread(list[e])] = INFINITY;
     if (tid == 0) sh.chosen = mine;
   } else {
-    if (!zero) {
+    if (!same) {
       // 2^62 over a power of two that the sums' magnitudes stay below
       const int top = static_cast<int>(__float_as_uint(size) >> 23) - 126;
       const float unit = power_of_two(max(-126, min(126, 61 - top)));
@@ -578,6 +617,7 @@ paged_select_kernel(const SelectParams p) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) y[i] = next[i];
         if (x + kSelWarps < mine * quads) load(x + kSelWarps);
+        if (finite && !is_finite(score[spread(list[e])])) continue;  // (has its key)
         long long key = kNoKey;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
