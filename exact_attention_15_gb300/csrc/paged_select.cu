@@ -149,7 +149,7 @@ cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
 //    the sums can be, so that they do not depend on an order (in 64-bit floating point where the sums
 //    are outside [2^-40, 2^100] or a query has an infinity). Ties go to the lower page. A page with an
 //    infinity or a NaN among its bounds has a key of its own and leaves the others what they are (one of
-//    4096 pages: 14 us; 8700 while it sent all to the second scores).
+//    4096 pages: 19 us, none 14; 8700 while it sent all to the second scores).
 // 4. The chosen pages are written in their order.
 template <int THREADS>  // (one warp has 160 pages at most)
 constexpr int select_bins = THREADS == 32 ? 256 : 1024;
@@ -224,6 +224,7 @@ struct SelectShared {
   uint32_t l1, k_most;       // largest sum of a query row's magnitudes; largest magnitude of the bounds
   uint32_t least, most;      // scores, ordered (the least as its complement)
   uint32_t sure, unsure, chosen;
+  uint32_t none;             // some bounds are infinities or NaN
   uint32_t bin, above;       // the bin that was looked for, and what lies above it
   uint32_t warp_sum[THREADS / 32];
   uint64_t full[THREADS / 32];
@@ -299,7 +300,7 @@ paged_select_kernel(const SelectParams p) {
   for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
   if (tid == 0) {
     sh.l1 = sh.k_most = sh.most = sh.least = 0;
-    sh.sure = sh.unsure = sh.chosen = 0;
+    sh.sure = sh.unsure = sh.chosen = sh.none = 0;
   }
   const uint32_t full = smem_addr(&sh.full[warp]);
   if (lane == 0) {
@@ -417,17 +418,6 @@ paged_select_kernel(const SelectParams p) {
   uint32_t k_most = 0;
   float least = INFINITY, most = -INFINITY;
   bool ok = true;
-  // The largest magnitude among the numbers of page i's bounds, this lane's quarter of them.
-  auto numbers_of = [&](int i) {
-    const int id = checked_page(s, __ldg(table + begin + min(i, n - 1)));
-    const uint32_t* at = static_cast<const uint32_t*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * D + qd * (D / 4);
-    uint32_t most = 0;
-    for (int x = 0; x < D / 4; ++x) {
-      const uint32_t w = __ldg(at + x) & 0x7fff7fffu;
-      most = __vmaxu2(most, w & ~__vcmpgeu2(w, 0x7f807f80u));
-    }
-    return most;
-  };
   for (int k = 0; k < my_tiles; ++k) {
     const int i0 = (warp + k * kSelWarps) * 16 + ar;
     // After a wait that ran out nothing more is copied, what is on its way is waited for once
@@ -439,7 +429,6 @@ paged_select_kernel(const SelectParams p) {
     }
     const uint8_t* pages_at = tile + ar * kStride + qd * 16;
     float best[2] = {-INFINITY, -INFINITY};
-    uint32_t page_most[2] = {0, 0};  // of this lane's columns
     for (int nt = 0; nt < q_tiles; ++nt) {
       const uint8_t* rows = qs + (nt * 8 + ar) * kStride + qd * 16;
       float acc[2][4];
@@ -460,7 +449,7 @@ paged_select_kernel(const SelectParams p) {
           for (int u = 0; u < 2; ++u) {
             const uint32_t x = __vmaxu2(a[u].x & 0x7fff7fffu, a[u].y & 0x7fff7fffu);
             const uint32_t y = __vmaxu2(a[u].z & 0x7fff7fffu, a[u].w & 0x7fff7fffu);
-            page_most[u] = __vmaxu2(page_most[u], __vmaxu2(x, y));
+            k_most = __vmaxu2(k_most, __vmaxu2(x, y));
           }
         }
       }
@@ -479,18 +468,41 @@ paged_select_kernel(const SelectParams p) {
       best[u] = max_nan(best[u], __shfl_xor_sync(0xffffffffu, best[u], 2));
       if (!ok) best[u] = 0.0f;
       const int i = i0 + 8 * u;
-      // A page with an infinity or a NaN among its bounds has a score that is none either, whatever the
-      // queries: it is no part of the scores' range, and of its bounds those that are numbers count.
-      if (!is_finite(best[u])) page_most[u] = numbers_of(i);
-      k_most = __vmaxu2(k_most, page_most[u]);
       if (i < n) {
         if (qd == 0) st_cluster_f32(scores_to + 4 * spread(score0 + i), best[u]);
-        if (is_finite(best[u])) {
-          least = fminf(least, best[u]);
-          most = fmaxf(most, best[u]);
-        }
+        least = fminf(least, best[u]);
+        most = fmaxf(most, best[u]);
       }
     }
+  }
+  // A page with an infinity or a NaN among its bounds has a score that is none either, whatever the queries: it
+  // is no part of the scores' range, and of its bounds those that are numbers count. Where this warp has
+  // met one its pages are gone through again, a lane for each.
+  if (__any_sync(0xffffffffu, __vcmpgeu2(k_most, 0x7f807f80u))) {
+    __syncwarp();  // (its lanes read each other's scores)
+    k_most = 0;
+    least = INFINITY;
+    most = -INFINITY;
+    for (int k = 0; k < my_tiles; ++k) {
+      const int i = (warp + k * kSelWarps) * 16 + (lane & 15);
+      if (i >= n) continue;
+      const int id = checked_page(s, __ldg(table + begin + i));
+      const uint4* at = static_cast<const uint4*>(p.bounds) + (static_cast<size_t>(id) * p.H_kv + h) * (D / 4);
+#pragma unroll 4
+      for (int x = 0; x < D / 4; ++x) {
+        const uint4 y = __ldg(at + x);
+        const uint32_t w[4] = {y.x & 0x7fff7fffu, y.y & 0x7fff7fffu, y.z & 0x7fff7fffu, y.w & 0x7fff7fffu};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k_most = __vmaxu2(k_most, w[e] & ~__vcmpgeu2(w[e], 0x7f807f80u));
+      }
+      const float x = __uint_as_float(ld_cluster_u32(scores_to + 4 * spread(score0 + i)));
+      if (is_finite(x)) {
+        least = fminf(least, x);
+        most = fmaxf(most, x);
+      }
+    }
+    if (lane == 0)
+      for (int r = 0; r < (p.gather ? 1 : ctas); ++r) max_cluster_u32(cluster_map(smem_addr(&sh.none), r), 1u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -535,6 +547,7 @@ paged_select_kernel(const SelectParams p) {
   const bool same = l1 != l1 || (product == 0.0f && (sh.l1 == 0 || sh.k_most == 0));
   const float size = same ? 0.0f : product;
   const bool finite = same || (size < kLargest && size > kSmallest);
+  const bool none = finite && (sh.none || l1 != l1);  // some scores are no numbers
   const float eps = size * kSumError;
   float lo = unordered(~sh.least), hi = unordered(sh.most);
   const float range = hi - lo;
@@ -544,7 +557,12 @@ paged_select_kernel(const SelectParams p) {
     // (plus infinity and NaN to the top, minus infinity to the bottom)
     auto bin_at = [](float at) { return static_cast<int>(fmaxf(0.0f, fminf(at, kBins - 1.0f))); };
     auto bin_of = [&](float x) { return bin_at((x - low) * inv); };
-    for (int i = tid; i < n; i += kSelThreads) atomicAdd(&sh.hist[bin_of(score[spread(i)])], 1u);
+    if (none) {
+      for (int i = tid; i < n; i += kSelThreads) atomicAdd(&sh.hist[bin_of(score[spread(i)])], 1u);
+    } else {  // (the same of numbers)
+      for (int i = tid; i < n; i += kSelThreads)
+        atomicAdd(&sh.hist[min(kBins - 1, static_cast<int>((score[spread(i)] - low) * inv))], 1u);
+    }
     sync();
     find_bin<kBins / kSelThreads>(sh, cluster, room);
     const int bin = sh.bin;
@@ -574,19 +592,23 @@ paged_select_kernel(const SelectParams p) {
   // ---- pages chosen for certain, and those to be scored again: a run of up to 32 a thread
   const int run = (n + kSelThreads - 1) / kSelThreads, run0 = tid * run, run_n = max(0, min(run, n - run0));
   uint32_t chosen = 0, unsure = 0;  // of the run, a bit each
+  auto cut = [&](auto numbers) {
 #pragma unroll 4
-  for (int i = 0; i < run_n; ++i) {
-    const float x = score[spread(run0 + i)];
-    const bool number = finite && is_finite(x), sure = number && x > high_cut;
-    chosen |= static_cast<uint32_t>(sure) << i;
-    unsure |= static_cast<uint32_t>(!sure && !(number && x < low_cut)) << i;
-  }
+    for (int i = 0; i < run_n; ++i) {
+      const float x = score[spread(run0 + i)];
+      const bool number = finite && (decltype(numbers)::value || is_finite(x)), sure = number && x > high_cut;
+      chosen |= static_cast<uint32_t>(sure) << i;
+      unsure |= static_cast<uint32_t>(!sure && !(number && x < low_cut)) << i;
+    }
+  };
+  if (none) cut(std::false_type{});
+  else cut(std::true_type{});
   for (uint32_t left = unsure; left; left &= left - 1) {
     const uint32_t at = atomicAdd(&sh.unsure, 1u);
     const int i = run0 + __ffs(left) - 1;
     const float x = score[spread(i)];
     list[at] = i;
-    list_key[at] = finite && !is_finite(x) ? key_of_none(x) : same ? 0 : kNoKey;
+    list_key[at] = none && !is_finite(x) ? key_of_none(x) : same ? 0 : kNoKey;
   }
   const uint32_t sures = __reduce_add_sync(0xffffffffu, __popc(chosen));
   if (lane == 0 && sures) atomicAdd(&sh.sure, sures);
@@ -617,7 +639,7 @@ paged_select_kernel(const SelectParams p) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) y[i] = next[i];
         if (x + kSelWarps < mine * quads) load(x + kSelWarps);
-        if (finite && !is_finite(score[spread(list[e])])) continue;  // (has its key)
+        if (none && !is_finite(score[spread(list[e])])) continue;  // (has its key)
         long long key = kNoKey;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
